@@ -310,6 +310,166 @@ int moe_router_topk_noalloc(void* stream, const void* router_w, const float* rou
  * the device, then clears the word. */
 int moe_router_topk_noalloc_status(int* device_status);
 
+/* ---- Serving operators beside the layer ----
+ * Block tables, an 8-bit KV cache with its attention, and expert routing from
+ * logits, for the parts of a decode step around moe_decode_forward (no
+ * counterpart in the pages, which describe the MoE half of a layer; the
+ * formulas are the plain ones stated at each call).  They need no handle:
+ * every call is asynchronous on `stream`, allocates nothing, never
+ * synchronises the host and may be captured into a CUDA graph.  Lengths live
+ * on the device, so a captured graph follows them.  A call checks what the
+ * host can see (null pointers, sizes, alignment) and reports it as a status;
+ * values it reads on the device (lengths, block ids, slots) are bounded there
+ * as each call states, so that no value makes it read or write out of range.
+ * A CUDA error already pending when a call starts is returned (MOE_ERR_CUDA)
+ * and nothing is launched.  Limits: 16,384 rows (requests) per call; device
+ * sm_103, else UNSUPPORTED. */
+
+/* Element type of queries, new keys and values, outputs and logits. */
+typedef enum {
+  MOE_DTYPE_BF16 = 0,
+  MOE_DTYPE_F16 = 1,
+  MOE_DTYPE_F32 = 2    /* logits of moe_route only */
+} moe_dtype;
+
+/* A paged KV cache in 8 bits.  Tokens live in blocks of block_size (16, 32,
+ * 64 or 128); element (block b, KV head h, token t of the block, dim j) of K
+ * is the E4M3 code at k[b * block_stride + h * head_stride + t * token_stride
+ * + j] and stands for code * 2^(k_scale[b * scale_stride + h] - 127): one
+ * E8M0 scale per (block, head), within 2^-60 .. 2^60 (bytes 67 .. 187; a byte
+ * outside reads as the nearest of these).  V likewise.  Strides are in bytes;
+ * block, head and token strides and the k and v pointers are multiples of 16,
+ * so blocks may be head-major or token-major, or views of one larger tensor.
+ * head_dim is 64 or 128; n_blocks * block_size < 2^31. */
+typedef struct {
+  uint8_t* k;
+  uint8_t* v;
+  uint8_t* k_scale;
+  uint8_t* v_scale;
+  int64_t block_stride, head_stride, token_stride;
+  int64_t scale_stride;
+  int32_t n_blocks, n_kv_heads, block_size, head_dim;
+} moe_kv_cache_t;
+
+/* Block tables and slot maps of one step, from request lengths.  Row r holds
+ * ctx_lens[r] cached tokens (in the first ceil(ctx / block_size) entries of
+ * its block_table row) and gets q_lens[r] new ones.  New blocks are taken in
+ * row order from the top of the stack free_list[0 .. *n_free): the i-th new
+ * block of the step is free_list[*n_free - 1 - i].  A row is served when its
+ * blocks fit max_blocks, its tokens (if any) fit n_slots and the stack still holds all
+ * the new blocks it needs (once the stack is short, later rows that need
+ * none are still served); a negative length leaves a row unserved, with no
+ * tokens.  Writes, with q_start[r] the sum of the q_lens before r:
+ *  - block_table: a served row's new entries; all others keep their values,
+ *  - seq_lens [n_rows]: ctx + q of a served row, ctx (0 if negative) of others,
+ *  - q_start [n_rows + 1],
+ *  - slot_map [n_slots]: token i of row r goes to slot
+ *    block * block_size + offset, at q_start[r] + i; -1 for the tokens of
+ *    unserved rows and past the last row,
+ *  - *n_free_out: blocks left on the stack, *n_unserved: rows not served.
+ * Outputs must not overlap inputs (n_free_out is not n_free).  Rows of
+ * block_table are table_stride entries apart.  *n_free is read as at most
+ * free_cap, the entries of free_list.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+int moe_kv_plan(void* stream, const int32_t* ctx_lens, const int32_t* q_lens, int n_rows,
+                int32_t* block_table, int64_t table_stride, int max_blocks,
+                const int32_t* free_list, int free_cap, const int32_t* n_free, int block_size,
+                int32_t* seq_lens, int32_t* q_start, int32_t* slot_map, int n_slots,
+                int32_t* n_free_out, int32_t* n_unserved);
+
+/* Give back the blocks of finished rows: for every row with finished[r] != 0,
+ * in row order, its ceil(seq_lens[r] / block_size) blocks are pushed on the
+ * stack free_list[0 .. *n_free) and seq_lens[r] becomes 0.  *n_free_out is the
+ * stack's new height (n_free_out may be n_free); pushes past free_cap are
+ * dropped.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+int moe_kv_release(void* stream, const uint8_t* finished, int n_rows, int32_t* seq_lens,
+                   const int32_t* block_table, int64_t table_stride, int max_blocks,
+                   int32_t* free_list, int free_cap, const int32_t* n_free, int block_size,
+                   int32_t* n_free_out);
+
+/* Write the keys and values of n_tokens new tokens into the cache.  k, v
+ * device [n_tokens][n_kv_heads][head_dim] of `dtype` (BF16 or F16), token and
+ * head strides in elements (multiples of 8; pointers 16-byte aligned), rows
+ * contiguous.  slot_map device [n_tokens]: block * block_size + offset per
+ * token; -1 (or any slot outside the cache) skips the token.  The tokens a
+ * step writes into one block are consecutive in the slot map, at consecutive
+ * ascending offsets, and the block holds the sequence's earlier tokens below
+ * them (what moe_kv_plan makes).  Per block, head and side: e is the smallest
+ * integer with max |finite value| <= 448 * 2^e, at least -60, at most 60; a
+ * block that already held tokens keeps its exponent if that is larger, and
+ * otherwise has their codes rounded to the new one.  Codes are value / 2^e
+ * rounded to the nearest E4M3 (ties to even), past 448 (infinities too) to
+ * 448; NaN stays NaN.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+int moe_kv_append(void* stream, const moe_kv_cache_t* cache, const void* k, const void* v,
+                  int dtype, int64_t k_token_stride, int64_t k_head_stride,
+                  int64_t v_token_stride, int64_t v_head_stride, const int32_t* slot_map,
+                  int n_tokens);
+
+/* Attention of new tokens over the cache.  Row r's queries are tokens
+ * q_start[r] .. q_start[r + 1) of q, the last of its seq_lens[r] cached tokens
+ * (query i of n sits at position p = seq_len - n + i; their keys are in the
+ * cache already).  Query head h reads KV head h / (n_heads / n_kv_heads).  A
+ * query sees the keys j < seq_len with j <= p (causal != 0) and j > p - window
+ * (window > 0), and not those of a block id outside the cache:
+ *   out = sum_j softmax_j(scale * q . k_j) v_j,  lse = ln sum_j exp(scale * q . k_j)
+ * (out 0 and lse -infinity when it sees none).  Keys and values it does not
+ * see do not reach its result, whatever they hold.  Products and sums are
+ * exact products summed in fp32; the probabilities enter the second product
+ * rounded to f16.
+ * seq_lens is read as at most max_blocks * block_size and q_start as within
+ * [0, n_tokens], not descending; rows of q past q_start[n_rows] are left
+ * alone.  max_q, the longest row's queries as the host knows it, only picks
+ * the kernel: any value gives the same result up to rounding. */
+typedef struct {
+  const void* q;            /* device [n_tokens][n_heads][head_dim] */
+  int64_t q_token_stride, q_head_stride;      /* elements, multiples of 8 */
+  void* out;                /* device, the same shape and type */
+  int64_t out_token_stride, out_head_stride;  /* elements, multiples of 8 */
+  float* lse;               /* device [n_tokens][n_heads], or NULL */
+  const int32_t* block_table;                 /* device [n_rows][max_blocks] */
+  int64_t table_stride;
+  const int32_t* seq_lens;  /* device [n_rows] */
+  const int32_t* q_start;   /* device [n_rows + 1] */
+  void* workspace;          /* device, moe_kv_attention_workspace bytes, 256-byte aligned */
+  size_t workspace_bytes;
+  int32_t dtype;            /* BF16 or F16 */
+  int32_t n_rows, n_tokens, n_heads, max_blocks, max_q;
+  int32_t causal;
+  int32_t window;           /* 0: none */
+  float scale;
+} moe_kv_attention_t;
+
+/* Errors: INVALID_ARG, UNSUPPORTED, ALLOC (workspace too small), CUDA.  The
+ * workspace holds nothing between calls; calls that overlap need one each. */
+int moe_kv_attention(void* stream, const moe_kv_cache_t* cache, const moe_kv_attention_t* args);
+
+/* Bytes of workspace moe_kv_attention needs on the current device, whatever
+ * the lengths (0 on error). */
+size_t moe_kv_attention_workspace(int head_dim);
+
+/* Expert routing from logits, for any number of rows.  Per row: score s_e =
+ * sigmoid(l_e) or softmax(l)_e in fp32 (all of a softmax row at -infinity:
+ * scores 0); experts are compared by s_e + bias_e (bias NULL: s_e).  With
+ * n_groups > 1 the experts form n_groups equal consecutive groups, a group
+ * counts with the sum of its group_top (1 or 2) best, and only the experts of
+ * the topk_groups best groups are left.  The top_k best are written in
+ * descending order; ties, of groups too, go to the lower index, and a NaN
+ * comes after everything else.  Weights are the unbiased scores, divided by
+ * their sum if renormalize (0 when the sum is 0), times routed_scale. */
+typedef struct {
+  int32_t n_experts;        /* <= 1024, a multiple of n_groups */
+  int32_t top_k;            /* <= 32, <= topk_groups * (n_experts / n_groups) */
+  int32_t scoring;          /* 0 sigmoid, 1 softmax */
+  int32_t n_groups, topk_groups, group_top;   /* n_groups <= 32 */
+  int32_t renormalize;
+  float routed_scale;
+} moe_route_t;
+
+/* logits device [n_rows][n_experts] of `dtype`, rows row_stride elements
+ * apart; bias device fp32 [n_experts] or NULL; idx device int32 and w device
+ * fp32 [n_rows][top_k].  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+int moe_route(void* stream, const moe_route_t* cfg, const void* logits, int dtype,
+              int64_t row_stride, int64_t n_rows, const float* bias, int32_t* idx, float* w);
+
 /* Human-readable name of a status code (static string). */
 const char* moe_status_string(int status);
 

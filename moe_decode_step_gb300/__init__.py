@@ -1,5 +1,7 @@
 """GB300-native (sm_103a) MoE decode layer: router + biased top-k, MXFP4 routed
-SwiGLU experts with weighted combine, bf16 shared expert, residual + RMSNorm.
+SwiGLU experts with weighted combine, bf16 shared expert, residual + RMSNorm;
+beside it the serving operators of a decode step (serving.py): block tables and
+slot maps, an 8-bit KV cache with its attention, expert routing from logits.
 
 The compute path is the CUDA library `libmoe_decode.so` behind the C ABI in
 include/moe_decode.h; this package only marshals arguments (PyTorch tensors
@@ -13,7 +15,9 @@ from ._binding import (MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR
                        MOE_ERR_ALLOC, MOE_ERR_TIMEOUT, MoEDims, MoEError, MoEWeights, check, lib,
                        status_string)
 
-__all__ = ["MoELayer", "MoEDims", "MoEWeights", "MoEError", "mxfp4_pack", "mxfp4_pack_device",
+from .serving import KVCache, KVPlan, kv_plan, kv_release, moe_route
+
+__all__ = ["KVCache", "KVPlan", "kv_plan", "kv_release", "moe_route", "MoELayer", "MoEDims", "MoEWeights", "MoEError", "mxfp4_pack", "mxfp4_pack_device",
            "mxfp4_repack", "mxfp4_retile_device",
            "mxfp4_packed_bytes", "status_string", "lib", "MOE_OK", "MOE_ERR_INVALID_ARG",
            "MOE_ERR_UNSUPPORTED", "MOE_ERR_CUDA", "MOE_ERR_ALLOC", "MOE_ERR_TIMEOUT"]

@@ -5,6 +5,7 @@ module raises instead of falling back to anything else.
 """
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoe_decode.so")
@@ -31,6 +32,15 @@ class MoEWeights(ctypes.Structure):
     _fields_ = [("router_w", _P), ("router_bias", _P), ("w_gu_q", _P), ("w_gu_s", _P),
                 ("w_d_q", _P), ("w_d_s", _P), ("shared_gu", _P), ("shared_d", _P),
                 ("rms_gamma", _P)]
+
+
+# moe_kv_cache_t, moe_kv_attention_t and moe_route_t in native layout: packing
+# one of these per call costs a fraction of filling a ctypes structure
+KV_CACHE = struct.Struct("4P4q4i")
+KV_ATTENTION = struct.Struct("P2qP2q2Pq3PN8if4x")
+ROUTE = struct.Struct("7if")
+
+DTYPE_BF16, DTYPE_F16, DTYPE_F32 = 0, 1, 2
 
 
 class MoEError(RuntimeError):
@@ -77,6 +87,17 @@ _PROTOS = {
                                                ctypes.c_int, ctypes.c_int, ctypes.c_float, _P,
                                                _P]),
     "moe_router_topk_noalloc_status": (ctypes.c_int, [_P]),
+    "moe_kv_plan": (ctypes.c_int, [_P, _P, _P, ctypes.c_int, _P, ctypes.c_int64, ctypes.c_int, _P,
+                                   ctypes.c_int, _P, ctypes.c_int, _P, _P, _P, ctypes.c_int, _P,
+                                   _P]),
+    "moe_kv_release": (ctypes.c_int, [_P, _P, ctypes.c_int, _P, _P, ctypes.c_int64, ctypes.c_int,
+                                      _P, ctypes.c_int, _P, ctypes.c_int, _P]),
+    "moe_kv_append": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int, ctypes.c_int64, ctypes.c_int64,
+                                     ctypes.c_int64, ctypes.c_int64, _P, ctypes.c_int]),
+    "moe_kv_attention": (ctypes.c_int, [_P, _P, _P]),
+    "moe_kv_attention_workspace": (ctypes.c_size_t, [ctypes.c_int]),
+    "moe_route": (ctypes.c_int, [_P, _P, _P, ctypes.c_int, ctypes.c_int64, ctypes.c_int64, _P, _P,
+                                 _P]),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "moe_last_cuda_error": (ctypes.c_int, []),
 }

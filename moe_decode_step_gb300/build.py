@@ -5,11 +5,12 @@ import subprocess
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libmoe_decode.so")
-SOURCES = ["csrc/moe_decode.cu", "csrc/noalloc.cu"]
+SOURCES = ["csrc/moe_decode.cu", "csrc/noalloc.cu", "csrc/kv.cu"]
 HEADERS = ["csrc/common.cuh", "csrc/mxfp4.cuh", "csrc/planes.cuh", "csrc/stream.cuh",
-           "csrc/tc.cuh", "csrc/topk.cuh", "csrc/tail.cuh"]
+           "csrc/tc.cuh", "csrc/topk.cuh", "csrc/tail.cuh", "csrc/kv_cache.cuh",
+           "csrc/kv_plan.cuh", "csrc/kv_append.cuh", "csrc/kv_attention.cuh", "csrc/route.cuh"]
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
-              "-Xcompiler", "-fPIC", "-shared"]
+              "-Xcompiler", "-fPIC", "-shared", "--threads", "4"]
 
 
 def _stale():

@@ -1,0 +1,221 @@
+// Block tables and slot maps from request lengths.
+//
+// Two prefix sums over the rows (new blocks, new tokens) decide everything:
+// each row's first entry on the free stack, its first token, and whether it
+// is served.  Every output entry then follows from its row's prefixes alone,
+// so the entries are written by as many CTAs as they keep busy, each of which
+// computes the sums over all rows for itself: 8 bytes per row, read from L2,
+// against a grid-wide wait or a second launch.
+#pragma once
+
+#include "kv_cache.cuh"
+
+namespace moe {
+
+constexpr int kPlanThreads = 512;
+constexpr int kPlanMaxRows = 16384;
+
+struct PlanArgs {
+  const int* ctx;
+  const int* q;
+  int rows;
+  int* table;
+  long long tstride;
+  int max_blocks;
+  const int* free_list;
+  int free_cap;
+  const int* n_free;
+  int bs_log2;
+  int* seq;
+  int* q_start;
+  int* slot;
+  int n_slots;
+  int* n_free_out;
+  int* n_unserved;
+};
+
+// Exclusive scan of two values per thread over the block; totals returned.
+__device__ __forceinline__ void plan_scan2(long long& a, long long& b, long long& ta,
+                                           long long& tb) {
+  __shared__ long long s_a[kPlanThreads / 32], s_b[kPlanThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long ia = a, ib = b;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long xa = __shfl_up_sync(0xffffffffu, ia, o);
+    const long long xb = __shfl_up_sync(0xffffffffu, ib, o);
+    if (lane >= o) {
+      ia += xa;
+      ib += xb;
+    }
+  }
+  if (lane == 31) {
+    s_a[warp] = ia;
+    s_b[warp] = ib;
+  }
+  __syncthreads();
+  long long ba = 0, bb = 0;
+  ta = tb = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    if (w == warp) {
+      ba = ta;
+      bb = tb;
+    }
+    ta += s_a[w];
+    tb += s_b[w];
+  }
+  __syncthreads();
+  a = ba + ia - a;
+  b = bb + ib - b;
+}
+
+struct PlanRow {
+  int ctx, q;
+  long long have, need;   // blocks held; new blocks, -1: the row cannot be served
+};
+
+__device__ __forceinline__ PlanRow plan_row(const PlanArgs& p, int r) {
+  PlanRow w;
+  w.ctx = p.ctx[r];
+  w.q = p.q[r];
+  const long long up = (1ll << p.bs_log2) - 1;
+  if (w.ctx < 0 || w.q < 0) {
+    w.have = 0;
+    w.need = -1;
+    w.ctx = max(w.ctx, 0);
+    w.q = 0;
+  } else {
+    w.have = (w.ctx + up) >> p.bs_log2;
+    const long long total = ((long long)w.ctx + w.q + up) >> p.bs_log2;
+    w.need = total <= p.max_blocks ? total - w.have : -1;
+  }
+  return w;
+}
+
+// Shared memory: first token of every row [rows + 1]; first new block [rows],
+// complemented (negative) when the row is not served.
+static __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanArgs p) {
+  extern __shared__ int plan_smem[];
+  int* s_tok = plan_smem;
+  int* s_blk = plan_smem + p.rows + 1;
+  __shared__ int s_unserved;
+  __shared__ long long s_used;
+  const int t = threadIdx.x;
+  const int per = (p.rows + kPlanThreads - 1) / kPlanThreads;
+  const int r0 = min(p.rows, t * per), r1 = min(p.rows, r0 + per);
+  const int n_free = min(max(*p.n_free, 0), p.free_cap);
+  long long blk = 0, tok = 0, tblk, ttok;
+  for (int r = r0; r < r1; ++r) {
+    const PlanRow w = plan_row(p, r);
+    blk += max(w.need, 0ll);
+    tok += w.q;
+  }
+  if (t == 0) {
+    s_unserved = 0;
+    s_used = 0;
+  }
+  plan_scan2(blk, tok, tblk, ttok);
+  long long used = 0;
+  int bad = 0;
+  for (int r = r0; r < r1; ++r) {
+    const PlanRow w = plan_row(p, r);
+    const bool served = w.need >= 0 && (w.need == 0 || blk + w.need <= n_free) &&
+                        (w.q == 0 || tok + w.q <= p.n_slots);
+    const int tok32 = (int)min(tok, (long long)INT32_MAX);
+    s_tok[r] = tok32;
+    s_blk[r] = served ? (int)min(blk, (long long)INT32_MAX) : -1;
+    if (blockIdx.x == 0) {
+      p.seq[r] = served ? w.ctx + w.q : w.ctx;
+      p.q_start[r] = tok32;
+    }
+    if (served && w.need > 0) used = blk + w.need;
+    bad += served ? 0 : 1;
+    blk += max(w.need, 0ll);
+    tok += w.q;
+  }
+  if (bad) atomicAdd(&s_unserved, bad);
+  if (used) atomicMax(&s_used, used);
+  if (t == 0) s_tok[p.rows] = (int)min(ttok, (long long)INT32_MAX);
+  __syncthreads();
+  if (blockIdx.x == 0 && t == 0) {
+    p.q_start[p.rows] = s_tok[p.rows];
+    *p.n_free_out = n_free - (int)s_used;
+    *p.n_unserved = s_unserved;
+  }
+  const int bs = 1 << p.bs_log2;
+  const int stride = gridDim.x * kPlanThreads;
+  // slots: the row by bisection of the first tokens
+  for (int i = blockIdx.x * kPlanThreads + t; i < p.n_slots; i += stride) {
+    int slot = -1;
+    if (i < s_tok[p.rows]) {
+      int lo = 0, hi = p.rows;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_tok[mid] <= i) lo = mid;
+        else hi = mid;
+      }
+      if (s_blk[lo] >= 0) {
+        const int ctx = p.ctx[lo], pos = ctx + i - s_tok[lo];
+        const int have = (int)(((long long)ctx + bs - 1) >> p.bs_log2), b = pos >> p.bs_log2;
+        const int id = b < have ? p.table[lo * p.tstride + b]
+                                : p.free_list[n_free - 1 - (s_blk[lo] + b - have)];
+        slot = id * bs + (pos & (bs - 1));
+      }
+    }
+    p.slot[i] = slot;
+  }
+  // new table entries, a warp per row
+  const int lane = t & 31;
+  for (int r = (blockIdx.x * kPlanThreads + t) >> 5; r < p.rows; r += stride >> 5) {
+    if (s_blk[r] < 0) continue;
+    const PlanRow w = plan_row(p, r);
+    for (int j = lane; j < w.need; j += 32)
+      p.table[r * p.tstride + w.have + j] = p.free_list[n_free - 1 - (s_blk[r] + j)];
+  }
+}
+
+struct ReleaseArgs {
+  const uint8_t* finished;
+  int rows;
+  int* seq;
+  const int* table;
+  long long tstride;
+  int max_blocks;
+  int* free_list;
+  int free_cap;
+  const int* n_free;
+  int bs_log2;
+  int* n_free_out;
+};
+
+// One CTA: the pushes are few and the stack's height is one word.
+static __global__ void __launch_bounds__(kPlanThreads) kv_release_kernel(const ReleaseArgs p) {
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int n_free = min(max(*p.n_free, 0), p.free_cap);
+  __shared__ long long s_first[kPlanThreads];
+  __shared__ int s_blocks[kPlanThreads];
+  long long base = n_free;
+  for (int r0 = 0; r0 < p.rows; r0 += kPlanThreads) {
+    const int r = r0 + t;
+    long long n = 0, unused = 0, total, tu;
+    if (r < p.rows && p.finished[r]) {
+      n = ((long long)max(p.seq[r], 0) + (1 << p.bs_log2) - 1) >> p.bs_log2;
+      n = min(n, (long long)p.max_blocks);
+      p.seq[r] = 0;
+    }
+    s_blocks[t] = (int)n;
+    plan_scan2(n, unused, total, tu);
+    s_first[t] = base + n;
+    __syncthreads();
+    for (int w = warp; w < kPlanThreads; w += kPlanThreads / 32)
+      for (int j = lane; j < s_blocks[w]; j += 32)
+        if (s_first[w] + j < p.free_cap)
+          p.free_list[s_first[w] + j] = p.table[(r0 + w) * p.tstride + j];
+    base += total;
+    __syncthreads();
+  }
+  if (t == 0) *p.n_free_out = (int)min(base, (long long)p.free_cap);
+}
+
+}  // namespace moe
