@@ -94,6 +94,31 @@ int cache_view(const moe_kv_cache_t* c, KvView* v) {
   return MOE_OK;
 }
 
+// Workspace of an attention call: a description and two slots per CTA.
+size_t desc_bytes(int n_sm) { return ((size_t)n_sm * 16 + 255) / 256 * 256; }
+int dec_slot(int d) { return d == 64 ? kDecSlot<64> : kDecSlot<128>; }
+
+template <int D>
+int launch_decode(const AttnArgs& a, int n_sm, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(
+      kv_attention_decode<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecShape<D>::SMEM);
+  if (e != cudaSuccess) return cuda_fail(e);
+  kv_attention_decode<D><<<n_sm, kDecThreads, DecShape<D>::SMEM, st>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e);
+  // the join starts while the first kernel drains and waits for it
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(n_sm, 4);
+  cfg.blockDim = dim3(D);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, kv_attention_join<D>, a)) != cudaSuccess) return cuda_fail(e);
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -183,7 +208,9 @@ int moe_kv_append(void* stream, const moe_kv_cache_t* cache, const void* k, cons
 
 size_t moe_kv_attention_workspace(int head_dim) {
   if (head_dim != 64 && head_dim != 128) return 0;
-  return 256;
+  const Device* dev;
+  if (this_device(&dev)) return 0;
+  return desc_bytes(dev->n_sm) + 2 * (size_t)dev->n_sm * dec_slot(head_dim) * 4;
 }
 
 int moe_kv_attention(void* stream, const moe_kv_cache_t* cache, const moe_kv_attention_t* args) {
@@ -203,7 +230,7 @@ int moe_kv_attention(void* stream, const moe_kv_cache_t* cache, const moe_kv_att
       ((t.q_token_stride | t.q_head_stride | t.out_token_stride | t.out_head_stride) & 7))
     return MOE_ERR_UNSUPPORTED;
   if (t.n_rows > kPlanMaxRows) return MOE_ERR_UNSUPPORTED;
-  if ((long long)t.max_blocks * cache->block_size > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if ((long long)t.max_blocks * cache->block_size > INT32_MAX - 128) return MOE_ERR_UNSUPPORTED;
   const Device* dev;
   if ((rc = begin(&dev))) return rc;
   if (t.workspace_bytes < moe_kv_attention_workspace(cache->head_dim)) return MOE_ERR_ALLOC;
@@ -228,10 +255,10 @@ int moe_kv_attention(void* stream, const moe_kv_cache_t* cache, const moe_kv_att
   a.window = t.window;
   a.scale_log2 = t.scale * 1.4426950408889634f;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const dim3 grid(t.n_tokens, (t.n_heads + kAttnSimpleWarps - 1) / kAttnSimpleWarps);
-  if (cache->head_dim == 64) kv_attention_simple<64><<<grid, 32 * kAttnSimpleWarps, 0, st>>>(a);
-  else kv_attention_simple<128><<<grid, 32 * kAttnSimpleWarps, 0, st>>>(a);
-  return end();
+  a.desc = static_cast<int*>(t.workspace);
+  a.partial = reinterpret_cast<float*>(static_cast<char*>(t.workspace) + desc_bytes(dev->n_sm));
+  return cache->head_dim == 64 ? launch_decode<64>(a, dev->n_sm, st)
+                               : launch_decode<128>(a, dev->n_sm, st);
 }
 
 int moe_route(void* stream, const moe_route_t* cfg, const void* logits, int dtype,
