@@ -44,7 +44,7 @@ int this_device(const Device** out) {
         (e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev)))
       return cuda_fail(e);
     d.sm103 = major == 10 && minor == 3;
-    d.n_sm = n_sm;
+    d.n_sm = std::min(n_sm, kJoinMax);
     d.known = true;   // concurrent first calls write the same values
   }
   *out = &d;
@@ -77,7 +77,8 @@ int cache_view(const moe_kv_cache_t* c, KvView* v) {
   v->bs_log2 = block_log2(c->block_size);
   if (v->bs_log2 < 0 || c->n_blocks < 1 || c->n_kv_heads < 1) return MOE_ERR_INVALID_ARG;
   if (c->head_dim != 64 && c->head_dim != 128) return MOE_ERR_UNSUPPORTED;
-  if ((long long)c->n_blocks * c->block_size > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if ((long long)c->n_blocks * c->block_size > INT32_MAX || c->n_kv_heads > 32767)
+    return MOE_ERR_UNSUPPORTED;
   if (misaligned(c->k, 16) || misaligned(c->v, 16) ||
       ((c->block_stride | c->head_stride | c->token_stride) & 15))
     return MOE_ERR_UNSUPPORTED;
@@ -99,7 +100,7 @@ size_t desc_bytes(int n_sm) { return ((size_t)n_sm * 16 + 255) / 256 * 256; }
 int dec_slot(int d) { return d == 64 ? kDecSlot<64> : kDecSlot<128>; }
 
 template <int D>
-int launch_decode(const AttnArgs& a, int n_sm, cudaStream_t st) {
+int launch_decode(const AttnArgs& a, int n_sm, int max_q, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(
       kv_attention_decode<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecShape<D>::SMEM);
   if (e != cudaSuccess) return cuda_fail(e);
@@ -107,8 +108,8 @@ int launch_decode(const AttnArgs& a, int n_sm, cudaStream_t st) {
   if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e);
   // the join starts while the first kernel drains and waits for it
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(n_sm, 4);
-  cfg.blockDim = dim3(D);
+  cfg.gridDim = dim3(n_sm, (unsigned)std::min(16ll, std::max(1ll, (long long)max_q * a.group)));
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -257,8 +258,8 @@ int moe_kv_attention(void* stream, const moe_kv_cache_t* cache, const moe_kv_att
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   a.desc = static_cast<int*>(t.workspace);
   a.partial = reinterpret_cast<float*>(static_cast<char*>(t.workspace) + desc_bytes(dev->n_sm));
-  return cache->head_dim == 64 ? launch_decode<64>(a, dev->n_sm, st)
-                               : launch_decode<128>(a, dev->n_sm, st);
+  return cache->head_dim == 64 ? launch_decode<64>(a, dev->n_sm, t.max_q, st)
+                               : launch_decode<128>(a, dev->n_sm, t.max_q, st);
 }
 
 int moe_route(void* stream, const moe_route_t* cfg, const void* logits, int dtype,

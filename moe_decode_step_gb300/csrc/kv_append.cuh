@@ -64,7 +64,8 @@ __device__ __forceinline__ void append_group(const AppendArgs& a, int s, int h, 
         uint32_t r[2] = {v.x, v.y};
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const uint32_t lo = e4m3x2_to_f16x2(r[j] & 0xFFFFu), hi = e4m3x2_to_f16x2(r[j] >> 16);
+          uint32_t lo, hi;
+          e4m3x4_to_f16x2(r[j], lo, hi);
           r[j] = f32x2_to_e4m3x2(f16_lo(lo) * down, f16_hi(lo) * down) |
                  f32x2_to_e4m3x2(f16_lo(hi) * down, f16_hi(hi) * down) << 16;
         }

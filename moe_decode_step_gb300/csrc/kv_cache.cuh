@@ -36,13 +36,12 @@ __device__ __forceinline__ int kv_block_exp(float amax) {
   return min(max(e, kKvExpMin), kKvExpMax);
 }
 
-// Two E4M3 codes (the low 16 bits) -> f16x2, exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
-  uint32_t h;
-  asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}"
-      : "=r"(h)
+// Four E4M3 codes -> two f16x2 (codes 0, 1 and 2, 3), exact.
+__device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
       : "r"(w));
-  return h;
 }
 
 // Two floats -> two E4M3 codes (a in the low byte): nearest, ties to even,
