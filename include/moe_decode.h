@@ -415,7 +415,7 @@ int moe_kv_append(void* stream, const moe_kv_cache_t* cache, const void* k, cons
  * see do not reach its result, whatever they hold.  Products and sums are
  * exact products summed in fp32; the probabilities enter the second product
  * rounded to f16.
- * max_blocks * block_size is below 2^31 - 128.  seq_lens is read as at most
+ * max_blocks * block_size and n_tokens * n_heads are below 2^31 - 128.  seq_lens is read as at most
  * max_blocks * block_size and q_start as within
  * [0, n_tokens], not descending; rows of q past q_start[n_rows] are left
  * alone.  max_q, the longest row's queries as the host knows it, only picks

@@ -95,20 +95,27 @@ int cache_view(const moe_kv_cache_t* c, KvView* v) {
   return MOE_OK;
 }
 
-// Workspace of an attention call: a description and two slots per CTA.
+// Workspace of an attention call: per CTA a description and its slots.
 size_t desc_bytes(int n_sm) { return ((size_t)n_sm * 16 + 255) / 256 * 256; }
-int dec_slot(int d) { return d == 64 ? kDecSlot<64> : kDecSlot<128>; }
-
 template <int D>
+size_t dec_floats_of() {
+  return std::max(DecShape<D, 1>::SLOTS * DecShape<D, 1>::SLOT,
+                  DecShape<D, 2>::SLOTS * DecShape<D, 2>::SLOT);
+}
+size_t dec_floats(int d) { return d == 64 ? dec_floats_of<64>() : dec_floats_of<128>(); }
+
+template <int D, int NT>
 int launch_decode(const AttnArgs& a, int n_sm, int max_q, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(
-      kv_attention_decode<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecShape<D>::SMEM);
+  using Sh = DecShape<D, NT>;
+  cudaError_t e = cudaFuncSetAttribute(kv_attention_decode<D, NT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
   if (e != cudaSuccess) return cuda_fail(e);
-  kv_attention_decode<D><<<n_sm, kDecThreads, DecShape<D>::SMEM, st>>>(a);
+  kv_attention_decode<D, NT><<<n_sm, Sh::THREADS, Sh::SMEM, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e);
   // the join starts while the first kernel drains and waits for it
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(n_sm, (unsigned)std::min(16ll, std::max(1ll, (long long)max_q * a.group)));
+  cfg.gridDim = dim3(n_sm, (unsigned)std::min<long long>(
+                               Sh::ROWS, std::max(1ll, (long long)max_q * a.group)));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -116,8 +123,15 @@ int launch_decode(const AttnArgs& a, int n_sm, int max_q, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, kv_attention_join<D>, a)) != cudaSuccess) return cuda_fail(e);
-  return MOE_OK;
+  e = cudaLaunchKernelEx(&cfg, kv_attention_join<D, NT>, a);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e);
+}
+
+template <int D>
+int launch_attention(const AttnArgs& a, int n_sm, int max_q, cudaStream_t st) {
+  // rows of the longest batch row per KV head, as far as the host knows
+  return (long long)max_q * a.group <= 8 ? launch_decode<D, 1>(a, n_sm, max_q, st)
+                                         : launch_decode<D, 2>(a, n_sm, max_q, st);
 }
 
 }  // namespace
@@ -211,7 +225,7 @@ size_t moe_kv_attention_workspace(int head_dim) {
   if (head_dim != 64 && head_dim != 128) return 0;
   const Device* dev;
   if (this_device(&dev)) return 0;
-  return desc_bytes(dev->n_sm) + 2 * (size_t)dev->n_sm * dec_slot(head_dim) * 4;
+  return desc_bytes(dev->n_sm) + dec_floats(head_dim) * (size_t)dev->n_sm * 4;
 }
 
 int moe_kv_attention(void* stream, const moe_kv_cache_t* cache, const moe_kv_attention_t* args) {
@@ -231,7 +245,9 @@ int moe_kv_attention(void* stream, const moe_kv_cache_t* cache, const moe_kv_att
       ((t.q_token_stride | t.q_head_stride | t.out_token_stride | t.out_head_stride) & 7))
     return MOE_ERR_UNSUPPORTED;
   if (t.n_rows > kPlanMaxRows) return MOE_ERR_UNSUPPORTED;
-  if ((long long)t.max_blocks * cache->block_size > INT32_MAX - 128) return MOE_ERR_UNSUPPORTED;
+  if ((long long)t.max_blocks * cache->block_size > INT32_MAX - 128 ||
+      (long long)t.n_tokens * t.n_heads > INT32_MAX)
+    return MOE_ERR_UNSUPPORTED;
   const Device* dev;
   if ((rc = begin(&dev))) return rc;
   if (t.workspace_bytes < moe_kv_attention_workspace(cache->head_dim)) return MOE_ERR_ALLOC;
@@ -258,8 +274,8 @@ int moe_kv_attention(void* stream, const moe_kv_cache_t* cache, const moe_kv_att
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   a.desc = static_cast<int*>(t.workspace);
   a.partial = reinterpret_cast<float*>(static_cast<char*>(t.workspace) + desc_bytes(dev->n_sm));
-  return cache->head_dim == 64 ? launch_decode<64>(a, dev->n_sm, t.max_q, st)
-                               : launch_decode<128>(a, dev->n_sm, t.max_q, st);
+  return cache->head_dim == 64 ? launch_attention<64>(a, dev->n_sm, t.max_q, st)
+                               : launch_attention<128>(a, dev->n_sm, t.max_q, st);
 }
 
 int moe_route(void* stream, const moe_route_t* cfg, const void* logits, int dtype,

@@ -19,7 +19,7 @@ struct AttnArgs {
   const int* q_start;
   int f16, rows, n_tokens, heads, group, max_blocks, causal, window;
   float scale_log2;   // scale * log2(e)
-  float* partial;     // two slots per CTA
+  float* partial;     // slots of partial sums
   int* desc;          // per CTA: the split tile it begins
 };
 
@@ -49,34 +49,42 @@ __device__ __forceinline__ void attn_seen(const AttnArgs& a, const AttnRow& w, i
 // Few query rows per KV head (decode, short verify steps): mma.sync
 // ---------------------------------------------------------------------------
 // The rows of one KV head (query i, head of the group: row i * group + head)
-// form tiles of 16, the M of one m16n8k16.  A call reads every visible byte of
-// the cache once per tile and does 4 * 16 * D operations on its 2 * D bytes a
-// token: at 16 rows 32 operations a byte, far below the tensor cores' balance,
-// so HBM bounds it and the layout serves the loads.
+// form tiles of 8 or 16 rows, one or two n-tiles of m16n8k16 products whose M
+// is 16 tokens (scores, transposed) or 16 dims (values): with the rows on the
+// short side 8 rows cost half of what they would as M, in MMAs, registers and
+// exponentials.  A call reads every visible byte of the cache once per tile
+// and does 4 * 16 * D operations on the 2 * D bytes of a token at 16 rows: 32
+// operations a byte, far below the tensor cores' balance, so HBM bounds it
+// and the layout serves the loads.
 //
 // Work: strips of 32 tokens of (row of the batch, KV head, tile), ordered in
-// that order; CTA i takes strips [i * per, (i + 1) * per), so that ragged
-// lengths leave every SM the same bytes.  Inside a CTA the strips go round
-// the warps, each with its own running maximum and sums, joined in shared
-// memory at the end of a tile; a tile cut by a CTA boundary leaves partial
-// sums in the workspace, which the second kernel joins in CTA order (results
-// do not depend on timing).
+// that order; CTA i takes strips [i * per, (i + 1) * per) and each of its
+// warps an equal run of them, so that ragged lengths leave every warp the same
+// bytes.  A warp works by itself: it writes the tiles that lie inside its run
+// and leaves partial sums of the one or two that its ends cut in the
+// workspace (4 KB against the run's bytes).  When its warps are done the CTA
+// joins them once, in strip order, and the tiles that its own ends cut go to
+// the second kernel, which joins them in CTA order: results do not depend on
+// timing.  (With the strips dealt round the warps and joined in shared memory
+// at the end of every tile, a tile cost about 6 us of barriers and refilling;
+// the CTAs with most tiles then took 274 us where the median took 219.)
 //
 // Loads: each thread copies (cp.async) exactly the 16-byte pieces that it
 // feeds to its own MMAs, into a ring of its own in shared memory, so a strip
 // needs no barrier at all; the ring only deepens the loads in flight (D = 128:
-// 8 warps x 2 strips x 8 KB = 128 KB an SM; 1 us of latency at 6.7 TB/s needs
-// 44 KB).  The contraction order of either product is free, so the pieces
-// need no shuffling: in each half of a strip (16 tokens) lane (g, t) = (lane /
-// 4, lane % 4) holds, for the scores, 16 consecutive dims (from 16 t, and from
-// 64 + 16 t) of keys g and g + 8, and for the values CH = D / 8 consecutive
-// dims (from CH g) of tokens 2t, 2t + 1, 2t + 8, 2t + 9, byte-transposed in
-// registers.  Codes become f16 exactly (cvt.rn.f16x2.e4m3x2); queries enter
-// as f16 scaled per row by a power of two, which keeps all of bf16's 8 bits.
-// What bounds the kernel beside HBM is instruction issue (a strip of 8 KB is
-// 64 MMAs, 128 conversions and about as much again of everything else), so a
-// strip is two halves long: one maximum, one vote and twice the independent
-// MMAs for 32 tokens.
+// 12 warps x 8 KB = 96 KB an SM; 1 us of latency at 6.7 TB/s needs 44 KB).
+// The contraction order of either product is free, so the pieces need no
+// shuffling: in each half of a strip (16 tokens) lane (g, t) = (lane / 4, lane
+// % 4) holds, for the scores, 16 consecutive dims (from 16 t, and from 64 + 16
+// t) of keys g and g + 8, and for the values CH = D / 8 consecutive dims (from
+// CH g) of tokens 2t, 2t + 1, 2t + 8, 2t + 9, byte-transposed in registers.
+// Codes become f16 exactly (cvt.rn.f16x2.e4m3x2); queries enter as f16 scaled
+// per row by a power of two, which keeps all of bf16's 8 bits.  The scores'
+// fragments become the weights' by movmatrix.
+// What bounds the kernel beside HBM is latency in the chain scores - maximum -
+// weights - values, hidden by 12 to 16 warps an SM, and instruction issue
+// (128 conversions a strip of 8 KB, 32 MMAs per n-tile), so a strip is two
+// halves long: one maximum and one vote for 32 tokens.
 //
 // Scales: a half lies in one block, so one exponent ek scales its scores and
 // one ev its values.  With t = score * log2(e) + ev the weights 2^(t - M), M
@@ -84,27 +92,22 @@ __device__ __forceinline__ void attn_seen(const AttnArgs& a, const AttnRow& w, i
 // which f16 holds, whatever the spread of the block scales.  The
 // denominator takes the same weights times 2^-ev in fp32 (|ev| <= 60 keeps
 // them inside its range).
-constexpr int kDecWarps = 8;
-constexpr int kDecThreads = 32 * kDecWarps;
-
-template <int D>
+template <int D, int NT>   // NT: n-tiles of 8 rows in a tile
 struct DecShape {
+  static constexpr int ROWS = 8 * NT;
   static constexpr int CH = D / 8;                 // value dims a lane holds per token
   static constexpr int KP = D / 32;                // 16-byte key pieces a lane and half (2 keys)
   static constexpr int VP = 4 * CH / 16;           // the same for values (4 tokens)
   static constexpr int HALF = 32 * 16 * (KP + VP); // bytes of one warp's half strip
-  static constexpr int STAGES = D == 64 ? 6 : 3;
-  static constexpr int RS = D + 8;                 // row stride of the join buffer (floats)
-  // ring, join buffer (4 rows a round), m, l and factor of every warp's rows,
-  // m, l and score factor of the tile's, queries
-  static constexpr int SMEM = kDecWarps * (STAGES * 2 * HALF + 4 * RS * 4 + 3 * 16 * 4) +
-                              3 * 16 * 4 + 16 * D * 2;
+  static constexpr int WARPS = NT == 1 ? (D == 128 ? 12 : 16) : (D == 128 ? 8 : 12);
+  static constexpr int THREADS = 32 * WARPS;
+  static constexpr int STAGES = 196608 / (WARPS * 2 * HALF);
+  static constexpr int SMEM = WARPS * STAGES * 2 * HALF;
+  // one slot of partial sums: O [ROWS][D] in dec_dim's column order, then m
+  // [ROWS] and l [ROWS]; a warp has two, a CTA two more
+  static constexpr int SLOT = ROWS * D + 2 * ROWS;
+  static constexpr int SLOTS = 2 * WARPS + 2;
 };
-
-// One slot of partial sums: O [16][D] in the join buffer's column order, then
-// M [16] and l [16].
-template <int D>
-constexpr int kDecSlot = 16 * D + 32;
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -131,16 +134,24 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A row's share of the work: M tiles of 16 rows, S strips each, from strip s0.
+// Transpose of an 8 x 8 matrix of 16-bit elements held as MMA fragments.
+__device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// A row's share of the work: M tiles of TILE rows, S strips each, from strip s0.
 struct DecRow {
   AttnRow w;
   int M, S, s0;
 };
 
+template <int TILE>
 __device__ __forceinline__ DecRow dec_row(const AttnArgs& a, int r) {
   DecRow x;
   x.w = attn_row(a, r);
-  x.M = (int)(((long long)x.w.n * a.group + 15) >> 4);
+  x.M = (int)(((long long)x.w.n * a.group + TILE - 1) / TILE);
   int lo, hi, unused;
   attn_seen(a, x.w, 0, lo, unused);
   attn_seen(a, x.w, x.w.n - 1, unused, hi);
@@ -160,6 +171,7 @@ struct DecCursor {
 };
 
 // To the next tile.
+template <int TILE>
 __device__ __forceinline__ void dec_next_tile(const AttnArgs& a, DecCursor& c) {
   c.s = 0;
   if (++c.m < c.x.M) return;
@@ -168,22 +180,23 @@ __device__ __forceinline__ void dec_next_tile(const AttnArgs& a, DecCursor& c) {
   c.h = 0;
   do {
     if (++c.r >= a.rows) return;
-    c.x = dec_row(a, c.r);
+    c.x = dec_row<TILE>(a, c.r);
   } while (c.x.M == 0);
 }
 
 // This CTA's strips [u0, u0 + n) and its cursor at u0; every thread calls.
 // Also `per`.  The sums over the rows are made by every CTA for itself.
+template <int TILE, int WARPS>
 __device__ __forceinline__ void dec_schedule(const AttnArgs& a, long long& u0, long long& n,
                                              long long& per, DecCursor& cur) {
-  __shared__ long long s_sum[kDecWarps];
+  __shared__ long long s_sum[WARPS];
   __shared__ long long s_left;
   __shared__ int s_row;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int chunk = (a.rows + kDecThreads - 1) / kDecThreads;
+  const int chunk = (a.rows + (32 * WARPS) - 1) / (32 * WARPS);
   const int r0 = min(a.rows, t * chunk), r1 = min(a.rows, r0 + chunk);
   long long sum = 0;
-  for (int r = r0; r < r1; ++r) sum += dec_units(a, dec_row(a, r));
+  for (int r = r0; r < r1; ++r) sum += dec_units(a, dec_row<TILE>(a, r));
   long long inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -194,18 +207,18 @@ __device__ __forceinline__ void dec_schedule(const AttnArgs& a, long long& u0, l
   __syncthreads();
   long long total = 0, base = 0;
 #pragma unroll
-  for (int w = 0; w < kDecWarps; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     if (w == warp) base = total;
     total += s_sum[w];
   }
-  per = max((total + gridDim.x - 1) / gridDim.x, (long long)kDecWarps);
+  per = max((total + gridDim.x - 1) / gridDim.x, (long long)WARPS);
   u0 = per * blockIdx.x;
   n = min(per, total - u0);
   long long before = base + inc - sum;
   if (n > 0 && u0 >= before && u0 < before + sum) {
     int r = r0;
     for (;; ++r) {
-      const long long k = dec_units(a, dec_row(a, r));
+      const long long k = dec_units(a, dec_row<TILE>(a, r));
       if (u0 < before + k) break;
       before += k;
     }
@@ -215,7 +228,7 @@ __device__ __forceinline__ void dec_schedule(const AttnArgs& a, long long& u0, l
   __syncthreads();
   if (n <= 0) return;
   cur.r = s_row;
-  cur.x = dec_row(a, cur.r);
+  cur.x = dec_row<TILE>(a, cur.r);
   const long long left = s_left;
   cur.s = (int)(left % cur.x.S);
   const int hm = (int)(left / cur.x.S);
@@ -254,7 +267,8 @@ __device__ __forceinline__ void dec_lane_lookup(const AttnArgs& a, DecLoader& l,
   if (l.next_cached) l.id = __ldg(a.table + l.r * a.table_stride + (p0 >> a.c.bs_log2));
   l.offset = p0 & ((1 << a.c.bs_log2) - 1);
 }
-__device__ __forceinline__ void dec_lane_advance(const AttnArgs& a, DecLoader& l, int n) {
+template <int TILE>
+__device__ __forceinline__ void dec_lane_advance(const AttnArgs& a, DecLoader& l, long long n) {
   l.left -= n;
   if (l.left <= 0) return;
   l.idx += n;
@@ -262,7 +276,7 @@ __device__ __forceinline__ void dec_lane_advance(const AttnArgs& a, DecLoader& l
     const long long units = dec_units(a, l.x);
     if (l.idx < units) return;
     l.idx -= units;
-    l.x = dec_row(a, ++l.r);
+    l.x = dec_row<TILE>(a, ++l.r);
   }
 }
 __device__ __forceinline__ void dec_lane_scales(const AttnArgs& a, DecLoader& l) {
@@ -287,17 +301,17 @@ struct DecOffsets {
   long long k0, k1, v0, v1;
 };
 
-template <int D>
+template <int D, int NT>
 __device__ __forceinline__ void dec_fetch(const AttnArgs& a, DecLoader& l, const DecOffsets& f,
                                           int strips, uint32_t ring, int lane) {
-  using Sh = DecShape<D>;
+  using Sh = DecShape<D, NT>;
   if (l.k < strips) {
     const int b = l.k & 15;
     if (b == 0 && l.k > 0) {
       dec_lane_take(a, l);
       l.sc_before = l.sc_now;
       l.sc_now = dec_pack_scales(l.id >= 0, l.sk, l.sv);
-      dec_lane_advance(a, l, 16 * kDecWarps);
+      dec_lane_advance<Sh::ROWS>(a, l, 16);
       dec_lane_lookup(a, l, lane);
     } else if (b == 8) {
       dec_lane_scales(a, l);
@@ -360,14 +374,22 @@ __device__ __forceinline__ uint32_t drop_nan4(uint32_t w, uint32_t& any) {
   return w & ~m;
 }
 
-// Rows of the tile: row j is query i = (16 m + j) / group of the batch row,
-// query head h * group + (16 m + j) % group.
+// Rows of the tile: row j is query i = (TILE m + j) / group of the batch row,
+// query head h * group + (TILE m + j) % group.
+template <int TILE>
 __device__ __forceinline__ bool dec_tile_row(const AttnArgs& a, const DecCursor& c, int j, int& i,
                                              int& head) {
-  const long long rho = (long long)c.m * 16 + j;
-  i = (int)(rho / a.group);
-  head = c.h * a.group + (int)(rho - (long long)i * a.group);
+  const unsigned rho = (unsigned)c.m * TILE + j;   // tokens * heads < 2^31
+  i = (int)(rho / (unsigned)a.group);
+  head = c.h * a.group + (int)(rho - (unsigned)i * (unsigned)a.group);
   return i < c.x.w.n;
+}
+
+// Dim of a column in the partial sums' order: column 16 j + 2 g + e is dim
+// CH g + 2 j + e (a lane's pairs adjacent, a warp's store contiguous).
+template <int D>
+__device__ __forceinline__ int dec_dim(int col) {
+  return ((col >> 1) & 7) * (D / 8) + 2 * (col >> 4) + (col & 1);
 }
 
 // Natural logarithm of the denominator from its reference (log2) and sum.
@@ -381,389 +403,456 @@ __device__ __forceinline__ float attn_factor(float m, float ref) {
   return m == -INFINITY ? (ref == -INFINITY ? 1.f : 0.f) : exp2_approx(m - ref);
 }
 
-template <int D>
-static __global__ void __launch_bounds__(kDecThreads, 1) kv_attention_decode(const AttnArgs a) {
-  using Sh = DecShape<D>;
-  constexpr int CH = Sh::CH, KS = D / 16;
+// Partial sums of a piece of a tile.
+struct DecPiece {
+  int state;       // 0: none, else 1 | begins its tile << 1 | ends it << 2
+  int r, h, m;
+  long long at;    // its first strip, in the CTA's order
+};
+
+template <int D, int NT>
+static __global__ void __launch_bounds__(DecShape<D, NT>::THREADS, 1)
+    kv_attention_decode(const AttnArgs a) {
+  using Sh = DecShape<D, NT>;
+  constexpr int CH = Sh::CH, KS = D / 16, ROWS = Sh::ROWS, W = Sh::WARPS;
   extern __shared__ __align__(128) uint8_t dec_smem[];
+  __shared__ DecPiece s_piece[2 * W];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  float* s_join = reinterpret_cast<float*>(dec_smem + kDecWarps * Sh::STAGES * 2 * Sh::HALF);
-  float* s_m = s_join + kDecWarps * 4 * Sh::RS;    // [warp][16]
-  float* s_l = s_m + kDecWarps * 16;
-  float* s_f = s_l + kDecWarps * 16;
-  float* s_tm = s_f + kDecWarps * 16;              // [16] of the tile
-  float* s_tl = s_tm + 16;
-  float* s_fac = s_tl + 16;                        // score factors, later the lse
-  uint16_t* s_q = reinterpret_cast<uint16_t*>(s_fac + 16);   // [16][D]; the output too
   const uint32_t ring = smem_addr(dec_smem) + warp * Sh::STAGES * 2 * Sh::HALF;
   const uint8_t* ringp = dec_smem + warp * Sh::STAGES * 2 * Sh::HALF;
+  float* slots = a.partial + (long long)blockIdx.x * Sh::SLOTS * Sh::SLOT;
 
   pdl_launch_dependents();
   long long u0, n_units, per;
   DecCursor cur;
-  dec_schedule(a, u0, n_units, per, cur);
+  dec_schedule<ROWS, W>(a, u0, n_units, per, cur);
   if (threadIdx.x == 0) a.desc[4 * blockIdx.x] = 0;
   if (n_units <= 0) return;
+  if (threadIdx.x < 2 * W) s_piece[threadIdx.x].state = 0;
+  __syncthreads();
 
-  DecLoader ld;
-  ld.r = cur.r;
-  ld.x = cur.x;
-  ld.idx = ((long long)cur.h * cur.x.M + cur.m) * cur.x.S + cur.s;
-  ld.left = n_units;
-  ld.k = 0;
-  ld.slot = 0;
-  ld.sc_before = 0;
-  dec_lane_advance(a, ld, warp + kDecWarps * (lane >> 1));
-  dec_lane_lookup(a, ld, lane);
-  dec_lane_scales(a, ld);
-  dec_lane_take(a, ld);
-  const bool exists = ld.id >= 0;
-  const uint32_t sk0 = ld.sk, sv0 = ld.sv;
-  const DecOffsets off = {g * a.c.tstride + t * 16, (g + 8) * a.c.tstride + t * 16,
-                          2 * t * a.c.tstride + g * CH, (2 * t + 8) * a.c.tstride + g * CH};
-  const int strips = (int)((n_units - warp + kDecWarps - 1) / kDecWarps);
+  // this warp's run: strips [first, first + n_warp) of the CTA's
+  const long long first = n_units * warp / W;
+  const int n_warp = (int)(n_units * (warp + 1) / W - first);
+  if (n_warp > 0) {
+    DecLoader ld;
+    ld.r = cur.r;
+    ld.x = cur.x;
+    ld.idx = ((long long)cur.h * cur.x.M + cur.m) * cur.x.S + cur.s;
+    ld.left = n_units;
+    dec_lane_advance<ROWS>(a, ld, first);
+    cur.r = ld.r;
+    cur.x = ld.x;
+    cur.s = (int)(ld.idx % cur.x.S);
+    cur.h = (int)(ld.idx / cur.x.S) / cur.x.M;
+    cur.m = (int)(ld.idx / cur.x.S) % cur.x.M;
+    ld.left = n_warp;
+    ld.k = 0;
+    ld.slot = 0;
+    ld.sc_before = 0;
+    dec_lane_advance<ROWS>(a, ld, lane >> 1);
+    dec_lane_lookup(a, ld, lane);
+    dec_lane_scales(a, ld);
+    dec_lane_take(a, ld);
+    const bool exists = ld.id >= 0;
+    const uint32_t sk0 = ld.sk, sv0 = ld.sv;
+    const DecOffsets off = {g * a.c.tstride + t * 16, (g + 8) * a.c.tstride + t * 16,
+                            2 * t * a.c.tstride + g * CH, (2 * t + 8) * a.c.tstride + g * CH};
 #pragma unroll 1
-  for (int i = 0; i < Sh::STAGES - 1; ++i) dec_fetch<D>(a, ld, off, strips, ring, lane);
-  ld.sc_now = dec_pack_scales(exists, sk0, sv0);
-  dec_lane_advance(a, ld, 16 * kDecWarps);
-  dec_lane_lookup(a, ld, lane);
-  int done = 0;                 // strips of the warp consumed
-  int slot_in = 0;              // ring slot of the next one
-
-  long long u = 0;              // strips done by the CTA, in its own order
-  int next = warp;              // this warp's next strip, relative to the tile's first
-  int part = 0;                 // tiles begun
-  while (u < n_units) {
-    const int nseg = (int)min((long long)(cur.x.S - cur.s), n_units - u);
-    const int real = (int)min(16ll, (long long)cur.x.w.n * a.group - 16ll * cur.m);
-    // ---- queries of the tile: f16 times 2^-shift, in shared memory; the
-    // scale's sign goes with them, so that the factors are positive ----
-    for (int j = warp; j < 16; j += kDecWarps) {
-      int i, head;
-      float v[D / 32];
-      float mx = 0.f;
-#pragma unroll
-      for (int k = 0; k < D / 32; ++k) v[k] = 0.f;
-      if (dec_tile_row(a, cur, j, i, head)) {
-        const uint16_t* q = a.q + (long long)(cur.x.w.tok + i) * a.q_ts + head * a.q_hs;
-#pragma unroll
-        for (int k = 0; k < D / 64; ++k) {
-          const float2 f =
-              unpack16(*reinterpret_cast<const uint32_t*>(q + 2 * lane + 64 * k), a.f16);
-          v[2 * k] = f.x;
-          v[2 * k + 1] = f.y;
-          mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
-        }
-      }
-      mx = warp_max(mx);
-      // the row's largest value in [2^13, 2^14): f16's exponents reach 2^-38 of it
-      const int be = (int)(__float_as_uint(mx) >> 23);
-      const int sh = be == 0 || be == 255 ? 0 : min(max(be - 140, -120), 120);
-      const float down =
-          a.scale_log2 == 0.f ? 0.f : (a.scale_log2 < 0.f ? -pow2f(-sh) : pow2f(-sh));
-#pragma unroll
-      for (int k = 0; k < D / 64; ++k)
-        *reinterpret_cast<uint32_t*>(s_q + j * D + 2 * lane + 64 * k) =
-            pack_f16x2(v[2 * k] * down, v[2 * k + 1] * down);
-      if (lane == 0) s_fac[j] = fabsf(a.scale_log2) * pow2f(sh);
-    }
-    __syncthreads();
-    uint32_t qf[KS][4];
-#pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      const int d = (k >> 2) * 64 + t * 16 + (k & 3) * 4;
-      const uint2 x = *reinterpret_cast<const uint2*>(s_q + g * D + d);
-      const uint2 y = *reinterpret_cast<const uint2*>(s_q + (g + 8) * D + d);
-      qf[k][0] = x.x;
-      qf[k][1] = y.x;
-      qf[k][2] = x.y;
-      qf[k][3] = y.y;
-    }
-    const float fac0 = s_fac[g], fac1 = s_fac[g + 8];
-    // what the lane's two rows see, and what every and any row of the tile sees
-    int i0, i1, hd, lo0, hi0, lo1, hi1, lo_all, hi_all, lo_any, hi_any;
-    if (!dec_tile_row(a, cur, g, i0, hd)) i0 = cur.x.w.n - 1;
-    if (!dec_tile_row(a, cur, g + 8, i1, hd)) i1 = cur.x.w.n - 1;
-    attn_seen(a, cur.x.w, i0, lo0, hi0);
-    attn_seen(a, cur.x.w, i1, lo1, hi1);
-    dec_tile_row(a, cur, 0, i0, hd);
-    if (!dec_tile_row(a, cur, 15, i1, hd)) i1 = cur.x.w.n - 1;
-    attn_seen(a, cur.x.w, i0, lo_any, hi_all);
-    attn_seen(a, cur.x.w, i1, lo_all, hi_any);
-
-    float o[CH][4];
-#pragma unroll
-    for (int j = 0; j < CH; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    for (int i = 0; i < Sh::STAGES - 1; ++i) dec_fetch<D, NT>(a, ld, off, n_warp, ring, lane);
+    ld.sc_now = dec_pack_scales(exists, sk0, sv0);
+    dec_lane_advance<ROWS>(a, ld, 16);
+    dec_lane_lookup(a, ld, lane);
+    int done = 0;      // strips consumed
+    int slot_in = 0;   // ring slot of the next one
+    int pieces = 0;    // partial sums left
 
 #pragma unroll 1
-    for (; next < nseg; next += kDecWarps) {
-      dec_fetch<D>(a, ld, off, strips, ring, lane);
-      cp_async_wait<Sh::STAGES - 1>();
-      const uint32_t meta0 = dec_scales(ld, done, 0), meta1 = dec_scales(ld, done, 1);
-      ++done;
-      __syncwarp();
-      const uint8_t* base = ringp + slot_in * (2 * Sh::HALF);
-      const uint8_t* sp = base + lane * 16;
-      const int p0 = (cur.x.s0 + cur.s + next) << 5;
-      slot_in = slot_in + 1 == Sh::STAGES ? 0 : slot_in + 1;
-      if (!((meta0 | meta1) >> 16) || p0 >= hi_any || p0 + 32 <= lo_any) continue;
-      // ---- scores ----
-      float s[4][4];
+    while (done < n_warp) {
+      const int nseg = min(cur.x.S - cur.s, n_warp - done);
+      // ---- queries: lane (g, t) takes 16 dims of row 8 q + g (from 16 t, and
+      // from 64 + 16 t), as f16 times 2^-shift; the scale's sign goes with
+      // them, so that the factors are positive ----
+      uint2 qf[NT][KS];
+      // the lane's rows of the scores, 8 q + 2t + r: score factor, what they see
+      float fac[NT][2], m[NT][2], l[NT][2];
+      int lo[NT][2], hi[NT][2], lo_all, hi_all, lo_any, hi_any, i0, i1, hd;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+      for (int q = 0; q < NT; ++q) {
+        uint4 w[D / 64][2];
+        float mx = 0.f;
+        const bool real = dec_tile_row<ROWS>(a, cur, 8 * q + g, i0, hd);
+        const uint16_t* src = a.q + (long long)(cur.x.w.tok + i0) * a.q_ts + hd * a.q_hs + t * 16;
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        uint4 w[4];
+        for (int c = 0; c < D / 64; ++c)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = *reinterpret_cast<const uint4*>(sp + (i >> 1) * Sh::HALF +
-                                                 ((i & 1) * (D / 64) + c) * 512);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t* q = qf[4 * c + k];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t b0, b1;
-            e4m3x4_to_f16x2(k == 0 ? w[i].x : k == 1 ? w[i].y : k == 2 ? w[i].z : w[i].w, b0, b1);
-            mma_f16_16816(s[i], q[0], q[1], q[2], q[3], b0, b1);
+          for (int i = 0; i < 2; ++i) {
+            w[c][i] = make_uint4(0, 0, 0, 0);
+            if (real) w[c][i] = *reinterpret_cast<const uint4*>(src + c * 64 + i * 8);
+            const float2 f0 = unpack16(w[c][i].x, a.f16), f1 = unpack16(w[c][i].y, a.f16),
+                         f2 = unpack16(w[c][i].z, a.f16), f3 = unpack16(w[c][i].w, a.f16);
+            mx = fmaxf(mx, fmaxf(fmaxf(fmaxf(fabsf(f0.x), fabsf(f0.y)), fmaxf(fabsf(f1.x), fabsf(f1.y))),
+                                 fmaxf(fmaxf(fabsf(f2.x), fabsf(f2.y)), fmaxf(fabsf(f3.x), fabsf(f3.y)))));
           }
-        }
-      }
-      // ---- weights ----
-      const float ke0 = pow2f((int)(meta0 & 0xFFu) - 128), ke1 = pow2f((int)(meta1 & 0xFFu) - 128);
-      const int ev0 = (int)((meta0 >> 8) & 0xFFu) - 128, ev1 = (int)((meta1 >> 8) & 0xFFu) - 128;
-      const float f00 = fac0 * ke0, f01 = fac0 * ke1, f10 = fac1 * ke0, f11 = fac1 * ke1;
-      const bool masked =
-          p0 + 32 > hi_all || p0 < lo_all || !((meta0 & meta1) >> 16);
-      if (masked) {
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        // the row's largest value in [2^13, 2^14): f16's exponents reach 2^-38 of it
+        const int be = (int)(__float_as_uint(mx) >> 23);
+        const int sh = be == 0 || be == 255 ? 0 : min(max(be - 140, -120), 120);
+        const float down =
+            a.scale_log2 == 0.f ? 0.f : (a.scale_log2 < 0.f ? -pow2f(-sh) : pow2f(-sh));
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int c = 0; c < D / 64; ++c)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int j = p0 + 8 * i + 2 * t + c;
-            const bool there = (i < 2 ? meta0 : meta1) >> 16;
-            if (!there || j < lo0 || j >= hi0) s[i][c] = -INFINITY;
-            if (!there || j < lo1 || j >= hi1) s[i][2 + c] = -INFINITY;
+          for (int i = 0; i < 2; ++i) {
+            const float2 f0 = unpack16(w[c][i].x, a.f16), f1 = unpack16(w[c][i].y, a.f16),
+                         f2 = unpack16(w[c][i].z, a.f16), f3 = unpack16(w[c][i].w, a.f16);
+            qf[q][4 * c + 2 * i] = make_uint2(pack_f16x2(f0.x * down, f0.y * down),
+                                              pack_f16x2(f1.x * down, f1.y * down));
+            qf[q][4 * c + 2 * i + 1] = make_uint2(pack_f16x2(f2.x * down, f2.y * down),
+                                                  pack_f16x2(f3.x * down, f3.y * down));
           }
-      }
-      // (a factor that underflowed to 0 makes NaN of -infinity, which fmaxf drops)
-      float x0 = fmaxf(fmaf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1])), f00, (float)ev0),
-                       fmaf(fmaxf(fmaxf(s[2][0], s[2][1]), fmaxf(s[3][0], s[3][1])), f01, (float)ev1));
-      float x1 = fmaxf(fmaf(fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3])), f10, (float)ev0),
-                       fmaf(fmaxf(fmaxf(s[2][2], s[2][3]), fmaxf(s[3][2], s[3][3])), f11, (float)ev1));
-      x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
-      x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
-      x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
-      x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
-      if (__any_sync(0xffffffffu, x0 > m0 || x1 > m1)) {
-        const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-        const float d0 = attn_factor(m0, n0), d1 = attn_factor(m1, n1);
-        m0 = n0;
-        m1 = n1;
-        l0 *= d0;
-        l1 *= d1;
+        const float mine = fabsf(a.scale_log2) * pow2f(sh);
 #pragma unroll
-        for (int j = 0; j < CH; ++j) {
-          o[j][0] *= d0;
-          o[j][1] *= d0;
-          o[j][2] *= d1;
-          o[j][3] *= d1;
+        for (int r = 0; r < 2; ++r) {
+          fac[q][r] = __shfl_sync(0xffffffffu, mine, 4 * (2 * t + r));
+          if (!dec_tile_row<ROWS>(a, cur, 8 * q + 2 * t + r, i0, hd)) i0 = cur.x.w.n - 1;
+          attn_seen(a, cur.x.w, i0, lo[q][r], hi[q][r]);
+          m[q][r] = -INFINITY;
+          l[q][r] = 0.f;
         }
       }
-      const float r0 = m0 == -INFINITY ? 0.f : m0, r1 = m1 == -INFINITY ? 0.f : m1;
-      const float c00 = (float)ev0 - r0, c01 = (float)ev1 - r0, c10 = (float)ev0 - r1,
-                  c11 = (float)ev1 - r1;
+      // what any and every row of the tile sees
+      dec_tile_row<ROWS>(a, cur, 0, i0, hd);
+      if (!dec_tile_row<ROWS>(a, cur, ROWS - 1, i1, hd)) i1 = cur.x.w.n - 1;
+      attn_seen(a, cur.x.w, i0, lo_any, hi_all);
+      attn_seen(a, cur.x.w, i1, lo_all, hi_any);
+
+      float o[NT][CH / 2][4];   // value tile j: dims CH g + 2j (0, 1), CH g + 2j + 1 (2, 3)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s[i][0] = exp2_approx(fmaf(s[i][0], i < 2 ? f00 : f01, i < 2 ? c00 : c01));
-        s[i][1] = exp2_approx(fmaf(s[i][1], i < 2 ? f00 : f01, i < 2 ? c00 : c01));
-        s[i][2] = exp2_approx(fmaf(s[i][2], i < 2 ? f10 : f11, i < 2 ? c10 : c11));
-        s[i][3] = exp2_approx(fmaf(s[i][3], i < 2 ? f10 : f11, i < 2 ? c10 : c11));
-      }
-      if (masked) {
+      for (int q = 0; q < NT; ++q)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int j = p0 + 8 * i + 2 * t + c;
-            const bool there = (i < 2 ? meta0 : meta1) >> 16;
-            if (!there || j < lo0 || j >= hi0) s[i][c] = 0.f;
-            if (!there || j < lo1 || j >= hi1) s[i][2 + c] = 0.f;
-          }
-      }
-      const float un0 = pow2f(-ev0), un1 = pow2f(-ev1);
-      l0 = fmaf(un0, (s[0][0] + s[0][1]) + (s[1][0] + s[1][1]), l0);
-      l1 = fmaf(un0, (s[0][2] + s[0][3]) + (s[1][2] + s[1][3]), l1);
-      l0 = fmaf(un1, (s[2][0] + s[2][1]) + (s[3][0] + s[3][1]), l0);
-      l1 = fmaf(un1, (s[2][2] + s[2][3]) + (s[3][2] + s[3][3]), l1);
-      // ---- values ----
-      uint32_t nan = 0;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const float(*ss)[4] = s + 2 * half;
-        const uint32_t pa0 = pack_f16x2(ss[0][0], ss[0][1]), pa1 = pack_f16x2(ss[0][2], ss[0][3]);
-        const uint32_t pa2 = pack_f16x2(ss[1][0], ss[1][1]), pa3 = pack_f16x2(ss[1][2], ss[1][3]);
-        const uint8_t* hp = sp + half * Sh::HALF;
-        uint32_t vw[4][CH / 4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (D == 128) {
-            const uint4 w = *reinterpret_cast<const uint4*>(hp + (Sh::KP + i) * 512);
-            vw[i][0] = w.x;
-            vw[i][1] = w.y;
-            vw[i][2] = w.z;
-            vw[i][3] = w.w;
-          } else {
-            const uint2 w =
-                *reinterpret_cast<const uint2*>(hp + (Sh::KP + (i >> 1)) * 512 + (i & 1) * 8);
-            vw[i][0] = w.x;
-            vw[i][1] = w.y;
-          }
-        }
-        if (masked) {
-          // a weight of 0 does not keep a NaN value out of the sums: NaN codes
-          // leave the product here and are given back to the rows that see them
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int c = 0; c < CH / 4; ++c) vw[i][c] = drop_nan4(vw[i][c], nan);
-        }
-#pragma unroll
-        for (int c = 0; c < CH / 4; ++c) {
-          uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
-          e4m3x4_to_f16x2(__byte_perm(vw[0][c], vw[1][c], 0x5140), a0, a1);
-          e4m3x4_to_f16x2(__byte_perm(vw[2][c], vw[3][c], 0x5140), b0, b1);
-          e4m3x4_to_f16x2(__byte_perm(vw[0][c], vw[1][c], 0x7362), a2, a3);
-          e4m3x4_to_f16x2(__byte_perm(vw[2][c], vw[3][c], 0x7362), b2, b3);
-          mma_f16_16816(o[4 * c], pa0, pa1, pa2, pa3, a0, b0);
-          mma_f16_16816(o[4 * c + 1], pa0, pa1, pa2, pa3, a1, b1);
-          mma_f16_16816(o[4 * c + 2], pa0, pa1, pa2, pa3, a2, b2);
-          mma_f16_16816(o[4 * c + 3], pa0, pa1, pa2, pa3, a3, b3);
-        }
-      }
-      if (masked && __any_sync(0xffffffffu, nan != 0)) {
-        // columns 2t, 2t + 1 of value tile j are dims CH (2t) + j, CH (2t + 1) + j:
-        // lanes 8t + tt and 8t + 4 + tt hold them for token pair tt
-        const float qnan = __int_as_float(0x7FFFFFFF);
+        for (int j = 0; j < CH / 2; ++j) o[q][j][0] = o[q][j][1] = o[q][j][2] = o[q][j][3] = 0.f;
+
 #pragma unroll 1
-        for (int tok = 0; tok < 32; ++tok) {
-          const int tt = (tok & 7) >> 1, i = (tok & 1) + 2 * ((tok >> 3) & 1), j = p0 + tok;
-          const bool there = ((tok < 16 ? meta0 : meta1) >> 16) != 0;
-          const bool see0 = there && j >= lo0 && j < hi0, see1 = there && j >= lo1 && j < hi1;
-          const uint8_t* hp = base + (tok >> 4) * Sh::HALF;
+      for (int st = 0; st < nseg; ++st) {
+        dec_fetch<D, NT>(a, ld, off, n_warp, ring, lane);
+        cp_async_wait<Sh::STAGES - 1>();
+        const uint32_t meta[2] = {dec_scales(ld, done, 0), dec_scales(ld, done, 1)};
+        ++done;
+        __syncwarp();
+        const uint8_t* base = ringp + slot_in * (2 * Sh::HALF);
+        const uint8_t* sp = base + lane * 16;
+        const int p0 = (cur.x.s0 + cur.s + st) << 5;
+        slot_in = slot_in + 1 == Sh::STAGES ? 0 : slot_in + 1;
+        if (!((meta[0] | meta[1]) >> 16) || p0 >= hi_any || p0 + 32 <= lo_any) continue;
+        // ---- scores: (tokens g, g + 8 of a half) x (rows 2t, 2t + 1) ----
+        float s[NT][2][4];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int src = 8 * t + 4 * c + tt;
-            const uint8_t* p = D == 128 ? hp + (Sh::KP + i) * 512 + src * 16
-                                        : hp + (Sh::KP + (i >> 1)) * 512 + src * 16 + (i & 1) * 8;
+        for (int q = 0; q < NT; ++q)
 #pragma unroll
-            for (int jj = 0; jj < CH; ++jj) {
-              if ((p[jj] & 0x7F) != 0x7F) continue;
-              if (see0) o[jj][c] = qnan;
-              if (see1) o[jj][2 + c] = qnan;
+          for (int h = 0; h < 2; ++h) s[q][h][0] = s[q][h][1] = s[q][h][2] = s[q][h][3] = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          uint4 w[2][2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              w[h][i] = *reinterpret_cast<const uint4*>(sp + h * Sh::HALF + (i * (D / 64) + c) * 512);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t a0, a1, a2, a3;
+              e4m3x4_to_f16x2(k == 0 ? w[h][0].x : k == 1 ? w[h][0].y : k == 2 ? w[h][0].z : w[h][0].w,
+                              a0, a2);
+              e4m3x4_to_f16x2(k == 0 ? w[h][1].x : k == 1 ? w[h][1].y : k == 2 ? w[h][1].z : w[h][1].w,
+                              a1, a3);
+#pragma unroll
+              for (int q = 0; q < NT; ++q)
+                mma_f16_16816(s[q][h], a0, a1, a2, a3, qf[q][4 * c + k].x, qf[q][4 * c + k].y);
             }
           }
         }
-        __syncwarp();
+        // ---- weights ----
+        float ke[2], ev[2], un[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int e = (int)((meta[h] >> 8) & 0xFFu) - 128;
+          ke[h] = pow2f((int)(meta[h] & 0xFFu) - 128);
+          ev[h] = (float)e;
+          un[h] = pow2f(-e);
+        }
+        const bool masked = p0 + 32 > hi_all || p0 < lo_all || !((meta[0] & meta[1]) >> 16);
+        if (masked) {
+#pragma unroll
+          for (int q = 0; q < NT; ++q)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {   // half i / 4, token g + 8 (i / 2 % 2), row i % 2
+              const int j = p0 + 16 * (i >> 2) + 8 * ((i >> 1) & 1) + g;
+              if (!(meta[i >> 2] >> 16) || j < lo[q][i & 1] || j >= hi[q][i & 1])
+                s[q][i >> 2][i & 3] = -INFINITY;
+            }
+        }
+        float x[NT][2];
+        bool up = false;
+#pragma unroll
+        for (int q = 0; q < NT; ++q)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            // (a factor that underflowed to 0 makes NaN of -infinity, which fmaxf drops)
+            float v = fmaxf(fmaf(fmaxf(s[q][0][r], s[q][0][2 + r]), fac[q][r] * ke[0], ev[0]),
+                            fmaf(fmaxf(s[q][1][r], s[q][1][2 + r]), fac[q][r] * ke[1], ev[1]));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+            x[q][r] = v;
+            up |= v > m[q][r];
+          }
+        if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+          for (int q = 0; q < NT; ++q)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float n = fmaxf(m[q][r], x[q][r]);
+              const float d = attn_factor(m[q][r], n);
+              m[q][r] = n;
+              l[q][r] *= d;
+#pragma unroll
+              for (int j = 0; j < CH / 2; ++j) {
+                o[q][j][r] *= d;
+                o[q][j][2 + r] *= d;
+              }
+            }
+        }
+        uint32_t pb[NT][2][2];
+#pragma unroll
+        for (int q = 0; q < NT; ++q) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float ref = m[q][r] == -INFINITY ? 0.f : m[q][r];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float f = fac[q][r] * ke[h], c = ev[h] - ref;
+              s[q][h][r] = exp2_approx(fmaf(s[q][h][r], f, c));
+              s[q][h][2 + r] = exp2_approx(fmaf(s[q][h][2 + r], f, c));
+            }
+          }
+          if (masked) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int j = p0 + 16 * (i >> 2) + 8 * ((i >> 1) & 1) + g;
+              if (!(meta[i >> 2] >> 16) || j < lo[q][i & 1] || j >= hi[q][i & 1])
+                s[q][i >> 2][i & 3] = 0.f;
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              l[q][r] = fmaf(un[h], s[q][h][r] + s[q][h][2 + r], l[q][r]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            pb[q][h][0] = movmatrix(pack_f16x2(s[q][h][0], s[q][h][1]));
+            pb[q][h][1] = movmatrix(pack_f16x2(s[q][h][2], s[q][h][3]));
+          }
+        }
+        // ---- values ----
+        uint32_t nan = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint8_t* hp = sp + h * Sh::HALF;
+          uint32_t vw[4][CH / 4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (D == 128) {
+              const uint4 w = *reinterpret_cast<const uint4*>(hp + (Sh::KP + i) * 512);
+              vw[i][0] = w.x;
+              vw[i][1] = w.y;
+              vw[i][2] = w.z;
+              vw[i][3] = w.w;
+            } else {
+              const uint2 w =
+                  *reinterpret_cast<const uint2*>(hp + (Sh::KP + (i >> 1)) * 512 + (i & 1) * 8);
+              vw[i][0] = w.x;
+              vw[i][1] = w.y;
+            }
+          }
+          if (masked) {
+            // a weight of 0 does not keep a NaN value out of the sums: NaN codes
+            // leave the product here and are given back to the rows that see them
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int c = 0; c < CH / 4; ++c) vw[i][c] = drop_nan4(vw[i][c], nan);
+          }
+#pragma unroll
+          for (int c = 0; c < CH / 4; ++c) {
+            uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
+            e4m3x4_to_f16x2(__byte_perm(vw[0][c], vw[1][c], 0x5140), a0, a1);
+            e4m3x4_to_f16x2(__byte_perm(vw[2][c], vw[3][c], 0x5140), a2, a3);
+            e4m3x4_to_f16x2(__byte_perm(vw[0][c], vw[1][c], 0x7362), b0, b1);
+            e4m3x4_to_f16x2(__byte_perm(vw[2][c], vw[3][c], 0x7362), b2, b3);
+#pragma unroll
+            for (int q = 0; q < NT; ++q) {
+              mma_f16_16816(o[q][2 * c], a0, a1, a2, a3, pb[q][h][0], pb[q][h][1]);
+              mma_f16_16816(o[q][2 * c + 1], b0, b1, b2, b3, pb[q][h][0], pb[q][h][1]);
+            }
+          }
+        }
+        if (masked && __any_sync(0xffffffffu, nan != 0)) {
+          // lanes 4g + tt hold dims CH g .. of tokens 2tt, 2tt + 1, 2tt + 8, 2tt + 9
+          const float qnan = __int_as_float(0x7FFFFFFF);
+#pragma unroll 1
+          for (int tok = 0; tok < 32; ++tok) {
+            const int i = (tok & 1) + 2 * ((tok >> 3) & 1), j = p0 + tok;
+            const bool there = ((tok < 16 ? meta[0] : meta[1]) >> 16) != 0;
+            const int src = 4 * g + ((tok & 7) >> 1);
+            const uint8_t* hp = base + (tok >> 4) * Sh::HALF + src * 16;
+            const uint8_t* p =
+                D == 128 ? hp + (Sh::KP + i) * 512 : hp + (Sh::KP + (i >> 1)) * 512 + (i & 1) * 8;
+#pragma unroll
+            for (int jj = 0; jj < CH; ++jj) {
+              if ((p[jj] & 0x7F) != 0x7F) continue;
+#pragma unroll
+              for (int q = 0; q < NT; ++q)
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                  if (there && j >= lo[q][r] && j < hi[q][r]) o[q][jj >> 1][2 * (jj & 1) + r] = qnan;
+            }
+          }
+          __syncwarp();
+        }
       }
-    }
-    next -= nseg;
 
-    // ---- join the warps' sums, four rows a round ----
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-    if (t == 0) {
-      s_m[warp * 16 + g] = m0;
-      s_m[warp * 16 + g + 8] = m1;
-      s_l[warp * 16 + g] = l0;
-      s_l[warp * 16 + g + 8] = l1;
-    }
-    __syncthreads();
-    if (threadIdx.x < kDecWarps * 16) {
-      const int row = threadIdx.x & 15;
-      float m = -INFINITY, l = 0.f;
+      // ---- the tile's end, or the run's ----
+      const bool begins = cur.s == 0, ends = cur.s + nseg == cur.x.S;
+      float* slot = slots + (2 * warp + pieces) * Sh::SLOT;
 #pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) m = fmaxf(m, s_m[w * 16 + row]);
-      s_f[threadIdx.x] = attn_factor(s_m[threadIdx.x], m);
-      if (threadIdx.x < 16) {
+      for (int q = 0; q < NT; ++q)
 #pragma unroll
-        for (int w = 0; w < kDecWarps; ++w)
-          l = fmaf(s_l[w * 16 + row], attn_factor(s_m[w * 16 + row], m), l);
-        s_tm[row] = m;
-        s_tl[row] = l;
-      }
-    }
-    __syncthreads();
-    const bool whole = cur.s == 0 && nseg == cur.x.S;
-    float* slot = a.partial + (2ll * blockIdx.x + (part > 0)) * kDecSlot<D>;
-    const float d0 = s_f[warp * 16 + g], d1 = s_f[warp * 16 + g + 8];
+        for (int r = 0; r < 2; ++r) {
+          float v = l[q][r];
+          v += __shfl_xor_sync(0xffffffffu, v, 4);
+          v += __shfl_xor_sync(0xffffffffu, v, 8);
+          v += __shfl_xor_sync(0xffffffffu, v, 16);
+          const int row = 8 * q + 2 * t + r;
+          if (!dec_tile_row<ROWS>(a, cur, row, i0, hd)) continue;
+          if (begins && ends) {
+            const float inv = attn_inverse(v);
+            const long long tok = cur.x.w.tok + i0;
+            uint16_t* dst = a.out + tok * a.o_ts + hd * a.o_hs + g * CH;
 #pragma unroll
-    for (int round = 0; round < 4; ++round) {
-      if (4 * round >= real) break;
-      float* dst = s_join + (warp * 4 + (g & 3)) * Sh::RS + 2 * t;
-      if ((g >> 2) == (round & 1)) {
+            for (int j = 0; j < CH / 2; j += 4)
+              *reinterpret_cast<uint4*>(dst + 2 * j) =
+                  make_uint4(pack16(o[q][j][r] * inv, o[q][j][2 + r] * inv, a.f16),
+                             pack16(o[q][j + 1][r] * inv, o[q][j + 1][2 + r] * inv, a.f16),
+                             pack16(o[q][j + 2][r] * inv, o[q][j + 2][2 + r] * inv, a.f16),
+                             pack16(o[q][j + 3][r] * inv, o[q][j + 3][2 + r] * inv, a.f16));
+            if (g == 0 && a.lse) a.lse[tok * a.heads + hd] = attn_lse(m[q][r], v);
+          } else {
 #pragma unroll
-        for (int j = 0; j < CH; ++j)
-          *reinterpret_cast<float2*>(dst + j * 8) =
-              round < 2 ? make_float2(o[j][0] * d0, o[j][1] * d0)
-                        : make_float2(o[j][2] * d1, o[j][3] * d1);
-      }
-      __syncthreads();
-      for (int e = threadIdx.x; e < 2 * D; e += kDecThreads) {
-        const int r = e / (D / 2), row = 4 * round + r, col = (e % (D / 2)) * 2;
-        float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kDecWarps; ++w) {
-          const float2 v = *reinterpret_cast<const float2*>(s_join + (w * 4 + r) * Sh::RS + col);
-          sum.x += v.x;
-          sum.y += v.y;
+            for (int j = 0; j < CH / 2; ++j)
+              *reinterpret_cast<float2*>(slot + row * D + j * 16 + 2 * g) =
+                  make_float2(o[q][j][r], o[q][j][2 + r]);
+            if (g == 0) {
+              slot[ROWS * D + row] = m[q][r];
+              slot[ROWS * D + ROWS + row] = v;
+            }
+          }
         }
-        if (whole) {
-          const float inv = attn_inverse(s_tl[row]);
-          uint16_t* so = s_q + row * D + (col >> 3);
-          so[(col & 7) * CH] = (uint16_t)pack16(sum.x * inv, 0.f, a.f16);
-          so[((col & 7) + 1) * CH] = (uint16_t)pack16(sum.y * inv, 0.f, a.f16);
-        } else {
-          *reinterpret_cast<float2*>(slot + row * D + col) = sum;
-        }
+      if (!(begins && ends)) {
+        if (lane == 0)
+          s_piece[2 * warp + pieces] = {1 | (begins ? 2 : 0) | (ends ? 4 : 0), cur.r, cur.h,
+                                         cur.m, first + done - nseg};
+        ++pieces;
       }
-      __syncthreads();
+      if (done < n_warp) dec_next_tile<ROWS>(a, cur);
     }
-    if (whole) {
-      for (int e = threadIdx.x; e < real * (D / 8); e += kDecThreads) {
-        const int row = e / (D / 8), d = (e % (D / 8)) * 8;
-        int i, head;
-        dec_tile_row(a, cur, row, i, head);
-        const long long tok = cur.x.w.tok + i;
-        *reinterpret_cast<uint4*>(a.out + tok * a.o_ts + head * a.o_hs + d) =
-            *reinterpret_cast<const uint4*>(s_q + row * D + d);
-        if (d == 0 && a.lse) a.lse[tok * a.heads + head] = attn_lse(s_tm[row], s_tl[row]);
-      }
-      __syncthreads();   // the queries of the next tile go into s_q
-    } else {
-      if (threadIdx.x < 16) {
-        slot[16 * D + threadIdx.x] = s_tm[threadIdx.x];
-        slot[16 * D + 16 + threadIdx.x] = s_tl[threadIdx.x];
-      }
-      if (cur.s == 0 && threadIdx.x == 0) {
-        // this CTA begins a tile that later CTAs go on with
-        const long long end = u0 + u + cur.x.S;   // the tile's end in strips of the call
-        int* d = a.desc + 4 * blockIdx.x;
-        d[1] = part > 0;
-        d[2] = cur.r;
-        d[3] = cur.h * cur.x.M + cur.m;
-        d[0] = (int)((end - 1) / per) - (int)blockIdx.x + 1;
-      }
-    }
-    u += nseg;
-    ++part;
-    if (u < n_units) dec_next_tile(a, cur);
+    cp_async_wait<0>();
   }
-  cp_async_wait<0>();
+  __syncthreads();
+
+  // ---- join the warps' pieces: consecutive pieces up to the next that begins
+  // a tile are one tile; an item (tile, row) a warp ----
+  const int state = lane < 2 * W ? s_piece[lane].state : 0;
+  const unsigned valid = __ballot_sync(0xffffffffu, state & 1);
+  const unsigned begin = __ballot_sync(0xffffffffu, (state & 3) == 3) & valid;
+  const unsigned end = __ballot_sync(0xffffffffu, (state & 5) == 5) & valid;
+  if (valid == 0) return;
+  const unsigned heads = begin | (valid & -valid);   // first piece of each tile
+  const int last = 31 - __clz(heads);
+  int item = warp;
+  for (unsigned rest = heads; rest; rest &= rest - 1) {
+    const int p = __ffs(rest) - 1;
+    const unsigned later = rest & (rest - 1);
+    const unsigned span = valid & ~((1u << p) - 1) & (later ? (later & -later) - 1 : ~0u);
+    const int tail = 31 - __clz(span);
+    const bool b = (begin >> p) & 1u, e = (end >> tail) & 1u;
+    DecCursor c;
+    c.r = s_piece[p].r;
+    c.h = s_piece[p].h;
+    c.m = s_piece[p].m;
+    c.x = dec_row<ROWS>(a, c.r);
+    // a tile that the CTA's own ends cut: its slot, 0 for the one from before
+    float* out = slots + (2 * W + (b ? 1 : 0)) * Sh::SLOT;
+    for (; item < ROWS; item += W) {
+      int i, head;
+      const bool real = dec_tile_row<ROWS>(a, c, item, i, head);
+      if (!real) continue;
+      const bool in = (span >> lane) & 1u;
+      const float* ps = slots + lane * Sh::SLOT + ROWS * D + item;
+      const float mk = in ? ps[0] : -INFINITY;
+      const float tm = warp_max(mk);
+      const float f = in ? attn_factor(mk, tm) : 0.f;
+      const float tl = warp_sum(in ? ps[ROWS] * f : 0.f);
+      float2 acc[D / 64];
+#pragma unroll
+      for (int k = 0; k < D / 64; ++k) acc[k] = make_float2(0.f, 0.f);
+#pragma unroll 4
+      for (int k = p; k <= tail; ++k) {
+        const float fk = __shfl_sync(0xffffffffu, f, k);
+        if (!((span >> k) & 1u)) continue;
+        const float* src = slots + k * Sh::SLOT + item * D + 2 * lane;
+#pragma unroll
+        for (int n = 0; n < D / 64; ++n) {
+          const float2 v = *reinterpret_cast<const float2*>(src + 64 * n);
+          acc[n].x = fmaf(v.x, fk, acc[n].x);
+          acc[n].y = fmaf(v.y, fk, acc[n].y);
+        }
+      }
+      if (b && e) {
+        const float inv = attn_inverse(tl);
+        const long long tok = c.x.w.tok + i;
+        uint16_t* dst = a.out + tok * a.o_ts + head * a.o_hs;
+#pragma unroll
+        for (int n = 0; n < D / 64; ++n)
+          *reinterpret_cast<uint32_t*>(dst + dec_dim<D>(2 * lane + 64 * n)) =
+              pack16(acc[n].x * inv, acc[n].y * inv, a.f16);
+        if (lane == 0 && a.lse) a.lse[tok * a.heads + head] = attn_lse(tm, tl);
+      } else {
+#pragma unroll
+        for (int n = 0; n < D / 64; ++n)
+          *reinterpret_cast<float2*>(out + item * D + 2 * lane + 64 * n) = acc[n];
+        if (lane == 0) {
+          out[ROWS * D + item] = tm;
+          out[ROWS * D + ROWS + item] = tl;
+        }
+      }
+    }
+    item -= ROWS;
+    if (p == last && b && !e && threadIdx.x == 0) {
+      // this CTA begins a tile that later CTAs go on with
+      const long long tile = u0 + s_piece[p].at;
+      int* d = a.desc + 4 * blockIdx.x;
+      d[1] = c.r;
+      d[2] = c.h;
+      d[3] = c.m;
+      d[0] = (int)((tile + c.x.S - 1) / per) - (int)blockIdx.x + 1;
+    }
+  }
 }
 
 // Join of the tiles cut by CTA boundaries: block (i, j) takes rows j, j +
@@ -773,9 +862,11 @@ static __global__ void __launch_bounds__(kDecThreads, 1) kv_attention_decode(con
 constexpr int kJoinThreads = 512;
 constexpr int kJoinMax = 1024;   // CTAs of the first kernel
 
-template <int D>
+template <int D, int NT>
 static __global__ void __launch_bounds__(kJoinThreads) kv_attention_join(const AttnArgs a) {
-  constexpr int NG = kJoinThreads / D;
+  using Sh = DecShape<D, NT>;
+  constexpr int NG = kJoinThreads / D, ROWS = 8 * NT;
+  constexpr long long SLOT = Sh::SLOTS * Sh::SLOT;   // floats between two CTAs' slots
   __shared__ float s_w[kJoinMax];
   __shared__ float s_red[kJoinThreads];
   const int t = threadIdx.x;
@@ -784,21 +875,21 @@ static __global__ void __launch_bounds__(kJoinThreads) kv_attention_join(const A
   const int n = d.x;
   if (n == 0) return;
   DecCursor c;
-  c.r = d.z;
-  c.x = dec_row(a, c.r);
-  c.h = d.w / c.x.M;
-  c.m = d.w - c.h * c.x.M;
+  c.r = d.y;
+  c.h = d.z;
+  c.m = d.w;
+  c.x = dec_row<ROWS>(a, c.r);
   // piece k: the tile's slot in CTA i + k (its first one, but for the beginning)
-  const float* first = a.partial + (2ll * blockIdx.x + d.y) * kDecSlot<D>;
-  const float* rest = a.partial + 2ll * blockIdx.x * kDecSlot<D>;
-  const int col = t % D, grp = t / D, dim = (col & 7) * (D / 8) + (col >> 3);
-  for (int row = blockIdx.y; row < 16; row += gridDim.y) {
+  const float* rest = a.partial + blockIdx.x * SLOT + 2 * Sh::WARPS * Sh::SLOT;
+  const float* first = rest + Sh::SLOT;
+  const int col = t % D, grp = t / D;
+  for (int row = blockIdx.y; row < ROWS; row += gridDim.y) {
     int i, head;
-    if (!dec_tile_row(a, c, row, i, head)) break;
+    if (!dec_tile_row<ROWS>(a, c, row, i, head)) break;
     float m = -INFINITY;
     for (int k = t; k < n; k += kJoinThreads) {
-      const float* p = k == 0 ? first : rest + 2ll * k * kDecSlot<D>;
-      const float v = p[16 * D + row];
+      const float* p = k == 0 ? first : rest + k * SLOT;
+      const float v = p[ROWS * D + row];
       s_w[k] = v;
       m = fmaxf(m, v);
     }
@@ -809,10 +900,10 @@ static __global__ void __launch_bounds__(kJoinThreads) kv_attention_join(const A
     m = warp_max(m);
     float l = 0.f;
     for (int k = t; k < n; k += kJoinThreads) {
-      const float* p = k == 0 ? first : rest + 2ll * k * kDecSlot<D>;
+      const float* p = k == 0 ? first : rest + k * SLOT;
       const float f = attn_factor(s_w[k], m);
       s_w[k] = f;
-      l = fmaf(p[16 * D + 16 + row], f, l);
+      l = fmaf(p[ROWS * D + ROWS + row], f, l);
     }
     l = warp_sum(l);
     __syncthreads();
@@ -824,7 +915,7 @@ static __global__ void __launch_bounds__(kJoinThreads) kv_attention_join(const A
     float sum = 0.f;
 #pragma unroll 4
     for (int k = grp; k < n; k += NG) {
-      const float* p = k == 0 ? first : rest + 2ll * k * kDecSlot<D>;
+      const float* p = k == 0 ? first : rest + k * SLOT;
       sum = fmaf(p[row * D + col], s_w[k], sum);
     }
     __syncthreads();
@@ -834,7 +925,7 @@ static __global__ void __launch_bounds__(kJoinThreads) kv_attention_join(const A
 #pragma unroll
       for (int w = 1; w < NG; ++w) sum += s_red[w * D + col];
       const long long tok = c.x.w.tok + i;
-      a.out[tok * a.o_ts + head * a.o_hs + dim] =
+      a.out[tok * a.o_ts + head * a.o_hs + dec_dim<D>(col)] =
           (uint16_t)pack16(sum * attn_inverse(l), 0.f, a.f16);
       if (a.lse && t == 0) a.lse[tok * a.heads + head] = attn_lse(m, l);
     }
