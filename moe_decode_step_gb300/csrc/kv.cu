@@ -44,7 +44,7 @@ int this_device(const Device** out) {
         (e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev)))
       return cuda_fail(e);
     d.sm103 = major == 10 && minor == 3;
-    d.n_sm = std::min(n_sm, kJoinMax);
+    d.n_sm = std::min(n_sm, kDecMaxCtas);
     d.known = true;   // concurrent first calls write the same values
   }
   *out = &d;
@@ -95,8 +95,8 @@ int cache_view(const moe_kv_cache_t* c, KvView* v) {
   return MOE_OK;
 }
 
-// Workspace of an attention call: per CTA a description and its slots.
-size_t desc_bytes(int n_sm) { return ((size_t)n_sm * 16 + 255) / 256 * 256; }
+// Workspace of an attention call: per CTA its counters and its slots.
+size_t arrived_bytes(int n_sm) { return ((size_t)n_sm * 16 + 255) / 256 * 256; }
 template <int D>
 size_t dec_floats_of() {
   return std::max(DecShape<D, 1>::SLOTS * DecShape<D, 1>::SLOT,
@@ -105,26 +105,21 @@ size_t dec_floats_of() {
 size_t dec_floats(int d) { return d == 64 ? dec_floats_of<64>() : dec_floats_of<128>(); }
 
 template <int D, int NT>
-int launch_decode(const AttnArgs& a, int n_sm, int max_q, cudaStream_t st) {
+int launch_decode(AttnArgs a, int n_sm, int max_q, cudaStream_t st) {
   using Sh = DecShape<D, NT>;
   cudaError_t e = cudaFuncSetAttribute(kv_attention_decode<D, NT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
   if (e != cudaSuccess) return cuda_fail(e);
-  kv_attention_decode<D, NT><<<n_sm, Sh::THREADS, Sh::SMEM, st>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e);
-  // the join starts while the first kernel drains and waits for it
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(n_sm, (unsigned)std::min<long long>(
-                               Sh::ROWS, std::max(1ll, (long long)max_q * a.group)));
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kv_attention_join<D, NT>, a);
-  return e == cudaSuccess ? MOE_OK : cuda_fail(e);
+  // strips the call can have at most, as far as the host knows; any grid is right
+  long long span = (long long)a.max_blocks << a.c.bs_log2;
+  if (a.window > 0) span = std::min(span, (long long)a.window + max_q + 32);
+  const long long tiles = std::max(1ll, ((long long)max_q * a.group + Sh::ROWS - 1) / Sh::ROWS);
+  const double strips = (double)a.rows * a.c.heads * tiles * (double)((span + 31) / 32);
+  const int grid = (int)std::min((double)n_sm, strips / Sh::WARPS + 1);
+  if ((e = cudaMemsetAsync(a.arrived, 0, (size_t)grid * 16, st)) != cudaSuccess)
+    return cuda_fail(e);
+  kv_attention_decode<D, NT><<<grid, Sh::THREADS, Sh::SMEM, st>>>(a);
+  return end();
 }
 
 template <int D>
@@ -225,7 +220,7 @@ size_t moe_kv_attention_workspace(int head_dim) {
   if (head_dim != 64 && head_dim != 128) return 0;
   const Device* dev;
   if (this_device(&dev)) return 0;
-  return desc_bytes(dev->n_sm) + dec_floats(head_dim) * (size_t)dev->n_sm * 4;
+  return arrived_bytes(dev->n_sm) + (size_t)dev->n_sm * dec_floats(head_dim) * 4;
 }
 
 int moe_kv_attention(void* stream, const moe_kv_cache_t* cache, const moe_kv_attention_t* args) {
@@ -272,8 +267,8 @@ int moe_kv_attention(void* stream, const moe_kv_cache_t* cache, const moe_kv_att
   a.window = t.window;
   a.scale_log2 = t.scale * 1.4426950408889634f;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  a.desc = static_cast<int*>(t.workspace);
-  a.partial = reinterpret_cast<float*>(static_cast<char*>(t.workspace) + desc_bytes(dev->n_sm));
+  a.arrived = static_cast<unsigned*>(t.workspace);
+  a.partial = reinterpret_cast<float*>(static_cast<char*>(t.workspace) + arrived_bytes(dev->n_sm));
   return cache->head_dim == 64 ? launch_attention<64>(a, dev->n_sm, t.max_q, st)
                                : launch_attention<128>(a, dev->n_sm, t.max_q, st);
 }

@@ -20,7 +20,7 @@ struct AttnArgs {
   int f16, rows, n_tokens, heads, group, max_blocks, causal, window;
   float scale_log2;   // scale * log2(e)
   float* partial;     // slots of partial sums
-  int* desc;          // per CTA: the split tile it begins
+  unsigned* arrived;  // four per CTA, zero when the kernel starts
 };
 
 // One row's queries: tokens [tok, tok + n), seq cached tokens.
@@ -59,15 +59,19 @@ __device__ __forceinline__ void attn_seen(const AttnArgs& a, const AttnRow& w, i
 //
 // Work: strips of 32 tokens of (row of the batch, KV head, tile), ordered in
 // that order; CTA i takes strips [i * per, (i + 1) * per) and each of its
-// warps an equal run of them, so that ragged lengths leave every warp the same
-// bytes.  A warp works by itself: it writes the tiles that lie inside its run
-// and leaves partial sums of the one or two that its ends cut in the
-// workspace (4 KB against the run's bytes).  When its warps are done the CTA
-// joins them once, in strip order, and the tiles that its own ends cut go to
-// the second kernel, which joins them in CTA order: results do not depend on
-// timing.  (With the strips dealt round the warps and joined in shared memory
-// at the end of every tile, a tile cost about 6 us of barriers and refilling;
-// the CTAs with most tiles then took 274 us where the median took 219.)
+// warps an equal run of them, whatever the rows' lengths.  A warp works by
+// itself: it writes the tiles that lie inside its run and keeps partial sums
+// of the one or two that its ends cut.  When its warps are done the CTA joins
+// them once, in strip order; of a tile that CTA ends cut, the CTA that arrives
+// last (a counter; nobody waits) joins the CTAs' sums in their order, in two
+// levels where they are more than 32: results do not depend on timing.  (With
+// the strips dealt round the warps and joined at the end of every tile, a tile
+// cost about 6 us of barriers and refilling; a second kernel for the CTAs'
+// sums 10 to 15 us against 4 inside.)
+// One CTA an SM, one share each: the SMs of full GPCs stream more slowly (at
+// 1.2 GB 40 of them took 230 us where the others took 200), but up to three
+// waves of smaller CTAs, two an SM, lost more in starts and joins (290 us
+// against 256).
 //
 // Loads: each thread copies (cp.async) exactly the 16-byte pieces that it
 // feeds to its own MMAs, into a ring of its own in shared memory, so a strip
@@ -102,11 +106,14 @@ struct DecShape {
   static constexpr int WARPS = NT == 1 ? (D == 128 ? 12 : 16) : (D == 128 ? 8 : 12);
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int STAGES = 196608 / (WARPS * 2 * HALF);
-  static constexpr int SMEM = WARPS * STAGES * 2 * HALF;
+  static constexpr int RING = STAGES * 2 * HALF;   // a warp's
+  static constexpr int SMEM = WARPS * RING;
   // one slot of partial sums: O [ROWS][D] in dec_dim's column order, then m
-  // [ROWS] and l [ROWS]; a warp has two, a CTA two more
+  // [ROWS] and l [ROWS].  A warp's last piece goes into its ring, its first
+  // one (if it has two) into a slot of the workspace, as do the CTA's sums
+  // of the tiles that its ends cut: one begun before it, one by it.
   static constexpr int SLOT = ROWS * D + 2 * ROWS;
-  static constexpr int SLOTS = 2 * WARPS + 2;
+  static constexpr int SLOTS = WARPS + 2;
 };
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -116,14 +123,17 @@ __device__ __forceinline__ float exp2_approx(float x) {
 }
 
 template <int BYTES>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool valid) {
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool valid,
+                                         uint64_t policy) {
   const int n = valid ? BYTES : 0;   // 0: the destination is zero-filled, src is not read
   if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(n)
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::128B [%0], [%1], 16, %2, %3;" ::"r"(
+                     dst),
+                 "l"(src), "r"(n), "l"(policy)
                  : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n)
+    asm volatile("cp.async.ca.shared.global.L2::cache_hint [%0], [%1], 8, %2, %3;" ::"r"(dst),
+                 "l"(src), "r"(n), "l"(policy)
                  : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
@@ -297,8 +307,11 @@ __device__ __forceinline__ uint32_t dec_pack_scales(bool exists, uint32_t sk, ui
 }
 
 // Byte offsets of a lane's pieces in a half: keys g, g + 8 and tokens 2t, 2t + 8.
+// The codes are read once: first out of L2, which keeps the kernel's own cold
+// code and the partial sums there.
 struct DecOffsets {
   long long k0, k1, v0, v1;
+  uint64_t policy;
 };
 
 template <int D, int NT>
@@ -333,11 +346,11 @@ __device__ __forceinline__ void dec_fetch(const AttnArgs& a, DecLoader& l, const
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
-            cp_async<16>(dst + (i * (D / 64) + c) * 512, src[i] + c * 64, true);
+            cp_async<16>(dst + (i * (D / 64) + c) * 512, src[i] + c * 64, true, f.policy);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if constexpr (D == 128) cp_async<16>(dst + (Sh::KP + i) * 512, src[2 + i], true);
-          else cp_async<8>(dst + (Sh::KP + (i >> 1)) * 512 + (i & 1) * 8, src[2 + i], true);
+          if constexpr (D == 128) cp_async<16>(dst + (Sh::KP + i) * 512, src[2 + i], true, f.policy);
+          else cp_async<8>(dst + (Sh::KP + (i >> 1)) * 512 + (i & 1) * 8, src[2 + i], true, f.policy);
         }
       } else {   // a row's end: what is not cached is zero-filled and not read
 #pragma unroll
@@ -345,13 +358,13 @@ __device__ __forceinline__ void dec_fetch(const AttnArgs& a, DecLoader& l, const
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
             cp_async<16>(dst + (i * (D / 64) + c) * 512,
-                         tok[i] < cached ? src[i] + c * 64 : a.c.k, tok[i] < cached);
+                         tok[i] < cached ? src[i] + c * 64 : a.c.k, tok[i] < cached, f.policy);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const bool in = tok[2 + i] < cached;
           const uint8_t* p = in ? src[2 + i] : a.c.v;
-          if constexpr (D == 128) cp_async<16>(dst + (Sh::KP + i) * 512, p, in);
-          else cp_async<8>(dst + (Sh::KP + (i >> 1)) * 512 + (i & 1) * 8, p, in);
+          if constexpr (D == 128) cp_async<16>(dst + (Sh::KP + i) * 512, p, in, f.policy);
+          else cp_async<8>(dst + (Sh::KP + (i >> 1)) * 512 + (i & 1) * 8, p, in, f.policy);
         }
       }
     }
@@ -406,9 +419,156 @@ __device__ __forceinline__ float attn_factor(float m, float ref) {
 // Partial sums of a piece of a tile.
 struct DecPiece {
   int state;       // 0: none, else 1 | begins its tile << 1 | ends it << 2
-  int r, h, m;
-  long long at;    // its first strip, in the CTA's order
+  int h, m, tok, n, S;
+  long long at;    // the tile's first strip, relative to the CTA's
 };
+
+// Partial sums to be joined: up to 32 pieces of one tile, those in `mask`,
+// into the output (dst null) or the slot `dst`, which may be one of theirs.
+// Piece k is in the workspace at base + k * stride (+ extra for k = 0), or, for
+// a CTA's own pieces (ring set), pieces 2w at base + w * stride and 2w + 1 at
+// ring + w * ring_stride.
+struct DecJob {
+  const float* base;
+  float* dst;
+  const float* ring;
+  long long stride, extra;
+  int ring_stride;
+  unsigned mask;
+  int h, m, tok, n;
+};
+
+// Where the joined rows go: the call's arguments, in shared memory.
+struct DecOut {
+  uint16_t* out;
+  float* lse;
+  long long o_ts, o_hs;
+  int heads, f16;
+  unsigned group;
+};
+
+// Rows `item`, item + step, ... of `jobs` jobs, the first rows of all of them
+// first; a warp a row, V columns a lane.  Small and not inlined: the code runs
+// a few times per launch, mostly fetched cold, and everything it reads but the
+// pieces is in shared memory.  What other CTAs wrote is read at L2, eight
+// pieces at once and without branches between: a round trip is 0.7 us.
+template <int D, int ROWS>
+__device__ __noinline__ void dec_join(const DecOut* to, const DecJob* job, int jobs, int item,
+                                      int step) {
+  constexpr int V = D / 32, B = 8;
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (; item < jobs * ROWS; item += step) {
+    const DecJob& b = job[item % jobs];
+    const int row = item / jobs;
+    const unsigned rho = (unsigned)b.m * ROWS + row;   // as in dec_tile_row
+    const int i = (int)(rho / to->group);
+    if (i >= b.n) continue;
+    const unsigned mask = b.mask;
+    const float* ring = b.ring;
+    const int col = V * lane, sh = ring ? 1 : 0;       // workspace piece k has mask bit k << sh
+    float mk = -INFINITY, lk = 0.f;
+    if ((mask >> lane) & 1u) {
+      if (ring && (lane & 1)) {
+        const float* ml = ring + (lane >> 1) * b.ring_stride + ROWS * D + row;
+        mk = ml[0];
+        lk = ml[ROWS];
+      } else {
+        const float* ml = b.base + (lane >> sh) * b.stride + (lane == 0 ? b.extra : 0) +
+                          ROWS * D + row;
+        mk = __ldcg(ml);
+        lk = __ldcg(ml + ROWS);
+      }
+    }
+    float acc[V];
+#pragma unroll
+    for (int n = 0; n < V; ++n) acc[n] = 0.f;
+    float tm = 0.f, f = 0.f, tl = 0.f;
+    const unsigned far = ring ? mask & 0x55555555u : mask;   // pieces in the workspace
+    const int k0 = far ? (__ffs(far) - 1) >> sh : 0, k1 = far ? (31 - __clz(far)) >> sh : -1;
+    bool first = true;
+#pragma unroll 1
+    for (int k = k0; first || k <= k1; k += B) {
+      float2 v[B][V / 2];
+      if (k <= k1) {
+#pragma unroll
+        for (int u = 0; u < B; ++u) {   // past the last one: the last again, weight 0
+          const int p = min(k + u, k1);
+          const float* src = b.base + p * b.stride + (p == 0 ? b.extra : 0) + row * D + col;
+#pragma unroll
+          for (int n = 0; n < V / 2; ++n)
+            v[u][n] = __ldcg(reinterpret_cast<const float2*>(src + 2 * n));
+        }
+      }
+      if (first) {
+        first = false;
+        tm = warp_max(mk);
+        f = (mask >> lane) & 1u ? attn_factor(mk, tm) : 0.f;
+        tl = warp_sum(lk * f);
+        if (ring) {
+#pragma unroll 4
+          for (int p = 0; p < 16; ++p) {
+            if (!((mask >> (2 * p + 1)) & 1u)) continue;
+            const float fk = __shfl_sync(0xffffffffu, f, 2 * p + 1);
+            const float* src = ring + p * b.ring_stride + row * D + col;
+#pragma unroll
+            for (int n = 0; n < V; ++n) acc[n] = fmaf(src[n], fk, acc[n]);
+          }
+        }
+      }
+      if (k <= k1) {
+#pragma unroll
+        for (int u = 0; u < B; ++u) {
+          const int bit = (k + u) << sh;
+          const bool in = k + u <= k1 && ((far >> bit) & 1u);
+          const float fk = __shfl_sync(0xffffffffu, f, bit & 31);
+#pragma unroll
+          for (int n = 0; n < V / 2; ++n) {   // (a slot not written may hold anything)
+            acc[2 * n] = fmaf(in ? v[u][n].x : 0.f, in ? fk : 0.f, acc[2 * n]);
+            acc[2 * n + 1] = fmaf(in ? v[u][n].y : 0.f, in ? fk : 0.f, acc[2 * n + 1]);
+          }
+        }
+      }
+    }
+    if (!b.dst) {
+      const float inv = attn_inverse(tl);
+      const long long tok = b.tok + i;
+      const int head = b.h * (int)to->group + (int)(rho - (unsigned)i * to->group);
+      uint16_t* out = to->out + tok * to->o_ts + head * to->o_hs;
+#pragma unroll
+      for (int n = 0; n < V; n += 2)
+        *reinterpret_cast<uint32_t*>(out + dec_dim<D>(col + n)) =
+            pack16(acc[n] * inv, acc[n + 1] * inv, to->f16);
+      if (lane == 0 && to->lse) to->lse[tok * to->heads + head] = attn_lse(tm, tl);
+    } else {
+      float* dst = b.dst;
+#pragma unroll
+      for (int n = 0; n < V; n += 2)
+        *reinterpret_cast<float2*>(dst + row * D + col + n) = make_float2(acc[n], acc[n + 1]);
+      if (lane == 0) {
+        dst[ROWS * D + row] = tm;
+        dst[ROWS * D + ROWS + row] = tl;
+      }
+    }
+  }
+}
+
+// The CTA's sums of a tile are in its slot: count them, and tell whether the
+// `n`-th has come.  Every thread calls.
+__device__ __forceinline__ bool dec_arrive(unsigned* counter, unsigned n) {
+  __shared__ unsigned s_old;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    s_old = atomicAdd(counter, 1u);
+    __threadfence();
+  }
+  __syncthreads();
+  return s_old == n - 1;
+}
+
+constexpr int kDecGroup = 32;                          // CTAs joined at once
+constexpr int kDecMaxCtas = kDecGroup * kDecGroup;     // in two levels
 
 template <int D, int NT>
 static __global__ void __launch_bounds__(DecShape<D, NT>::THREADS, 1)
@@ -417,19 +577,20 @@ static __global__ void __launch_bounds__(DecShape<D, NT>::THREADS, 1)
   constexpr int CH = Sh::CH, KS = D / 16, ROWS = Sh::ROWS, W = Sh::WARPS;
   extern __shared__ __align__(128) uint8_t dec_smem[];
   __shared__ DecPiece s_piece[2 * W];
+  __shared__ DecOut s_out;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const uint32_t ring = smem_addr(dec_smem) + warp * Sh::STAGES * 2 * Sh::HALF;
-  const uint8_t* ringp = dec_smem + warp * Sh::STAGES * 2 * Sh::HALF;
+  const uint32_t ring = smem_addr(dec_smem) + warp * Sh::RING;
+  uint8_t* ringp = dec_smem + warp * Sh::RING;
   float* slots = a.partial + (long long)blockIdx.x * Sh::SLOTS * Sh::SLOT;
 
-  pdl_launch_dependents();
   long long u0, n_units, per;
   DecCursor cur;
   dec_schedule<ROWS, W>(a, u0, n_units, per, cur);
-  if (threadIdx.x == 0) a.desc[4 * blockIdx.x] = 0;
   if (n_units <= 0) return;
   if (threadIdx.x < 2 * W) s_piece[threadIdx.x].state = 0;
+  if (threadIdx.x == 0)
+    s_out = {a.out, a.lse, a.o_ts, a.o_hs, a.heads, a.f16, (unsigned)a.group};
   __syncthreads();
 
   // this warp's run: strips [first, first + n_warp) of the CTA's
@@ -458,7 +619,8 @@ static __global__ void __launch_bounds__(DecShape<D, NT>::THREADS, 1)
     const bool exists = ld.id >= 0;
     const uint32_t sk0 = ld.sk, sv0 = ld.sv;
     const DecOffsets off = {g * a.c.tstride + t * 16, (g + 8) * a.c.tstride + t * 16,
-                            2 * t * a.c.tstride + g * CH, (2 * t + 8) * a.c.tstride + g * CH};
+                            2 * t * a.c.tstride + g * CH, (2 * t + 8) * a.c.tstride + g * CH,
+                            policy_evict_first()};
 #pragma unroll 1
     for (int i = 0; i < Sh::STAGES - 1; ++i) dec_fetch<D, NT>(a, ld, off, n_warp, ring, lane);
     ld.sc_now = dec_pack_scales(exists, sk0, sv0);
@@ -466,7 +628,6 @@ static __global__ void __launch_bounds__(DecShape<D, NT>::THREADS, 1)
     dec_lane_lookup(a, ld, lane);
     int done = 0;      // strips consumed
     int slot_in = 0;   // ring slot of the next one
-    int pieces = 0;    // partial sums left
 
 #pragma unroll 1
     while (done < n_warp) {
@@ -727,9 +888,14 @@ static __global__ void __launch_bounds__(DecShape<D, NT>::THREADS, 1)
         }
       }
 
-      // ---- the tile's end, or the run's ----
-      const bool begins = cur.s == 0, ends = cur.s + nseg == cur.x.S;
-      float* slot = slots + (2 * warp + pieces) * Sh::SLOT;
+      // ---- the tile's end, or the run's: then the ring is free ----
+      const long long at = first + done - nseg - cur.s;
+      const bool begins = cur.s == 0, ends = cur.s + nseg == cur.x.S, last = done == n_warp;
+      if (last) {
+        cp_async_wait<0>();
+        __syncwarp();
+      }
+      float* slot = last ? reinterpret_cast<float*>(ringp) : slots + warp * Sh::SLOT;
 #pragma unroll
       for (int q = 0; q < NT; ++q)
 #pragma unroll
@@ -763,15 +929,11 @@ static __global__ void __launch_bounds__(DecShape<D, NT>::THREADS, 1)
             }
           }
         }
-      if (!(begins && ends)) {
-        if (lane == 0)
-          s_piece[2 * warp + pieces] = {1 | (begins ? 2 : 0) | (ends ? 4 : 0), cur.r, cur.h,
-                                         cur.m, first + done - nseg};
-        ++pieces;
-      }
-      if (done < n_warp) dec_next_tile<ROWS>(a, cur);
+      if (!(begins && ends) && lane == 0)
+        s_piece[2 * warp + last] = {1 | (begins ? 2 : 0) | (ends ? 4 : 0), cur.h, cur.m,
+                                    cur.x.w.tok, cur.x.w.n, cur.x.S, at};
+      if (!last) dec_next_tile<ROWS>(a, cur);
     }
-    cp_async_wait<0>();
   }
   __syncthreads();
 
@@ -783,153 +945,61 @@ static __global__ void __launch_bounds__(DecShape<D, NT>::THREADS, 1)
   const unsigned end = __ballot_sync(0xffffffffu, (state & 5) == 5) & valid;
   if (valid == 0) return;
   const unsigned heads = begin | (valid & -valid);   // first piece of each tile
-  const int last = 31 - __clz(heads);
-  int item = warp;
-  for (unsigned rest = heads; rest; rest &= rest - 1) {
-    const int p = __ffs(rest) - 1;
-    const unsigned later = rest & (rest - 1);
-    const unsigned span = valid & ~((1u << p) - 1) & (later ? (later & -later) - 1 : ~0u);
-    const int tail = 31 - __clz(span);
-    const bool b = (begin >> p) & 1u, e = (end >> tail) & 1u;
-    DecCursor c;
-    c.r = s_piece[p].r;
-    c.h = s_piece[p].h;
-    c.m = s_piece[p].m;
-    c.x = dec_row<ROWS>(a, c.r);
-    // a tile that the CTA's own ends cut: its slot, 0 for the one from before
-    float* out = slots + (2 * W + (b ? 1 : 0)) * Sh::SLOT;
-    for (; item < ROWS; item += W) {
-      int i, head;
-      const bool real = dec_tile_row<ROWS>(a, c, item, i, head);
-      if (!real) continue;
-      const bool in = (span >> lane) & 1u;
-      const float* ps = slots + lane * Sh::SLOT + ROWS * D + item;
-      const float mk = in ? ps[0] : -INFINITY;
-      const float tm = warp_max(mk);
-      const float f = in ? attn_factor(mk, tm) : 0.f;
-      const float tl = warp_sum(in ? ps[ROWS] * f : 0.f);
-      float2 acc[D / 64];
-#pragma unroll
-      for (int k = 0; k < D / 64; ++k) acc[k] = make_float2(0.f, 0.f);
-#pragma unroll 4
-      for (int k = p; k <= tail; ++k) {
-        const float fk = __shfl_sync(0xffffffffu, f, k);
-        if (!((span >> k) & 1u)) continue;
-        const float* src = slots + k * Sh::SLOT + item * D + 2 * lane;
-#pragma unroll
-        for (int n = 0; n < D / 64; ++n) {
-          const float2 v = *reinterpret_cast<const float2*>(src + 64 * n);
-          acc[n].x = fmaf(v.x, fk, acc[n].x);
-          acc[n].y = fmaf(v.y, fk, acc[n].y);
-        }
-      }
-      if (b && e) {
-        const float inv = attn_inverse(tl);
-        const long long tok = c.x.w.tok + i;
-        uint16_t* dst = a.out + tok * a.o_ts + head * a.o_hs;
-#pragma unroll
-        for (int n = 0; n < D / 64; ++n)
-          *reinterpret_cast<uint32_t*>(dst + dec_dim<D>(2 * lane + 64 * n)) =
-              pack16(acc[n].x * inv, acc[n].y * inv, a.f16);
-        if (lane == 0 && a.lse) a.lse[tok * a.heads + head] = attn_lse(tm, tl);
-      } else {
-#pragma unroll
-        for (int n = 0; n < D / 64; ++n)
-          *reinterpret_cast<float2*>(out + item * D + 2 * lane + 64 * n) = acc[n];
-        if (lane == 0) {
-          out[ROWS * D + item] = tm;
-          out[ROWS * D + ROWS + item] = tl;
-        }
-      }
-    }
-    item -= ROWS;
-    if (p == last && b && !e && threadIdx.x == 0) {
-      // this CTA begins a tile that later CTAs go on with
-      const long long tile = u0 + s_piece[p].at;
-      int* d = a.desc + 4 * blockIdx.x;
-      d[1] = c.r;
-      d[2] = c.h;
-      d[3] = c.m;
-      d[0] = (int)((tile + c.x.S - 1) / per) - (int)blockIdx.x + 1;
-    }
+  __shared__ DecJob s_job[2 * W];
+  __shared__ int s_open[2];   // pieces of the tiles that the CTA's own ends cut
+  const int jobs = __popc(heads);
+  if (threadIdx.x < 2) s_open[threadIdx.x] = -1;
+  __syncthreads();
+  if (warp == 0 && ((heads >> lane) & 1u)) {
+    const unsigned later = heads & ~((2u << lane) - 1);
+    const unsigned span =
+        valid & ~((1u << lane) - 1) & (later ? (later & -later) - 1 : ~0u);
+    const bool b = (begin >> lane) & 1u, e = (end >> (31 - __clz(span))) & 1u;
+    const DecPiece& p = s_piece[lane];
+    s_job[__popc(heads & ((1u << lane) - 1))] = {
+        slots, b && e ? nullptr : slots + (W + (b ? 1 : 0)) * Sh::SLOT,
+        reinterpret_cast<const float*>(dec_smem), Sh::SLOT, 0, Sh::RING / 4, span, p.h,
+        p.m, p.tok, p.n};
+    if (!(b && e)) s_open[b ? 1 : 0] = lane;
   }
-}
+  __syncthreads();
+  dec_join<D, ROWS>(&s_out, s_job, jobs, warp, W);
 
-// Join of the tiles cut by CTA boundaries: block (i, j) takes rows j, j +
-// gridDim.y, ... of the tile that CTA i began, if any.  The partial sums of
-// CTAs i, i + 1, ... go round groups of D threads, four loads in flight each,
-// and the groups' sums are added in order.
-constexpr int kJoinThreads = 512;
-constexpr int kJoinMax = 1024;   // CTAs of the first kernel
-
-template <int D, int NT>
-static __global__ void __launch_bounds__(kJoinThreads) kv_attention_join(const AttnArgs a) {
-  using Sh = DecShape<D, NT>;
-  constexpr int NG = kJoinThreads / D, ROWS = 8 * NT;
-  constexpr long long SLOT = Sh::SLOTS * Sh::SLOT;   // floats between two CTAs' slots
-  __shared__ float s_w[kJoinMax];
-  __shared__ float s_red[kJoinThreads];
-  const int t = threadIdx.x;
-  pdl_wait_prerequisites();
-  const int4 d = *reinterpret_cast<const int4*>(a.desc + 4 * blockIdx.x);
-  const int n = d.x;
-  if (n == 0) return;
-  DecCursor c;
-  c.r = d.y;
-  c.h = d.z;
-  c.m = d.w;
-  c.x = dec_row<ROWS>(a, c.r);
-  // piece k: the tile's slot in CTA i + k (its first one, but for the beginning)
-  const float* rest = a.partial + blockIdx.x * SLOT + 2 * Sh::WARPS * Sh::SLOT;
-  const float* first = rest + Sh::SLOT;
-  const int col = t % D, grp = t / D;
-  for (int row = blockIdx.y; row < ROWS; row += gridDim.y) {
-    int i, head;
-    if (!dec_tile_row<ROWS>(a, c, row, i, head)) break;
-    float m = -INFINITY;
-    for (int k = t; k < n; k += kJoinThreads) {
-      const float* p = k == 0 ? first : rest + k * SLOT;
-      const float v = p[ROWS * D + row];
-      s_w[k] = v;
-      m = fmaxf(m, v);
+  // ---- and the CTAs' sums ----
+#pragma unroll 1
+  for (int o = 0; o < 2; ++o) {
+    const int first_piece = s_open[o];
+    if (first_piece < 0) continue;
+    const DecPiece& p = s_piece[first_piece];
+    const long long tile = u0 + p.at;
+    const int c0 = (int)(tile / per), n = (int)((tile + p.S - 1) / per) - c0 + 1;
+    const int grp = ((int)blockIdx.x - c0) / kDecGroup;
+    const int in_grp = min(kDecGroup, n - grp * kDecGroup);
+    // counters of CTA c: the tile it begins, that tile's first group, and the
+    // later group of a tile begun before that starts with c
+    unsigned* counters[2] = {a.arrived + 4 * (c0 + grp * kDecGroup) + (grp ? 2 : 1),
+                             a.arrived + 4 * c0};
+    // CTA c0's slot is its second, the others' their first
+    constexpr long long stride = (long long)Sh::SLOTS * Sh::SLOT;
+    float* base = a.partial + c0 * stride + W * Sh::SLOT;
+#pragma unroll 1
+    for (int level = 0; level < 2; ++level) {
+      // 0: the CTAs of one group; 1: the groups, each in its first CTA's slot
+      const int groups = (n + kDecGroup - 1) / kDecGroup;
+      if (!dec_arrive(level ? counters[1] : counters[0], level ? groups : in_grp)) break;
+      if (threadIdx.x == 0) {
+        float* from = base + (level ? 0 : grp * kDecGroup * stride);
+        const long long extra = level == 0 && grp > 0 ? 0 : Sh::SLOT;
+        const bool final = level == 1 || groups == 1;
+        const int count = level ? groups : in_grp;
+        s_job[0] = {from, final ? nullptr : from + extra, nullptr,
+                    level ? kDecGroup * stride : stride, extra, 0, ~0u >> (32 - count), p.h, p.m,
+                    p.tok, p.n};
+      }
+      __syncthreads();
+      dec_join<D, ROWS>(&s_out, s_job, 1, warp, W);
+      if (groups == 1) break;
     }
-    m = warp_max(m);
-    if ((t & 31) == 0) s_red[t >> 5] = m;
-    __syncthreads();
-    m = s_red[t & 15];
-    m = warp_max(m);
-    float l = 0.f;
-    for (int k = t; k < n; k += kJoinThreads) {
-      const float* p = k == 0 ? first : rest + k * SLOT;
-      const float f = attn_factor(s_w[k], m);
-      s_w[k] = f;
-      l = fmaf(p[ROWS * D + ROWS + row], f, l);
-    }
-    l = warp_sum(l);
-    __syncthreads();
-    if ((t & 31) == 0) s_red[t >> 5] = l;
-    __syncthreads();
-    l = 0.f;
-#pragma unroll
-    for (int w = 0; w < kJoinThreads / 32; ++w) l += s_red[w];
-    float sum = 0.f;
-#pragma unroll 4
-    for (int k = grp; k < n; k += NG) {
-      const float* p = k == 0 ? first : rest + k * SLOT;
-      sum = fmaf(p[row * D + col], s_w[k], sum);
-    }
-    __syncthreads();
-    s_red[t] = sum;
-    __syncthreads();
-    if (grp == 0) {
-#pragma unroll
-      for (int w = 1; w < NG; ++w) sum += s_red[w * D + col];
-      const long long tok = c.x.w.tok + i;
-      a.out[tok * a.o_ts + head * a.o_hs + dec_dim<D>(col)] =
-          (uint16_t)pack16(sum * attn_inverse(l), 0.f, a.f16);
-      if (a.lse && t == 0) a.lse[tok * a.heads + head] = attn_lse(m, l);
-    }
-    __syncthreads();
   }
 }
 
