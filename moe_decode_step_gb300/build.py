@@ -7,8 +7,9 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libmoe_decode.so")
 SOURCES = ["csrc/moe_decode.cu", "csrc/noalloc.cu", "csrc/kv.cu"]
 HEADERS = ["csrc/common.cuh", "csrc/mxfp4.cuh", "csrc/planes.cuh", "csrc/stream.cuh",
-           "csrc/tc.cuh", "csrc/topk.cuh", "csrc/tail.cuh", "csrc/kv_cache.cuh",
-           "csrc/kv_plan.cuh", "csrc/kv_append.cuh", "csrc/kv_attention.cuh", "csrc/route.cuh"]
+           "csrc/tc.cuh", "csrc/tcgen05.cuh", "csrc/topk.cuh", "csrc/tail.cuh", "csrc/kv_cache.cuh",
+           "csrc/kv_plan.cuh", "csrc/kv_append.cuh", "csrc/kv_attention.cuh",
+           "csrc/kv_attention_tc.cuh", "csrc/route.cuh"]
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-shared", "--threads", "4"]
 

@@ -7,6 +7,7 @@
 
 #include "kv_append.cuh"
 #include "kv_attention.cuh"
+#include "kv_attention_tc.cuh"
 #include "kv_plan.cuh"
 #include "moe_decode.h"
 #include "route.cuh"
@@ -99,8 +100,8 @@ int cache_view(const moe_kv_cache_t* c, KvView* v) {
 size_t arrived_bytes(int n_sm) { return ((size_t)n_sm * 16 + 255) / 256 * 256; }
 template <int D>
 size_t dec_floats_of() {
-  return std::max(DecShape<D, 1>::SLOTS * DecShape<D, 1>::SLOT,
-                  DecShape<D, 2>::SLOTS * DecShape<D, 2>::SLOT);
+  return std::max({DecShape<D, 1>::SLOTS * DecShape<D, 1>::SLOT,
+                   DecShape<D, 2>::SLOTS * DecShape<D, 2>::SLOT, 2 * PrShape<D, true>::SLOT});
 }
 size_t dec_floats(int d) { return d == 64 ? dec_floats_of<64>() : dec_floats_of<128>(); }
 
@@ -122,8 +123,22 @@ int launch_decode(AttnArgs a, int n_sm, int max_q, cudaStream_t st) {
   return end();
 }
 
+template <int D, bool PAIR>
+int launch_tensor(const AttnArgs& a, int n_sm, cudaStream_t st) {
+  using Sh = PrShape<D, PAIR>;
+  cudaError_t e = cudaFuncSetAttribute(kv_attention_tc<D, PAIR>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if ((e = cudaMemsetAsync(a.arrived, 0, (size_t)n_sm * 16, st)) != cudaSuccess)
+    return cuda_fail(e);
+  kv_attention_tc<D, PAIR><<<n_sm, kPrThreads, Sh::SMEM, st>>>(a);
+  return end();
+}
+
 template <int D>
 int launch_attention(const AttnArgs& a, int n_sm, int max_q, cudaStream_t st) {
+  if ((long long)max_q * a.group > 128) return launch_tensor<D, true>(a, n_sm, st);
+  if ((long long)max_q * a.group > 64) return launch_tensor<D, false>(a, n_sm, st);
   // rows of the longest batch row per KV head, as far as the host knows
   return (long long)max_q * a.group <= 8 ? launch_decode<D, 1>(a, n_sm, max_q, st)
                                          : launch_decode<D, 2>(a, n_sm, max_q, st);

@@ -452,7 +452,8 @@ struct DecOut {
 // a few times per launch, mostly fetched cold, and everything it reads but the
 // pieces is in shared memory.  What other CTAs wrote is read at L2, eight
 // pieces at once and without branches between: a round trip is 0.7 us.
-template <int D, int ROWS>
+// (ORDERED: the pieces' columns are the dims themselves.)
+template <int D, int ROWS, bool ORDERED = false>
 __device__ __noinline__ void dec_join(const DecOut* to, const DecJob* job, int jobs, int item,
                                       int step) {
   constexpr int V = D / 32, B = 8;
@@ -537,7 +538,7 @@ __device__ __noinline__ void dec_join(const DecOut* to, const DecJob* job, int j
       uint16_t* out = to->out + tok * to->o_ts + head * to->o_hs;
 #pragma unroll
       for (int n = 0; n < V; n += 2)
-        *reinterpret_cast<uint32_t*>(out + dec_dim<D>(col + n)) =
+        *reinterpret_cast<uint32_t*>(out + (ORDERED ? col + n : dec_dim<D>(col + n))) =
             pack16(acc[n] * inv, acc[n + 1] * inv, to->f16);
       if (lane == 0 && to->lse) to->lse[tok * to->heads + head] = attn_lse(tm, tl);
     } else {

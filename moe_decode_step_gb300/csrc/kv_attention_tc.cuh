@@ -1,0 +1,923 @@
+// Attention over the 8-bit cache for many query rows per KV head (verify
+// steps, prompts): tcgen05 tensor cores.
+//
+// An item is TILE rows (query i, head of the group: row i * group + head) of
+// one KV head of one batch row: 256 as two streams of 128 rows that share
+// every tile of 128 keys (PAIR), or 128 rows whose two streams take the even
+// and the odd tiles of keys (a batch row of at most 128 rows).  The streams
+// alternate on the tensor cores: while one's scores (S = Q K^T, M = 128 rows,
+// N = 128 keys) go through the softmax, the other's products run.
+//
+// Roles (13 warps): warps 0..3 and 4..7, one stream each, a thread a row:
+// scores from tensor memory, running maximum and sum, weights back into tensor
+// memory (in the columns of their scores) as the A operand of O += P V; warps
+// 8..11 fetch codes, convert them to f16 and lay them out in shared memory as
+// K-major core matrices (K rows = keys, V^T rows = dims, transposed in
+// registers); warp 12 issues the MMAs.  Accumulators and S live in tensor
+// memory (2 x 128 columns of S, 2 x D of O).
+//
+// Bounds: 4 * 128 * 128 * D operations of a pair of products take 0.67 us of
+// an SM's tensor cores at D = 128; beside them 128 x 128 exponentials and
+// their arithmetic per stream and tile, and 32 KB of codes to convert per tile
+// of keys, which two streams share.
+//
+// Scales and weights as in kv_attention.cuh: t = score * log2(e) + ev per 16
+// keys, weights 2^(t - M).  M follows the maximum only when it grows by more
+// than 2^8, so that O in tensor memory is rarely rescaled; weights stay below
+// 2^8, far inside f16.
+//
+// Work split and joins as there, in tiles of 128 keys: CTA i takes tiles
+// [i * per, (i + 1) * per) of the order (batch row, row tile, KV head, keys).
+#pragma once
+
+#include "kv_attention.cuh"
+#include "tcgen05.cuh"
+
+namespace moe {
+
+constexpr int kPrWarps = 13;
+constexpr int kPrThreads = 32 * kPrWarps;
+constexpr int kPrKeys = 128;
+
+template <int D, bool PAIR>
+struct PrShape {
+  static constexpr int TILE = PAIR ? 256 : 128;
+  // byte distances in the operands: K and Q by 8 dims, V^T by 8 keys; padded
+  // so that the converters' 16-byte stores hit all banks
+  static constexpr int QLBO = 2048, KLBO = 2080, VSBO = 144, VLBO = D / 8 * VSBO + 16;
+  static constexpr int QBYTES = D / 8 * QLBO, KBYTES = D / 8 * KLBO, VBYTES = 16 * VLBO;
+  static constexpr int KOFF = (PAIR ? 2 : 1) * QBYTES, VOFF = KOFF + 2 * KBYTES;
+  static constexpr int SMEM = VOFF + 2 * VBYTES;
+  // a slot of partial sums: O [TILE][D], m [TILE], l [TILE]; two a CTA
+  static constexpr int SLOT = TILE * D + 2 * TILE;
+  static constexpr int OCOL = 256;   // tensor memory: S at 0 and 128, O at OCOL + D t
+};
+
+// ---- tensor memory, 32 lanes x 32 columns a warp ----
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+// D += A B with A (f16, two of K a column) in tensor memory.
+__device__ __forceinline__ void umma_f16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Instruction descriptor, kind::f16: f16 x f16 -> fp32, both K-major, M = 128.
+__device__ __forceinline__ constexpr uint32_t umma_idesc_f16(uint32_t N) {
+  return (1u << 4) | ((N >> 3) << 17) | ((128u >> 4) << 24);
+}
+// Generic writes to shared memory become visible to the tensor cores.
+__device__ __forceinline__ void fence_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// ---------------------------------------------------------------------------
+// Items and schedule
+// ---------------------------------------------------------------------------
+// Tiles of keys of the item of row tile m: [s0, s0 + S).
+template <int TILE>
+__device__ __forceinline__ void pr_span(const AttnArgs& a, const AttnRow& w, int m, int& s0,
+                                        int& S) {
+  const unsigned g = (unsigned)a.group;
+  const int i0 = (int)((unsigned)TILE * m / g);
+  const int i1 = min(w.n - 1, (int)(((unsigned)TILE * m + TILE - 1) / g));
+  int lo, hi, unused;
+  attn_seen(a, w, i0, lo, unused);
+  attn_seen(a, w, i1, unused, hi);
+  s0 = lo >> 7;
+  S = max(1, (int)(((unsigned)hi + 127) >> 7) - s0);   // nothing seen: one tile, for the zeros
+}
+
+template <int TILE>
+__device__ __forceinline__ int pr_tiles(const AttnArgs& a, const AttnRow& w) {
+  return (int)(((unsigned)w.n * (unsigned)a.group + TILE - 1) / TILE);
+}
+
+struct PrCursor {
+  int r, m, h, s;   // batch row, row tile, KV head, next tile of keys (from s0)
+  AttnRow w;
+  int M, s0, S;
+};
+
+template <int TILE>
+__device__ __forceinline__ void pr_next_item(const AttnArgs& a, PrCursor& c) {
+  c.s = 0;
+  if (++c.h < a.c.heads) return;
+  c.h = 0;
+  if (++c.m >= c.M) {
+    c.m = 0;
+    do {
+      if (++c.r >= a.rows) return;
+      c.w = attn_row(a, c.r);
+      c.M = pr_tiles<TILE>(a, c.w);
+    } while (c.M == 0);
+  }
+  pr_span<TILE>(a, c.w, c.m, c.s0, c.S);
+}
+
+// Sum of S over a batch row's row tiles: by the lane alone, or (coop) with the
+// warp's lanes taking m = lane, lane + 32, ...
+template <int TILE>
+__device__ __forceinline__ long long pr_row_tiles(const AttnArgs& a, const AttnRow& w, int first,
+                                                  int step) {
+  const int M = pr_tiles<TILE>(a, w);
+  long long sum = 0;
+  for (int m = first; m < M; m += step) {
+    int s0, S;
+    pr_span<TILE>(a, w, m, s0, S);
+    sum += S;
+  }
+  return sum;
+}
+
+// Tiles of keys of batch row r, every lane of a warp with its own r (r < 0:
+// none); rows of many row tiles are summed by the whole warp.
+template <int TILE>
+__device__ __forceinline__ long long pr_warp_tiles(const AttnArgs& a, int r) {
+  constexpr int kAlone = 8;
+  AttnRow w{0, 0, 0};
+  if (r >= 0) w = attn_row(a, r);
+  const bool big = pr_tiles<TILE>(a, w) > kAlone;
+  long long sum = big ? 0 : pr_row_tiles<TILE>(a, w, 0, 1);
+  for (unsigned rest = __ballot_sync(0xffffffffu, big); rest; rest &= rest - 1) {
+    const int src = __ffs(rest) - 1;
+    const AttnRow o{0, __shfl_sync(0xffffffffu, w.n, src), __shfl_sync(0xffffffffu, w.seq, src)};
+    long long v = pr_row_tiles<TILE>(a, o, threadIdx.x & 31, 32);
+#pragma unroll
+    for (int k = 16; k; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
+    if ((threadIdx.x & 31) == src) sum = v;
+  }
+  return sum * a.c.heads;
+}
+
+// This CTA's tiles [u0, u0 + n) and its cursor at u0; every thread calls.
+template <int TILE>
+__device__ __forceinline__ void pr_schedule(const AttnArgs& a, long long& u0, long long& n,
+                                            long long& per, PrCursor& cur) {
+  __shared__ long long s_sum[kPrWarps];
+  __shared__ long long s_left;
+  __shared__ int s_row, s_m;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int chunk = (a.rows + kPrWarps - 1) / kPrWarps;
+  const int r0 = min(a.rows, warp * chunk), r1 = min(a.rows, r0 + chunk);
+  long long sum = 0;
+  for (int r = r0; r < r1; r += 32) sum += pr_warp_tiles<TILE>(a, r + lane < r1 ? r + lane : -1);
+#pragma unroll
+  for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+  if (lane == 0) s_sum[warp] = sum;
+  __syncthreads();
+  long long total = 0, before = 0;
+  for (int w = 0; w < kPrWarps; ++w) {
+    if (w == warp) before = total;
+    total += s_sum[w];
+  }
+  per = max((total + gridDim.x - 1) / gridDim.x, 2ll);
+  u0 = per * blockIdx.x;
+  n = min(per, total - u0);
+  if (n > 0 && u0 >= before && u0 < before + sum) {
+    for (int r = r0;; r += 32) {
+      const long long v = pr_warp_tiles<TILE>(a, r + lane < r1 ? r + lane : -1);
+      long long inc = v;
+#pragma unroll
+      for (int k = 1; k < 32; k <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, inc, k);
+        if (lane >= k) inc += o;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, before + inc > u0);
+      if (!past) {
+        before += __shfl_sync(0xffffffffu, inc, 31);
+        continue;
+      }
+      const int src = __ffs(past) - 1;
+      before += __shfl_sync(0xffffffffu, inc - v, src);
+      // the row tile: lanes take 32 of them at a time
+      const AttnRow w = attn_row(a, r + src);
+      for (int m = 0;; m += 32) {
+        int s0, S = 0;
+        if (m + lane < pr_tiles<TILE>(a, w)) pr_span<TILE>(a, w, m + lane, s0, S);
+        const long long x = (long long)S * a.c.heads;
+        long long y = x;
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+          const long long o = __shfl_up_sync(0xffffffffu, y, k);
+          if (lane >= k) y += o;
+        }
+        const unsigned in = __ballot_sync(0xffffffffu, before + y > u0);
+        if (!in) {
+          before += __shfl_sync(0xffffffffu, y, 31);
+          continue;
+        }
+        const int mm = __ffs(in) - 1;
+        before += __shfl_sync(0xffffffffu, y - x, mm);
+        if (lane == 0) {
+          s_row = r + src;
+          s_m = m + mm;
+          s_left = u0 - before;
+        }
+        break;
+      }
+      break;
+    }
+  }
+  __syncthreads();
+  if (n <= 0) return;
+  cur.r = s_row;
+  cur.m = s_m;
+  cur.w = attn_row(a, cur.r);
+  cur.M = pr_tiles<TILE>(a, cur.w);
+  pr_span<TILE>(a, cur.w, cur.m, cur.s0, cur.S);
+  cur.h = (int)(s_left / cur.S);
+  cur.s = (int)(s_left - (long long)cur.h * cur.S);
+}
+
+// What every and any row of the item sees.
+template <int TILE>
+__device__ __forceinline__ void pr_seen(const AttnArgs& a, const PrCursor& c, int& lo_all,
+                                        int& hi_all) {
+  const unsigned g = (unsigned)a.group;
+  int unused;
+  attn_seen(a, c.w, (int)((unsigned)TILE * c.m / g), unused, hi_all);
+  attn_seen(a, c.w, min(c.w.n - 1, (int)(((unsigned)TILE * c.m + TILE - 1) / g)), lo_all, unused);
+}
+
+// Keys at p0 .. p0 + 127 that some row of the item does not see.
+__device__ __forceinline__ bool pr_masked(int p0, int lo_all, int hi_all) {
+  return p0 + kPrKeys > hi_all || p0 < lo_all;
+}
+
+// ---------------------------------------------------------------------------
+// Shared state
+// ---------------------------------------------------------------------------
+struct PrShared {
+  uint64_t kfull[2], kempty[2], vfull[2], vempty[2];   // by stage of keys
+  uint64_t sfull[2], pfull[2], ofull[2], qfull[2];     // by stream
+  uint32_t tmem;
+  int dead;                 // a wait ran out
+  int nan[8];               // by segment: a NaN value in a masked tile
+  int open[2];              // the CTA's tiles cut by its ends: set
+  DecPiece piece[2];        // and which they are
+  float4 scale[4][8];       // by tile of keys: 2^ek, ev, 2^-ev of 16 keys each
+  float m1[128], l1[128];   // the second stream's, when the two are joined
+  unsigned nan1[4][128];
+  DecOut out;
+  DecJob job;
+};
+
+// Waits for a phase, two seconds at most; then marks the CTA dead, whose waits
+// all end at once and whose results become NaN.
+__device__ __forceinline__ void pr_wait(uint64_t* bar, uint32_t parity, PrShared& sh) {
+  if (mbar_try_wait(bar, parity)) return;
+  const unsigned long long t0 = global_ns();
+  for (;;) {
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(bar, parity)) return;
+    if (*(volatile int*)&sh.dead) return;
+    if (global_ns() - t0 > kWaitLimitNs) {
+      *(volatile int*)&sh.dead = 1;
+      return;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Converters (warps 8..11): a tile of keys from codes to f16 operands
+// ---------------------------------------------------------------------------
+struct PrTile {      // a tile of keys as one lane sees it
+  int id;            // lanes 0..7: block of the lane's 16 keys, -1: none
+  int p0, seq, h, seg;
+  bool masked, there;   // there: the tile exists
+};
+
+template <int TILE>
+struct PrFeed {      // walks the CTA's tiles of keys
+  PrCursor c;
+  long long left;
+  int seg, lo_all, hi_all;
+
+  __device__ __forceinline__ void take(const AttnArgs& a, PrTile& t, int lane) {
+    t.there = left > 0;
+    t.id = -1;
+    if (!t.there) return;
+    t.p0 = (c.s0 + c.s) << 7;
+    t.seq = c.w.seq;
+    t.h = c.h;
+    t.seg = seg;
+    t.masked = pr_masked(t.p0, lo_all, hi_all);
+    const int p = t.p0 + 16 * lane;
+    if (lane < 8 && p < t.seq) t.id = __ldg(a.table + c.r * a.table_stride + (p >> a.c.bs_log2));
+    if (--left > 0 && ++c.s == c.S) {
+      pr_next_item<TILE>(a, c);
+      ++seg;
+      pr_seen<TILE>(a, c, lo_all, hi_all);
+    }
+  }
+};
+
+template <int D, bool PAIR>
+__device__ __forceinline__ void pr_convert(const AttnArgs& a, PrShared& sh, uint8_t* smem,
+                                           const PrCursor& start, long long n_units) {
+  using S = PrShape<D, PAIR>;
+  constexpr int KN = D / 16;               // key pieces of 16 bytes a thread
+  constexpr int VW = D / 64;               // 8-byte words of a thread's value pieces
+  const int ct = threadIdx.x - 256, lane = ct & 31, warp = ct >> 5;
+  // key pieces: token kt + ks i, dims 16 kc ..
+  const int kc = D == 128 ? lane >> 2 : (lane >> 2) & 3;
+  const int kt = D == 128 ? warp * 4 + (lane & 3) : warp * 8 + (lane >> 4) * 4 + (lane & 3);
+  constexpr int ks = D == 128 ? 16 : 32;
+  // value pieces: tokens 8 vg .. + 7, dims (D / 8) vc ..
+  const int vc = D == 128 ? (lane & 3) + 4 * ((lane >> 3) & 1) : lane & 7;
+  const int vg = D == 128 ? warp * 4 + ((lane >> 2) & 1) + 2 * ((lane >> 4) & 1)
+                          : warp * 4 + (lane >> 3);
+  PrFeed<S::TILE> feed;
+  feed.c = start;
+  feed.left = n_units;
+  feed.seg = 0;
+  pr_seen<S::TILE>(a, start, feed.lo_all, feed.hi_all);
+  PrTile t0, t1, t2;      // being converted, being fetched, being looked up
+  uint4 kr[KN];
+  uint2 vr[8][VW];
+  const int bs1 = (1 << a.c.bs_log2) - 1;
+
+  auto fetch_k = [&](const PrTile& t) {
+#pragma unroll
+    for (int i = 0; i < KN; ++i) {
+      const int tok = kt + ks * i;
+      const int id = __shfl_sync(0xffffffffu, t.id, tok >> 4);
+      kr[i] = make_uint4(0, 0, 0, 0);
+      if (t.there && id >= 0 && id < a.c.n_blocks && t.p0 + tok < t.seq)
+        kr[i] = __ldg(reinterpret_cast<const uint4*>(
+            a.c.k + (long long)id * a.c.bstride + (long long)t.h * a.c.hstride +
+            (long long)((t.p0 + tok) & bs1) * a.c.tstride + kc * 16));
+    }
+  };
+  auto fetch_v = [&](const PrTile& t) {
+    const int id = __shfl_sync(0xffffffffu, t.id, vg >> 1);
+    const bool ok = t.there && id >= 0 && id < a.c.n_blocks;
+    const uint8_t* src = a.c.v + (long long)(ok ? id : 0) * a.c.bstride +
+                         (long long)t.h * a.c.hstride +
+                         (long long)((t.p0 + 8 * vg) & bs1) * a.c.tstride + vc * (D / 8);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+      for (int w = 0; w < VW; ++w) vr[i][w] = make_uint2(0, 0);
+      if (ok && t.p0 + 8 * vg + i < t.seq) {
+        if constexpr (VW == 2) {
+          const uint4 x = __ldg(reinterpret_cast<const uint4*>(src + i * a.c.tstride));
+          vr[i][0] = make_uint2(x.x, x.y);
+          vr[i][1] = make_uint2(x.z, x.w);
+        } else {
+          vr[i][0] = __ldg(reinterpret_cast<const uint2*>(src + i * a.c.tstride));
+        }
+      }
+    }
+  };
+
+  feed.take(a, t0, lane);
+  feed.take(a, t1, lane);
+  fetch_k(t0);
+  fetch_v(t0);
+#pragma unroll 1
+  for (int n = 0; t0.there; ++n) {
+    const int stage = n & 1, use = n >> 1;
+    feed.take(a, t2, lane);
+    // scales of the tile, from the first converter warp
+    uint32_t ek = 0, ev = 0;
+    const bool block = t0.id >= 0 && t0.id < a.c.n_blocks;
+    if (warp == 0 && lane < 8 && block) {
+      const long long at = (long long)t0.id * a.c.sstride + t0.h;
+      ek = __ldg(a.c.ks + at);
+      ev = __ldg(a.c.vs + at);
+    }
+    // ---- keys ----
+    if (use > 0) pr_wait(&sh.kempty[stage], (use - 1) & 1, sh);
+    uint8_t* kd = smem + S::KOFF + stage * S::KBYTES + 2 * kc * S::KLBO;
+#pragma unroll
+    for (int i = 0; i < KN; ++i) {
+      const int tok = kt + ks * i;
+      uint8_t* d = kd + tok * 16;   // 8-token groups are 128 bytes apart
+      uint4 x, y;
+      e4m3x4_to_f16x2(kr[i].x, x.x, x.y);
+      e4m3x4_to_f16x2(kr[i].y, x.z, x.w);
+      e4m3x4_to_f16x2(kr[i].z, y.x, y.y);
+      e4m3x4_to_f16x2(kr[i].w, y.z, y.w);
+      *reinterpret_cast<uint4*>(d) = x;
+      *reinterpret_cast<uint4*>(d + S::KLBO) = y;
+    }
+    if (warp == 0 && lane < 8) {
+      const int e = kv_exp(ev);
+      // a block outside the cache: weights 0
+      sh.scale[n & 3][lane] = block ? make_float4(pow2f(kv_exp(ek)), (float)e, pow2f(-e), 0.f)
+                                    : make_float4(0.f, -INFINITY, 0.f, 0.f);
+    }
+    fence_async_shared();
+    mbar_arrive(&sh.kfull[stage]);
+    fetch_k(t1);
+    // ---- values, transposed: 8 tokens of a dim are 16 bytes ----
+    if (use > 0) pr_wait(&sh.vempty[stage], (use - 1) & 1, sh);
+    if (t0.masked) {
+      // a weight of 0 does not keep a NaN out of the sums: NaN codes leave here
+      // and are given back to the rows that see them at the item's end
+      uint32_t any = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+          vr[i][w].x = drop_nan4(vr[i][w].x, any);
+          vr[i][w].y = drop_nan4(vr[i][w].y, any);
+        }
+      if (any) atomicOr(&sh.nan[t0.seg & 7], 1);
+    }
+    uint8_t* vd = smem + S::VOFF + stage * S::VBYTES + vg * S::VLBO + vc * (D / 64) * S::VSBO;
+#pragma unroll
+    for (int q = 0; q < 2 * VW; ++q) {   // 4 dims at a time
+      uint32_t f[4][4];                  // [dim][token pair]
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const uint32_t x = (q & 1) ? vr[2 * p][q >> 1].y : vr[2 * p][q >> 1].x;
+        const uint32_t y = (q & 1) ? vr[2 * p + 1][q >> 1].y : vr[2 * p + 1][q >> 1].x;
+        e4m3x4_to_f16x2(__byte_perm(x, y, 0x5140), f[0][p], f[1][p]);
+        e4m3x4_to_f16x2(__byte_perm(x, y, 0x7362), f[2][p], f[3][p]);
+      }
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const int j = 4 * q + d;         // dim of the thread's
+        *reinterpret_cast<uint4*>(vd + (j >> 3) * S::VSBO + (j & 7) * 16) =
+            make_uint4(f[d][0], f[d][1], f[d][2], f[d][3]);
+      }
+    }
+    fence_async_shared();
+    mbar_arrive(&sh.vfull[stage]);
+    fetch_v(t1);
+    t0 = t1;
+    t1 = t2;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// MMA issuer (one thread)
+// ---------------------------------------------------------------------------
+template <int D, bool PAIR>
+__device__ __forceinline__ void pr_mma(const AttnArgs& a, PrShared& sh, uint8_t* smem,
+                                       PrCursor c, long long n_units) {
+  using S = PrShape<D, PAIR>;
+  const uint32_t T = sh.tmem, base = smem_addr(smem);
+  const uint32_t id_s = umma_idesc_f16(kPrKeys), id_o = umma_idesc_f16(D);
+  int n0 = 0, seg = 0;
+  uint32_t cnt[2] = {0, 0};   // tiles of each stream so far
+
+  auto scores = [&](int t, int stage) {
+    const uint64_t dq = umma_desc(base + (PAIR ? t * S::QBYTES : 0), S::QLBO, 128);
+    const uint64_t dk = umma_desc(base + S::KOFF + stage * S::KBYTES, S::KLBO, 128);
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)
+      umma_f16(T + 128 * t, dq + (2 * S::QLBO / 16) * k, dk + (2 * S::KLBO / 16) * k, id_s, k > 0);
+    umma_commit(&sh.sfull[t]);
+  };
+  auto values = [&](int t, int stage, bool add) {
+    const uint64_t dv = umma_desc(base + S::VOFF + stage * S::VBYTES, S::VLBO, S::VSBO);
+#pragma unroll
+    for (int k = 0; k < kPrKeys / 16; ++k)
+      umma_f16_ta(T + S::OCOL + D * t, T + 128 * t + 8 * k, dv + (2 * S::VLBO / 16) * k, id_o,
+                  add || k > 0);
+    umma_commit(&sh.ofull[t]);
+  };
+  auto wait_k = [&](int n) { pr_wait(&sh.kfull[n & 1], (n >> 1) & 1, sh); };
+  auto wait_v = [&](int n) { pr_wait(&sh.vfull[n & 1], (n >> 1) & 1, sh); };
+
+  while (n_units > 0) {
+    const int nseg = (int)min((long long)(c.S - c.s), n_units);
+    pr_wait(&sh.qfull[0], seg & 1, sh);
+    if (PAIR) pr_wait(&sh.qfull[1], seg & 1, sh);
+    if (PAIR) {
+      wait_k(n0);
+      tc_fence_after();
+      scores(0, n0 & 1);
+      scores(1, n0 & 1);
+      umma_commit(&sh.kempty[n0 & 1]);
+      for (int j = 0; j < nseg; ++j) {
+        const int n = n0 + j;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          pr_wait(&sh.pfull[t], cnt[t] & 1, sh);
+          ++cnt[t];
+          if (t == 0) wait_v(n);
+          tc_fence_after();
+          values(t, n & 1, j > 0);
+          if (t == 1) umma_commit(&sh.vempty[n & 1]);
+          if (j + 1 < nseg) {
+            if (t == 0) wait_k(n + 1);
+            tc_fence_after();
+            scores(t, (n + 1) & 1);
+            if (t == 1) umma_commit(&sh.kempty[(n + 1) & 1]);
+          }
+        }
+      }
+    } else {
+      for (int t = 0; t < 2 && t < nseg; ++t) {
+        wait_k(n0 + t);
+        tc_fence_after();
+        scores(t, (n0 + t) & 1);
+        umma_commit(&sh.kempty[(n0 + t) & 1]);
+      }
+      for (int j = 0; j < nseg; ++j) {
+        const int n = n0 + j, t = j & 1;
+        pr_wait(&sh.pfull[t], (t ? cnt[1] : cnt[0]) & 1, sh);
+        if (t) ++cnt[1];
+        else ++cnt[0];
+        wait_v(n);
+        tc_fence_after();
+        values(t, n & 1, j >= 2);
+        umma_commit(&sh.vempty[n & 1]);
+        if (j + 2 < nseg) {
+          wait_k(n + 2);
+          tc_fence_after();
+          scores(t, n & 1);
+          umma_commit(&sh.kempty[n & 1]);
+        }
+      }
+    }
+    n0 += nseg;
+    n_units -= nseg;
+    ++seg;
+    if (n_units > 0) pr_next_item<S::TILE>(a, c);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Softmax (warps 0..7): a thread a row of its stream
+// ---------------------------------------------------------------------------
+// Barrier of both streams' threads.
+__device__ __forceinline__ void pr_streams_sync() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
+
+// Dims (bits) in which the row sees a NaN value among the masked tiles of
+// keys [first, end) (step `step`) of the item: the rare path.
+template <int D>
+__device__ __noinline__ void pr_nan_dims(const AttnArgs& a, const PrCursor& c, int first, int end,
+                                         int step, int lo, int hi, int lo_all, int hi_all,
+                                         unsigned* bits) {
+  for (int s = first; s < end; s += step) {
+    const int p0 = (c.s0 + s) << 7;
+    if (!pr_masked(p0, lo_all, hi_all)) continue;
+    for (int j = max(p0, lo); j < min(p0 + kPrKeys, hi); ++j) {
+      const int id = a.table[c.r * a.table_stride + (j >> a.c.bs_log2)];
+      if (id < 0 || id >= a.c.n_blocks) continue;
+      const uint8_t* v = a.c.v + (long long)id * a.c.bstride + (long long)c.h * a.c.hstride +
+                         (long long)(j & ((1 << a.c.bs_log2) - 1)) * a.c.tstride;
+      for (int d = 0; d < D; ++d)
+        if ((v[d] & 0x7F) == 0x7F) bits[d >> 5] |= 1u << (d & 31);
+    }
+  }
+}
+
+template <int D, bool PAIR>
+__device__ __forceinline__ void pr_softmax(const AttnArgs& a, PrShared& sh, uint8_t* smem,
+                                           PrCursor c, long long n_units) {
+  using S = PrShape<D, PAIR>;
+  const int t = threadIdx.x >> 7, row = threadIdx.x & 127, warp = (threadIdx.x >> 5) & 3;
+  const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+  const uint32_t ts = sh.tmem + lanes + 128 * t, to = sh.tmem + lanes + S::OCOL + D * t;
+  float* slots = a.partial + 2ll * blockIdx.x * S::SLOT;
+  uint32_t cnt = 0;     // tiles of this stream so far
+  int n0 = 0, seg = 0;
+  long long done = 0;
+#pragma unroll 1
+  while (done < n_units) {
+    const int nseg = (int)min((long long)(c.S - c.s), n_units - done);
+    int lo_all, hi_all, lo, hi;
+    pr_seen<S::TILE>(a, c, lo_all, hi_all);
+    // ---- this row's query as f16 times 2^-shift (the stream's own half, or
+    // the first stream's threads for both) ----
+    const unsigned rho = (unsigned)c.m * S::TILE + (PAIR ? 128 * t : 0) + row;
+    const int i = (int)(rho / (unsigned)a.group);
+    const int head = c.h * a.group + (int)(rho - (unsigned)i * (unsigned)a.group);
+    const bool real = i < c.w.n;
+    attn_seen(a, c.w, min(i, c.w.n - 1), lo, hi);
+    if (!PAIR) pr_streams_sync();   // both streams are through with the last item's queries
+    float fac = 0.f;
+    {
+      const uint16_t* q = a.q + (long long)(c.w.tok + (real ? i : 0)) * a.q_ts + head * a.q_hs;
+      uint8_t* dst = smem + (PAIR ? t * S::QBYTES : 0) + row * 16;
+      float mx = 0.f;
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k) {
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (real) w = *reinterpret_cast<const uint4*>(q + 8 * k);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = unpack16(u[e], a.f16);
+          mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      }
+      const int be = (int)(__float_as_uint(mx) >> 23);
+      const int shift = be == 0 || be == 255 ? 0 : min(max(be - 140, -120), 120);
+      const float down =
+          a.scale_log2 == 0.f ? 0.f : (a.scale_log2 < 0.f ? -pow2f(-shift) : pow2f(-shift));
+      fac = fabsf(a.scale_log2) * pow2f(shift);
+      if (PAIR || t == 0) {
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) {
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (real) w = *reinterpret_cast<const uint4*>(q + 8 * k);
+          const float2 f0 = unpack16(w.x, a.f16), f1 = unpack16(w.y, a.f16),
+                       f2 = unpack16(w.z, a.f16), f3 = unpack16(w.w, a.f16);
+          *reinterpret_cast<uint4*>(dst + k * S::QLBO) = make_uint4(
+              pack_f16x2(f0.x * down, f0.y * down), pack_f16x2(f1.x * down, f1.y * down),
+              pack_f16x2(f2.x * down, f2.y * down), pack_f16x2(f3.x * down, f3.y * down));
+        }
+        fence_async_shared();
+      }
+      mbar_arrive(&sh.qfull[PAIR ? t : 0]);
+    }
+
+    float m = -INFINITY, l = 0.f;
+    int mine = 0;       // tiles of this stream in the segment
+#pragma unroll 1
+    for (int j = PAIR ? 0 : t; j < nseg; j += PAIR ? 1 : 2, ++mine, ++cnt) {
+      const int p0 = (c.s0 + c.s + j) << 7;
+      const float4* sc = sh.scale[(n0 + j) & 3];
+      const bool masked = pr_masked(p0, lo_all, hi_all);
+      pr_wait(&sh.sfull[t], cnt & 1, sh);
+      __syncwarp();
+      tc_fence_after();
+      // ---- maximum ----
+      float x = -INFINITY;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        float s[64];
+        tmem_ld32(ts + 64 * hf, s);
+        tmem_ld32(ts + 64 * hf + 32, s + 32);
+        tmem_wait_ld();
+        if (masked) {
+#pragma unroll
+          for (int k = 0; k < 64; ++k) {
+            const int key = p0 + 64 * hf + k;
+            if (key < lo || key >= hi) s[k] = -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          float v = fmaxf(s[16 * b], s[16 * b + 1]);
+#pragma unroll
+          for (int k = 2; k < 16; ++k) v = fmaxf(v, s[16 * b + k]);
+          const float4 f = sc[4 * hf + b];
+          x = fmaxf(x, fmaf(v, fac * f.x, f.y));   // NaN (-infinity times 0) drops out
+        }
+      }
+      // ---- a new reference, O brought to it ----
+      const bool grow = x > (m == -INFINITY ? -INFINITY : m + 8.f);
+      const float down = grow ? attn_factor(m, x) : 1.f;
+      if (grow) m = x;
+      l *= down;
+      if (mine > 0) {
+        if (__any_sync(0xffffffffu, grow)) {
+          pr_wait(&sh.ofull[t], (cnt - 1) & 1, sh);
+          __syncwarp();
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {
+            float o[32];
+            tmem_ld32(to + 32 * k, o);
+            tmem_wait_ld();
+            uint32_t r[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(o[e] * down);
+            tmem_st32(to + 32 * k, r);
+          }
+        }
+      }
+      const float ref = m == -INFINITY ? 0.f : m;
+      // ---- weights, into the columns of the scores ----
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        float s[64];
+        tmem_ld32(ts + 64 * hf, s);
+        tmem_ld32(ts + 64 * hf + 32, s + 32);
+        tmem_wait_ld();
+        uint32_t p[32];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const float4 f = sc[4 * hf + b];
+          const float g = fac * f.x, off = f.y - ref;
+          float sum = 0.f;
+#pragma unroll
+          for (int k = 0; k < 16; k += 2) {
+            float u = exp2_approx(fmaf(s[16 * b + k], g, off));
+            float v = exp2_approx(fmaf(s[16 * b + k + 1], g, off));
+            if (masked) {
+              const int key = p0 + 64 * hf + 16 * b + k;
+              if (key < lo || key >= hi) u = 0.f;
+              if (key + 1 < lo || key + 1 >= hi) v = 0.f;
+            }
+            sum += u + v;
+            p[8 * b + k / 2] = pack_f16x2(u, v);
+          }
+          l = fmaf(f.z, sum, l);
+        }
+        tmem_st32(ts + 32 * hf, p);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&sh.pfull[t]);
+    }
+
+    // ---- the item's end, or the CTA's ----
+    if (mine > 0) pr_wait(&sh.ofull[t], (cnt - 1) & 1, sh);
+    unsigned bits[4] = {0, 0, 0, 0};
+    if (*(volatile int*)&sh.nan[seg & 7])
+      pr_nan_dims<D>(a, c, c.s + (PAIR ? 0 : t), c.s + nseg, PAIR ? 1 : 2, lo, hi, lo_all, hi_all,
+                     bits);
+    const bool begins = c.s == 0, ends = c.s + nseg == c.S;
+    float f0 = 1.f, f1 = 0.f;   // factors of this stream's sums and of the other's
+    if (!PAIR) {
+      // the first stream's threads join both: the second's O lies in the same
+      // lanes of tensor memory
+      tc_fence_before();
+      if (t == 1) {
+        sh.m1[row] = m;
+        sh.l1[row] = l;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) sh.nan1[k][row] = bits[k];
+      }
+      pr_streams_sync();
+      if (t == 0) {
+        const float m1 = sh.m1[row], mx = fmaxf(m, m1);
+        f0 = attn_factor(m, mx);
+        f1 = nseg > 1 ? attn_factor(m1, mx) : 0.f;
+        l = l * f0 + (nseg > 1 ? sh.l1[row] * f1 : 0.f);
+        m = mx;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) bits[k] |= sh.nan1[k][row];
+      }
+    }
+    __syncwarp();
+    tc_fence_after();
+    if (*(volatile int*)&sh.dead) l = __int_as_float(0x7FFFFFFF);
+    if (PAIR || t == 0) {
+      const float inv = attn_inverse(l);
+      const long long tok = c.w.tok + i;
+      float* slot = slots + (begins ? S::SLOT : 0);
+      const int srow = (PAIR ? 128 * t : 0) + row;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        float o[16];
+        __syncwarp();
+        tmem_ld16(to + 16 * k, o);
+        if (!PAIR && nseg > 1) {
+          float o1[16];
+          tmem_ld16(to + D + 16 * k, o1);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = fmaf(o1[e], f1, o[e] * f0);
+        } else {
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if ((bits[k >> 1] >> (16 * (k & 1) + e)) & 1u) o[e] = __int_as_float(0x7FFFFFFF);
+        if (real && begins && ends) {
+          uint16_t* dst = a.out + tok * a.o_ts + head * a.o_hs + 16 * k;
+#pragma unroll
+          for (int e = 0; e < 16; e += 8)
+            *reinterpret_cast<uint4*>(dst + e) =
+                make_uint4(pack16(o[e] * inv, o[e + 1] * inv, a.f16),
+                           pack16(o[e + 2] * inv, o[e + 3] * inv, a.f16),
+                           pack16(o[e + 4] * inv, o[e + 5] * inv, a.f16),
+                           pack16(o[e + 6] * inv, o[e + 7] * inv, a.f16));
+        } else if (real) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<float4*>(slot + (long long)srow * D + 16 * k + e) =
+                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+      }
+      if (real) {
+        if (begins && ends) {
+          if (a.lse) a.lse[tok * a.heads + head] = attn_lse(m, l);
+        } else {
+          slot[S::TILE * D + srow] = m;
+          slot[S::TILE * D + S::TILE + srow] = l;
+        }
+      }
+    if (!(begins && ends) && threadIdx.x == 0) {
+        sh.open[begins] = 1;
+        sh.piece[begins] = {1 | (begins ? 2 : 0) | (ends ? 4 : 0), c.h, c.m, c.w.tok, c.w.n, c.S,
+                            done - c.s};
+      }
+    }
+    if (threadIdx.x == 0) sh.nan[(seg + 4) & 7] = 0;
+    tc_fence_before();
+    done += nseg;
+    n0 += nseg;
+    ++seg;
+    if (done < n_units) pr_next_item<S::TILE>(a, c);
+  }
+}
+
+template <int D, bool PAIR>
+static __global__ void __launch_bounds__(kPrThreads, 1) kv_attention_tc(const AttnArgs a) {
+  using S = PrShape<D, PAIR>;
+  extern __shared__ __align__(128) uint8_t pr_smem[];
+  __shared__ PrShared sh;
+  const int warp = threadIdx.x >> 5;
+  long long u0, n_units, per;
+  PrCursor cur;
+  pr_schedule<S::TILE>(a, u0, n_units, per, cur);
+  if (n_units <= 0) return;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sh.kfull[s], 128);
+      mbar_init(&sh.kempty[s], 1);
+      mbar_init(&sh.vfull[s], 128);
+      mbar_init(&sh.vempty[s], 1);
+      mbar_init(&sh.sfull[s], 1);
+      mbar_init(&sh.pfull[s], 128);
+      mbar_init(&sh.ofull[s], 1);
+      mbar_init(&sh.qfull[s], PAIR ? 128 : 256);
+      sh.open[s] = 0;
+    }
+    for (int s = 0; s < 8; ++s) sh.nan[s] = 0;
+    sh.dead = 0;
+    sh.out = {a.out, a.lse, a.o_ts, a.o_hs, a.heads, a.f16, (unsigned)a.group};
+    fence_barrier_init();
+  }
+  if (warp == 12) tmem_alloc(&sh.tmem);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+
+  if (warp < 8) {
+    pr_softmax<D, PAIR>(a, sh, pr_smem, cur, n_units);
+  } else if (warp < 12) {
+    pr_convert<D, PAIR>(a, sh, pr_smem, cur, n_units);
+  } else if ((threadIdx.x & 31) == 0) {
+    pr_mma<D, PAIR>(a, sh, pr_smem, cur, n_units);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(sh.tmem);
+  }
+
+  // ---- items that the CTA's ends cut: joined by the last CTA to arrive ----
+#pragma unroll 1
+  for (int o = 0; o < 2; ++o) {
+    if (!sh.open[o]) continue;
+    const DecPiece& p = sh.piece[o];
+    const long long tile = u0 + p.at;
+    const int c0 = (int)(tile / per), n = (int)((tile + p.S - 1) / per) - c0 + 1;
+    const int grp = ((int)blockIdx.x - c0) / kDecGroup;
+    const int in_grp = min(kDecGroup, n - grp * kDecGroup);
+    unsigned* counters[2] = {a.arrived + 4 * (c0 + grp * kDecGroup) + (grp ? 2 : 1),
+                             a.arrived + 4 * c0};
+    constexpr long long stride = 2ll * S::SLOT;
+    float* base = a.partial + c0 * stride;
+#pragma unroll 1
+    for (int level = 0; level < 2; ++level) {
+      const int groups = (n + kDecGroup - 1) / kDecGroup;
+      if (!dec_arrive(level ? counters[1] : counters[0], level ? groups : in_grp)) break;
+      if (threadIdx.x == 0) {
+        float* from = base + (level ? 0 : grp * kDecGroup * stride);
+        const long long extra = level == 0 && grp > 0 ? 0 : S::SLOT;
+        const bool final = level == 1 || groups == 1;
+        const int count = level ? groups : in_grp;
+        sh.job = {from, final ? nullptr : from + extra, nullptr,
+                  level ? kDecGroup * stride : stride, extra, 0, ~0u >> (32 - count), p.h, p.m,
+                  p.tok, p.n};
+      }
+      __syncthreads();
+      dec_join<D, S::TILE, true>(&sh.out, &sh.job, 1, warp, kPrWarps);
+      if (groups == 1) break;
+    }
+  }
+}
+
+}  // namespace moe

@@ -53,97 +53,19 @@
 
 #include "common.cuh"
 #include "planes.cuh"
+#include "tcgen05.cuh"
 
 namespace moe {
 
 // ---------------------------------------------------------------------------
-// tcgen05 / UMMA wrappers
+// Constants of the path (wrappers: tcgen05.cuh)
 // ---------------------------------------------------------------------------
-constexpr int kTcCols = 512;        // tensor-memory columns a CTA allocates (one CTA per SM)
 constexpr int kTcRmax = 8;          // pairs per pass: N = 8 planes x 8 pairs = 64 columns
 constexpr int kTcMaxCtas = 256;     // partial slots / flags in the workspace
 constexpr int kTcDStride = 128;     // two accumulators of up to 128 columns
 constexpr int kTcSfaCol = 256;      // D buffers take columns [0, 256)
 constexpr int kTcXchg = 2 * 64 * 16;   // floats of the SwiGLU exchange (two buffers)
 
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-// Whole warp: allocate kTcCols columns, address written to *dst.
-__device__ __forceinline__ void tmem_alloc(uint32_t* dst) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                   smem_addr(dst)),
-               "n"(kTcCols)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(kTcCols)
-               : "memory");
-}
-// 32 lanes x 32 bits, 2 consecutive columns per thread.
-__device__ __forceinline__ void tmem_st2(uint32_t taddr, uint32_t a, uint32_t b) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(taddr), "r"(a), "r"(b)
-               : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-// 32 lanes x 32 bits, 16 consecutive columns per thread (no wait).
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tmem_wait_ld() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-// Shared-memory matrix descriptor: no swizzle, K-major core matrices of 8
-// rows x 16 bytes; lbo = byte distance between core matrices along K, sbo =
-// between groups of 8 rows.
-__device__ __forceinline__ uint64_t umma_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)((lbo >> 4) & 0x3FFFu) << 16 |
-         (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 | (uint64_t)1 << 46;
-}
-// Instruction descriptor, kind::mxf4: E2M1 x E2M1, E8M0 scales, both K-major,
-// M = 128, N columns; a_sf / b_sf select the scale byte pair of the step.
-__device__ __forceinline__ uint32_t umma_idesc_mxf4(uint32_t a_sf, uint32_t b_sf, uint32_t N) {
-  return (b_sf << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | (1u << 23) | (8u << 24) |
-         (a_sf << 29);
-}
-__device__ __forceinline__ void umma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                          uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
-      "[%5], p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-      : "memory");
-}
-// Copy 32 rows x 16 bytes of scales from shared memory into 4 columns of all
-// four lane quarters.
-__device__ __forceinline__ void umma_sf_copy(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
-               : "memory");
-}
-// Arrive once on `bar` when every tcgen05 operation this thread issued so far
-// has completed.
-__device__ __forceinline__ void umma_commit(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-          smem_addr(bar))
-      : "memory");
-}
 // The four epilogue warps only (named barrier 2).
 __device__ __forceinline__ void tc_epi_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
 
@@ -670,20 +592,6 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_addr(dst)),
       "l"(map), "r"(c0), "r"(c1), "r"(smem_addr(bar)), "l"(policy)
-      : "memory");
-}
-
-// Instruction descriptor, kind::f16: bf16 x bf16 -> fp32, both K-major,
-// M = 128, N columns.
-__device__ __forceinline__ uint32_t umma_idesc_bf16(uint32_t N) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((128u >> 4) << 24);
-}
-__device__ __forceinline__ void umma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                         uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
