@@ -138,7 +138,7 @@ int launch_tensor(const AttnArgs& a, int n_sm, cudaStream_t st) {
 template <int D>
 int launch_attention(const AttnArgs& a, int n_sm, int max_q, cudaStream_t st) {
   if ((long long)max_q * a.group > 128) return launch_tensor<D, true>(a, n_sm, st);
-  if ((long long)max_q * a.group > 64) return launch_tensor<D, false>(a, n_sm, st);
+  if ((long long)max_q * a.group > 16) return launch_tensor<D, false>(a, n_sm, st);
   // rows of the longest batch row per KV head, as far as the host knows
   return (long long)max_q * a.group <= 8 ? launch_decode<D, 1>(a, n_sm, max_q, st)
                                          : launch_decode<D, 2>(a, n_sm, max_q, st);

@@ -8,13 +8,14 @@
 // alternate on the tensor cores: while one's scores (S = Q K^T, M = 128 rows,
 // N = 128 keys) go through the softmax, the other's products run.
 //
-// Roles (13 warps): warps 0..3 and 4..7, one stream each, a thread a row:
-// scores from tensor memory, running maximum and sum, weights back into tensor
-// memory (in the columns of their scores) as the A operand of O += P V; warps
-// 8..11 fetch codes, convert them to f16 and lay them out in shared memory as
-// K-major core matrices (K rows = keys, V^T rows = dims, transposed in
-// registers); warp 12 issues the MMAs.  Accumulators and S live in tensor
-// memory (2 x 128 columns of S, 2 x D of O).
+// Roles (12 warps, 168 registers a thread): warps 0..3 and 4..7, one stream
+// each, a thread a row: scores from tensor memory, running maximum and sum,
+// weights back into tensor memory (in the columns of their scores) as the A
+// operand of O += P V; the stream's first thread then issues its products, the
+// values' and the next scores', which the stream waits for anyway.  Warps 8..11
+// fetch codes, convert them to f16 and lay them out in shared memory as K-major
+// core matrices (K rows = keys, V^T rows = dims, transposed in registers).
+// Accumulators and S live in tensor memory (2 x 128 columns of S, 2 x D of O).
 //
 // Bounds: 4 * 128 * 128 * D operations of a pair of products take 0.67 us of
 // an SM's tensor cores at D = 128; beside them 128 x 128 exponentials and
@@ -35,7 +36,7 @@
 
 namespace moe {
 
-constexpr int kPrWarps = 13;
+constexpr int kPrWarps = 12;
 constexpr int kPrThreads = 32 * kPrWarps;
 constexpr int kPrKeys = 128;
 
@@ -46,8 +47,11 @@ struct PrShape {
   // so that the converters' 16-byte stores hit all banks
   static constexpr int QLBO = 2048, KLBO = 2080, VSBO = 144, VLBO = D / 8 * VSBO + 16;
   static constexpr int QBYTES = D / 8 * QLBO, KBYTES = D / 8 * KLBO, VBYTES = 16 * VLBO;
-  static constexpr int KOFF = (PAIR ? 2 : 1) * QBYTES, VOFF = KOFF + 2 * KBYTES;
-  static constexpr int SMEM = VOFF + 2 * VBYTES;
+  // queries, one tile of keys, two of values, and three half tiles of codes
+  // (keys or values) on their way: a tile and a half ahead of the converters
+  static constexpr int KOFF = (PAIR ? 2 : 1) * QBYTES, VOFF = KOFF + KBYTES;
+  static constexpr int ROFF = VOFF + 2 * VBYTES, RAW = kPrKeys * D, RAWS = 3;
+  static constexpr int SMEM = ROFF + RAWS * RAW;
   // a slot of partial sums: O [TILE][D], m [TILE], l [TILE]; two a CTA
   static constexpr int SLOT = TILE * D + 2 * TILE;
   static constexpr int OCOL = 256;   // tensor memory: S at 0 and 128, O at OCOL + D t
@@ -68,6 +72,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
@@ -78,6 +90,19 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
       "r"(r[30]), "r"(r[31])
       : "memory");
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ void fma_f32x2(float& a, float& b, float g, float off) {
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\t"
+      "mov.b64 z, {%3, %3};\n\tfma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(g), "f"(off));
+}
+__device__ __forceinline__ void add_f32x2(float& a, float& b, float x, float y) {
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+      "add.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(x), "f"(y));
 }
 // D += A B with A (f16, two of K a column) in tensor memory.
 __device__ __forceinline__ void umma_f16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
@@ -275,8 +300,10 @@ __device__ __forceinline__ bool pr_masked(int p0, int lo_all, int hi_all) {
 // Shared state
 // ---------------------------------------------------------------------------
 struct PrShared {
-  uint64_t kfull[2], kempty[2], vfull[2], vempty[2];   // by stage of keys
-  uint64_t sfull[2], pfull[2], ofull[2], qfull[2];     // by stream
+  // operands: tile n of keys uses barriers n & 1 (the keys' one buffer too: the
+  // second stream may wait for a tile while the one before is not there yet)
+  uint64_t kfull[2], kempty[2], vfull[2], vempty[2];
+  uint64_t sfull[2], ofull[2];                   // products of each stream
   uint32_t tmem;
   int dead;                 // a wait ran out
   int nan[8];               // by segment: a NaN value in a masked tile
@@ -339,18 +366,27 @@ struct PrFeed {      // walks the CTA's tiles of keys
   }
 };
 
+__device__ __forceinline__ uint64_t policy_evict_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+
+// Each thread copies (cp.async) the pieces that it converts itself into a ring
+// of its own, so the copies need no barrier.  (Fetched into registers half a
+// tile ahead, a tile took 4,700 cycles, mostly waiting.)
 template <int D, bool PAIR>
 __device__ __forceinline__ void pr_convert(const AttnArgs& a, PrShared& sh, uint8_t* smem,
                                            const PrCursor& start, long long n_units) {
   using S = PrShape<D, PAIR>;
   constexpr int KN = D / 16;               // key pieces of 16 bytes a thread
-  constexpr int VW = D / 64;               // 8-byte words of a thread's value pieces
+  constexpr int VB = D / 8;                // bytes of a value piece, 8 of them a thread
   const int ct = threadIdx.x - 256, lane = ct & 31, warp = ct >> 5;
   // key pieces: token kt + ks i, dims 16 kc ..
   const int kc = D == 128 ? lane >> 2 : (lane >> 2) & 3;
   const int kt = D == 128 ? warp * 4 + (lane & 3) : warp * 8 + (lane >> 4) * 4 + (lane & 3);
   constexpr int ks = D == 128 ? 16 : 32;
-  // value pieces: tokens 8 vg .. + 7, dims (D / 8) vc ..
+  // value pieces: tokens 8 vg .. + 7, dims VB vc ..
   const int vc = D == 128 ? (lane & 3) + 4 * ((lane >> 3) & 1) : lane & 7;
   const int vg = D == 128 ? warp * 4 + ((lane >> 2) & 1) + 2 * ((lane >> 4) & 1)
                           : warp * 4 + (lane >> 3);
@@ -359,73 +395,84 @@ __device__ __forceinline__ void pr_convert(const AttnArgs& a, PrShared& sh, uint
   feed.left = n_units;
   feed.seg = 0;
   pr_seen<S::TILE>(a, start, feed.lo_all, feed.hi_all);
-  PrTile t0, t1, t2;      // being converted, being fetched, being looked up
-  uint4 kr[KN];
-  uint2 vr[8][VW];
+  PrTile t0, t1, t2, t3;      // being converted, the two being fetched, being looked up
   const int bs1 = (1 << a.c.bs_log2) - 1;
+  // codes that one row tile reads leave L2 first; those of a prompt are read again
+  const uint64_t policy = PAIR ? policy_evict_normal() : policy_evict_first();
+  const uint32_t raw = smem_addr(smem) + S::ROFF;
+  int in_slot = 0, out_slot = 0;
 
   auto fetch_k = [&](const PrTile& t) {
+    const uint32_t dst = raw + in_slot * S::RAW + ct * 16;
+    in_slot = in_slot + 1 == S::RAWS ? 0 : in_slot + 1;
 #pragma unroll
     for (int i = 0; i < KN; ++i) {
       const int tok = kt + ks * i;
       const int id = __shfl_sync(0xffffffffu, t.id, tok >> 4);
-      kr[i] = make_uint4(0, 0, 0, 0);
-      if (t.there && id >= 0 && id < a.c.n_blocks && t.p0 + tok < t.seq)
-        kr[i] = __ldg(reinterpret_cast<const uint4*>(
-            a.c.k + (long long)id * a.c.bstride + (long long)t.h * a.c.hstride +
-            (long long)((t.p0 + tok) & bs1) * a.c.tstride + kc * 16));
+      const bool in = t.there && id >= 0 && id < a.c.n_blocks && t.p0 + tok < t.seq;
+      const uint8_t* src = a.c.k;
+      if (in)
+        src += (long long)id * a.c.bstride + (long long)t.h * a.c.hstride +
+               (long long)((t.p0 + tok) & bs1) * a.c.tstride + kc * 16;
+      cp_async<16>(dst + i * 2048, src, in, policy);
     }
+    cp_async_commit();
   };
+  // a thread's bytes of a slot are the same for keys and values: nobody else
+  // may still be reading them
+  auto piece = [](int i) { return VB == 16 ? i * 2048 : (i >> 1) * 2048 + (i & 1) * 8; };
   auto fetch_v = [&](const PrTile& t) {
+    const uint32_t dst = raw + in_slot * S::RAW + ct * 16;
+    in_slot = in_slot + 1 == S::RAWS ? 0 : in_slot + 1;
     const int id = __shfl_sync(0xffffffffu, t.id, vg >> 1);
     const bool ok = t.there && id >= 0 && id < a.c.n_blocks;
-    const uint8_t* src = a.c.v + (long long)(ok ? id : 0) * a.c.bstride +
-                         (long long)t.h * a.c.hstride +
-                         (long long)((t.p0 + 8 * vg) & bs1) * a.c.tstride + vc * (D / 8);
+    const uint8_t* src = a.c.v;
+    if (ok)
+      src += (long long)id * a.c.bstride + (long long)t.h * a.c.hstride +
+             (long long)((t.p0 + 8 * vg) & bs1) * a.c.tstride + vc * VB;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-#pragma unroll
-      for (int w = 0; w < VW; ++w) vr[i][w] = make_uint2(0, 0);
-      if (ok && t.p0 + 8 * vg + i < t.seq) {
-        if constexpr (VW == 2) {
-          const uint4 x = __ldg(reinterpret_cast<const uint4*>(src + i * a.c.tstride));
-          vr[i][0] = make_uint2(x.x, x.y);
-          vr[i][1] = make_uint2(x.z, x.w);
-        } else {
-          vr[i][0] = __ldg(reinterpret_cast<const uint2*>(src + i * a.c.tstride));
-        }
-      }
+      const bool in = ok && t.p0 + 8 * vg + i < t.seq;
+      cp_async<VB>(dst + piece(i), in ? src + i * a.c.tstride : a.c.v, in, policy);
+    }
+    cp_async_commit();
+  };
+  // scale bytes of a tile, lanes 0..7 of the first converter warp
+  uint32_t ek = 0, ev = 0;
+  auto fetch_scales = [&](const PrTile& t) {
+    if (warp == 0 && t.id >= 0 && t.id < a.c.n_blocks) {
+      const long long at = (long long)t.id * a.c.sstride + t.h;
+      ek = __ldg(a.c.ks + at);
+      ev = __ldg(a.c.vs + at);
     }
   };
 
   feed.take(a, t0, lane);
   feed.take(a, t1, lane);
+  feed.take(a, t2, lane);
   fetch_k(t0);
   fetch_v(t0);
+  fetch_k(t1);
+  fetch_scales(t0);
 #pragma unroll 1
   for (int n = 0; t0.there; ++n) {
-    const int stage = n & 1, use = n >> 1;
-    feed.take(a, t2, lane);
-    // scales of the tile, from the first converter warp
-    uint32_t ek = 0, ev = 0;
+    feed.take(a, t3, lane);
     const bool block = t0.id >= 0 && t0.id < a.c.n_blocks;
-    if (warp == 0 && lane < 8 && block) {
-      const long long at = (long long)t0.id * a.c.sstride + t0.h;
-      ek = __ldg(a.c.ks + at);
-      ev = __ldg(a.c.vs + at);
-    }
     // ---- keys ----
-    if (use > 0) pr_wait(&sh.kempty[stage], (use - 1) & 1, sh);
-    uint8_t* kd = smem + S::KOFF + stage * S::KBYTES + 2 * kc * S::KLBO;
+    if (n > 0) pr_wait(&sh.kempty[(n - 1) & 1], ((n - 1) >> 1) & 1, sh);
+    cp_async_wait<2>();
+    const uint8_t* from = smem + S::ROFF + out_slot * S::RAW;
+    out_slot = out_slot + 1 == S::RAWS ? 0 : out_slot + 1;
+    uint8_t* kd = smem + S::KOFF + 2 * kc * S::KLBO;
 #pragma unroll
     for (int i = 0; i < KN; ++i) {
-      const int tok = kt + ks * i;
-      uint8_t* d = kd + tok * 16;   // 8-token groups are 128 bytes apart
+      uint8_t* d = kd + (kt + ks * i) * 16;   // 8-token groups are 128 bytes apart
+      const uint4 w = *reinterpret_cast<const uint4*>(from + ct * 16 + i * 2048);
       uint4 x, y;
-      e4m3x4_to_f16x2(kr[i].x, x.x, x.y);
-      e4m3x4_to_f16x2(kr[i].y, x.z, x.w);
-      e4m3x4_to_f16x2(kr[i].z, y.x, y.y);
-      e4m3x4_to_f16x2(kr[i].w, y.z, y.w);
+      e4m3x4_to_f16x2(w.x, x.x, x.y);
+      e4m3x4_to_f16x2(w.y, x.z, x.w);
+      e4m3x4_to_f16x2(w.z, y.x, y.y);
+      e4m3x4_to_f16x2(w.w, y.z, y.w);
       *reinterpret_cast<uint4*>(d) = x;
       *reinterpret_cast<uint4*>(d + S::KLBO) = y;
     }
@@ -436,33 +483,47 @@ __device__ __forceinline__ void pr_convert(const AttnArgs& a, PrShared& sh, uint
                                     : make_float4(0.f, -INFINITY, 0.f, 0.f);
     }
     fence_async_shared();
-    mbar_arrive(&sh.kfull[stage]);
-    fetch_k(t1);
+    mbar_arrive(&sh.kfull[n & 1]);
+    fetch_scales(t1);
+    fetch_v(t1);
     // ---- values, transposed: 8 tokens of a dim are 16 bytes ----
-    if (use > 0) pr_wait(&sh.vempty[stage], (use - 1) & 1, sh);
+    const int stage = n & 1;
+    if (n > 1) pr_wait(&sh.vempty[stage], ((n >> 1) - 1) & 1, sh);
+    cp_async_wait<2>();
+    from = smem + S::ROFF + out_slot * S::RAW + ct * 16;
+    out_slot = out_slot + 1 == S::RAWS ? 0 : out_slot + 1;
+    uint8_t* vd = smem + S::VOFF + stage * S::VBYTES + vg * S::VLBO + vc * (D / 64) * S::VSBO;
+    uint32_t vr[8][VB / 4], any = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (VB == 16) {
+        const uint4 x = *reinterpret_cast<const uint4*>(from + piece(i));
+        vr[i][0] = x.x;
+        vr[i][1] = x.y;
+        vr[i][2] = x.z;
+        vr[i][3] = x.w;
+      } else {
+        const uint2 x = *reinterpret_cast<const uint2*>(from + piece(i));
+        vr[i][0] = x.x;
+        vr[i][1] = x.y;
+      }
+    }
     if (t0.masked) {
       // a weight of 0 does not keep a NaN out of the sums: NaN codes leave here
       // and are given back to the rows that see them at the item's end
-      uint32_t any = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int w = 0; w < VW; ++w) {
-          vr[i][w].x = drop_nan4(vr[i][w].x, any);
-          vr[i][w].y = drop_nan4(vr[i][w].y, any);
-        }
+        for (int w = 0; w < VB / 4; ++w) vr[i][w] = drop_nan4(vr[i][w], any);
       if (any) atomicOr(&sh.nan[t0.seg & 7], 1);
     }
-    uint8_t* vd = smem + S::VOFF + stage * S::VBYTES + vg * S::VLBO + vc * (D / 64) * S::VSBO;
 #pragma unroll
-    for (int q = 0; q < 2 * VW; ++q) {   // 4 dims at a time
+    for (int q = 0; q < VB / 4; ++q) {   // 4 dims at a time
       uint32_t f[4][4];                  // [dim][token pair]
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
-        const uint32_t x = (q & 1) ? vr[2 * p][q >> 1].y : vr[2 * p][q >> 1].x;
-        const uint32_t y = (q & 1) ? vr[2 * p + 1][q >> 1].y : vr[2 * p + 1][q >> 1].x;
-        e4m3x4_to_f16x2(__byte_perm(x, y, 0x5140), f[0][p], f[1][p]);
-        e4m3x4_to_f16x2(__byte_perm(x, y, 0x7362), f[2][p], f[3][p]);
+        e4m3x4_to_f16x2(__byte_perm(vr[2 * p][q], vr[2 * p + 1][q], 0x5140), f[0][p], f[1][p]);
+        e4m3x4_to_f16x2(__byte_perm(vr[2 * p][q], vr[2 * p + 1][q], 0x7362), f[2][p], f[3][p]);
       }
 #pragma unroll
       for (int d = 0; d < 4; ++d) {
@@ -473,107 +534,58 @@ __device__ __forceinline__ void pr_convert(const AttnArgs& a, PrShared& sh, uint
     }
     fence_async_shared();
     mbar_arrive(&sh.vfull[stage]);
-    fetch_v(t1);
+    fetch_k(t2);
     t0 = t1;
     t1 = t2;
+    t2 = t3;
   }
+  cp_async_wait<0>();
 }
 
 // ---------------------------------------------------------------------------
-// MMA issuer (one thread)
+// Products of stream t, issued by its first thread; n: the tile of keys
 // ---------------------------------------------------------------------------
 template <int D, bool PAIR>
-__device__ __forceinline__ void pr_mma(const AttnArgs& a, PrShared& sh, uint8_t* smem,
-                                       PrCursor c, long long n_units) {
+__device__ __forceinline__ void pr_scores(PrShared& sh, uint32_t base, uint32_t T, int t, int n) {
   using S = PrShape<D, PAIR>;
-  const uint32_t T = sh.tmem, base = smem_addr(smem);
-  const uint32_t id_s = umma_idesc_f16(kPrKeys), id_o = umma_idesc_f16(D);
-  int n0 = 0, seg = 0;
-  uint32_t cnt[2] = {0, 0};   // tiles of each stream so far
-
-  auto scores = [&](int t, int stage) {
-    const uint64_t dq = umma_desc(base + (PAIR ? t * S::QBYTES : 0), S::QLBO, 128);
-    const uint64_t dk = umma_desc(base + S::KOFF + stage * S::KBYTES, S::KLBO, 128);
+  pr_wait(&sh.kfull[n & 1], (n >> 1) & 1, sh);
+  tc_fence_after();
+  const uint64_t dq = umma_desc(base + (PAIR ? t * S::QBYTES : 0), S::QLBO, 128);
+  const uint64_t dk = umma_desc(base + S::KOFF, S::KLBO, 128);
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k)
-      umma_f16(T + 128 * t, dq + (2 * S::QLBO / 16) * k, dk + (2 * S::KLBO / 16) * k, id_s, k > 0);
-    umma_commit(&sh.sfull[t]);
-  };
-  auto values = [&](int t, int stage, bool add) {
-    const uint64_t dv = umma_desc(base + S::VOFF + stage * S::VBYTES, S::VLBO, S::VSBO);
+  for (int k = 0; k < D / 16; ++k)
+    umma_f16(T + 128 * t, dq + (2 * S::QLBO / 16) * k, dk + (2 * S::KLBO / 16) * k,
+             umma_idesc_f16(kPrKeys), k > 0);
+  umma_commit(&sh.sfull[t]);
+  umma_commit(&sh.kempty[n & 1]);
+}
+template <int D, bool PAIR>
+__device__ __forceinline__ void pr_values(PrShared& sh, uint32_t base, uint32_t T, int t, int n,
+                                          bool add) {
+  using S = PrShape<D, PAIR>;
+  pr_wait(&sh.vfull[n & 1], (n >> 1) & 1, sh);
+  tc_fence_after();
+  const uint64_t dv = umma_desc(base + S::VOFF + (n & 1) * S::VBYTES, S::VLBO, S::VSBO);
 #pragma unroll
-    for (int k = 0; k < kPrKeys / 16; ++k)
-      umma_f16_ta(T + S::OCOL + D * t, T + 128 * t + 8 * k, dv + (2 * S::VLBO / 16) * k, id_o,
-                  add || k > 0);
-    umma_commit(&sh.ofull[t]);
-  };
-  auto wait_k = [&](int n) { pr_wait(&sh.kfull[n & 1], (n >> 1) & 1, sh); };
-  auto wait_v = [&](int n) { pr_wait(&sh.vfull[n & 1], (n >> 1) & 1, sh); };
-
-  while (n_units > 0) {
-    const int nseg = (int)min((long long)(c.S - c.s), n_units);
-    pr_wait(&sh.qfull[0], seg & 1, sh);
-    if (PAIR) pr_wait(&sh.qfull[1], seg & 1, sh);
-    if (PAIR) {
-      wait_k(n0);
-      tc_fence_after();
-      scores(0, n0 & 1);
-      scores(1, n0 & 1);
-      umma_commit(&sh.kempty[n0 & 1]);
-      for (int j = 0; j < nseg; ++j) {
-        const int n = n0 + j;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          pr_wait(&sh.pfull[t], cnt[t] & 1, sh);
-          ++cnt[t];
-          if (t == 0) wait_v(n);
-          tc_fence_after();
-          values(t, n & 1, j > 0);
-          if (t == 1) umma_commit(&sh.vempty[n & 1]);
-          if (j + 1 < nseg) {
-            if (t == 0) wait_k(n + 1);
-            tc_fence_after();
-            scores(t, (n + 1) & 1);
-            if (t == 1) umma_commit(&sh.kempty[(n + 1) & 1]);
-          }
-        }
-      }
-    } else {
-      for (int t = 0; t < 2 && t < nseg; ++t) {
-        wait_k(n0 + t);
-        tc_fence_after();
-        scores(t, (n0 + t) & 1);
-        umma_commit(&sh.kempty[(n0 + t) & 1]);
-      }
-      for (int j = 0; j < nseg; ++j) {
-        const int n = n0 + j, t = j & 1;
-        pr_wait(&sh.pfull[t], (t ? cnt[1] : cnt[0]) & 1, sh);
-        if (t) ++cnt[1];
-        else ++cnt[0];
-        wait_v(n);
-        tc_fence_after();
-        values(t, n & 1, j >= 2);
-        umma_commit(&sh.vempty[n & 1]);
-        if (j + 2 < nseg) {
-          wait_k(n + 2);
-          tc_fence_after();
-          scores(t, n & 1);
-          umma_commit(&sh.kempty[n & 1]);
-        }
-      }
-    }
-    n0 += nseg;
-    n_units -= nseg;
-    ++seg;
-    if (n_units > 0) pr_next_item<S::TILE>(a, c);
-  }
+  for (int k = 0; k < kPrKeys / 16; ++k)
+    umma_f16_ta(T + S::OCOL + D * t, T + 128 * t + 8 * k, dv + (2 * S::VLBO / 16) * k,
+                umma_idesc_f16(D), add || k > 0);
+  umma_commit(&sh.ofull[t]);
+  umma_commit(&sh.vempty[n & 1]);
 }
 
 // ---------------------------------------------------------------------------
 // Softmax (warps 0..7): a thread a row of its stream
 // ---------------------------------------------------------------------------
-// Barrier of both streams' threads.
-__device__ __forceinline__ void pr_streams_sync() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
+// Barriers of one stream's threads and of both streams'.
+__device__ __forceinline__ void pr_stream_sync(int t) {
+  __syncwarp();
+  asm volatile("bar.sync %0, 128;" ::"r"(5 + t) : "memory");
+}
+__device__ __forceinline__ void pr_streams_sync() {
+  __syncwarp();
+  asm volatile("bar.sync 3, 256;" ::: "memory");
+}
 
 // Dims (bits) in which the row sees a NaN value among the masked tiles of
 // keys [first, end) (step `step`) of the item: the rare path.
@@ -600,8 +612,9 @@ __device__ __forceinline__ void pr_softmax(const AttnArgs& a, PrShared& sh, uint
                                            PrCursor c, long long n_units) {
   using S = PrShape<D, PAIR>;
   const int t = threadIdx.x >> 7, row = threadIdx.x & 127, warp = (threadIdx.x >> 5) & 3;
+  const uint32_t T = sh.tmem, base = smem_addr(smem);
   const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-  const uint32_t ts = sh.tmem + lanes + 128 * t, to = sh.tmem + lanes + S::OCOL + D * t;
+  const uint32_t ts = T + lanes + 128 * t, to = T + lanes + S::OCOL + D * t;
   float* slots = a.partial + 2ll * blockIdx.x * S::SLOT;
   uint32_t cnt = 0;     // tiles of this stream so far
   int n0 = 0, seg = 0;
@@ -639,7 +652,7 @@ __device__ __forceinline__ void pr_softmax(const AttnArgs& a, PrShared& sh, uint
       const int shift = be == 0 || be == 255 ? 0 : min(max(be - 140, -120), 120);
       const float down =
           a.scale_log2 == 0.f ? 0.f : (a.scale_log2 < 0.f ? -pow2f(-shift) : pow2f(-shift));
-      fac = fabsf(a.scale_log2) * pow2f(shift);
+      fac = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2) * pow2f(shift);
       if (PAIR || t == 0) {
 #pragma unroll
         for (int k = 0; k < D / 8; ++k) {
@@ -653,8 +666,12 @@ __device__ __forceinline__ void pr_softmax(const AttnArgs& a, PrShared& sh, uint
         }
         fence_async_shared();
       }
-      mbar_arrive(&sh.qfull[PAIR ? t : 0]);
     }
+    // the queries are in place (and O of the last item read): the first scores
+    tc_fence_before();
+    if (PAIR) pr_stream_sync(t);
+    else pr_streams_sync();
+    if (row == 0 && (PAIR || t < nseg)) pr_scores<D, PAIR>(sh, base, T, t, n0 + (PAIR ? 0 : t));
 
     float m = -INFINITY, l = 0.f;
     int mine = 0;       // tiles of this stream in the segment
@@ -666,85 +683,83 @@ __device__ __forceinline__ void pr_softmax(const AttnArgs& a, PrShared& sh, uint
       pr_wait(&sh.sfull[t], cnt & 1, sh);
       __syncwarp();
       tc_fence_after();
-      // ---- maximum ----
-      float x = -INFINITY;
+      // Weights against the running reference in one pass over the scores, in
+      // registers until the tile's maximum is known; where a row of the warp
+      // outgrows its reference by 2^8 (its first tile, then rarely) O and the
+      // sums follow, and the pass is made again.
+      uint32_t p[kPrKeys / 2];
+#pragma unroll 1
+      for (;;) {
+        const float ref = m == -INFINITY ? 0.f : m;
+        float x = -INFINITY, lt = 0.f;
+        __syncwarp();
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        float s[64];
-        tmem_ld32(ts + 64 * hf, s);
-        tmem_ld32(ts + 64 * hf + 32, s + 32);
-        tmem_wait_ld();
-        if (masked) {
+        for (int c32 = 0; c32 < kPrKeys; c32 += 32) {
+          float s[32];
+          tmem_ld32(ts + c32, s);
+          tmem_wait_ld();
+          if (masked) {
+            const int from = lo - p0 - c32;
+            const unsigned len = (unsigned)max(hi - lo, 0);
 #pragma unroll
-          for (int k = 0; k < 64; ++k) {
-            const int key = p0 + 64 * hf + k;
-            if (key < lo || key >= hi) s[k] = -INFINITY;
+            for (int k = 0; k < 32; ++k)
+              if ((unsigned)(k - from) >= len) s[k] = -INFINITY;
+          }
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const float4 f = sc[c32 / 16 + b];
+            // (a factor of 0 would make NaN of a masked score)
+            const float g = fmaxf(fac * f.x, 1e-38f), off = f.y - ref;
+            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+            for (int k = 16 * b; k < 16 * b + 16; k += 2) {
+              fma_f32x2(s[k], s[k + 1], g, off);
+              x = fmaxf(fmaxf(x, s[k]), s[k + 1]);
+              s[k] = exp2_approx(s[k]);
+              s[k + 1] = exp2_approx(s[k + 1]);
+              add_f32x2(s0, s1, s[k], s[k + 1]);
+              p[(c32 + k) / 2] = pack_f16x2(s[k], s[k + 1]);
+            }
+            lt = fmaf(f.z, s0 + s1, lt);
           }
         }
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          float v = fmaxf(s[16 * b], s[16 * b + 1]);
-#pragma unroll
-          for (int k = 2; k < 16; ++k) v = fmaxf(v, s[16 * b + k]);
-          const float4 f = sc[4 * hf + b];
-          x = fmaxf(x, fmaf(v, fac * f.x, f.y));   // NaN (-infinity times 0) drops out
+        const bool grow = x > (m == -INFINITY ? -INFINITY : 8.f);
+        if (!__any_sync(0xffffffffu, grow)) {
+          l += lt;
+          break;
         }
-      }
-      // ---- a new reference, O brought to it ----
-      const bool grow = x > (m == -INFINITY ? -INFINITY : m + 8.f);
-      const float down = grow ? attn_factor(m, x) : 1.f;
-      if (grow) m = x;
-      l *= down;
-      if (mine > 0) {
-        if (__any_sync(0xffffffffu, grow)) {
+        const float next = ref + x;
+        const float down = grow ? attn_factor(m, next) : 1.f;
+        if (grow) m = next;
+        l *= down;
+        if (mine > 0) {
           pr_wait(&sh.ofull[t], (cnt - 1) & 1, sh);
           __syncwarp();
           tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < D / 32; ++k) {
-            float o[32];
-            tmem_ld32(to + 32 * k, o);
+#pragma unroll 1
+          for (int k = 0; k < D / 16; ++k) {
+            float o[16];
+            tmem_ld16(to + 16 * k, o);
             tmem_wait_ld();
-            uint32_t r[32];
+            uint32_t r[16];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(o[e] * down);
-            tmem_st32(to + 32 * k, r);
+            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(o[e] * down);
+            tmem_st16(to + 16 * k, r);
           }
         }
       }
-      const float ref = m == -INFINITY ? 0.f : m;
-      // ---- weights, into the columns of the scores ----
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        float s[64];
-        tmem_ld32(ts + 64 * hf, s);
-        tmem_ld32(ts + 64 * hf + 32, s + 32);
-        tmem_wait_ld();
-        uint32_t p[32];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const float4 f = sc[4 * hf + b];
-          const float g = fac * f.x, off = f.y - ref;
-          float sum = 0.f;
-#pragma unroll
-          for (int k = 0; k < 16; k += 2) {
-            float u = exp2_approx(fmaf(s[16 * b + k], g, off));
-            float v = exp2_approx(fmaf(s[16 * b + k + 1], g, off));
-            if (masked) {
-              const int key = p0 + 64 * hf + 16 * b + k;
-              if (key < lo || key >= hi) u = 0.f;
-              if (key + 1 < lo || key + 1 >= hi) v = 0.f;
-            }
-            sum += u + v;
-            p[8 * b + k / 2] = pack_f16x2(u, v);
-          }
-          l = fmaf(f.z, sum, l);
-        }
-        tmem_st32(ts + 32 * hf, p);
-      }
+      // into the columns of the scores
+      __syncwarp();
+      tmem_st32(ts, p);
+      tmem_st32(ts + 32, p + 32);
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(&sh.pfull[t]);
+      pr_stream_sync(t);
+      if (row == 0) {
+        constexpr int step = PAIR ? 1 : 2;
+        pr_values<D, PAIR>(sh, base, T, t, n0 + j, mine > 0);
+        if (j + step < nseg) pr_scores<D, PAIR>(sh, base, T, t, n0 + j + step);
+      }
     }
 
     // ---- the item's end, or the CTA's ----
@@ -853,13 +868,11 @@ static __global__ void __launch_bounds__(kPrThreads, 1) kv_attention_tc(const At
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sh.kfull[s], 128);
-      mbar_init(&sh.kempty[s], 1);
+      mbar_init(&sh.kempty[s], PAIR ? 2 : 1);   // streams that read it
       mbar_init(&sh.vfull[s], 128);
-      mbar_init(&sh.vempty[s], 1);
+      mbar_init(&sh.vempty[s], PAIR ? 2 : 1);
       mbar_init(&sh.sfull[s], 1);
-      mbar_init(&sh.pfull[s], 128);
       mbar_init(&sh.ofull[s], 1);
-      mbar_init(&sh.qfull[s], PAIR ? 128 : 256);
       sh.open[s] = 0;
     }
     for (int s = 0; s < 8; ++s) sh.nan[s] = 0;
@@ -867,21 +880,17 @@ static __global__ void __launch_bounds__(kPrThreads, 1) kv_attention_tc(const At
     sh.out = {a.out, a.lse, a.o_ts, a.o_hs, a.heads, a.f16, (unsigned)a.group};
     fence_barrier_init();
   }
-  if (warp == 12) tmem_alloc(&sh.tmem);
+  __syncwarp();
+  if (warp == 0) tmem_alloc(&sh.tmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
 
-  if (warp < 8) {
-    pr_softmax<D, PAIR>(a, sh, pr_smem, cur, n_units);
-  } else if (warp < 12) {
-    pr_convert<D, PAIR>(a, sh, pr_smem, cur, n_units);
-  } else if ((threadIdx.x & 31) == 0) {
-    pr_mma<D, PAIR>(a, sh, pr_smem, cur, n_units);
-  }
+  if (warp < 8) pr_softmax<D, PAIR>(a, sh, pr_smem, cur, n_units);
+  else pr_convert<D, PAIR>(a, sh, pr_smem, cur, n_units);
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 0) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(sh.tmem);
