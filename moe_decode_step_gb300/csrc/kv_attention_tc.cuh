@@ -11,7 +11,7 @@
 // Roles (12 warps, 168 registers a thread): warps 0..3 and 4..7, one stream
 // each, a thread a row: scores from tensor memory, running maximum and sum,
 // weights back into tensor memory (in the columns of their scores) as the A
-// operand of O += P V; the stream's first thread then issues its products, the
+// operand of O += P V; the stream's first warp then issues its products, the
 // values' and the next scores', which the stream waits for anyway.  Warps 8..11
 // fetch codes, convert them to f16 and lay them out in shared memory as K-major
 // core matrices (K rows = keys, V^T rows = dims, transposed in registers).
@@ -43,10 +43,14 @@ constexpr int kPrKeys = 128;
 template <int D, bool PAIR>
 struct PrShape {
   static constexpr int TILE = PAIR ? 256 : 128;
-  // byte distances in the operands: K and Q by 8 dims, V^T by 8 keys; padded
-  // so that the converters' 16-byte stores hit all banks
-  static constexpr int QLBO = 2048, KLBO = 2080, VSBO = 144, VLBO = D / 8 * VSBO + 16;
-  static constexpr int QBYTES = D / 8 * QLBO, KBYTES = D / 8 * KLBO, VBYTES = 16 * VLBO;
+  // All operands lie as 8 x 16 byte core matrices (8 rows or keys, 8 dims),
+  // 128 bytes each, the 16 of 8 dims one after the other: element (row, dim) at
+  // GROUP (dim / 8) + 16 row + 2 (dim % 8).  Q and K are K-major operands of
+  // the scores in this order, V an MN-major one of the values (N = dims).  The
+  // 16 bytes that pad a group of K and V spread the converters' stores over the
+  // banks.
+  static constexpr int QGROUP = 2048, GROUP = 2064;
+  static constexpr int QBYTES = D / 8 * QGROUP, KBYTES = D / 8 * GROUP, VBYTES = KBYTES;
   // queries, one tile of keys, two of values, and three half tiles of codes
   // (keys or values) on their way: a tile and a half ahead of the converters
   static constexpr int KOFF = (PAIR ? 2 : 1) * QBYTES, VOFF = KOFF + KBYTES;
@@ -117,6 +121,7 @@ __device__ __forceinline__ void umma_f16_ta(uint32_t d, uint32_t a, uint64_t b, 
 __device__ __forceinline__ constexpr uint32_t umma_idesc_f16(uint32_t N) {
   return (1u << 4) | ((N >> 3) << 17) | ((128u >> 4) << 24);
 }
+constexpr uint32_t kUmmaTransposeB = 1u << 16;   // B is MN-major
 // Generic writes to shared memory become visible to the tensor cores.
 __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -317,13 +322,23 @@ struct PrShared {
 };
 
 // Waits for a phase, two seconds at most; then marks the CTA dead, whose waits
-// all end at once and whose results become NaN.
+// all end at once and whose results become NaN.  The hint lets the hardware
+// suspend the thread: threads that poll take issue slots and shared-memory
+// cycles from the ones that work (a tile took 1.5 times as long).
+__device__ __forceinline__ bool pr_try_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(1000000u)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ void pr_wait(uint64_t* bar, uint32_t parity, PrShared& sh) {
-  if (mbar_try_wait(bar, parity)) return;
+  if (pr_try_wait(bar, parity)) return;
   const unsigned long long t0 = global_ns();
-  for (;;) {
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait(bar, parity)) return;
+  while (!pr_try_wait(bar, parity)) {
     if (*(volatile int*)&sh.dead) return;
     if (global_ns() - t0 > kWaitLimitNs) {
       *(volatile int*)&sh.dead = 1;
@@ -374,22 +389,16 @@ __device__ __forceinline__ uint64_t policy_evict_normal() {
 
 // Each thread copies (cp.async) the pieces that it converts itself into a ring
 // of its own, so the copies need no barrier.  (Fetched into registers half a
-// tile ahead, a tile took 4,700 cycles, mostly waiting.)
+// tile ahead, a tile took 4,700 cycles, mostly waiting.)  A piece is 16 dims of
+// a key; four neighbouring lanes take neighbouring pieces (with neighbouring
+// keys a copy of 512 bytes took 37 cycles of the L1).
 template <int D, bool PAIR>
 __device__ __forceinline__ void pr_convert(const AttnArgs& a, PrShared& sh, uint8_t* smem,
                                            const PrCursor& start, long long n_units) {
   using S = PrShape<D, PAIR>;
-  constexpr int KN = D / 16;               // key pieces of 16 bytes a thread
-  constexpr int VB = D / 8;                // bytes of a value piece, 8 of them a thread
+  constexpr int C = D / 64;                // pieces of a key a thread, 4 keys
   const int ct = threadIdx.x - 256, lane = ct & 31, warp = ct >> 5;
-  // key pieces: token kt + ks i, dims 16 kc ..
-  const int kc = D == 128 ? lane >> 2 : (lane >> 2) & 3;
-  const int kt = D == 128 ? warp * 4 + (lane & 3) : warp * 8 + (lane >> 4) * 4 + (lane & 3);
-  constexpr int ks = D == 128 ? 16 : 32;
-  // value pieces: tokens 8 vg .. + 7, dims VB vc ..
-  const int vc = D == 128 ? (lane & 3) + 4 * ((lane >> 3) & 1) : lane & 7;
-  const int vg = D == 128 ? warp * 4 + ((lane >> 2) & 1) + 2 * ((lane >> 4) & 1)
-                          : warp * 4 + (lane >> 3);
+  const int chunk = lane & 3, key = 32 * warp + (lane >> 2);   // keys key + 8 i, dims 16 (chunk + 4 c)
   PrFeed<S::TILE> feed;
   feed.c = start;
   feed.left = n_units;
@@ -399,43 +408,58 @@ __device__ __forceinline__ void pr_convert(const AttnArgs& a, PrShared& sh, uint
   const int bs1 = (1 << a.c.bs_log2) - 1;
   // codes that one row tile reads leave L2 first; those of a prompt are read again
   const uint64_t policy = PAIR ? policy_evict_normal() : policy_evict_first();
-  const uint32_t raw = smem_addr(smem) + S::ROFF;
+  const uint32_t raw = smem_addr(smem) + S::ROFF + ct * 16;
   int in_slot = 0, out_slot = 0;
 
-  auto fetch_k = [&](const PrTile& t) {
-    const uint32_t dst = raw + in_slot * S::RAW + ct * 16;
+  auto fetch = [&](const PrTile& t, const uint8_t* codes) {
+    const uint32_t dst = raw + in_slot * S::RAW;
     in_slot = in_slot + 1 == S::RAWS ? 0 : in_slot + 1;
+    // the warp's 32 keys lie in two groups of 16, each in one block
 #pragma unroll
-    for (int i = 0; i < KN; ++i) {
-      const int tok = kt + ks * i;
-      const int id = __shfl_sync(0xffffffffu, t.id, tok >> 4);
-      const bool in = t.there && id >= 0 && id < a.c.n_blocks && t.p0 + tok < t.seq;
-      const uint8_t* src = a.c.k;
-      if (in)
+    for (int g = 0; g < 2; ++g) {
+      const int id = __shfl_sync(0xffffffffu, t.id, 2 * warp + g);
+      const int k = key + 16 * g;
+      const int left = t.there && id >= 0 && id < a.c.n_blocks ? t.seq - t.p0 - k : 0;
+      const uint8_t* src = codes;
+      if (left > 0)
         src += (long long)id * a.c.bstride + (long long)t.h * a.c.hstride +
-               (long long)((t.p0 + tok) & bs1) * a.c.tstride + kc * 16;
-      cp_async<16>(dst + i * 2048, src, in, policy);
+               (long long)((t.p0 + k) & bs1) * a.c.tstride + chunk * 16;
+      const uint8_t* src1 = left > 8 ? src + 8 * a.c.tstride : codes;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        cp_async<16>(dst + (2 * g * C + c) * 2048, src + (left > 0 ? 64 * c : 0), left > 0, policy);
+        cp_async<16>(dst + ((2 * g + 1) * C + c) * 2048, src1 + (left > 8 ? 64 * c : 0), left > 8,
+                     policy);
+      }
     }
     cp_async_commit();
   };
-  // a thread's bytes of a slot are the same for keys and values: nobody else
-  // may still be reading them
-  auto piece = [](int i) { return VB == 16 ? i * 2048 : (i >> 1) * 2048 + (i & 1) * 8; };
-  auto fetch_v = [&](const PrTile& t) {
-    const uint32_t dst = raw + in_slot * S::RAW + ct * 16;
-    in_slot = in_slot + 1 == S::RAWS ? 0 : in_slot + 1;
-    const int id = __shfl_sync(0xffffffffu, t.id, vg >> 1);
-    const bool ok = t.there && id >= 0 && id < a.c.n_blocks;
-    const uint8_t* src = a.c.v;
-    if (ok)
-      src += (long long)id * a.c.bstride + (long long)t.h * a.c.hstride +
-             (long long)((t.p0 + 8 * vg) & bs1) * a.c.tstride + vc * VB;
+  auto convert = [&](uint8_t* to, bool drop) {
+    const uint8_t* from = smem + S::ROFF + out_slot * S::RAW + ct * 16;
+    out_slot = out_slot + 1 == S::RAWS ? 0 : out_slot + 1;
+    uint32_t any = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const bool in = ok && t.p0 + 8 * vg + i < t.seq;
-      cp_async<VB>(dst + piece(i), in ? src + i * a.c.tstride : a.c.v, in, policy);
-    }
-    cp_async_commit();
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        uint4 w = *reinterpret_cast<const uint4*>(from + (i * C + c) * 2048);
+        if (drop) {
+          w.x = drop_nan4(w.x, any);
+          w.y = drop_nan4(w.y, any);
+          w.z = drop_nan4(w.z, any);
+          w.w = drop_nan4(w.w, any);
+        }
+        uint8_t* d = to + 2 * (chunk + 4 * c) * S::GROUP + (key + 8 * i) * 16;
+        uint4 x, y;
+        e4m3x4_to_f16x2(w.x, x.x, x.y);
+        e4m3x4_to_f16x2(w.y, x.z, x.w);
+        e4m3x4_to_f16x2(w.z, y.x, y.y);
+        e4m3x4_to_f16x2(w.w, y.z, y.w);
+        *reinterpret_cast<uint4*>(d) = x;
+        *reinterpret_cast<uint4*>(d + S::GROUP) = y;
+      }
+    fence_async_shared();
+    return any;
   };
   // scale bytes of a tile, lanes 0..7 of the first converter warp
   uint32_t ek = 0, ev = 0;
@@ -450,9 +474,9 @@ __device__ __forceinline__ void pr_convert(const AttnArgs& a, PrShared& sh, uint
   feed.take(a, t0, lane);
   feed.take(a, t1, lane);
   feed.take(a, t2, lane);
-  fetch_k(t0);
-  fetch_v(t0);
-  fetch_k(t1);
+  fetch(t0, a.c.k);
+  fetch(t0, a.c.v);
+  fetch(t1, a.c.k);
   fetch_scales(t0);
 #pragma unroll 1
   for (int n = 0; t0.there; ++n) {
@@ -461,80 +485,25 @@ __device__ __forceinline__ void pr_convert(const AttnArgs& a, PrShared& sh, uint
     // ---- keys ----
     if (n > 0) pr_wait(&sh.kempty[(n - 1) & 1], ((n - 1) >> 1) & 1, sh);
     cp_async_wait<2>();
-    const uint8_t* from = smem + S::ROFF + out_slot * S::RAW;
-    out_slot = out_slot + 1 == S::RAWS ? 0 : out_slot + 1;
-    uint8_t* kd = smem + S::KOFF + 2 * kc * S::KLBO;
-#pragma unroll
-    for (int i = 0; i < KN; ++i) {
-      uint8_t* d = kd + (kt + ks * i) * 16;   // 8-token groups are 128 bytes apart
-      const uint4 w = *reinterpret_cast<const uint4*>(from + ct * 16 + i * 2048);
-      uint4 x, y;
-      e4m3x4_to_f16x2(w.x, x.x, x.y);
-      e4m3x4_to_f16x2(w.y, x.z, x.w);
-      e4m3x4_to_f16x2(w.z, y.x, y.y);
-      e4m3x4_to_f16x2(w.w, y.z, y.w);
-      *reinterpret_cast<uint4*>(d) = x;
-      *reinterpret_cast<uint4*>(d + S::KLBO) = y;
-    }
     if (warp == 0 && lane < 8) {
       const int e = kv_exp(ev);
       // a block outside the cache: weights 0
       sh.scale[n & 3][lane] = block ? make_float4(pow2f(kv_exp(ek)), (float)e, pow2f(-e), 0.f)
                                     : make_float4(0.f, -INFINITY, 0.f, 0.f);
     }
-    fence_async_shared();
+    convert(smem + S::KOFF, false);
     mbar_arrive(&sh.kfull[n & 1]);
     fetch_scales(t1);
-    fetch_v(t1);
-    // ---- values, transposed: 8 tokens of a dim are 16 bytes ----
+    fetch(t1, a.c.v);
+    // ---- values ----
     const int stage = n & 1;
     if (n > 1) pr_wait(&sh.vempty[stage], ((n >> 1) - 1) & 1, sh);
     cp_async_wait<2>();
-    from = smem + S::ROFF + out_slot * S::RAW + ct * 16;
-    out_slot = out_slot + 1 == S::RAWS ? 0 : out_slot + 1;
-    uint8_t* vd = smem + S::VOFF + stage * S::VBYTES + vg * S::VLBO + vc * (D / 64) * S::VSBO;
-    uint32_t vr[8][VB / 4], any = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if constexpr (VB == 16) {
-        const uint4 x = *reinterpret_cast<const uint4*>(from + piece(i));
-        vr[i][0] = x.x;
-        vr[i][1] = x.y;
-        vr[i][2] = x.z;
-        vr[i][3] = x.w;
-      } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(from + piece(i));
-        vr[i][0] = x.x;
-        vr[i][1] = x.y;
-      }
-    }
-    if (t0.masked) {
-      // a weight of 0 does not keep a NaN out of the sums: NaN codes leave here
-      // and are given back to the rows that see them at the item's end
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int w = 0; w < VB / 4; ++w) vr[i][w] = drop_nan4(vr[i][w], any);
-      if (any) atomicOr(&sh.nan[t0.seg & 7], 1);
-    }
-#pragma unroll
-    for (int q = 0; q < VB / 4; ++q) {   // 4 dims at a time
-      uint32_t f[4][4];                  // [dim][token pair]
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        e4m3x4_to_f16x2(__byte_perm(vr[2 * p][q], vr[2 * p + 1][q], 0x5140), f[0][p], f[1][p]);
-        e4m3x4_to_f16x2(__byte_perm(vr[2 * p][q], vr[2 * p + 1][q], 0x7362), f[2][p], f[3][p]);
-      }
-#pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        const int j = 4 * q + d;         // dim of the thread's
-        *reinterpret_cast<uint4*>(vd + (j >> 3) * S::VSBO + (j & 7) * 16) =
-            make_uint4(f[d][0], f[d][1], f[d][2], f[d][3]);
-      }
-    }
-    fence_async_shared();
+    // a weight of 0 does not keep a NaN out of the sums: in masked tiles NaN
+    // codes leave here and are given back to the rows that see them at the end
+    if (convert(smem + S::VOFF + stage * S::VBYTES, t0.masked)) atomicOr(&sh.nan[t0.seg & 7], 1);
     mbar_arrive(&sh.vfull[stage]);
-    fetch_k(t2);
+    fetch(t2, a.c.k);
     t0 = t1;
     t1 = t2;
     t2 = t3;
@@ -543,35 +512,83 @@ __device__ __forceinline__ void pr_convert(const AttnArgs& a, PrShared& sh, uint
 }
 
 // ---------------------------------------------------------------------------
-// Products of stream t, issued by its first thread; n: the tile of keys
+// Products of a stream, issued by its first warp; n: the tile of keys
 // ---------------------------------------------------------------------------
-template <int D, bool PAIR>
-__device__ __forceinline__ void pr_scores(PrShared& sh, uint32_t base, uint32_t T, int t, int n) {
-  using S = PrShape<D, PAIR>;
+// All lanes of the warp run this code and one issues: stream and stage are
+// template arguments and tensor memory is allocated whole (address 0), so that
+// every operand of an MMA is a constant of the code.  (Built in one thread's
+// registers, the operands of an MMA cost 145 cycles to issue, more than twice
+// its time on the tensor cores.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+__device__ __forceinline__ void pr_wait_keys(PrShared& sh, int n) {
   pr_wait(&sh.kfull[n & 1], (n >> 1) & 1, sh);
-  tc_fence_after();
-  const uint64_t dq = umma_desc(base + (PAIR ? t * S::QBYTES : 0), S::QLBO, 128);
-  const uint64_t dk = umma_desc(base + S::KOFF, S::KLBO, 128);
+}
+__device__ __forceinline__ void pr_wait_values(PrShared& sh, int n) {
+  pr_wait(&sh.vfull[n & 1], (n >> 1) & 1, sh);
+}
+// The streams that share tiles of keys issue in turns (their first warps meet
+// at a barrier of their own, where nobody polls): the queue of the tensor cores
+// is short, so two streams that issue together both wait for both, compute
+// their softmax together, and the tensor cores idle meanwhile.
+__device__ __forceinline__ void pr_take_turn(int t) {
+  asm volatile("bar.sync %0, 64;" ::"r"(8 + t) : "memory");
+}
+__device__ __forceinline__ void pr_pass_turn(int t) {
+  asm volatile("bar.arrive %0, 64;" ::"r"(8 + (t ^ 1)) : "memory");
+}
+
+template <int D, bool PAIR, int T>
+__device__ __forceinline__ void pr_scores_of(PrShared& sh, uint32_t base, int n) {
+  using S = PrShape<D, PAIR>;
+  if (elect_one()) {
+    const uint64_t dq = umma_desc(base + (PAIR ? T * S::QBYTES : 0), S::QGROUP, 128);
+    const uint64_t dk = umma_desc(base + S::KOFF, S::GROUP, 128);
 #pragma unroll
-  for (int k = 0; k < D / 16; ++k)
-    umma_f16(T + 128 * t, dq + (2 * S::QLBO / 16) * k, dk + (2 * S::KLBO / 16) * k,
-             umma_idesc_f16(kPrKeys), k > 0);
-  umma_commit(&sh.sfull[t]);
-  umma_commit(&sh.kempty[n & 1]);
+    for (int k = 0; k < D / 16; ++k)
+      umma_f16(128 * T, dq + (2 * S::QGROUP / 16) * k, dk + (2 * S::GROUP / 16) * k,
+               umma_idesc_f16(kPrKeys), k > 0);
+    umma_commit(&sh.sfull[T]);
+    umma_commit(&sh.kempty[n & 1]);
+  }
+  __syncwarp();
 }
 template <int D, bool PAIR>
-__device__ __forceinline__ void pr_values(PrShared& sh, uint32_t base, uint32_t T, int t, int n,
-                                          bool add) {
+__device__ __forceinline__ void pr_scores(PrShared& sh, uint32_t base, int t, int n) {
+  if (t == 0) pr_scores_of<D, PAIR, 0>(sh, base, n);
+  else pr_scores_of<D, PAIR, 1>(sh, base, n);
+}
+template <int D, bool PAIR, int T, int STAGE>
+__device__ __forceinline__ void pr_values_of(PrShared& sh, uint32_t base, uint32_t add) {
   using S = PrShape<D, PAIR>;
-  pr_wait(&sh.vfull[n & 1], (n >> 1) & 1, sh);
-  tc_fence_after();
-  const uint64_t dv = umma_desc(base + S::VOFF + (n & 1) * S::VBYTES, S::VLBO, S::VSBO);
+  if (elect_one()) {
+    // MN-major: 128 bytes between groups of 8 keys, GROUP between groups of 8 dims
+    const uint64_t dv = umma_desc(base + S::VOFF + STAGE * S::VBYTES, 128, S::GROUP);
+    constexpr uint32_t idesc = umma_idesc_f16(D) | kUmmaTransposeB;
+    umma_f16_ta(S::OCOL + D * T, 128 * T, dv, idesc, add);
 #pragma unroll
-  for (int k = 0; k < kPrKeys / 16; ++k)
-    umma_f16_ta(T + S::OCOL + D * t, T + 128 * t + 8 * k, dv + (2 * S::VLBO / 16) * k,
-                umma_idesc_f16(D), add || k > 0);
-  umma_commit(&sh.ofull[t]);
-  umma_commit(&sh.vempty[n & 1]);
+    for (int k = 1; k < kPrKeys / 16; ++k)
+      umma_f16_ta(S::OCOL + D * T, 128 * T + 8 * k, dv + (256 / 16) * k, idesc, 1);
+    umma_commit(&sh.ofull[T]);
+    umma_commit(&sh.vempty[STAGE]);
+  }
+  __syncwarp();
+}
+template <int D, bool PAIR>
+__device__ __forceinline__ void pr_values(PrShared& sh, uint32_t base, int t, int n, bool add) {
+  if (t == 0) {
+    if (n & 1) pr_values_of<D, PAIR, 0, 1>(sh, base, add);
+    else pr_values_of<D, PAIR, 0, 0>(sh, base, add);
+  } else {
+    if (n & 1) pr_values_of<D, PAIR, 1, 1>(sh, base, add);
+    else pr_values_of<D, PAIR, 1, 0>(sh, base, add);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -612,13 +629,14 @@ __device__ __forceinline__ void pr_softmax(const AttnArgs& a, PrShared& sh, uint
                                            PrCursor c, long long n_units) {
   using S = PrShape<D, PAIR>;
   const int t = threadIdx.x >> 7, row = threadIdx.x & 127, warp = (threadIdx.x >> 5) & 3;
-  const uint32_t T = sh.tmem, base = smem_addr(smem);
-  const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-  const uint32_t ts = T + lanes + 128 * t, to = T + lanes + S::OCOL + D * t;
+  const uint32_t base = smem_addr(smem);
+  const uint32_t lanes = (uint32_t)(32 * warp) << 16;   // (tensor memory begins at 0)
+  const uint32_t ts = lanes + 128 * t, to = lanes + S::OCOL + D * t;
   float* slots = a.partial + 2ll * blockIdx.x * S::SLOT;
   uint32_t cnt = 0;     // tiles of this stream so far
   int n0 = 0, seg = 0;
   long long done = 0;
+  if (PAIR && t == 1 && warp == 0) pr_pass_turn(1);   // the first turn is stream 0's
 #pragma unroll 1
   while (done < n_units) {
     const int nseg = (int)min((long long)(c.S - c.s), n_units - done);
@@ -660,7 +678,7 @@ __device__ __forceinline__ void pr_softmax(const AttnArgs& a, PrShared& sh, uint
           if (real) w = *reinterpret_cast<const uint4*>(q + 8 * k);
           const float2 f0 = unpack16(w.x, a.f16), f1 = unpack16(w.y, a.f16),
                        f2 = unpack16(w.z, a.f16), f3 = unpack16(w.w, a.f16);
-          *reinterpret_cast<uint4*>(dst + k * S::QLBO) = make_uint4(
+          *reinterpret_cast<uint4*>(dst + k * S::QGROUP) = make_uint4(
               pack_f16x2(f0.x * down, f0.y * down), pack_f16x2(f1.x * down, f1.y * down),
               pack_f16x2(f2.x * down, f2.y * down), pack_f16x2(f3.x * down, f3.y * down));
         }
@@ -671,7 +689,12 @@ __device__ __forceinline__ void pr_softmax(const AttnArgs& a, PrShared& sh, uint
     tc_fence_before();
     if (PAIR) pr_stream_sync(t);
     else pr_streams_sync();
-    if (row == 0 && (PAIR || t < nseg)) pr_scores<D, PAIR>(sh, base, T, t, n0 + (PAIR ? 0 : t));
+    if (warp == 0 && (PAIR || t < nseg)) {
+      pr_wait_keys(sh, n0 + (PAIR ? 0 : t));
+      __syncwarp();
+      tc_fence_after();
+      pr_scores<D, PAIR>(sh, base, t, n0 + (PAIR ? 0 : t));
+    }
 
     float m = -INFINITY, l = 0.f;
     int mine = 0;       // tiles of this stream in the segment
@@ -693,11 +716,13 @@ __device__ __forceinline__ void pr_softmax(const AttnArgs& a, PrShared& sh, uint
         const float ref = m == -INFINITY ? 0.f : m;
         float x = -INFINITY, lt = 0.f;
         __syncwarp();
+        float sb[2][32];   // scores, the next 32 on their way
+        tmem_ld32(ts, sb[0]);
 #pragma unroll
         for (int c32 = 0; c32 < kPrKeys; c32 += 32) {
-          float s[32];
-          tmem_ld32(ts + c32, s);
+          float* s = sb[(c32 / 32) & 1];
           tmem_wait_ld();
+          if (c32 + 32 < kPrKeys) tmem_ld32(ts + c32 + 32, sb[(c32 / 32 + 1) & 1]);
           if (masked) {
             const int from = lo - p0 - c32;
             const unsigned len = (unsigned)max(hi - lo, 0);
@@ -755,10 +780,17 @@ __device__ __forceinline__ void pr_softmax(const AttnArgs& a, PrShared& sh, uint
       tmem_wait_st();
       tc_fence_before();
       pr_stream_sync(t);
-      if (row == 0) {
+      if (warp == 0) {
         constexpr int step = PAIR ? 1 : 2;
-        pr_values<D, PAIR>(sh, base, T, t, n0 + j, mine > 0);
-        if (j + step < nseg) pr_scores<D, PAIR>(sh, base, T, t, n0 + j + step);
+        const bool more = j + step < nseg;
+        pr_wait_values(sh, n0 + j);
+        if (more) pr_wait_keys(sh, n0 + j + step);
+        __syncwarp();
+        if (PAIR) pr_take_turn(t);
+        tc_fence_after();
+        pr_values<D, PAIR>(sh, base, t, n0 + j, mine > 0);
+        if (more) pr_scores<D, PAIR>(sh, base, t, n0 + j + step);
+        if (PAIR) pr_pass_turn(t);
       }
     }
 
@@ -886,6 +918,7 @@ static __global__ void __launch_bounds__(kPrThreads, 1) kv_attention_tc(const At
   __syncthreads();
   tc_fence_after();
 
+  if (threadIdx.x == 0 && sh.tmem != 0) sh.dead = 1;   // never: all of it was allocated
   if (warp < 8) pr_softmax<D, PAIR>(a, sh, pr_smem, cur, n_units);
   else pr_convert<D, PAIR>(a, sh, pr_smem, cur, n_units);
   tc_fence_before();
