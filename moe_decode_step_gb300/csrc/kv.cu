@@ -144,6 +144,16 @@ int launch_attention(const AttnArgs& a, int n_sm, int max_q, cudaStream_t st) {
                                          : launch_decode<D, 2>(a, n_sm, max_q, st);
 }
 
+// Shared memory only where groups go through it (sizes that are no power of
+// two from 4 to 128, or experts one a load).
+void launch_route(void (*kernel)(RouteArgs), const RouteArgs& a, int regs, bool vec,
+                  unsigned grid, cudaStream_t st) {
+  const int size = a.E / a.groups;
+  const bool shuffles = vec && (size & (size - 1)) == 0 && size >= 4 && size <= 128;
+  const int smem = a.groups > 1 && !shuffles ? kRouteWarps * regs * 32 * 4 : 0;
+  kernel<<<grid, 32 * kRouteWarps, smem, st>>>(a);
+}
+
 }  // namespace
 
 extern "C" {
@@ -310,11 +320,20 @@ int moe_route(void* stream, const moe_route_t* cfg, const void* logits, int dtyp
               c.n_groups, c.topk_groups, c.group_top, c.renormalize != 0, c.routed_scale};
   const unsigned grid = (unsigned)((n_rows + kRouteWarps - 1) / kRouteWarps);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int threads = 32 * kRouteWarps;
-  if (c.n_experts <= 64) route_kernel<2><<<grid, threads, 0, st>>>(a);
-  else if (c.n_experts <= 256) route_kernel<8><<<grid, threads, 0, st>>>(a);
-  else if (c.n_experts <= 512) route_kernel<16><<<grid, threads, 0, st>>>(a);
-  else route_kernel<32><<<grid, threads, 0, st>>>(a);
+  // four experts a load where every row allows it
+  const int size = dtype == MOE_DTYPE_F32 ? 4 : 2;
+  const bool vec = c.n_experts >= 128 && row_stride % 4 == 0 && !misaligned(logits, 4 * size);
+  const int n = c.n_experts;
+  if (vec) {
+    if (n <= 128) launch_route(route_kernel<1, 4>, a, 4, vec, grid, st);
+    else if (n <= 256) launch_route(route_kernel<2, 4>, a, 8, vec, grid, st);
+    else if (n <= 512) launch_route(route_kernel<4, 4>, a, 16, vec, grid, st);
+    else launch_route(route_kernel<8, 4>, a, 32, vec, grid, st);
+  } else {
+    if (n <= 64) launch_route(route_kernel<2, 1>, a, 2, vec, grid, st);
+    else if (n <= 256) launch_route(route_kernel<8, 1>, a, 8, vec, grid, st);
+    else launch_route(route_kernel<32, 1>, a, 32, vec, grid, st);
+  }
   return end();
 }
 
