@@ -57,10 +57,22 @@ __device__ __forceinline__ float route_rcp(float x) {
   return y;
 }
 
+// 1 / (1 + e^-x): an e^-x that is subnormal does not count beside 1.
+__device__ __forceinline__ float route_sigmoid(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * -1.4426950408889634f));
+  return route_rcp(1.f + y);
+}
+
 // The two best of (a1, a2) and (b1, b2).
-__device__ __forceinline__ void route_merge2(float& a1, float& a2, float b1, float b2) {
-  a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
-  a1 = fmaxf(a1, b1);
+__device__ __forceinline__ void route_merge2(uint32_t& a1, uint32_t& a2, uint32_t b1,
+                                             uint32_t b2) {
+  a2 = max(min(a1, b1), max(a2, b2));
+  a1 = max(a1, b1);
+}
+// The score of a key; -inf for NaN and for experts that are out.
+__device__ __forceinline__ float route_score(uint32_t key) {
+  return key > 1u ? __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key) : -INFINITY;
 }
 
 // CH: chunks of 32 V experts a row has at most; V: experts of a chunk a lane.
@@ -117,16 +129,32 @@ static __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Ro
     for (int i = 0; i < N; ++i) s[i] *= inv;
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = route_rcp(1.f + route_exp(-s[i]));
+    for (int i = 0; i < N; ++i) s[i] = route_sigmoid(s[i]);
   }
   if (a.bias) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (expert(i) < a.E) s[i] += __ldg(a.bias + expert(i));
+    for (int c = 0; c < CH; ++c) {
+      const int e = 32 * V * c + V * lane;
+      if (V == 4 && e + 3 < a.E) {
+        const float4 f = __ldg(reinterpret_cast<const float4*>(a.bias + e));
+        s[V * c] += f.x;
+        s[V * c + 1 % V] += f.y;
+        s[V * c + 2 % V] += f.z;
+        s[V * c + 3 % V] += f.w;
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (e + v < a.E) s[V * c + v] += __ldg(a.bias + e + v);
+      }
+    }
   }
   uint32_t key[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) key[i] = expert(i) < a.E ? route_key(s[i]) : 0u;
+  for (int i = 0; i < N; ++i) key[i] = route_key(s[i]);
+  if (a.E != 32 * N) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) key[i] = expert(i) < a.E ? key[i] : 0u;
+  }
 
   // ---- groups ----
   if (a.groups > 1) {
@@ -139,35 +167,35 @@ static __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Ro
       const int from = lane * size;                    // group `lane`'s first expert
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        float t1 = -INFINITY, t2 = -INFINITY;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float x = key[V * c + v] > 1u ? s[V * c + v] : -INFINITY;
-          route_merge2(t1, t2, x, -INFINITY);
-        }
+        const uint32_t* x = key + V * c;
+        uint32_t t1 = max(x[0], x[1 % V]), t2 = min(x[0], x[1 % V]);
+        route_merge2(t1, t2, max(x[2 % V], x[3 % V]), min(x[2 % V], x[3 % V]));
         for (int o = 1; o < per; o <<= 1) {
-          const float o1 = __shfl_xor_sync(0xffffffffu, t1, o);
-          const float o2 = __shfl_xor_sync(0xffffffffu, t2, o);
+          const uint32_t o1 = __shfl_xor_sync(0xffffffffu, t1, o);
+          const uint32_t o2 = __shfl_xor_sync(0xffffffffu, t2, o);
           route_merge2(t1, t2, o1, o2);
         }
-        const float g = __shfl_sync(0xffffffffu, two ? t1 + t2 : t1, (from >> 2) & 31);
+        const float f1 = route_score(t1);
+        const float g =
+            __shfl_sync(0xffffffffu, two ? f1 + route_score(t2) : f1, (from >> 2) & 31);
         if (lane < a.groups && (from >> 7) == c) score = g;
       }
     } else {
-      extern __shared__ float route_smem[];
-      float* sel = route_smem + warp * N * 32;
+      extern __shared__ uint32_t route_smem[];
+      uint32_t* sel = route_smem + warp * N * 32;
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        if (expert(i) < a.E) sel[expert(i)] = key[i] > 1u ? s[i] : -INFINITY;
+        if (expert(i) < a.E) sel[expert(i)] = key[i];
       __syncwarp();
       if (lane < a.groups) {
-        float t1 = -INFINITY, t2 = -INFINITY;
-        for (int j = 0; j < size; ++j) route_merge2(t1, t2, sel[lane * size + j], -INFINITY);
-        score = two ? t1 + t2 : t1;
+        uint32_t t1 = 0u, t2 = 0u;
+        for (int j = 0; j < size; ++j) route_merge2(t1, t2, sel[lane * size + j], 0u);
+        score = two ? route_score(t1) + route_score(t2) : route_score(t1);
       }
     }
     const uint32_t gk = lane < a.groups ? route_key(score) : 0u;
     int rank = 0;   // groups before this one
+#pragma unroll 8
     for (int g = 0; g < a.groups; ++g) {
       const uint32_t o = __shfl_sync(0xffffffffu, gk, g);
       rank += o > gk || (o == gk && g < lane);
@@ -189,41 +217,41 @@ static __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Ro
   }
 
   // ---- the k best ----
-  uint32_t b1, b2;   // the lane's best two left, and where
-  int i1, i2;
-  auto look = [&]() {
-    b1 = b2 = 0u;
-    i1 = i2 = 0;
+  uint32_t b1 = 0u, b2 = 0u;   // the lane's best two left, and which experts
+  int e1 = 0, e2 = 0;          // (less V * lane)
 #pragma unroll
-    for (int i = 0; i < N; ++i) {   // ascending experts: the first of equals stays ahead
-      if (key[i] > b1) {
-        b2 = b1;
-        i2 = i1;
-        b1 = key[i];
-        i1 = i;
-      } else if (key[i] > b2) {
-        b2 = key[i];
-        i2 = i;
-      }
-    }
-  };
-  look();
+  for (int i = 0; i < N; ++i) {   // ascending experts: the first of equals stays ahead
+    const uint32_t x = key[i];
+    const bool first = x > b1, second = x > b2;
+    const int e = 32 * V * (i / V) + i % V;
+    b2 = first ? b1 : second ? x : b2;
+    e2 = first ? e1 : second ? e : e2;
+    b1 = first ? x : b1;
+    e1 = first ? e : e1;
+  }
   int mine = 0;
+#pragma unroll 1
   for (int j = 0; j < a.k; ++j) {
     const uint32_t top = __reduce_max_sync(0xffffffffu, b1);
-    const int e1 = 32 * V * (i1 / V) + V * lane + i1 % V;
-    const int e = __reduce_min_sync(0xffffffffu, b1 == top ? e1 : 0x7FFFFFFF);
-    if (lane == j) mine = e;
-    const bool out = b1 == top && e1 == e;
-    if (out) {
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (i == i1) key[i] = 0u;
+    const int ex = e1 + V * lane;
+    const int e = __reduce_min_sync(0xffffffffu, b1 == top ? ex : 0x7FFFFFFF);
+    mine = lane == j ? e : mine;
+    if (ex == e && b1 == top) {
+      const int last = e1;
       b1 = b2;
-      i1 = i2;
+      e1 = e2;
       b2 = 0u;
+      if (b1 == 0u) {   // the best of those after the one just taken
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int n = 32 * V * (i / V) + i % V;
+          if ((key[i] < top || (key[i] == top && n > last)) && key[i] > b1) {
+            b1 = key[i];
+            e1 = n;
+          }
+        }
+      }
     }
-    if (__any_sync(0xffffffffu, out && b1 == 0u)) look();
   }
 
   // ---- weights of the selected, from their logits ----
@@ -235,7 +263,7 @@ static __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Ro
   const float sum = warp_sum(v);
   if (lane < a.k) {
     a.idx[row * a.k + lane] = mine;
-    a.w[row * a.k + lane] = a.scale * (a.renorm ? (sum == 0.f ? 0.f : v / sum) : v);
+    a.w[row * a.k + lane] = a.scale * (a.renorm ? (sum == 0.f ? 0.f : __fdividef(v, sum)) : v);
   }
 }
 

@@ -32,12 +32,12 @@ def _raw_stream(stream, device):
     return stream.cuda_stream
 
 
-def _empty(stream, shape, dtype, device):
+def _empty(stream, dtype, device, *shape):
     """A new tensor whose memory belongs to the stream the call runs on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(*shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(*shape, dtype=dtype, device=device)
 
 
 def _want(ok, name, what, t):
@@ -49,8 +49,8 @@ def _want(ok, name, what, t):
 
 def _vector(t, n, dtype, name, device):
     """A contiguous 1-D tensor of n elements (n None: any)."""
-    if (t.dtype != dtype or t.dim() != 1 or (n is not None and t.shape[0] != n)
-            or t.device != device or not t.is_contiguous()):
+    if (t.dtype != dtype or t.device != device or not t.is_contiguous()
+            or (t.dim() != 1 if n is None else t.shape != (n,))):
         _want(False, name, f"{dtype} [{'n' if n is None else n}] contiguous on {device}", t)
 
 
@@ -89,18 +89,19 @@ def kv_plan(ctx_lens, q_lens, block_table, free_list, n_free, block_size, n_slot
     n_slots = int(n_slots)
     _want(n_slots >= 0, "n_slots", "a number of slots >= 0", n_slots)
     raw = _raw_stream(stream, dev)
-    # one allocation, cut so that every part is 16-byte aligned
-    a, b = (rows + 3) // 4 * 4, (rows + 4) // 4 * 4
-    buf = _empty(stream, (8 + a + b + n_slots,), torch.int32, dev)
-    p = KVPlan(buf[8:8 + rows], buf[8 + a:9 + a + rows], buf[8 + a + b:], buf[:1], buf[4:5])
+    # one allocation, cut in one operation
+    buf = _empty(stream, torch.int32, dev, n_slots + 2 * rows + 3)
+    slots, lens, start, left, unserved = buf.split_with_sizes([n_slots, rows, rows + 1, 1, 1])
     at = buf.data_ptr()
+    at_lens = at + 4 * n_slots
+    at_left = at_lens + 8 * rows + 4
     rc = lib().moe_kv_plan(raw, ctx_lens.data_ptr(), q_lens.data_ptr(), rows,
                            block_table.data_ptr(), stride, block_table.shape[1],
                            free_list.data_ptr(), free_list.shape[0], n_free.data_ptr(),
-                           int(block_size), at + 32, at + 32 + 4 * a, at + 32 + 4 * (a + b),
-                           n_slots, at, at + 16)
+                           int(block_size), at_lens, at_lens + 4 * rows, at, n_slots, at_left,
+                           at_left + 4)
     check(rc, "moe_kv_plan")
-    return p
+    return KVPlan(lens, start, slots, left, unserved)
 
 
 def kv_release(finished, seq_lens, block_table, free_list, n_free, block_size, stream=None):
@@ -204,12 +205,12 @@ class KVCache:
         table_stride = _table(block_table, rows, dev)
         raw = _raw_stream(stream, dev)
         if out is None:
-            out = _empty(stream, q.shape, q.dtype, dev)
+            out = _empty(stream, q.dtype, dev, tokens, heads, d)
         elif (out.shape != q.shape or out.dtype != q.dtype or out.device != dev
                 or out.stride(2) != 1):
             _want(False, "out", "the shape and type of q, last dimension contiguous", out)
-        lse = _empty(stream, (tokens, heads), torch.float32, dev) if return_lse else None
-        ws = _empty(stream, (self._workspace,), torch.uint8, dev)
+        lse = _empty(stream, torch.float32, dev, tokens, heads) if return_lse else None
+        ws = _empty(stream, torch.uint8, dev, self._workspace)
         qs, os = q.stride(), out.stride()
         args = KV_ATTENTION.pack(
             q.data_ptr(), qs[0], qs[1], out.data_ptr(), os[0], os[1],
@@ -240,12 +241,12 @@ def moe_route(logits, top_k, bias=None, scoring="sigmoid", n_groups=1, topk_grou
     shape = (rows, top_k)
     if idx is None:
         _want(top_k >= 1, "top_k", "at least 1", top_k)
-        idx = _empty(stream, shape, torch.int32, dev)
+        idx = _empty(stream, torch.int32, dev, rows, top_k)
     elif (idx.dtype != torch.int32 or tuple(idx.shape) != shape or idx.device != dev
             or not idx.is_contiguous()):
         _want(False, "idx", f"torch.int32 {shape} contiguous on {dev}", idx)
     if w is None:
-        w = _empty(stream, shape, torch.float32, dev)
+        w = _empty(stream, torch.float32, dev, rows, top_k)
     elif (w.dtype != torch.float32 or tuple(w.shape) != shape or w.device != dev
             or not w.is_contiguous()):
         _want(False, "w", f"torch.float32 {shape} contiguous on {dev}", w)
