@@ -115,8 +115,8 @@ int launch_decode(AttnArgs a, int n_sm, int max_q, cudaStream_t st) {
   long long span = (long long)a.max_blocks << a.c.bs_log2;
   if (a.window > 0) span = std::min(span, (long long)a.window + max_q + 32);
   const long long tiles = std::max(1ll, ((long long)max_q * a.group + Sh::ROWS - 1) / Sh::ROWS);
-  const double strips = (double)a.rows * a.c.heads * tiles * (double)((span + 31) / 32);
-  const int grid = (int)std::min((double)n_sm, strips / Sh::WARPS + 1);
+  const double all = (double)a.rows * a.c.heads * tiles;
+  const int grid = (int)std::min((double)n_sm, all * (double)((span + 31) / 32) / Sh::WARPS + all + 1);
   if ((e = cudaMemsetAsync(a.arrived, 0, (size_t)grid * 16, st)) != cudaSuccess)
     return cuda_fail(e);
   kv_attention_decode<D, NT><<<grid, Sh::THREADS, Sh::SMEM, st>>>(a);

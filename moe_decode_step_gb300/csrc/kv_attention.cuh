@@ -194,56 +194,107 @@ __device__ __forceinline__ void dec_next_tile(const AttnArgs& a, DecCursor& c) {
   } while (c.x.M == 0);
 }
 
-// This CTA's strips [u0, u0 + n) and its cursor at u0; every thread calls.
-// Also `per`.  The sums over the rows are made by every CTA for itself.
-template <int TILE, int WARPS>
-__device__ __forceinline__ void dec_schedule(const AttnArgs& a, long long& u0, long long& n,
-                                             long long& per, DecCursor& cur) {
+// Exclusive prefix over the CTA's threads, and the total; every thread calls.
+template <int WARPS>
+__device__ __forceinline__ long long dec_scan(long long v, long long& total) {
   __shared__ long long s_sum[WARPS];
-  __shared__ long long s_left;
-  __shared__ int s_row;
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int chunk = (a.rows + (32 * WARPS) - 1) / (32 * WARPS);
-  const int r0 = min(a.rows, t * chunk), r1 = min(a.rows, r0 + chunk);
-  long long sum = 0;
-  for (int r = r0; r < r1; ++r) sum += dec_units(a, dec_row<TILE>(a, r));
-  long long inc = sum;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long inc = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += v;
+    const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
   }
+  __syncthreads();
   if (lane == 31) s_sum[warp] = inc;
   __syncthreads();
-  long long total = 0, base = 0;
+  long long base = 0;
+  total = 0;
 #pragma unroll
   for (int w = 0; w < WARPS; ++w) {
     if (w == warp) base = total;
     total += s_sum[w];
   }
-  per = max((total + gridDim.x - 1) / gridDim.x, (long long)WARPS);
-  u0 = per * blockIdx.x;
-  n = min(per, total - u0);
-  long long before = base + inc - sum;
-  if (n > 0 && u0 >= before && u0 < before + sum) {
+  return base + inc - v;
+}
+
+// A CTA's share: n strips from the cursor on, u0 the first in the order of all.
+// Either `per` strips a CTA throughout, or (per 0) the CTAs c0 .. c0 + ctas - 1
+// share the one tile that this CTA works on.
+struct DecShare {
+  long long u0, n, per;
+  int c0, ctas;
+  DecCursor cur;
+};
+
+// Strips a CTA may have more when its share is of one tile: a tile cut by a
+// CTA's end costs that CTA a second tile's joins, some 5 us.  Two tiles of 8,192
+// strips: 57 us so, 70 us by equal shares; 64 tiles of 128 strips want equal
+// shares (54 strips against 94).
+constexpr int kDecSlack = 16;
+
+// Every thread calls.  The sums over the rows are made by every CTA for itself.
+template <int TILE, int WARPS>
+__device__ __forceinline__ void dec_schedule(const AttnArgs& a, DecShare& sh) {
+  __shared__ long long s_left;
+  __shared__ int s_row;
+  const int t = threadIdx.x;
+  const int chunk = (a.rows + (32 * WARPS) - 1) / (32 * WARPS);
+  const int r0 = min(a.rows, t * chunk), r1 = min(a.rows, r0 + chunk);
+  long long sum = 0, tiles = 0, total, n_tiles;
+  for (int r = r0; r < r1; ++r) {
+    const DecRow x = dec_row<TILE>(a, r);
+    sum += dec_units(a, x);
+    tiles += (long long)a.c.heads * x.M;
+  }
+  long long before = dec_scan<WARPS>(sum, total);
+  dec_scan<WARPS>(tiles, n_tiles);
+  const long long even = max((total + gridDim.x - 1) / gridDim.x, (long long)WARPS);
+  // the tiles' CTAs, ceil(S / most) each, are at most total / most + n_tiles
+  const long long spare = (long long)gridDim.x - n_tiles;
+  const long long most = spare > 0 ? max((total + spare - 1) / spare, (long long)WARPS) : 0;
+  const bool apart = spare > 0 && most <= even + kDecSlack;
+  long long at = even * blockIdx.x;   // in strips, or in CTAs
+  if (apart) {
+    sum = 0;
+    for (int r = r0; r < r1; ++r) {
+      const DecRow x = dec_row<TILE>(a, r);
+      sum += (long long)a.c.heads * x.M * ((x.S + most - 1) / most);
+    }
+    before = dec_scan<WARPS>(sum, total);
+    at = blockIdx.x;
+  }
+  sh.per = apart ? 0 : even;
+  sh.u0 = apart ? 0 : at;
+  sh.n = apart ? (at < total ? 1 : 0) : min(even, total - at);
+  if (at >= before && at < before + sum) {
     int r = r0;
     for (;; ++r) {
-      const long long k = dec_units(a, dec_row<TILE>(a, r));
-      if (u0 < before + k) break;
+      const DecRow x = dec_row<TILE>(a, r);
+      const long long k =
+          apart ? (long long)a.c.heads * x.M * ((x.S + most - 1) / most) : dec_units(a, x);
+      if (at < before + k) break;
       before += k;
     }
     s_row = r;
-    s_left = u0 - before;
+    s_left = at - before;
   }
   __syncthreads();
-  if (n <= 0) return;
+  if (sh.n <= 0) return;
+  DecCursor& cur = sh.cur;
   cur.r = s_row;
   cur.x = dec_row<TILE>(a, cur.r);
-  const long long left = s_left;
-  cur.s = (int)(left % cur.x.S);
-  const int hm = (int)(left / cur.x.S);
+  const int S = cur.x.S, parts = apart ? (int)((S + most - 1) / most) : S;
+  const int hm = (int)(s_left / parts), part = (int)(s_left - (long long)hm * parts);
   cur.m = hm % cur.x.M;
   cur.h = hm / cur.x.M;
+  cur.s = part;
+  if (apart) {
+    cur.s = (int)((long long)S * part / parts);
+    sh.n = (long long)S * (part + 1) / parts - cur.s;
+    sh.c0 = blockIdx.x - part;
+    sh.ctas = parts;
+  }
 }
 
 // What one warp loads ahead.  Block ids and scales are two dependent misses to
@@ -448,128 +499,194 @@ struct DecOut {
 };
 
 // Rows `item`, item + step, ... of `jobs` jobs, the first rows of all of them
-// first; a warp a row, V columns a lane.  Small and not inlined: the code runs
-// a few times per launch, mostly fetched cold, and everything it reads but the
-// pieces is in shared memory.  What other CTAs wrote is read at L2, eight
-// pieces at once and without branches between: a round trip is 0.7 us.
+// first; R rows a warp at once, V columns a lane.  Small and not inlined: the
+// code runs a few times per launch, mostly fetched cold, and everything it
+// reads but the pieces is in shared memory.  What other CTAs wrote is read at
+// L2, B pieces of R rows at once and without branches between: a round trip is
+// 0.7 us, and what follows it as long again.
 // (ORDERED: the pieces' columns are the dims themselves.)
 template <int D, int ROWS, bool ORDERED = false>
 __device__ __noinline__ void dec_join(const DecOut* to, const DecJob* job, int jobs, int item,
                                       int step) {
-  constexpr int V = D / 32, B = 8;
+  constexpr int V = D / 32, R = ROWS > 8 ? 2 : 1, B = 16 / R;
   const int lane = threadIdx.x & 31;
 #pragma unroll 1
-  for (; item < jobs * ROWS; item += step) {
-    const DecJob& b = job[item % jobs];
-    const int row = item / jobs;
-    const unsigned rho = (unsigned)b.m * ROWS + row;   // as in dec_tile_row
-    const int i = (int)(rho / to->group);
-    if (i >= b.n) continue;
-    const unsigned mask = b.mask;
-    const float* ring = b.ring;
-    const int col = V * lane, sh = ring ? 1 : 0;       // workspace piece k has mask bit k << sh
-    float mk = -INFINITY, lk = 0.f;
-    if ((mask >> lane) & 1u) {
-      if (ring && (lane & 1)) {
-        const float* ml = ring + (lane >> 1) * b.ring_stride + ROWS * D + row;
-        mk = ml[0];
-        lk = ml[ROWS];
-      } else {
-        const float* ml = b.base + (lane >> sh) * b.stride + (lane == 0 ? b.extra : 0) +
-                          ROWS * D + row;
-        mk = __ldcg(ml);
-        lk = __ldcg(ml + ROWS);
+  for (; item < jobs * ROWS; item += step * R) {
+    const DecJob* b[R];
+    int row[R], i[R], head[R], k1[R];
+    unsigned far[R];
+    bool real[R];
+    float mk[R], lk[R];
+    int last = 0;
+#pragma unroll
+    for (int x = 0; x < R; ++x) {
+      const int it = min(item + x * step, jobs * ROWS - 1);
+      b[x] = job + it % jobs;
+      row[x] = it / jobs;
+      const unsigned rho = (unsigned)b[x]->m * ROWS + row[x];   // as in dec_tile_row
+      i[x] = (int)(rho / to->group);
+      head[x] = b[x]->h * (int)to->group + (int)(rho - (unsigned)i[x] * to->group);
+      real[x] = item + x * step < jobs * ROWS && i[x] < b[x]->n;
+      const float* ring = b[x]->ring;
+      const int sh = ring ? 1 : 0;       // workspace piece k has mask bit k << sh
+      mk[x] = -INFINITY;
+      lk[x] = 0.f;
+      const unsigned mask = real[x] ? b[x]->mask : 0u;
+      if ((mask >> lane) & 1u) {
+        if (ring && (lane & 1)) {
+          const float* ml = ring + (lane >> 1) * b[x]->ring_stride + ROWS * D + row[x];
+          mk[x] = ml[0];
+          lk[x] = ml[ROWS];
+        } else {
+          const float* ml = b[x]->base + (lane >> sh) * b[x]->stride +
+                            (lane == 0 ? b[x]->extra : 0) + ROWS * D + row[x];
+          mk[x] = __ldcg(ml);
+          lk[x] = __ldcg(ml + ROWS);
+        }
       }
+      far[x] = ring ? mask & 0x55555555u : mask;   // pieces in the workspace
+      k1[x] = far[x] ? (31 - __clz(far[x])) >> sh : -1;
+      last = max(last, k1[x]);
     }
-    float acc[V];
+    bool any = false;
 #pragma unroll
-    for (int n = 0; n < V; ++n) acc[n] = 0.f;
-    float tm = 0.f, f = 0.f, tl = 0.f;
-    const unsigned far = ring ? mask & 0x55555555u : mask;   // pieces in the workspace
-    const int k0 = far ? (__ffs(far) - 1) >> sh : 0, k1 = far ? (31 - __clz(far)) >> sh : -1;
-    bool first = true;
+    for (int x = 0; x < R; ++x) any |= real[x];
+    if (!any) continue;
+    float acc[R][V], tm[R], f[R], tl[R];
 #pragma unroll 1
-    for (int k = k0; first || k <= k1; k += B) {
-      float2 v[B][V / 2];
-      if (k <= k1) {
+    for (int k = 0; k <= last; k += B) {
+      float2 v[R][B][V / 2];
 #pragma unroll
-        for (int u = 0; u < B; ++u) {   // past the last one: the last again, weight 0
-          const int p = min(k + u, k1);
-          const float* src = b.base + p * b.stride + (p == 0 ? b.extra : 0) + row * D + col;
+      for (int x = 0; x < R; ++x)
+#pragma unroll
+        for (int u = 0; u < B; ++u) {   // what is not there has weight 0
+          const int sh = b[x]->ring ? 1 : 0;
+          const bool in = (far[x] >> ((k + u) << sh)) & 1u;
+          const float* src = b[x]->base + (k + u) * b[x]->stride +
+                             (k + u == 0 ? b[x]->extra : 0) + row[x] * D + V * lane;
 #pragma unroll
           for (int n = 0; n < V / 2; ++n)
-            v[u][n] = __ldcg(reinterpret_cast<const float2*>(src + 2 * n));
+            v[x][u][n] = in ? __ldcg(reinterpret_cast<const float2*>(src + 2 * n))
+                            : make_float2(0.f, 0.f);
         }
-      }
-      if (first) {
-        first = false;
-        tm = warp_max(mk);
-        f = (mask >> lane) & 1u ? attn_factor(mk, tm) : 0.f;
-        tl = warp_sum(lk * f);
-        if (ring) {
-#pragma unroll 4
-          for (int p = 0; p < 16; ++p) {
-            if (!((mask >> (2 * p + 1)) & 1u)) continue;
-            const float fk = __shfl_sync(0xffffffffu, f, 2 * p + 1);
-            const float* src = ring + p * b.ring_stride + row * D + col;
+      if (k == 0) {
 #pragma unroll
-            for (int n = 0; n < V; ++n) acc[n] = fmaf(src[n], fk, acc[n]);
+        for (int x = 0; x < R; ++x) tm[x] = warp_max(mk[x]);
+#pragma unroll
+        for (int x = 0; x < R; ++x) {
+          f[x] = mk[x] == -INFINITY && lk[x] == 0.f ? 0.f : attn_factor(mk[x], tm[x]);
+          tl[x] = warp_sum(lk[x] * f[x]);
+#pragma unroll
+          for (int n = 0; n < V; ++n) acc[x][n] = 0.f;
+          if (b[x]->ring) {
+#pragma unroll 4
+            for (int p = 0; p < 16; ++p) {
+              const float fk = __shfl_sync(0xffffffffu, f[x], 2 * p + 1);
+              if (!((b[x]->mask >> (2 * p + 1)) & 1u)) continue;
+              const float* src = b[x]->ring + p * b[x]->ring_stride + row[x] * D + V * lane;
+#pragma unroll
+              for (int n = 0; n < V; ++n) acc[x][n] = fmaf(src[n], fk, acc[x][n]);
+            }
           }
         }
       }
-      if (k <= k1) {
+#pragma unroll
+      for (int x = 0; x < R; ++x)
 #pragma unroll
         for (int u = 0; u < B; ++u) {
-          const int bit = (k + u) << sh;
-          const bool in = k + u <= k1 && ((far >> bit) & 1u);
-          const float fk = __shfl_sync(0xffffffffu, f, bit & 31);
+          const float fk = __shfl_sync(0xffffffffu, f[x], ((k + u) << (b[x]->ring ? 1 : 0)) & 31);
 #pragma unroll
-          for (int n = 0; n < V / 2; ++n) {   // (a slot not written may hold anything)
-            acc[2 * n] = fmaf(in ? v[u][n].x : 0.f, in ? fk : 0.f, acc[2 * n]);
-            acc[2 * n + 1] = fmaf(in ? v[u][n].y : 0.f, in ? fk : 0.f, acc[2 * n + 1]);
+          for (int n = 0; n < V / 2; ++n) {
+            acc[x][2 * n] = fmaf(v[x][u][n].x, fk, acc[x][2 * n]);
+            acc[x][2 * n + 1] = fmaf(v[x][u][n].y, fk, acc[x][2 * n + 1]);
           }
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < R; ++x) {
+      if (!real[x]) continue;
+      if (!b[x]->dst) {
+        const float inv = attn_inverse(tl[x]);
+        const long long tok = b[x]->tok + i[x];
+        uint16_t* out = to->out + tok * to->o_ts + head[x] * to->o_hs;
+#pragma unroll
+        for (int n = 0; n < V; n += 2)
+          *reinterpret_cast<uint32_t*>(
+              out + (ORDERED ? V * lane + n : dec_dim<D>(V * lane + n))) =
+              pack16(acc[x][n] * inv, acc[x][n + 1] * inv, to->f16);
+        if (lane == 0 && to->lse) to->lse[tok * to->heads + head[x]] = attn_lse(tm[x], tl[x]);
+      } else {
+        float* dst = b[x]->dst;
+#pragma unroll
+        for (int n = 0; n < V; n += 2)
+          *reinterpret_cast<float2*>(dst + row[x] * D + V * lane + n) =
+              make_float2(acc[x][n], acc[x][n + 1]);
+        if (lane == 0) {
+          dst[ROWS * D + row[x]] = tm[x];
+          dst[ROWS * D + ROWS + row[x]] = tl[x];
         }
       }
     }
-    if (!b.dst) {
-      const float inv = attn_inverse(tl);
-      const long long tok = b.tok + i;
-      const int head = b.h * (int)to->group + (int)(rho - (unsigned)i * to->group);
-      uint16_t* out = to->out + tok * to->o_ts + head * to->o_hs;
-#pragma unroll
-      for (int n = 0; n < V; n += 2)
-        *reinterpret_cast<uint32_t*>(out + (ORDERED ? col + n : dec_dim<D>(col + n))) =
-            pack16(acc[n] * inv, acc[n + 1] * inv, to->f16);
-      if (lane == 0 && to->lse) to->lse[tok * to->heads + head] = attn_lse(tm, tl);
-    } else {
-      float* dst = b.dst;
-#pragma unroll
-      for (int n = 0; n < V; n += 2)
-        *reinterpret_cast<float2*>(dst + row * D + col + n) = make_float2(acc[n], acc[n + 1]);
-      if (lane == 0) {
-        dst[ROWS * D + row] = tm;
-        dst[ROWS * D + ROWS + row] = tl;
-      }
-    }
   }
 }
 
-// The CTA's sums of a tile are in its slot: count them, and tell whether the
-// `n`-th has come.  Every thread calls.
-__device__ __forceinline__ bool dec_arrive(unsigned* counter, unsigned n) {
-  __shared__ unsigned s_old;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    s_old = atomicAdd(counter, 1u);
-    __threadfence();
-  }
-  __syncthreads();
-  return s_old == n - 1;
-}
-
-constexpr int kDecGroup = 32;                          // CTAs joined at once
+constexpr int kDecGroup = 16;                          // CTAs joined at once
 constexpr int kDecMaxCtas = kDecGroup * kDecGroup;     // in two levels
+
+// The sums of tiles that the CTA's own ends cut are in its slots (p0: of a
+// tile begun before, p1: of one that it begins; null: none), at `base` + the
+// CTA * STRIDE (+ SLOT for the CTA that begins the tile): count them, and
+// whoever comes last joins.  Level 0: the CTAs of one group; level 1: the
+// groups, each in its first CTA's slot.  Both tiles are counted before either
+// is joined: others may wait for this CTA's sums.  Every thread calls.
+template <int D, int ROWS, int WARPS, int STRIDE, int SLOT, bool ORDERED>
+__device__ __forceinline__ void dec_join_ctas(const AttnArgs& a, float* base,
+                                              const DecShare& share, const DecPiece* p0,
+                                              const DecPiece* p1, const DecOut* to, DecJob* job) {
+  __shared__ int s_jobs;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const DecPiece* p = lane == 0 ? p0 : p1;
+  bool open = lane < 2 && p;
+  int c0 = share.c0, n = share.ctas;
+  if (warp == 0 && open && share.per) {
+    const long long tile = share.u0 + p->at;
+    c0 = (int)(tile / share.per);
+    n = (int)((tile + p->S - 1) / share.per) - c0 + 1;
+  }
+#pragma unroll 1
+  for (int level = 0; level < 2; ++level) {
+    __syncthreads();
+    if (warp == 0) {
+      const int groups = (n + kDecGroup - 1) / kDecGroup;
+      const int grp = level ? 0 : ((int)blockIdx.x - c0) / kDecGroup;
+      const int count = level ? groups : min(kDecGroup, n - grp * kDecGroup);
+      bool won = false;
+      if (open) {
+        // counters of CTA c: the tile it begins, that tile's first group, and
+        // the later group of a tile begun before that starts with c
+        unsigned* counter = a.arrived + 4 * (c0 + grp * kDecGroup) + (level ? 0 : grp ? 2 : 1);
+        __threadfence();
+        won = atomicAdd(counter, 1u) == (unsigned)count - 1;
+        __threadfence();
+      }
+      const unsigned m = __ballot_sync(0xffffffffu, won);
+      if (won) {
+        float* from = base + (long long)(c0 + grp * kDecGroup) * STRIDE;
+        const int extra = grp > 0 ? 0 : SLOT;
+        const bool final = level == 1 || groups == 1;
+        job[__popc(m & ((1u << lane) - 1))] = {
+            from, final ? nullptr : from + extra, nullptr,
+            (long long)(level ? kDecGroup : 1) * STRIDE, extra, 0, ~0u >> (32 - count),
+            p->h, p->m, p->tok, p->n};
+      }
+      open = won && groups > 1;
+      if (lane == 0) s_jobs = __popc(m);
+    }
+    __syncthreads();
+    if (s_jobs == 0) return;
+    dec_join<D, ROWS, ORDERED>(to, job, s_jobs, warp, WARPS);
+  }
+}
 
 template <int D, int NT>
 static __global__ void __launch_bounds__(DecShape<D, NT>::THREADS, 1)
@@ -585,10 +702,11 @@ static __global__ void __launch_bounds__(DecShape<D, NT>::THREADS, 1)
   uint8_t* ringp = dec_smem + warp * Sh::RING;
   float* slots = a.partial + (long long)blockIdx.x * Sh::SLOTS * Sh::SLOT;
 
-  long long u0, n_units, per;
-  DecCursor cur;
-  dec_schedule<ROWS, W>(a, u0, n_units, per, cur);
+  DecShare share;
+  dec_schedule<ROWS, W>(a, share);
+  const long long n_units = share.n;
   if (n_units <= 0) return;
+  DecCursor& cur = share.cur;
   if (threadIdx.x < 2 * W) s_piece[threadIdx.x].state = 0;
   if (threadIdx.x == 0)
     s_out = {a.out, a.lse, a.o_ts, a.o_hs, a.heads, a.f16, (unsigned)a.group};
@@ -890,7 +1008,6 @@ static __global__ void __launch_bounds__(DecShape<D, NT>::THREADS, 1)
       }
 
       // ---- the tile's end, or the run's: then the ring is free ----
-      const long long at = first + done - nseg - cur.s;
       const bool begins = cur.s == 0, ends = cur.s + nseg == cur.x.S, last = done == n_warp;
       if (last) {
         cp_async_wait<0>();
@@ -932,7 +1049,8 @@ static __global__ void __launch_bounds__(DecShape<D, NT>::THREADS, 1)
         }
       if (!(begins && ends) && lane == 0)
         s_piece[2 * warp + last] = {1 | (begins ? 2 : 0) | (ends ? 4 : 0), cur.h, cur.m,
-                                    cur.x.w.tok, cur.x.w.n, cur.x.S, at};
+                                    cur.x.w.tok, cur.x.w.n, cur.x.S,
+                                    first + done - nseg - cur.s};
       if (!last) dec_next_tile<ROWS>(a, cur);
     }
   }
@@ -966,42 +1084,9 @@ static __global__ void __launch_bounds__(DecShape<D, NT>::THREADS, 1)
   __syncthreads();
   dec_join<D, ROWS>(&s_out, s_job, jobs, warp, W);
 
-  // ---- and the CTAs' sums ----
-#pragma unroll 1
-  for (int o = 0; o < 2; ++o) {
-    const int first_piece = s_open[o];
-    if (first_piece < 0) continue;
-    const DecPiece& p = s_piece[first_piece];
-    const long long tile = u0 + p.at;
-    const int c0 = (int)(tile / per), n = (int)((tile + p.S - 1) / per) - c0 + 1;
-    const int grp = ((int)blockIdx.x - c0) / kDecGroup;
-    const int in_grp = min(kDecGroup, n - grp * kDecGroup);
-    // counters of CTA c: the tile it begins, that tile's first group, and the
-    // later group of a tile begun before that starts with c
-    unsigned* counters[2] = {a.arrived + 4 * (c0 + grp * kDecGroup) + (grp ? 2 : 1),
-                             a.arrived + 4 * c0};
-    // CTA c0's slot is its second, the others' their first
-    constexpr long long stride = (long long)Sh::SLOTS * Sh::SLOT;
-    float* base = a.partial + c0 * stride + W * Sh::SLOT;
-#pragma unroll 1
-    for (int level = 0; level < 2; ++level) {
-      // 0: the CTAs of one group; 1: the groups, each in its first CTA's slot
-      const int groups = (n + kDecGroup - 1) / kDecGroup;
-      if (!dec_arrive(level ? counters[1] : counters[0], level ? groups : in_grp)) break;
-      if (threadIdx.x == 0) {
-        float* from = base + (level ? 0 : grp * kDecGroup * stride);
-        const long long extra = level == 0 && grp > 0 ? 0 : Sh::SLOT;
-        const bool final = level == 1 || groups == 1;
-        const int count = level ? groups : in_grp;
-        s_job[0] = {from, final ? nullptr : from + extra, nullptr,
-                    level ? kDecGroup * stride : stride, extra, 0, ~0u >> (32 - count), p.h, p.m,
-                    p.tok, p.n};
-      }
-      __syncthreads();
-      dec_join<D, ROWS>(&s_out, s_job, 1, warp, W);
-      if (groups == 1) break;
-    }
-  }
+  dec_join_ctas<D, ROWS, W, Sh::SLOTS * Sh::SLOT, Sh::SLOT, false>(
+      a, a.partial + W * Sh::SLOT, share, s_open[0] < 0 ? nullptr : s_piece + s_open[0],
+      s_open[1] < 0 ? nullptr : s_piece + s_open[1], &s_out, s_job);
 }
 
 }  // namespace moe

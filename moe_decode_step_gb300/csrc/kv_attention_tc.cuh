@@ -318,7 +318,7 @@ struct PrShared {
   float m1[128], l1[128];   // the second stream's, when the two are joined
   unsigned nan1[4][128];
   DecOut out;
-  DecJob job;
+  DecJob job[2];
 };
 
 // Waits for a phase, two seconds at most; then marks the CTA dead, whose waits
@@ -929,37 +929,10 @@ static __global__ void __launch_bounds__(kPrThreads, 1) kv_attention_tc(const At
     tmem_dealloc(sh.tmem);
   }
 
-  // ---- items that the CTA's ends cut: joined by the last CTA to arrive ----
-#pragma unroll 1
-  for (int o = 0; o < 2; ++o) {
-    if (!sh.open[o]) continue;
-    const DecPiece& p = sh.piece[o];
-    const long long tile = u0 + p.at;
-    const int c0 = (int)(tile / per), n = (int)((tile + p.S - 1) / per) - c0 + 1;
-    const int grp = ((int)blockIdx.x - c0) / kDecGroup;
-    const int in_grp = min(kDecGroup, n - grp * kDecGroup);
-    unsigned* counters[2] = {a.arrived + 4 * (c0 + grp * kDecGroup) + (grp ? 2 : 1),
-                             a.arrived + 4 * c0};
-    constexpr long long stride = 2ll * S::SLOT;
-    float* base = a.partial + c0 * stride;
-#pragma unroll 1
-    for (int level = 0; level < 2; ++level) {
-      const int groups = (n + kDecGroup - 1) / kDecGroup;
-      if (!dec_arrive(level ? counters[1] : counters[0], level ? groups : in_grp)) break;
-      if (threadIdx.x == 0) {
-        float* from = base + (level ? 0 : grp * kDecGroup * stride);
-        const long long extra = level == 0 && grp > 0 ? 0 : S::SLOT;
-        const bool final = level == 1 || groups == 1;
-        const int count = level ? groups : in_grp;
-        sh.job = {from, final ? nullptr : from + extra, nullptr,
-                  level ? kDecGroup * stride : stride, extra, 0, ~0u >> (32 - count), p.h, p.m,
-                  p.tok, p.n};
-      }
-      __syncthreads();
-      dec_join<D, S::TILE, true>(&sh.out, &sh.job, 1, warp, kPrWarps);
-      if (groups == 1) break;
-    }
-  }
+  // ---- items that the CTA's ends cut ----
+  dec_join_ctas<D, S::TILE, kPrWarps, 2 * S::SLOT, S::SLOT, true>(
+      a, a.partial, {u0, n_units, per, 0, 0, {}}, sh.open[0] ? &sh.piece[0] : nullptr,
+      sh.open[1] ? &sh.piece[1] : nullptr, &sh.out, sh.job);
 }
 
 }  // namespace moe
