@@ -219,33 +219,38 @@ __device__ __forceinline__ long long dec_scan(long long v, long long& total) {
 }
 
 // A CTA's share: n strips from the cursor on, u0 the first in the order of all.
-// Either `per` strips a CTA throughout, or (per 0) the CTAs c0 .. c0 + ctas - 1
-// share the one tile that this CTA works on.
+// Either `per` strips a CTA before cuts are moved, or (per 0) the CTAs c0 ..
+// c0 + ctas - 1 share the one tile that this CTA works on.
 struct DecShare {
   long long u0, n, per;
   int c0, ctas;
   DecCursor cur;
 };
 
-// Strips a CTA may have more when its share is of one tile: a tile cut by a
-// CTA's end costs that CTA a second tile's joins, some 5 us.  Two tiles of 8,192
-// strips: 57 us so, 70 us by equal shares; 64 tiles of 128 strips want equal
-// shares (54 strips against 94).
-constexpr int kDecSlack = 16;
+// Equal shares cut tiles anywhere, and a tile cut by a CTA's end costs that CTA
+// a second tile's joins, some 5 us.  So few tiles are split each on its own, if
+// no CTA then has more than kDecSlack strips over the equal share, and many
+// tiles of no more strips than that stay whole, if the equal share is four
+// times as much.  Against equal shares: 2 tiles of 8,192 strips 57 us (70), 64
+// of 128 strips 37.5 (39.6), 64 of 47 strips 27.3 (31.4), 1,024 of 33 strips
+// 45.7 (47.7).
+constexpr int kDecSlack = 40;
 
 // Every thread calls.  The sums over the rows are made by every CTA for itself.
 template <int TILE, int WARPS>
 __device__ __forceinline__ void dec_schedule(const AttnArgs& a, DecShare& sh) {
-  __shared__ long long s_left;
+  __shared__ long long s_left, s_cut[2];
   __shared__ int s_row;
   const int t = threadIdx.x;
   const int chunk = (a.rows + (32 * WARPS) - 1) / (32 * WARPS);
   const int r0 = min(a.rows, t * chunk), r1 = min(a.rows, r0 + chunk);
   long long sum = 0, tiles = 0, total, n_tiles;
+  bool large = false;
   for (int r = r0; r < r1; ++r) {
     const DecRow x = dec_row<TILE>(a, r);
     sum += dec_units(a, x);
     tiles += (long long)a.c.heads * x.M;
+    large |= x.S > kDecSlack;
   }
   long long before = dec_scan<WARPS>(sum, total);
   dec_scan<WARPS>(tiles, n_tiles);
@@ -255,7 +260,30 @@ __device__ __forceinline__ void dec_schedule(const AttnArgs& a, DecShare& sh) {
   const long long most = spare > 0 ? max((total + spare - 1) / spare, (long long)WARPS) : 0;
   const bool apart = spare > 0 && most <= even + kDecSlack;
   long long at = even * blockIdx.x;   // in strips, or in CTAs
-  if (apart) {
+  long long n = min(even, total - at);
+  if (!apart && !__syncthreads_or(large) && even >= 4 * kDecSlack) {
+    // whole tiles: those that begin in the CTA's equal share
+    if (t < 2) s_cut[t] = total;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const long long x = at + k * even;
+      long long y = before;
+      if (x >= total || x < before || x >= before + sum) continue;
+      for (int r = r0;; ++r) {
+        const DecRow w = dec_row<TILE>(a, r);
+        const long long units = dec_units(a, w);
+        if (x < y + units) {
+          s_cut[k] = y + (x - y + w.S - 1) / w.S * w.S;
+          break;
+        }
+        y += units;
+      }
+    }
+    __syncthreads();
+    at = s_cut[0];
+    n = s_cut[1] - at;
+  } else if (apart) {
     sum = 0;
     for (int r = r0; r < r1; ++r) {
       const DecRow x = dec_row<TILE>(a, r);
@@ -266,8 +294,8 @@ __device__ __forceinline__ void dec_schedule(const AttnArgs& a, DecShare& sh) {
   }
   sh.per = apart ? 0 : even;
   sh.u0 = apart ? 0 : at;
-  sh.n = apart ? (at < total ? 1 : 0) : min(even, total - at);
-  if (at >= before && at < before + sum) {
+  sh.n = apart ? (at < total ? 1 : 0) : n;
+  if (sh.n > 0 && at >= before && at < before + sum) {
     int r = r0;
     for (;; ++r) {
       const DecRow x = dec_row<TILE>(a, r);
