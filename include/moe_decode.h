@@ -419,7 +419,9 @@ int moe_kv_append(void* stream, const moe_kv_cache_t* cache, const void* k, cons
  * max_blocks * block_size and q_start as within
  * [0, n_tokens], not descending; rows of q past q_start[n_rows] are left
  * alone.  max_q, the longest row's queries as the host knows it, only picks
- * the kernel: any value gives the same result up to rounding. */
+ * the kernel: any value gives the same result up to rounding.  The tensor-core
+ * kernel's waits between its warps are bounded: one that runs out (none does on a
+ * device that works) leaves NaN in the rows it was for. */
 typedef struct {
   const void* q;            /* device [n_tokens][n_heads][head_dim] */
   int64_t q_token_stride, q_head_stride;      /* elements, multiples of 8 */
@@ -449,7 +451,8 @@ size_t moe_kv_attention_workspace(int head_dim);
 
 /* Expert routing from logits, for any number of rows.  Per row: score s_e =
  * sigmoid(l_e) or softmax(l)_e in fp32 (all of a softmax row at -infinity:
- * scores 0); experts are compared by s_e + bias_e (bias NULL: s_e).  With
+ * scores 0); experts are compared by s_e + bias_e (bias NULL: s_e), the s_e
+ * of this comparison within 3e-7 of themselves.  With
  * n_groups > 1 the experts form n_groups equal consecutive groups, a group
  * counts with the sum of its group_top (1 or 2) best, and only the experts of
  * the topk_groups best groups are left.  The top_k best are written in
