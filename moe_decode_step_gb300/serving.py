@@ -89,9 +89,10 @@ def kv_plan(ctx_lens, q_lens, block_table, free_list, n_free, block_size, n_slot
     n_slots = int(n_slots)
     _want(n_slots >= 0, "n_slots", "a number of slots >= 0", n_slots)
     raw = _raw_stream(stream, dev)
-    # one allocation, cut in one operation
+    # one allocation, cut in one operation (no gradients: the form that keeps no record)
     buf = _empty(stream, torch.int32, dev, n_slots + 2 * rows + 3)
-    slots, lens, start, left, unserved = buf.split_with_sizes([n_slots, rows, rows + 1, 1, 1])
+    slots, lens, start, left, unserved = torch.unsafe_split_with_sizes(
+        buf, [n_slots, rows, rows + 1, 1, 1])
     at = buf.data_ptr()
     at_lens = at + 4 * n_slots
     at_left = at_lens + 8 * rows + 4
