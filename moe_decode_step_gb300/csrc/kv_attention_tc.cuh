@@ -418,25 +418,39 @@ __device__ __forceinline__ void pr_convert(const AttnArgs& a, PrShared& sh, uint
   const uint32_t raw = smem_addr(smem) + S::ROFF + ct * 16;
   int in_slot = 0, out_slot = 0;
 
-  auto fetch = [&](const PrTile& t, const uint8_t* codes) {
-    const uint32_t dst = raw + in_slot * S::RAW;
-    in_slot = in_slot + 1 == S::RAWS ? 0 : in_slot + 1;
+  // where a lane's keys of a tile lie, and how many of each group of 16, from
+  // its first on, are cached: the same for keys and values
+  struct Place {
+    long long at[2];
+    int left[2];
+  };
+  auto place = [&](const PrTile& t) {
+    Place w;
     // the warp's 32 keys lie in two groups of 16, each in one block
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       const int id = __shfl_sync(0xffffffffu, t.id, 2 * warp + g);
       const int k = key + 16 * g;
-      const int left = t.there && id >= 0 && id < a.c.n_blocks ? t.seq - t.p0 - k : 0;
-      const uint8_t* src = codes;
-      if (left > 0)
-        src += (long long)id * a.c.bstride + (long long)t.h * a.c.hstride +
-               (long long)((t.p0 + k) & bs1) * a.c.tstride + chunk * 16;
-      const uint8_t* src1 = left > 8 ? src + 8 * a.c.tstride : codes;
+      w.left[g] = t.there && id >= 0 && id < a.c.n_blocks ? t.seq - t.p0 - k : 0;
+      w.at[g] = w.left[g] > 0 ? (long long)id * a.c.bstride + (long long)t.h * a.c.hstride +
+                                    (long long)((t.p0 + k) & bs1) * a.c.tstride + chunk * 16
+                              : 0;
+    }
+    return w;
+  };
+  const long long ts8 = 8 * a.c.tstride;
+  auto fetch = [&](const Place& w, const uint8_t* codes) {
+    const uint32_t dst = raw + in_slot * S::RAW;
+    in_slot = in_slot + 1 == S::RAWS ? 0 : in_slot + 1;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const uint8_t* src = codes + w.at[g];
+      const bool in = w.left[g] > 0, in1 = w.left[g] > 8;
+      const uint8_t* src1 = in1 ? src + ts8 : codes;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        cp_async<16>(dst + (2 * g * C + c) * 2048, src + (left > 0 ? 64 * c : 0), left > 0, policy);
-        cp_async<16>(dst + ((2 * g + 1) * C + c) * 2048, src1 + (left > 8 ? 64 * c : 0), left > 8,
-                     policy);
+        cp_async<16>(dst + (2 * g * C + c) * 2048, src + (in ? 64 * c : 0), in, policy);
+        cp_async<16>(dst + ((2 * g + 1) * C + c) * 2048, src1 + (in1 ? 64 * c : 0), in1, policy);
       }
     }
     cp_async_commit();
@@ -445,23 +459,30 @@ __device__ __forceinline__ void pr_convert(const AttnArgs& a, PrShared& sh, uint
     const uint8_t* from = smem + S::ROFF + out_slot * S::RAW + ct * 16;
     out_slot = out_slot + 1 == S::RAWS ? 0 : out_slot + 1;
     uint32_t any = 0;
+    uint4 w[4 * C];   // all loads first: the stores could be to what they read
+#pragma unroll
+    for (int i = 0; i < 4 * C; ++i) w[i] = *reinterpret_cast<const uint4*>(from + i * 2048);
+    if (drop) {
+#pragma unroll
+      for (int i = 0; i < 4 * C; ++i) {
+        w[i].x = drop_nan4(w[i].x, any);
+        w[i].y = drop_nan4(w[i].y, any);
+        w[i].z = drop_nan4(w[i].z, any);
+        w[i].w = drop_nan4(w[i].w, any);
+      }
+    }
+    uint8_t* d0 = to + 2 * chunk * S::GROUP + key * 16;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        uint4 w = *reinterpret_cast<const uint4*>(from + (i * C + c) * 2048);
-        if (drop) {
-          w.x = drop_nan4(w.x, any);
-          w.y = drop_nan4(w.y, any);
-          w.z = drop_nan4(w.z, any);
-          w.w = drop_nan4(w.w, any);
-        }
-        uint8_t* d = to + 2 * (chunk + 4 * c) * S::GROUP + (key + 8 * i) * 16;
+        const uint4& v = w[i * C + c];
+        uint8_t* d = d0 + 8 * c * S::GROUP + 8 * i * 16;
         uint4 x, y;
-        e4m3x4_to_f16x2(w.x, x.x, x.y);
-        e4m3x4_to_f16x2(w.y, x.z, x.w);
-        e4m3x4_to_f16x2(w.z, y.x, y.y);
-        e4m3x4_to_f16x2(w.w, y.z, y.w);
+        e4m3x4_to_f16x2(v.x, x.x, x.y);
+        e4m3x4_to_f16x2(v.y, x.z, x.w);
+        e4m3x4_to_f16x2(v.z, y.x, y.y);
+        e4m3x4_to_f16x2(v.w, y.z, y.w);
         *reinterpret_cast<uint4*>(d) = x;
         *reinterpret_cast<uint4*>(d + S::GROUP) = y;
       }
@@ -481,9 +502,11 @@ __device__ __forceinline__ void pr_convert(const AttnArgs& a, PrShared& sh, uint
   feed.take(a, t0, lane);
   feed.take(a, t1, lane);
   feed.take(a, t2, lane);
-  fetch(t0, a.c.k);
-  fetch(t0, a.c.v);
-  fetch(t1, a.c.k);
+  Place p1 = place(t0), p2;   // of the two tiles being fetched
+  fetch(p1, a.c.k);
+  fetch(p1, a.c.v);
+  p1 = place(t1);
+  fetch(p1, a.c.k);
   fetch_scales(t0);
 #pragma unroll 1
   for (int n = 0; t0.there; ++n) {
@@ -501,7 +524,8 @@ __device__ __forceinline__ void pr_convert(const AttnArgs& a, PrShared& sh, uint
     convert(smem + S::KOFF, false);
     mbar_arrive(&sh.kfull[n & 1]);
     fetch_scales(t1);
-    fetch(t1, a.c.v);
+    fetch(p1, a.c.v);
+    p2 = place(t2);
     // ---- values ----
     const int stage = n & 1;
     if (n > 1) pr_wait(&sh.vempty[stage], ((n >> 1) - 1) & 1, sh);
@@ -510,7 +534,8 @@ __device__ __forceinline__ void pr_convert(const AttnArgs& a, PrShared& sh, uint
     // codes leave here and are given back to the rows that see them at the end
     if (convert(smem + S::VOFF + stage * S::VBYTES, t0.masked)) atomicOr(&sh.nan[t0.seg & 7], 1);
     mbar_arrive(&sh.vfull[stage]);
-    fetch(t2, a.c.k);
+    fetch(p2, a.c.k);
+    p1 = p2;
     t0 = t1;
     t1 = t2;
     t2 = t3;
