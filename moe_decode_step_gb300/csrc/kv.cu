@@ -135,13 +135,24 @@ int launch_tensor(const AttnArgs& a, int n_sm, cudaStream_t st) {
   return end();
 }
 
+// The kernel by the rows (queries times heads) of a KV head in the longest batch
+// row, as far as the host knows.  Measured, 64 heads over 8 of 128, 8 batch rows
+// of 4,090 to 8,185 tokens:
+//  - up to 8 rows, one n-tile a warp; to 32, two: 81 us at 32 rows, 92 on
+//    tcgen05; at 48 rows 106 against 96.  Where a row has few tokens the
+//    tcgen05 kernel's start counts: to 64 rows with 500 to 900 tokens 28 us
+//    against 54, with 1,000 to 2,000 65 against 67.
+//  - then one row tile whose streams share its keys: 219 us at 384 rows against
+//    267 in pairs of row tiles, 271 against 270 at 512, 484 against 441 at
+//    1,024; with 32 heads of 64 and 600 rows 192 against 224.
 template <int D>
 int launch_attention(const AttnArgs& a, int n_sm, int max_q, cudaStream_t st) {
-  if ((long long)max_q * a.group > 128) return launch_tensor<D, true>(a, n_sm, st);
-  if ((long long)max_q * a.group > 16) return launch_tensor<D, false>(a, n_sm, st);
-  // rows of the longest batch row per KV head, as far as the host knows
-  return (long long)max_q * a.group <= 8 ? launch_decode<D, 1>(a, n_sm, max_q, st)
-                                         : launch_decode<D, 2>(a, n_sm, max_q, st);
+  const long long rows = (long long)max_q * a.group;
+  const long long tokens = (long long)a.max_blocks << a.c.bs_log2;
+  if (rows <= 8) return launch_decode<D, 1>(a, n_sm, max_q, st);
+  if (rows <= 32 || (rows <= 64 && tokens <= 1024)) return launch_decode<D, 2>(a, n_sm, max_q, st);
+  if (rows <= 65536 / D) return launch_tensor<D, false>(a, n_sm, st);
+  return launch_tensor<D, true>(a, n_sm, st);
 }
 
 // Shared memory only where groups go through it (sizes that are no power of

@@ -31,11 +31,12 @@
 // [i * per, (i + 1) * per) of the order (batch row, row tile, KV head, keys).
 //
 // Measured at D = 128: prompts of 2,049 to 4,096 tokens behind 4,097 to 8,191,
-// 32 heads over 8: 1,028 us, 835 TFLOP/s, 44% of the dense rate: 5,500 cycles
-// a tile of 256 x 128, of which the products take 2,100, a stream's softmax
-// 2,400 and the converters 4,700, which share issue slots and shared memory's
-// bandwidth with both.  8 rows of 8 queries, 64 heads over 8, 4,090 to 8,185
-// tokens: 98 us, the converters' 5,500 cycles a tile of 128 x 128.
+// 32 heads over 8: 960 us, 895 TFLOP/s, 47% of the dense rate: 5,000 cycles a
+// tile of 256 x 128, of which the products take 2,100; no unit is busy more
+// than 40% of the time, the chain scores, softmax, values of two streams is
+// (a softmax 2,400 cycles beside the other stream and the converters).  8 rows
+// of 8 queries, 64 heads over 8, 4,090 to 8,185 tokens: 86 us, the converters'
+// 4,600 cycles a tile of 128 x 128.
 #pragma once
 
 #include "kv_attention.cuh"
