@@ -4,7 +4,7 @@
 // An item is TILE rows (query i, head of the group: row i * group + head) of
 // one KV head of one batch row: 256 as two streams of 128 rows that share
 // every tile of 128 keys (PAIR), or 128 rows whose two streams take the even
-// and the odd tiles of keys (a batch row of at most 128 rows).  The streams
+// and the odd tiles of keys (the launch says when).  The streams
 // alternate on the tensor cores: while one's scores (S = Q K^T, M = 128 rows,
 // N = 128 keys) go through the softmax, the other's products run.
 //
@@ -413,8 +413,12 @@ __device__ __forceinline__ void pr_convert(const AttnArgs& a, PrShared& sh, uint
   feed.seg = 0;
   pr_seen<S::TILE>(a, start, feed.lo_all, feed.hi_all);
   PrTile t0, t1, t2, t3;      // being converted, the two being fetched, being looked up
+  // (a tile of keys begins with a block)
   const int bs1 = (1 << a.c.bs_log2) - 1;
-  // codes that one row tile reads leave L2 first; those of a prompt are read again
+  const long long in_block[2] = {(key & bs1) * a.c.tstride + chunk * 16,
+                                 ((key + 16) & bs1) * a.c.tstride + chunk * 16};
+  // codes that few row tiles read leave L2 first (8 row tiles: 441 us against 454
+  // when they may stay); those of a prompt are read again
   const uint64_t policy = PAIR ? policy_evict_normal() : policy_evict_first();
   const uint32_t raw = smem_addr(smem) + S::ROFF + ct * 16;
   int in_slot = 0, out_slot = 0;
@@ -427,15 +431,15 @@ __device__ __forceinline__ void pr_convert(const AttnArgs& a, PrShared& sh, uint
   };
   auto place = [&](const PrTile& t) {
     Place w;
+    const long long block =
+        t.id >= 0 && t.id < a.c.n_blocks
+            ? (long long)t.id * a.c.bstride + (long long)t.h * a.c.hstride : -1;
     // the warp's 32 keys lie in two groups of 16, each in one block
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      const int id = __shfl_sync(0xffffffffu, t.id, 2 * warp + g);
-      const int k = key + 16 * g;
-      w.left[g] = t.there && id >= 0 && id < a.c.n_blocks ? t.seq - t.p0 - k : 0;
-      w.at[g] = w.left[g] > 0 ? (long long)id * a.c.bstride + (long long)t.h * a.c.hstride +
-                                    (long long)((t.p0 + k) & bs1) * a.c.tstride + chunk * 16
-                              : 0;
+      const long long at = __shfl_sync(0xffffffffu, block, 2 * warp + g);
+      w.left[g] = t.there && at >= 0 ? t.seq - t.p0 - key - 16 * g : 0;
+      w.at[g] = w.left[g] > 0 ? at + in_block[g] : 0;
     }
     return w;
   };
