@@ -531,77 +531,63 @@ struct DecOut {
   unsigned group;
 };
 
-// Rows `item`, item + step, ... of `jobs` jobs, the first rows of all of them
-// first; R rows a warp at once, V columns a lane.  Small and not inlined: the
-// code runs a few times per launch, mostly fetched cold, and everything it
+// Groups `item`, item + step, ... of R rows of `jobs` jobs, the first rows of
+// all of them first; a warp a group, V columns a lane.  Small and not inlined:
+// the code runs a few times per launch, mostly fetched cold, and everything it
 // reads but the pieces is in shared memory.  What other CTAs wrote is read at
 // L2, B pieces of R rows at once and without branches between: a round trip is
-// 0.7 us, and what follows it as long again.
+// 0.7 us, and what follows it as long again.  (128 rows of a tcgen05 tile, R 2
+// and B 8: 20 us for two tiles of four pieces.)
 // (ORDERED: the pieces' columns are the dims themselves.)
 template <int D, int ROWS, bool ORDERED = false>
 __device__ __noinline__ void dec_join(const DecOut* to, const DecJob* job, int jobs, int item,
                                       int step) {
-  constexpr int V = D / 32, R = ROWS > 8 ? 2 : 1, B = 16 / R;
+  constexpr int V = D / 32, R = ROWS > 16 ? 4 : ROWS > 8 ? 2 : 1, B = 16 / R;
   const int lane = threadIdx.x & 31;
 #pragma unroll 1
-  for (; item < jobs * ROWS; item += step * R) {
-    const DecJob* b[R];
-    int row[R], i[R], head[R], k1[R];
-    unsigned far[R];
-    bool real[R];
+  for (; item < jobs * (ROWS / R); item += step) {
+    const DecJob& b = job[item % jobs];
+    const int row = item / jobs * R;
+    const unsigned rho = (unsigned)b.m * ROWS + row;   // as in dec_tile_row
+    if ((int)(rho / to->group) >= b.n) continue;
+    const float* ring = b.ring;
+    const int sh = ring ? 1 : 0;                       // workspace piece k has mask bit k << sh
+    const unsigned mask = b.mask, far = ring ? mask & 0x55555555u : mask;
+    const int last = far ? (31 - __clz(far)) >> sh : 0;
     float mk[R], lk[R];
-    int last = 0;
 #pragma unroll
     for (int x = 0; x < R; ++x) {
-      const int it = min(item + x * step, jobs * ROWS - 1);
-      b[x] = job + it % jobs;
-      row[x] = it / jobs;
-      const unsigned rho = (unsigned)b[x]->m * ROWS + row[x];   // as in dec_tile_row
-      i[x] = (int)(rho / to->group);
-      head[x] = b[x]->h * (int)to->group + (int)(rho - (unsigned)i[x] * to->group);
-      real[x] = item + x * step < jobs * ROWS && i[x] < b[x]->n;
-      const float* ring = b[x]->ring;
-      const int sh = ring ? 1 : 0;       // workspace piece k has mask bit k << sh
       mk[x] = -INFINITY;
       lk[x] = 0.f;
-      const unsigned mask = real[x] ? b[x]->mask : 0u;
       if ((mask >> lane) & 1u) {
         if (ring && (lane & 1)) {
-          const float* ml = ring + (lane >> 1) * b[x]->ring_stride + ROWS * D + row[x];
+          const float* ml = ring + (lane >> 1) * b.ring_stride + ROWS * D + row + x;
           mk[x] = ml[0];
           lk[x] = ml[ROWS];
         } else {
-          const float* ml = b[x]->base + (lane >> sh) * b[x]->stride +
-                            (lane == 0 ? b[x]->extra : 0) + ROWS * D + row[x];
+          const float* ml = b.base + (lane >> sh) * b.stride + (lane == 0 ? b.extra : 0) +
+                            ROWS * D + row + x;
           mk[x] = __ldcg(ml);
           lk[x] = __ldcg(ml + ROWS);
         }
       }
-      far[x] = ring ? mask & 0x55555555u : mask;   // pieces in the workspace
-      k1[x] = far[x] ? (31 - __clz(far[x])) >> sh : -1;
-      last = max(last, k1[x]);
     }
-    bool any = false;
-#pragma unroll
-    for (int x = 0; x < R; ++x) any |= real[x];
-    if (!any) continue;
     float acc[R][V], tm[R], f[R], tl[R];
 #pragma unroll 1
     for (int k = 0; k <= last; k += B) {
       float2 v[R][B][V / 2];
 #pragma unroll
-      for (int x = 0; x < R; ++x)
+      for (int u = 0; u < B; ++u) {   // what is not there has weight 0
+        const bool in = (far >> ((k + u) << sh)) & 1u;
+        const float* src = b.base + (k + u) * b.stride + (k + u == 0 ? b.extra : 0) + row * D +
+                           V * lane;
 #pragma unroll
-        for (int u = 0; u < B; ++u) {   // what is not there has weight 0
-          const int sh = b[x]->ring ? 1 : 0;
-          const bool in = (far[x] >> ((k + u) << sh)) & 1u;
-          const float* src = b[x]->base + (k + u) * b[x]->stride +
-                             (k + u == 0 ? b[x]->extra : 0) + row[x] * D + V * lane;
+        for (int x = 0; x < R; ++x)
 #pragma unroll
           for (int n = 0; n < V / 2; ++n)
-            v[x][u][n] = in ? __ldcg(reinterpret_cast<const float2*>(src + 2 * n))
+            v[x][u][n] = in ? __ldcg(reinterpret_cast<const float2*>(src + x * D + 2 * n))
                             : make_float2(0.f, 0.f);
-        }
+      }
       if (k == 0) {
 #pragma unroll
         for (int x = 0; x < R; ++x) tm[x] = warp_max(mk[x]);
@@ -611,14 +597,17 @@ __device__ __noinline__ void dec_join(const DecOut* to, const DecJob* job, int j
           tl[x] = warp_sum(lk[x] * f[x]);
 #pragma unroll
           for (int n = 0; n < V; ++n) acc[x][n] = 0.f;
-          if (b[x]->ring) {
+        }
+        if (ring) {
 #pragma unroll 4
-            for (int p = 0; p < 16; ++p) {
-              const float fk = __shfl_sync(0xffffffffu, f[x], 2 * p + 1);
-              if (!((b[x]->mask >> (2 * p + 1)) & 1u)) continue;
-              const float* src = b[x]->ring + p * b[x]->ring_stride + row[x] * D + V * lane;
+          for (int p = 0; p < 16; ++p) {
+            const float* src = ring + p * b.ring_stride + row * D + V * lane;
 #pragma unroll
-              for (int n = 0; n < V; ++n) acc[x][n] = fmaf(src[n], fk, acc[x][n]);
+            for (int x = 0; x < R; ++x) {
+              const float fk = __shfl_sync(0xffffffffu, f[x], 2 * p + 1);
+              if (!((mask >> (2 * p + 1)) & 1u)) continue;
+#pragma unroll
+              for (int n = 0; n < V; ++n) acc[x][n] = fmaf(src[x * D + n], fk, acc[x][n]);
             }
           }
         }
@@ -627,7 +616,7 @@ __device__ __noinline__ void dec_join(const DecOut* to, const DecJob* job, int j
       for (int x = 0; x < R; ++x)
 #pragma unroll
         for (int u = 0; u < B; ++u) {
-          const float fk = __shfl_sync(0xffffffffu, f[x], ((k + u) << (b[x]->ring ? 1 : 0)) & 31);
+          const float fk = __shfl_sync(0xffffffffu, f[x], ((k + u) << sh) & 31);
 #pragma unroll
           for (int n = 0; n < V / 2; ++n) {
             acc[x][2 * n] = fmaf(v[x][u][n].x, fk, acc[x][2 * n]);
@@ -637,26 +626,27 @@ __device__ __noinline__ void dec_join(const DecOut* to, const DecJob* job, int j
     }
 #pragma unroll
     for (int x = 0; x < R; ++x) {
-      if (!real[x]) continue;
-      if (!b[x]->dst) {
+      const int i = (int)((rho + x) / to->group);
+      if (i >= b.n) break;
+      if (!b.dst) {
         const float inv = attn_inverse(tl[x]);
-        const long long tok = b[x]->tok + i[x];
-        uint16_t* out = to->out + tok * to->o_ts + head[x] * to->o_hs;
+        const long long tok = b.tok + i;
+        const int head = b.h * (int)to->group + (int)(rho + x - (unsigned)i * to->group);
+        uint16_t* out = to->out + tok * to->o_ts + head * to->o_hs;
 #pragma unroll
         for (int n = 0; n < V; n += 2)
           *reinterpret_cast<uint32_t*>(
               out + (ORDERED ? V * lane + n : dec_dim<D>(V * lane + n))) =
               pack16(acc[x][n] * inv, acc[x][n + 1] * inv, to->f16);
-        if (lane == 0 && to->lse) to->lse[tok * to->heads + head[x]] = attn_lse(tm[x], tl[x]);
+        if (lane == 0 && to->lse) to->lse[tok * to->heads + head] = attn_lse(tm[x], tl[x]);
       } else {
-        float* dst = b[x]->dst;
+        float* dst = b.dst + (row + x) * D + V * lane;
 #pragma unroll
         for (int n = 0; n < V; n += 2)
-          *reinterpret_cast<float2*>(dst + row[x] * D + V * lane + n) =
-              make_float2(acc[x][n], acc[x][n + 1]);
+          *reinterpret_cast<float2*>(dst + n) = make_float2(acc[x][n], acc[x][n + 1]);
         if (lane == 0) {
-          dst[ROWS * D + row[x]] = tm[x];
-          dst[ROWS * D + ROWS + row[x]] = tl[x];
+          b.dst[ROWS * D + row + x] = tm[x];
+          b.dst[ROWS * D + ROWS + row + x] = tl[x];
         }
       }
     }
