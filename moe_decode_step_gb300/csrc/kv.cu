@@ -141,7 +141,7 @@ int launch_tensor(const AttnArgs& a, int n_sm, cudaStream_t st) {
 //  - up to 8 rows, one n-tile a warp; to 32, two: 81 us at 32 rows, 92 on
 //    tcgen05; at 48 rows 106 against 96.  Where a row has few tokens the
 //    tcgen05 kernel's start counts: to 64 rows with 500 to 900 tokens 28 us
-//    against 54, with 1,000 to 2,000 65 against 67.
+//    against 52, with 1,000 to 2,000 65 against 60.
 //  - then one row tile whose streams share its keys: 219 us at 384 rows against
 //    267 in pairs of row tiles, 271 against 270 at 512, 484 against 441 at
 //    1,024; with 32 heads of 64 and 600 rows 192 against 224.

@@ -27,16 +27,16 @@
 // than 2^8, so that O in tensor memory is rarely rescaled; weights stay below
 // 2^8, far inside f16.
 //
-// Work split and joins as there, in tiles of 128 keys: CTA i takes tiles
-// [i * per, (i + 1) * per) of the order (batch row, row tile, KV head, keys).
+// Work split and joins as there, in tiles of 128 keys in the order (batch row,
+// row tile, KV head, keys).
 //
 // Measured at D = 128: prompts of 2,049 to 4,096 tokens behind 4,097 to 8,191,
 // 32 heads over 8: 960 us, 895 TFLOP/s, 47% of the dense rate: 5,000 cycles a
 // tile of 256 x 128, of which the products take 2,100; no unit is busy more
 // than 40% of the time, the chain scores, softmax, values of two streams is
 // (a softmax 2,400 cycles beside the other stream and the converters).  8 rows
-// of 8 queries, 64 heads over 8, 4,090 to 8,185 tokens: 86 us, the converters'
-// 4,600 cycles a tile of 128 x 128.
+// of 8 queries, 64 heads over 8, 4,090 to 8,185 tokens: 81 us, of which 11 before
+// the first scores, 1.6 a tile of 128 x 128 (the converters'), 15 for the joins.
 #pragma once
 
 #include "kv_attention.cuh"
@@ -47,6 +47,13 @@ namespace moe {
 constexpr int kPrWarps = 12;
 constexpr int kPrThreads = 32 * kPrWarps;
 constexpr int kPrKeys = 128;
+// Tiles of keys a CTA takes at least (64 queries of 300 tokens: 40 us, with 2
+// tiles 55), and may take over an equal share to keep to one item (few items
+// are then split each on its own, as in kv_attention.cuh: 4 rows of 64 queries
+// and 64 to 500 tokens 38 us against 76, 4 of 16 and 4,090 to 8,185 tokens 78
+// against 97, 8 queries of 40,000 tokens 91 against 108).
+constexpr int kPrLeast = 4;
+constexpr int kPrSlack = 16;
 
 template <int D, bool PAIR>
 struct PrShape {
@@ -179,34 +186,37 @@ __device__ __forceinline__ void pr_next_item(const AttnArgs& a, PrCursor& c) {
   pr_span<TILE>(a, c.w, c.m, c.s0, c.S);
 }
 
-// Sum of S over a batch row's row tiles: by the lane alone, or (coop) with the
-// warp's lanes taking m = lane, lane + 32, ...
+// Parts of at most `most` tiles of keys that an item of S is cut into.
+__device__ __forceinline__ int pr_parts(int S, int most) { return (S - 1) / most + 1; }
+
+// Sum of the parts over a batch row's row tiles: by the lane alone, or with
+// the warp's lanes taking m = lane, lane + 32, ...
 template <int TILE>
-__device__ __forceinline__ long long pr_row_tiles(const AttnArgs& a, const AttnRow& w, int first,
-                                                  int step) {
+__device__ __forceinline__ long long pr_row_tiles(const AttnArgs& a, const AttnRow& w, int most,
+                                                  int first, int step) {
   const int M = pr_tiles<TILE>(a, w);
   long long sum = 0;
   for (int m = first; m < M; m += step) {
     int s0, S;
     pr_span<TILE>(a, w, m, s0, S);
-    sum += S;
+    sum += pr_parts(S, most);
   }
   return sum;
 }
 
-// Tiles of keys of batch row r, every lane of a warp with its own r (r < 0:
+// The same of batch row r, every lane of a warp with its own r (r < 0:
 // none); rows of many row tiles are summed by the whole warp.
 template <int TILE>
-__device__ __forceinline__ long long pr_warp_tiles(const AttnArgs& a, int r) {
+__device__ __forceinline__ long long pr_warp_tiles(const AttnArgs& a, int most, int r) {
   constexpr int kAlone = 8;
   AttnRow w{0, 0, 0};
   if (r >= 0) w = attn_row(a, r);
   const bool big = pr_tiles<TILE>(a, w) > kAlone;
-  long long sum = big ? 0 : pr_row_tiles<TILE>(a, w, 0, 1);
+  long long sum = big ? 0 : pr_row_tiles<TILE>(a, w, most, 0, 1);
   for (unsigned rest = __ballot_sync(0xffffffffu, big); rest; rest &= rest - 1) {
     const int src = __ffs(rest) - 1;
     const AttnRow o{0, __shfl_sync(0xffffffffu, w.n, src), __shfl_sync(0xffffffffu, w.seq, src)};
-    long long v = pr_row_tiles<TILE>(a, o, threadIdx.x & 31, 32);
+    long long v = pr_row_tiles<TILE>(a, o, most, threadIdx.x & 31, 32);
 #pragma unroll
     for (int k = 16; k; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
     if ((threadIdx.x & 31) == src) sum = v;
@@ -214,33 +224,55 @@ __device__ __forceinline__ long long pr_warp_tiles(const AttnArgs& a, int r) {
   return sum * a.c.heads;
 }
 
-// This CTA's tiles [u0, u0 + n) and its cursor at u0; every thread calls.
+// This CTA's share of the tiles of keys and its cursor there; every thread calls.
 template <int TILE>
-__device__ __forceinline__ void pr_schedule(const AttnArgs& a, long long& u0, long long& n,
-                                            long long& per, PrCursor& cur) {
-  __shared__ long long s_sum[kPrWarps];
+__device__ __forceinline__ void pr_schedule(const AttnArgs& a, DecShare& sh, PrCursor& cur) {
+  __shared__ long long s_sum[2][kPrWarps];
   __shared__ long long s_left;
   __shared__ int s_row, s_m;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int chunk = (a.rows + kPrWarps - 1) / kPrWarps;
   const int r0 = min(a.rows, warp * chunk), r1 = min(a.rows, r0 + chunk);
-  long long sum = 0;
-  for (int r = r0; r < r1; r += 32) sum += pr_warp_tiles<TILE>(a, r + lane < r1 ? r + lane : -1);
+  auto sums = [&](int most, int set) {
+    long long v = 0;
+    for (int r = r0; r < r1; r += 32)
+      v += pr_warp_tiles<TILE>(a, most, r + lane < r1 ? r + lane : -1);
 #pragma unroll
-  for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-  if (lane == 0) s_sum[warp] = sum;
+    for (int k = 16; k; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
+    if (lane == 0) s_sum[set][warp] = v;
+    return v;
+  };
+  long long sum = sums(1, 0), total = 0, items = 0, before = 0;
+  sums(INT32_MAX, 1);
   __syncthreads();
-  long long total = 0, before = 0;
   for (int w = 0; w < kPrWarps; ++w) {
     if (w == warp) before = total;
-    total += s_sum[w];
+    total += s_sum[0][w];
+    items += s_sum[1][w];
   }
-  per = max((total + gridDim.x - 1) / gridDim.x, 2ll);
-  u0 = per * blockIdx.x;
-  n = min(per, total - u0);
-  if (n > 0 && u0 >= before && u0 < before + sum) {
+  // few items: each split on its own (as in dec_schedule)
+  const long long even = max((total + gridDim.x - 1) / gridDim.x, (long long)kPrLeast);
+  const long long spare = (long long)gridDim.x - items;
+  const long long share = spare > 0 ? max((total + spare - 1) / spare, (long long)kPrLeast) : 0;
+  const bool apart = spare > 0 && share <= even + kPrSlack;
+  const int most = apart ? (int)share : 1;
+  if (apart) {
+    __syncthreads();
+    sum = sums(most, 0);
+    __syncthreads();
+    total = before = 0;
+    for (int w = 0; w < kPrWarps; ++w) {
+      if (w == warp) before = total;
+      total += s_sum[0][w];
+    }
+  }
+  const long long u0 = apart ? blockIdx.x : even * blockIdx.x;
+  sh.per = apart ? 0 : even;
+  sh.u0 = apart ? 0 : u0;
+  sh.n = apart ? (u0 < total ? 1 : 0) : min(even, total - u0);
+  if (sh.n > 0 && u0 >= before && u0 < before + sum) {
     for (int r = r0;; r += 32) {
-      const long long v = pr_warp_tiles<TILE>(a, r + lane < r1 ? r + lane : -1);
+      const long long v = pr_warp_tiles<TILE>(a, most, r + lane < r1 ? r + lane : -1);
       long long inc = v;
 #pragma unroll
       for (int k = 1; k < 32; k <<= 1) {
@@ -259,7 +291,7 @@ __device__ __forceinline__ void pr_schedule(const AttnArgs& a, long long& u0, lo
       for (int m = 0;; m += 32) {
         int s0, S = 0;
         if (m + lane < pr_tiles<TILE>(a, w)) pr_span<TILE>(a, w, m + lane, s0, S);
-        const long long x = (long long)S * a.c.heads;
+        const long long x = S ? (long long)pr_parts(S, most) * a.c.heads : 0;
         long long y = x;
 #pragma unroll
         for (int k = 1; k < 32; k <<= 1) {
@@ -284,14 +316,22 @@ __device__ __forceinline__ void pr_schedule(const AttnArgs& a, long long& u0, lo
     }
   }
   __syncthreads();
-  if (n <= 0) return;
+  if (sh.n <= 0) return;
   cur.r = s_row;
   cur.m = s_m;
   cur.w = attn_row(a, cur.r);
   cur.M = pr_tiles<TILE>(a, cur.w);
   pr_span<TILE>(a, cur.w, cur.m, cur.s0, cur.S);
-  cur.h = (int)(s_left / cur.S);
-  cur.s = (int)(s_left - (long long)cur.h * cur.S);
+  const int parts = pr_parts(cur.S, most);
+  cur.h = (int)(s_left / parts);
+  const int part = (int)(s_left - (long long)cur.h * parts);
+  cur.s = part;
+  if (apart) {
+    cur.s = (int)((long long)cur.S * part / parts);
+    sh.n = (long long)cur.S * (part + 1) / parts - cur.s;
+    sh.c0 = blockIdx.x - part;
+    sh.ctas = parts;
+  }
 }
 
 // What every and any row of the item sees.
@@ -326,6 +366,7 @@ struct PrShared {
   float m1[128], l1[128];   // the second stream's, when the two are joined
   unsigned nan1[4][128];
   DecOut out;
+  DecShare share;
   DecJob job[2];
 };
 
@@ -930,9 +971,10 @@ static __global__ void __launch_bounds__(kPrThreads, 1) kv_attention_tc(const At
   extern __shared__ __align__(128) uint8_t pr_smem[];
   __shared__ PrShared sh;
   const int warp = threadIdx.x >> 5;
-  long long u0, n_units, per;
+  DecShare share;
   PrCursor cur;
-  pr_schedule<S::TILE>(a, u0, n_units, per, cur);
+  pr_schedule<S::TILE>(a, share, cur);
+  const long long n_units = share.n;
   if (n_units <= 0) return;
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -946,6 +988,7 @@ static __global__ void __launch_bounds__(kPrThreads, 1) kv_attention_tc(const At
     }
     for (int s = 0; s < 8; ++s) sh.nan[s] = 0;
     sh.dead = 0;
+    sh.share = share;
     sh.out = {a.out, a.lse, a.o_ts, a.o_hs, a.heads, a.f16, (unsigned)a.group};
     fence_barrier_init();
   }
@@ -968,7 +1011,7 @@ static __global__ void __launch_bounds__(kPrThreads, 1) kv_attention_tc(const At
 
   // ---- items that the CTA's ends cut ----
   dec_join_ctas<D, S::TILE, kPrWarps, 2 * S::SLOT, S::SLOT, true>(
-      a, a.partial, {u0, n_units, per, 0, 0, {}}, sh.open[0] ? &sh.piece[0] : nullptr,
+      a, a.partial, sh.share, sh.open[0] ? &sh.piece[0] : nullptr,
       sh.open[1] ? &sh.piece[1] : nullptr, &sh.out, sh.job);
 }
 
