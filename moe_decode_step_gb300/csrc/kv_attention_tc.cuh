@@ -35,7 +35,7 @@
 // tile of 256 x 128, of which the products take 2,100; no unit is busy more
 // than 40% of the time, the chain scores, softmax, values of two streams is
 // (a softmax 2,400 cycles beside the other stream and the converters).  8 rows
-// of 8 queries, 64 heads over 8, 4,090 to 8,185 tokens: 81 us, of which 11 before
+// of 8 queries, 64 heads over 8, 4,090 to 8,185 tokens: 77 us, of which 11 before
 // the first scores, 1.6 a tile of 128 x 128 (the converters'), 15 for the joins.
 #pragma once
 
@@ -51,9 +51,10 @@ constexpr int kPrKeys = 128;
 // tiles 55), and may take over an equal share to keep to one item (few items
 // are then split each on its own, as in kv_attention.cuh: 4 rows of 64 queries
 // and 64 to 500 tokens 38 us against 76, 4 of 16 and 4,090 to 8,185 tokens 78
-// against 97, 8 queries of 40,000 tokens 91 against 108).
+// against 97, 8 queries of 40,000 tokens 91 against 108, 8 rows of 8 and 4,090 to
+// 8,185 77 against 82; with up to 16 tiles more 86).
 constexpr int kPrLeast = 4;
-constexpr int kPrSlack = 16;
+constexpr int kPrSlack = 8;
 
 template <int D, bool PAIR>
 struct PrShape {
@@ -250,20 +251,32 @@ __device__ __forceinline__ void pr_schedule(const AttnArgs& a, DecShare& sh, PrC
     total += s_sum[0][w];
     items += s_sum[1][w];
   }
-  // few items: each split on its own (as in dec_schedule)
+  // few items: each split on its own (as in dec_schedule) into parts of at most
+  // `most` tiles, if there are no more parts than CTAs; with most = total / spare
+  // there never are
   const long long even = max((total + gridDim.x - 1) / gridDim.x, (long long)kPrLeast);
   const long long spare = (long long)gridDim.x - items;
-  const long long share = spare > 0 ? max((total + spare - 1) / spare, (long long)kPrLeast) : 0;
-  const bool apart = spare > 0 && share <= even + kPrSlack;
-  const int most = apart ? (int)share : 1;
-  if (apart) {
+  int most = 1;
+  bool apart = false;
+  if (spare >= 0 && total > 0) {
+    most = (int)(even + kPrSlack);
+    if (spare > 0)
+      most = (int)min((long long)most, max((total + spare - 1) / spare, (long long)kPrLeast));
     __syncthreads();
-    sum = sums(most, 0);
+    const long long parts = sums(most, 0);
     __syncthreads();
-    total = before = 0;
+    long long all = 0, first = 0;
     for (int w = 0; w < kPrWarps; ++w) {
-      if (w == warp) before = total;
-      total += s_sum[0][w];
+      if (w == warp) first = all;
+      all += s_sum[0][w];
+    }
+    apart = all <= gridDim.x;
+    if (apart) {
+      sum = parts;
+      total = all;
+      before = first;
+    } else {
+      most = 1;
     }
   }
   const long long u0 = apart ? blockIdx.x : even * blockIdx.x;
