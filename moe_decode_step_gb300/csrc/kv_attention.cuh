@@ -495,6 +495,9 @@ __device__ __forceinline__ float attn_lse(float m, float l) {
 }
 // 1 / l; 0 where nothing was seen, NaN where the sum is.
 __device__ __forceinline__ float attn_inverse(float l) { return l > 0.f ? 1.f / l : l; }
+// Scores past this are so far apart in fp32 (2^-2 and more) that t - M rounded
+// once is no weight any more: t is rounded first, as M was, and t - M is exact.
+constexpr float kAttnLarge = 4194304.f;   // 2^22
 // 2^(m - ref) with both -infinity (nothing seen) giving 1.
 __device__ __forceinline__ float attn_factor(float m, float ref) {
   return m == -INFINITY ? (ref == -INFINITY ? 1.f : 0.f) : exp2_approx(m - ref);
@@ -832,6 +835,8 @@ static __global__ void __launch_bounds__(DecShape<D, NT>::THREADS, 1)
       attn_seen(a, cur.x.w, i0, lo_any, hi_all);
       attn_seen(a, cur.x.w, i1, lo_all, hi_any);
 
+      bool large = false;       // some row's reference is past kAttnLarge
+
       float o[NT][CH / 2][4];   // value tile j: dims CH g + 2j (0, 1), CH g + 2j + 1 (2, 3)
 #pragma unroll
       for (int q = 0; q < NT; ++q)
@@ -915,11 +920,13 @@ static __global__ void __launch_bounds__(DecShape<D, NT>::THREADS, 1)
             up |= v > m[q][r];
           }
         if (__any_sync(0xffffffffu, up)) {
+          bool past = false;
 #pragma unroll
           for (int q = 0; q < NT; ++q)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
               const float n = fmaxf(m[q][r], x[q][r]);
+              past |= n > -INFINITY && fabsf(n) >= kAttnLarge;
               const float d = attn_factor(m[q][r], n);
               m[q][r] = n;
               l[q][r] *= d;
@@ -929,6 +936,7 @@ static __global__ void __launch_bounds__(DecShape<D, NT>::THREADS, 1)
                 o[q][j][2 + r] *= d;
               }
             }
+          large |= __any_sync(0xffffffffu, past);
         }
         uint32_t pb[NT][2][2];
 #pragma unroll
@@ -939,8 +947,13 @@ static __global__ void __launch_bounds__(DecShape<D, NT>::THREADS, 1)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const float f = fac[q][r] * ke[h], c = ev[h] - ref;
-              s[q][h][r] = exp2_approx(fmaf(s[q][h][r], f, c));
-              s[q][h][2 + r] = exp2_approx(fmaf(s[q][h][2 + r], f, c));
+              float t0 = fmaf(s[q][h][r], f, c), t1 = fmaf(s[q][h][2 + r], f, c);
+              if (large) {
+                t0 = fmaf(s[q][h][r], f, ev[h]) - ref;
+                t1 = fmaf(s[q][h][2 + r], f, ev[h]) - ref;
+              }
+              s[q][h][r] = exp2_approx(t0);
+              s[q][h][2 + r] = exp2_approx(t1);
             }
           }
           if (masked) {

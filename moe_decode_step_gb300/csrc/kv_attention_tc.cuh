@@ -111,6 +111,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ void fma_f32x2(float& a, float& b, float g, float off) {
   asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\t"
@@ -715,6 +721,81 @@ __device__ __noinline__ void pr_nan_dims(const AttnArgs& a, const PrCursor& c, i
   }
 }
 
+// The row's sums in tensor memory times `by`.
+template <int D>
+__device__ __forceinline__ void pr_scale_sums(uint32_t to, float by) {
+#pragma unroll 1
+  for (int k = 0; k < D / 16; ++k) {
+    float o[16];
+    tmem_ld16(to + 16 * k, o);
+    tmem_wait_ld();
+    uint32_t r[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(o[e] * by);
+    tmem_st16(to + 16 * k, r);
+  }
+}
+
+// A tile's weights where a row of the warp has scores past kAttnLarge: two
+// passes, the maximum of t, then t - M, which is exact near M.  (M alone, its
+// rounding as large as the growth that a pass allows, need not settle.)  The
+// weights go into the columns of scores that are read already.  ofull: the
+// sums' barrier, null where the segment has none yet; returns M and the sum.
+template <int D>
+__device__ __noinline__ float2 pr_weights_large(PrShared& sh, const float4* sc, uint32_t ts,
+                                                uint32_t to, int from, unsigned len, float fac,
+                                                float m, float l, uint64_t* ofull,
+                                                uint32_t parity) {
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < kPrKeys; c += 16) {
+    float s[16];
+    tmem_ld16(ts + c, s);
+    tmem_wait_ld();
+    const float4 f = sc[c / 16];
+    const float g = fmaxf(fac * f.x, 1e-38f);
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      if ((unsigned)(c + k - from) < len) top = fmaxf(top, fmaf(s[k], g, f.y));
+  }
+  const bool grow = top - m > 8.f;   // (no: nothing seen, or both infinite)
+  if (__any_sync(0xffffffffu, grow)) {
+    const float down = grow ? attn_factor(m, top) : 1.f;
+    if (grow) m = top;
+    l *= down;
+    if (ofull) {
+      pr_wait(ofull, parity, sh);
+      __syncwarp();
+      tc_fence_after();
+      pr_scale_sums<D>(to, down);
+    }
+  }
+  const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+  for (int c = 0; c < kPrKeys; c += 16) {
+    float s[16];
+    uint32_t p[8];
+    __syncwarp();
+    tmem_ld16(ts + c, s);
+    tmem_wait_ld();
+    const float4 f = sc[c / 16];
+    const float g = fmaxf(fac * f.x, 1e-38f);
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; k += 2) {
+#pragma unroll
+      for (int e = k; e < k + 2; ++e) {
+        s[e] = (unsigned)(c + e - from) < len ? exp2_approx(fmaf(s[e], g, f.y) - ref) : 0.f;
+        sum += s[e];
+      }
+      p[k / 2] = pack_f16x2(s[k], s[k + 1]);
+    }
+    l = fmaf(f.z, sum, l);
+    tmem_st8(ts + c / 2, p);
+  }
+  return make_float2(m, l);
+}
+
 template <int D, bool PAIR>
 __device__ __forceinline__ void pr_softmax(const AttnArgs& a, PrShared& sh, uint8_t* smem,
                                            PrCursor c, long long n_units) {
@@ -800,7 +881,8 @@ __device__ __forceinline__ void pr_softmax(const AttnArgs& a, PrShared& sh, uint
       // Weights against the running reference in one pass over the scores, in
       // registers until the tile's maximum is known; where a row of the warp
       // outgrows its reference by 2^8 (its first tile, then rarely) O and the
-      // sums follow, and the pass is made again.
+      // sums follow, and the pass is made again: once, as the new reference is
+      // within 1 of the maximum below kAttnLarge.
       uint32_t p[kPrKeys / 2];
 #pragma unroll 1
       for (;;) {
@@ -839,12 +921,26 @@ __device__ __forceinline__ void pr_softmax(const AttnArgs& a, PrShared& sh, uint
             lt = fmaf(f.z, s0 + s1, lt);
           }
         }
-        const bool grow = x > (m == -INFINITY ? -INFINITY : 8.f);
+        // (nothing seen yet, or a reference that t - M is not to be rounded against)
+        const bool any = !(fabsf(m) < kAttnLarge);
+        const bool grow = x > (any ? -INFINITY : 8.f);
         if (!__any_sync(0xffffffffu, grow)) {
+          // into the columns of the scores
           l += lt;
+          __syncwarp();
+          tmem_st32(ts, p);
+          tmem_st32(ts + 32, p + 32);
           break;
         }
         const float next = ref + x;
+        if (__any_sync(0xffffffffu, grow && (!(fabsf(next) < kAttnLarge) || (any && m != -INFINITY)))) {
+          const float2 r = pr_weights_large<D>(
+              sh, sc, ts, to, masked ? lo - p0 : 0, masked ? (unsigned)max(hi - lo, 0) : kPrKeys,
+              fac, m, l, mine > 0 ? &sh.ofull[t] : nullptr, (cnt - 1) & 1);
+          m = r.x;
+          l = r.y;
+          break;
+        }
         const float down = grow ? attn_factor(m, next) : 1.f;
         if (grow) m = next;
         l *= down;
@@ -852,22 +948,9 @@ __device__ __forceinline__ void pr_softmax(const AttnArgs& a, PrShared& sh, uint
           pr_wait(&sh.ofull[t], (cnt - 1) & 1, sh);
           __syncwarp();
           tc_fence_after();
-#pragma unroll 1
-          for (int k = 0; k < D / 16; ++k) {
-            float o[16];
-            tmem_ld16(to + 16 * k, o);
-            tmem_wait_ld();
-            uint32_t r[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(o[e] * down);
-            tmem_st16(to + 16 * k, r);
-          }
+          pr_scale_sums<D>(to, down);
         }
       }
-      // into the columns of the scores
-      __syncwarp();
-      tmem_st32(ts, p);
-      tmem_st32(ts + 32, p + 32);
       tmem_wait_st();
       tc_fence_before();
       pr_stream_sync(t);

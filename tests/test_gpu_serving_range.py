@@ -1,0 +1,81 @@
+"""GPU tests of the serving operators at the edges of what their calls accept:
+block scales at both ends of their range, keys that lead the softmax by far,
+scores so large that fp32 steps over whole octaves, lengths past 31 bits.
+Attention goes through all four kernels; tolerances as in test_gpu_serving.py."""
+import numpy as np
+import pytest
+import torch
+
+import moe_decode_step_gb300 as M
+
+import _serving as ref
+import test_gpu_serving as base
+from test_gpu_serving_paths import ANNOUNCED, _run
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+every_kernel = pytest.mark.parametrize("rows", ANNOUNCED.values(), ids=ANNOUNCED)
+
+
+# ---------------------------------------------------------------------------
+# Attention: large scores
+# ---------------------------------------------------------------------------
+def _scores(c, r, i, h):
+    """Scores (times scale 1) of query i of row r, head h, over the row's cached tokens, and
+    the largest sum of magnitudes."""
+    k = ref.read_cache(c.codes[0], c.scale[0])
+    j = np.arange(int(c.seq[r]))
+    kk = k[c.table[r, j // c.bs], h // (c.heads // c.hkv), j % c.bs]
+    q = base._np(c.q.double())[c.q_start[r] + i, h]
+    return kk @ q, (np.abs(kk) @ np.abs(q)).max()
+
+
+@every_kernel
+@pytest.mark.parametrize("v_exp", [(-9, -6), (-60, -40), (40, 60)])
+@pytest.mark.parametrize("log_q", [18, 22, 25, 28, 34, 60])
+def test_large_scores_take_the_best_key(log_q, v_exp, rows):
+    """Scores of about 2^log_q, whose own fp32 spacing is up to 2^36: a softmax over them is
+    the best key wherever it leads by more than the scores' rounding (d 2^-24 of their absolute
+    sum) and 30 nats; the result is then its value, rounded once."""
+    c = base.Case([(200, 1), (90, 6), (600, 2), (3, 40)], 16, 2, 128, 16, seed=log_q, v_exp=v_exp,
+                  q_std=2.0 ** (log_q - 3.0))
+    out, lse = _run(c, rows, scale=1.0, causal=False)
+    got, gl = base._np(out.double()), base._np(lse).astype(np.float64)
+    assert np.isfinite(got).all() and np.isfinite(gl).all()
+    v = ref.read_cache(c.codes[1], c.scale[1])
+    seen = 0
+    for r, (_, n) in enumerate(c.lens):
+        for i in range(n):
+            for h in range(c.heads):
+                s, span = _scores(c, r, i, h)
+                top = np.argsort(s)[::-1][:2]
+                noise = 2 * c.d * 2.0 ** -24 * span
+                t = c.q_start[r] + i
+                assert abs(gl[t, h] - s[top[0]]) <= noise + np.log(len(s)) + 2.0 ** -22 * abs(s[top[0]])
+                if s[top[0]] - s[top[1]] < 2 * noise + 30:
+                    continue
+                seen += 1
+                j = top[0]
+                want = v[c.table[r, j // c.bs], h // 8, j % c.bs]
+                # beside the result's rounding the weight's own, and e^-30 of every other value
+                rest = len(s) * np.exp(-30.0) * np.nanmax(np.abs(v[c.table[r, :-(-len(s) // c.bs)], h // 8]))
+                assert (np.abs(got[t, h] - want) <= (2.0 ** -8 + 2.0 ** -11) * np.abs(want) + rest).all()
+    assert seen > 300
+
+
+@every_kernel
+def test_rows_beside_a_row_of_large_scores_stay_exact(rows):
+    """One query and one head of huge values among ordinary ones of the same tile."""
+    c = base.Case([(300, 1), (64, 7), (5, 30)], 16, 2, 128, 32, seed=2)
+    q = c.q.clone()
+    q[:, 3] *= 2.0 ** 30
+    q[4] *= 2.0 ** 40
+    plain = c.expect(128 ** -0.5)
+    out, lse = _run(c, rows, q=q)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    keep = np.ones(plain[1].shape, bool)
+    keep[:, 3] = keep[4] = False
+    o, l, mag, span = (x[keep][:, None] for x in plain)
+    base.check(c, out[torch.from_numpy(keep).to(DEV)][:, None], lse[torch.from_numpy(keep).to(DEV)][:, None],
+               (o, l, mag, span))
