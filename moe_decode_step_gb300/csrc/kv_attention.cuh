@@ -96,11 +96,14 @@ __device__ __forceinline__ void attn_seen(const AttnArgs& a, const AttnRow& w, i
 // halves long: one maximum and one vote for 32 tokens.
 //
 // Scales: a half lies in one block, so one exponent ek scales its scores and
-// one ev its values.  With t = score * log2(e) + ev the weights 2^(t - M), M
-// the running maximum of t, are the values' true relative sizes: in (0, 1],
-// which f16 holds, whatever the spread of the block scales.  The
-// denominator takes the same weights times 2^-ev in fp32 (|ev| <= 60 keeps
-// them inside its range).
+// one ev its values.  With t = score * log2(e) + ev the weights 2^(t - M) are
+// the values' true relative sizes, whatever the spread of the block scales.
+// M is the running maximum of t less kDecLead: the largest weight is 2^13, so
+// that f16 keeps all its bits down to 2^-27 of it, and what many keys far
+// behind a leading one add up to is not rounded away.  The denominator takes
+// the same weights times 2^-ev in fp32 (|ev| <= 60 keeps them inside its range).
+constexpr float kDecLead = 13.f;
+
 template <int D, int NT>   // NT: n-tiles of 8 rows in a tile
 struct DecShape {
   static constexpr int ROWS = 8 * NT;
@@ -916,8 +919,8 @@ static __global__ void __launch_bounds__(DecShape<D, NT>::THREADS, 1)
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-            x[q][r] = v;
-            up |= v > m[q][r];
+            x[q][r] = v - kDecLead;
+            up |= x[q][r] > m[q][r];
           }
         if (__any_sync(0xffffffffu, up)) {
           bool past = false;
@@ -951,6 +954,9 @@ static __global__ void __launch_bounds__(DecShape<D, NT>::THREADS, 1)
               if (large) {
                 t0 = fmaf(s[q][h][r], f, ev[h]) - ref;
                 t1 = fmaf(s[q][h][2 + r], f, ev[h]) - ref;
+                // (the lead rounded up to a step of t; a NaN stays)
+                t0 = t0 > 15.f ? 15.f : t0;
+                t1 = t1 > 15.f ? 15.f : t1;
               }
               s[q][h][r] = exp2_approx(t0);
               s[q][h][2 + r] = exp2_approx(t1);

@@ -23,9 +23,10 @@
 // of keys, which two streams share.
 //
 // Scales and weights as in kv_attention.cuh: t = score * log2(e) + ev per 16
-// keys, weights 2^(t - M).  M follows the maximum only when it grows by more
-// than 2^8, so that O in tensor memory is rarely rescaled; weights stay below
-// 2^8, far inside f16.
+// keys, weights 2^(t - M).  M is set 7 below the maximum, and again only when
+// a weight passes 2^15, so that O in tensor memory is rarely rescaled and the
+// largest weight stays between 2^7 and 2^15: f16 keeps all bits of keys up to
+// 2^21 behind a leading one.  (Prompts 937 us; set 8 below 948, 10 below 993.)
 //
 // Work split and joins as there, in tiles of 128 keys in the order (batch row,
 // row tile, KV head, keys).
@@ -55,6 +56,7 @@ constexpr int kPrKeys = 128;
 // 8,185 77 against 82; with up to 16 tiles more 86).
 constexpr int kPrLeast = 4;
 constexpr int kPrSlack = 8;
+constexpr float kPrLead = 7.f, kPrGrow = 15.f;   // the largest weight: set to, at most (log2)
 
 template <int D, bool PAIR>
 struct PrShape {
@@ -758,10 +760,12 @@ __device__ __noinline__ float2 pr_weights_large(PrShared& sh, const float4* sc, 
     for (int k = 0; k < 16; ++k)
       if ((unsigned)(c + k - from) < len) top = fmaxf(top, fmaf(s[k], g, f.y));
   }
-  const bool grow = top - m > 8.f;   // (no: nothing seen, or both infinite)
+  const bool grow = top - m > kPrGrow;   // (no: nothing seen, or both infinite)
   if (__any_sync(0xffffffffu, grow)) {
-    const float down = grow ? attn_factor(m, top) : 1.f;
-    if (grow) m = top;
+    float next = top - kPrLead;
+    if (top - next > kPrGrow) next = top;   // a step of t is as wide
+    const float down = grow ? attn_factor(m, next) : 1.f;
+    if (grow) m = next;
     l *= down;
     if (ofull) {
       pr_wait(ofull, parity, sh);
@@ -880,9 +884,9 @@ __device__ __forceinline__ void pr_softmax(const AttnArgs& a, PrShared& sh, uint
       tc_fence_after();
       // Weights against the running reference in one pass over the scores, in
       // registers until the tile's maximum is known; where a row of the warp
-      // outgrows its reference by 2^8 (its first tile, then rarely) O and the
-      // sums follow, and the pass is made again: once, as the new reference is
-      // within 1 of the maximum below kAttnLarge.
+      // outgrows its reference (its first tile, then rarely) O and the sums
+      // follow, and the pass is made again: once, as the new reference is within
+      // 1 of its place below kAttnLarge.
       uint32_t p[kPrKeys / 2];
 #pragma unroll 1
       for (;;) {
@@ -923,7 +927,7 @@ __device__ __forceinline__ void pr_softmax(const AttnArgs& a, PrShared& sh, uint
         }
         // (nothing seen yet, or a reference that t - M is not to be rounded against)
         const bool any = !(fabsf(m) < kAttnLarge);
-        const bool grow = x > (any ? -INFINITY : 8.f);
+        const bool grow = x > (any ? -INFINITY : kPrGrow);
         if (!__any_sync(0xffffffffu, grow)) {
           // into the columns of the scores
           l += lt;
@@ -932,7 +936,7 @@ __device__ __forceinline__ void pr_softmax(const AttnArgs& a, PrShared& sh, uint
           tmem_st32(ts + 32, p + 32);
           break;
         }
-        const float next = ref + x;
+        const float next = ref + x - kPrLead;
         if (__any_sync(0xffffffffu, grow && (!(fabsf(next) < kAttnLarge) || (any && m != -INFINITY)))) {
           const float2 r = pr_weights_large<D>(
               sh, sc, ts, to, masked ? lo - p0 : 0, masked ? (unsigned)max(hi - lo, 0) : kPrKeys,

@@ -79,3 +79,33 @@ def test_rows_beside_a_row_of_large_scores_stay_exact(rows):
     o, l, mag, span = (x[keep][:, None] for x in plain)
     base.check(c, out[torch.from_numpy(keep).to(DEV)][:, None], lse[torch.from_numpy(keep).to(DEV)][:, None],
                (o, l, mag, span))
+
+
+# ---------------------------------------------------------------------------
+# Attention: a key that leads
+# ---------------------------------------------------------------------------
+def _leading(lead, value_exp, heads=16, n=4096, q=1, d=128, seed=0):
+    """A row whose first key leads the others by some `lead` nats; its values are zeros, or in a
+    block whose scale is `value_exp` octaves above the others'."""
+    c = base.Case([(n - q, q)], heads, 2, d, 16, seed=seed, k_exp=(-9, -9), v_exp=(-8, -8), q_std=0.25)
+    c.q[:, :, 0] = 8.0
+    k, v = c.codes
+    k[:, :, :, 0] = np.where((k[:, :, :, 0] & 127) == 127, k[:, :, :, 0], 0)   # dim 0 is the lead's alone
+    first = c.table[0, 0]
+    k[first, :, 0] = 0
+    k[first, :, 0, 0] = 0x7E                        # 448 * 2^-9 * 8 = 7
+    if value_exp:
+        c.scale[1, first] += value_exp
+    else:
+        v[first, :, 0] = 0
+    return c, lead / 7.0
+
+
+@every_kernel
+@pytest.mark.parametrize("lead,value_exp", [(10, 0), (14, 0), (15, 0), (16, 0), (17, 0), (18, 0),
+                                            (8, 6), (8, 10), (0, 14)])
+def test_keys_behind_a_leading_one_keep_their_bits(lead, value_exp, rows):
+    for q in (1, 5):
+        c, scale = _leading(lead, value_exp, q=q, seed=lead + value_exp)
+        out, lse = _run(c, rows, scale=scale)
+        base.check(c, out, lse, c.expect(scale), (lead, value_exp, q))
