@@ -413,8 +413,10 @@ int moe_kv_append(void* stream, const moe_kv_cache_t* cache, const void* k, cons
  *   out = sum_j softmax_j(scale * q . k_j) v_j,  lse = ln sum_j exp(scale * q . k_j)
  * (out 0 and lse -infinity when it sees none).  Keys and values it does not
  * see do not reach its result, whatever they hold.  Products and sums are
- * exact products summed in fp32; the probabilities enter the second product
- * rounded to f16.
+ * exact products summed in fp32; lse's sum takes its terms in fp32, whatever
+ * the scales.  A key's weight in the second product, its probability times its
+ * block's V scale, is rounded to f16 beside the row's largest: to 2^-11 of
+ * itself down to 2^-21 of that one, to 2^-32 of that one below.
  * max_blocks * block_size and n_tokens * n_heads are below 2^31 - 128.  seq_lens is read as at most
  * max_blocks * block_size and q_start as within
  * [0, n_tokens], not descending; rows of q past q_start[n_rows] are left

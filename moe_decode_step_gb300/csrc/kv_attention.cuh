@@ -101,7 +101,9 @@ __device__ __forceinline__ void attn_seen(const AttnArgs& a, const AttnRow& w, i
 // M is the running maximum of t less kDecLead: the largest weight is 2^13, so
 // that f16 keeps all its bits down to 2^-27 of it, and what many keys far
 // behind a leading one add up to is not rounded away.  The denominator takes
-// the same weights times 2^-ev in fp32 (|ev| <= 60 keeps them inside its range).
+// the same weights times 2^-ev in fp32; blocks of ev below kKvExpLow (zeros, or
+// values below 2^-19) take theirs with 2^(kKvExpLow - ev) more, which the
+// second product's do not have.
 constexpr float kDecLead = 13.f;
 
 template <int D, int NT>   // NT: n-tiles of 8 rows in a tile
@@ -501,9 +503,11 @@ __device__ __forceinline__ float attn_inverse(float l) { return l > 0.f ? 1.f / 
 // Scores past this are so far apart in fp32 (2^-2 and more) that t - M rounded
 // once is no weight any more: t is rounded first, as M was, and t - M is exact.
 constexpr float kAttnLarge = 4194304.f;   // 2^22
-// 2^(m - ref) with both -infinity (nothing seen) giving 1.
-__device__ __forceinline__ float attn_factor(float m, float ref) {
-  return m == -INFINITY ? (ref == -INFINITY ? 1.f : 0.f) : exp2_approx(m - ref);
+// 2^((m - ref) / 2) with both -infinity (nothing seen) giving 1.  Sums of the
+// values take its square; the denominator takes it twice: between blocks of
+// exponents -60 and 60 the square may underflow where the denominator counts.
+__device__ __forceinline__ float attn_half_factor(float m, float ref) {
+  return m == -INFINITY ? (ref == -INFINITY ? 1.f : 0.f) : exp2_approx(0.5f * (m - ref));
 }
 
 // Partial sums of a piece of a tile.
@@ -599,8 +603,10 @@ __device__ __noinline__ void dec_join(const DecOut* to, const DecJob* job, int j
         for (int x = 0; x < R; ++x) tm[x] = warp_max(mk[x]);
 #pragma unroll
         for (int x = 0; x < R; ++x) {
-          f[x] = mk[x] == -INFINITY && lk[x] == 0.f ? 0.f : attn_factor(mk[x], tm[x]);
-          tl[x] = warp_sum(lk[x] * f[x]);
+          const float h =
+              mk[x] == -INFINITY && lk[x] == 0.f ? 0.f : attn_half_factor(mk[x], tm[x]);
+          f[x] = h * h;
+          tl[x] = warp_sum(lk[x] * h * h);
 #pragma unroll
           for (int n = 0; n < V; ++n) acc[x][n] = 0.f;
         }
@@ -888,14 +894,18 @@ static __global__ void __launch_bounds__(DecShape<D, NT>::THREADS, 1)
           }
         }
         // ---- weights ----
-        float ke[2], ev[2], un[2];
+        float ke[2], ev[2], un[2];   // ev: down to kKvExpLow
+        int more[2];                 // what is left of it below that
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int e = (int)((meta[h] >> 8) & 0xFFu) - 128;
           ke[h] = pow2f((int)(meta[h] & 0xFFu) - 128);
-          ev[h] = (float)e;
-          un[h] = pow2f(-e);
+          more[h] = max(kKvExpLow - e, 0);
+          ev[h] = (float)(e + more[h]);
+          un[h] = pow2f(-e - more[h]);
         }
+        const bool low = (more[0] | more[1]) != 0;
+        const float evt[2] = {ev[0] - (float)more[0], ev[1] - (float)more[1]};
         const bool masked = p0 + 32 > hi_all || p0 < lo_all || !((meta[0] & meta[1]) >> 16);
         if (masked) {
 #pragma unroll
@@ -914,8 +924,8 @@ static __global__ void __launch_bounds__(DecShape<D, NT>::THREADS, 1)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             // (a factor that underflowed to 0 makes NaN of -infinity, which fmaxf drops)
-            float v = fmaxf(fmaf(fmaxf(s[q][0][r], s[q][0][2 + r]), fac[q][r] * ke[0], ev[0]),
-                            fmaf(fmaxf(s[q][1][r], s[q][1][2 + r]), fac[q][r] * ke[1], ev[1]));
+            float v = fmaxf(fmaf(fmaxf(s[q][0][r], s[q][0][2 + r]), fac[q][r] * ke[0], evt[0]),
+                            fmaf(fmaxf(s[q][1][r], s[q][1][2 + r]), fac[q][r] * ke[1], evt[1]));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
@@ -930,9 +940,9 @@ static __global__ void __launch_bounds__(DecShape<D, NT>::THREADS, 1)
             for (int r = 0; r < 2; ++r) {
               const float n = fmaxf(m[q][r], x[q][r]);
               past |= n > -INFINITY && fabsf(n) >= kAttnLarge;
-              const float d = attn_factor(m[q][r], n);
+              const float half = attn_half_factor(m[q][r], n), d = half * half;
               m[q][r] = n;
-              l[q][r] *= d;
+              l[q][r] = l[q][r] * half * half;
 #pragma unroll
               for (int j = 0; j < CH / 2; ++j) {
                 o[q][j][r] *= d;
@@ -952,12 +962,14 @@ static __global__ void __launch_bounds__(DecShape<D, NT>::THREADS, 1)
               const float f = fac[q][r] * ke[h], c = ev[h] - ref;
               float t0 = fmaf(s[q][h][r], f, c), t1 = fmaf(s[q][h][2 + r], f, c);
               if (large) {
-                t0 = fmaf(s[q][h][r], f, ev[h]) - ref;
-                t1 = fmaf(s[q][h][2 + r], f, ev[h]) - ref;
+                const float b = (float)more[h];
+                t0 = fmaf(s[q][h][r], f, evt[h]) - ref;
+                t1 = fmaf(s[q][h][2 + r], f, evt[h]) - ref;
                 // (the lead rounded up to a step of t; a NaN stays)
-                t0 = t0 > 15.f ? 15.f : t0;
-                t1 = t1 > 15.f ? 15.f : t1;
+                t0 = (t0 > 15.f ? 15.f : t0) + b;
+                t1 = (t1 > 15.f ? 15.f : t1) + b;
               }
+
               s[q][h][r] = exp2_approx(t0);
               s[q][h][2 + r] = exp2_approx(t1);
             }
@@ -975,6 +987,12 @@ static __global__ void __launch_bounds__(DecShape<D, NT>::THREADS, 1)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
               l[q][r] = fmaf(un[h], s[q][h][r] + s[q][h][2 + r], l[q][r]);
+          if (low) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s[q][h][i] *= pow2f(-more[h]);
+          }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             pb[q][h][0] = movmatrix(pack_f16x2(s[q][h][0], s[q][h][1]));

@@ -56,6 +56,7 @@ constexpr int kPrKeys = 128;
 // 8,185 77 against 82; with up to 16 tiles more 86).
 constexpr int kPrLeast = 4;
 constexpr int kPrSlack = 8;
+constexpr float kPrFar = 0x1p100f;               // an exponent that no score comes near
 constexpr float kPrLead = 7.f, kPrGrow = 15.f;   // the largest weight: set to, at most (log2)
 
 template <int D, bool PAIR>
@@ -383,7 +384,9 @@ struct PrShared {
   int nan[8];               // by segment: a NaN value in a masked tile
   int open[2];              // the CTA's tiles cut by its ends: set
   DecPiece piece[2];        // and which they are
-  float4 scale[4][8];       // by tile of keys: 2^ek, ev, 2^-ev of 16 keys each
+  // by tile of keys, of 16 keys each: 2^ek, ev, 2^-ev, ev; where ev is below
+  // kKvExpLow: 2^ek, kPrFar, 2^-kKvExpLow, ev
+  float4 scale[4][8];
   float m1[128], l1[128];   // the second stream's, when the two are joined
   unsigned nan1[4][128];
   DecOut out;
@@ -585,8 +588,10 @@ __device__ __forceinline__ void pr_convert(const AttnArgs& a, PrShared& sh, uint
     if (warp == 0 && lane < 8) {
       const int e = kv_exp(ev);
       // a block outside the cache: weights 0
-      sh.scale[n & 3][lane] = block ? make_float4(pow2f(kv_exp(ek)), (float)e, pow2f(-e), 0.f)
-                                    : make_float4(0.f, -INFINITY, 0.f, 0.f);
+      sh.scale[n & 3][lane] =
+          block ? make_float4(pow2f(kv_exp(ek)), e < kKvExpLow ? kPrFar : (float)e,
+                              pow2f(-max(e, kKvExpLow)), (float)e)
+                : make_float4(0.f, -INFINITY, 0.f, -INFINITY);
     }
     convert(smem + S::KOFF, false);
     mbar_arrive(&sh.kfull[n & 1]);
@@ -738,13 +743,15 @@ __device__ __forceinline__ void pr_scale_sums(uint32_t to, float by) {
   }
 }
 
-// A tile's weights where a row of the warp has scores past kAttnLarge: two
-// passes, the maximum of t, then t - M, which is exact near M.  (M alone, its
-// rounding as large as the growth that a pass allows, need not settle.)  The
+// A tile's weights where a row of the warp has scores past kAttnLarge, or sees
+// keys whose ev is below kKvExpLow (an exponent of kPrFar stands for it, so
+// that the pass over the scores ends up here): two passes, the maximum of t,
+// then t - M, which is exact near M.  (M alone, its rounding as large as the
+// growth that a pass allows, need not settle.)  The
 // weights go into the columns of scores that are read already.  ofull: the
 // sums' barrier, null where the segment has none yet; returns M and the sum.
 template <int D>
-__device__ __noinline__ float2 pr_weights_large(PrShared& sh, const float4* sc, uint32_t ts,
+__device__ __noinline__ float2 pr_weights_apart(PrShared& sh, const float4* sc, uint32_t ts,
                                                 uint32_t to, int from, unsigned len, float fac,
                                                 float m, float l, uint64_t* ofull,
                                                 uint32_t parity) {
@@ -758,15 +765,15 @@ __device__ __noinline__ float2 pr_weights_large(PrShared& sh, const float4* sc, 
     const float g = fmaxf(fac * f.x, 1e-38f);
 #pragma unroll
     for (int k = 0; k < 16; ++k)
-      if ((unsigned)(c + k - from) < len) top = fmaxf(top, fmaf(s[k], g, f.y));
+      if ((unsigned)(c + k - from) < len) top = fmaxf(top, fmaf(s[k], g, f.w));
   }
   const bool grow = top - m > kPrGrow;   // (no: nothing seen, or both infinite)
   if (__any_sync(0xffffffffu, grow)) {
     float next = top - kPrLead;
     if (top - next > kPrGrow) next = top;   // a step of t is as wide
-    const float down = grow ? attn_factor(m, next) : 1.f;
+    const float half = grow ? attn_half_factor(m, next) : 1.f, down = half * half;
     if (grow) m = next;
-    l *= down;
+    l = l * half * half;
     if (ofull) {
       pr_wait(ofull, parity, sh);
       __syncwarp();
@@ -784,15 +791,17 @@ __device__ __noinline__ float2 pr_weights_large(PrShared& sh, const float4* sc, 
     tmem_wait_ld();
     const float4 f = sc[c / 16];
     const float g = fmaxf(fac * f.x, 1e-38f);
+    const int more = max(kKvExpLow - max((int)f.w, kKvExpMin), 0);
+    const float by = pow2f(-more);
     float sum = 0.f;
 #pragma unroll
     for (int k = 0; k < 16; k += 2) {
 #pragma unroll
       for (int e = k; e < k + 2; ++e) {
-        s[e] = (unsigned)(c + e - from) < len ? exp2_approx(fmaf(s[e], g, f.y) - ref) : 0.f;
+        s[e] = (unsigned)(c + e - from) < len ? exp2_approx(fmaf(s[e], g, f.w) - ref + more) : 0.f;
         sum += s[e];
       }
-      p[k / 2] = pack_f16x2(s[k], s[k + 1]);
+      p[k / 2] = pack_f16x2(s[k] * by, s[k + 1] * by);
     }
     l = fmaf(f.z, sum, l);
     tmem_st8(ts + c / 2, p);
@@ -938,16 +947,16 @@ __device__ __forceinline__ void pr_softmax(const AttnArgs& a, PrShared& sh, uint
         }
         const float next = ref + x - kPrLead;
         if (__any_sync(0xffffffffu, grow && (!(fabsf(next) < kAttnLarge) || (any && m != -INFINITY)))) {
-          const float2 r = pr_weights_large<D>(
+          const float2 r = pr_weights_apart<D>(
               sh, sc, ts, to, masked ? lo - p0 : 0, masked ? (unsigned)max(hi - lo, 0) : kPrKeys,
               fac, m, l, mine > 0 ? &sh.ofull[t] : nullptr, (cnt - 1) & 1);
           m = r.x;
           l = r.y;
           break;
         }
-        const float down = grow ? attn_factor(m, next) : 1.f;
+        const float half = grow ? attn_half_factor(m, next) : 1.f, down = half * half;
         if (grow) m = next;
-        l *= down;
+        l = l * half * half;
         if (mine > 0) {
           pr_wait(&sh.ofull[t], (cnt - 1) & 1, sh);
           __syncwarp();
@@ -993,9 +1002,10 @@ __device__ __forceinline__ void pr_softmax(const AttnArgs& a, PrShared& sh, uint
       pr_streams_sync();
       if (t == 0) {
         const float m1 = sh.m1[row], mx = fmaxf(m, m1);
-        f0 = attn_factor(m, mx);
-        f1 = nseg > 1 ? attn_factor(m1, mx) : 0.f;
-        l = l * f0 + (nseg > 1 ? sh.l1[row] * f1 : 0.f);
+        const float h0 = attn_half_factor(m, mx), h1 = nseg > 1 ? attn_half_factor(m1, mx) : 0.f;
+        f0 = h0 * h0;
+        f1 = h1 * h1;
+        l = l * h0 * h0 + (nseg > 1 ? sh.l1[row] * h1 * h1 : 0.f);
         m = mx;
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) bits[k] |= sh.nan1[k][row];

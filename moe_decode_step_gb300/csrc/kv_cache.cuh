@@ -10,6 +10,11 @@
 namespace moe {
 
 constexpr int kKvExpMin = -60, kKvExpMax = 60;   // scale exponents of a block
+// Attention's weights carry the values' exponent ev down to this one only; the
+// rest of a smaller one multiplies them where they meet the values.  A weight
+// relative to M, which a key of exponent 60 may have set, so stays above
+// 2^-126 as long as the key counts in the denominator: 60 + 28 + 38 = 126.
+constexpr int kKvExpLow = -28;
 
 struct KvView {
   uint8_t* k;

@@ -109,3 +109,39 @@ def test_keys_behind_a_leading_one_keep_their_bits(lead, value_exp, rows):
         c, scale = _leading(lead, value_exp, q=q, seed=lead + value_exp)
         out, lse = _run(c, rows, scale=scale)
         base.check(c, out, lse, c.expect(scale), (lead, value_exp, q))
+
+
+# ---------------------------------------------------------------------------
+# Attention: block scales at the ends of their range
+# ---------------------------------------------------------------------------
+@every_kernel
+@pytest.mark.parametrize("behind", [0, 4, 8, 20, 40])
+def test_small_values_count_in_the_denominator(behind, rows):
+    """One key at V exponent 60, the others at -60 and `behind` bits behind it: their weights are
+    2^-120 of its own beside the values, but count in full in the sum."""
+    for heads, lo in ((16, -60), (2, -60), (16, -29), (16, -28)):
+        c = base.Case([(1000, 1), (300, 3)], heads, 2, 128, 16, seed=1, k_exp=(-9, -9), v_exp=(lo, lo),
+                      q_std=0.0)
+        for r in range(2):
+            first = c.table[r, 0]
+            c.scale[1, first] = 60 + 127
+            c.codes[0, first, :, 0] = 0
+            c.codes[0, first, :, 0, 0] = 0x7E       # 448 * 2^-9
+            c.codes[1, first, :, 1:] = 0            # the block's other values are zeros
+        c.q[:, :, 0] = 8.0
+        for b in range(c.n_blocks):
+            c.codes[0, b, :, :, 0] = np.where((c.codes[0, b, :, :, 0] & 127) == 127,
+                                              c.codes[0, b, :, :, 0], 0)
+        for r in range(2):
+            c.codes[0, c.table[r, 0], :, 0, 0] = 0x7E
+        scale = max(behind, 1e-3) * np.log(2.0) / 7.0
+        out, lse = _run(c, rows, scale=scale)
+        base.check(c, out, lse, c.expect(scale), (heads, lo))
+
+
+@every_kernel
+def test_scales_over_the_whole_range(rows):
+    for v_exp in ((-60, 60), (-60, -20), (-30, -26), (-60, -60)):
+        c = base.Case([(200, 1), (90, 6), (600, 2)], 16, 2, 128, 16, seed=8, v_exp=v_exp)
+        out, lse = _run(c, rows, scale=0.02)
+        base.check(c, out, lse, c.expect(0.02), v_exp)
