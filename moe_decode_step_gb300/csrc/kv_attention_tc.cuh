@@ -835,11 +835,16 @@ __device__ __forceinline__ void pr_softmax(const AttnArgs& a, PrShared& sh, uint
     const bool real = i < c.w.n;
     attn_seen(a, c.w, min(i, c.w.n - 1), lo, hi);
     if (!PAIR) pr_streams_sync();   // both streams are through with the last item's queries
+    // A query of infinities or NaN is NaN where it sees a key, and 0 where it sees
+    // only blocks outside the cache, whose scores it would make NaN too: it goes
+    // in as zeros, and the sum of what it saw becomes NaN at the end.
+    bool poison;
     float fac = 0.f;
     {
       const uint16_t* q = a.q + (long long)(c.w.tok + (real ? i : 0)) * a.q_ts + head * a.q_hs;
       uint8_t* dst = smem + (PAIR ? t * S::QBYTES : 0) + row * 16;
       float mx = 0.f;
+      bool finite = true;
 #pragma unroll
       for (int k = 0; k < D / 8; ++k) {
         uint4 w = make_uint4(0, 0, 0, 0);
@@ -849,6 +854,7 @@ __device__ __forceinline__ void pr_softmax(const AttnArgs& a, PrShared& sh, uint
         for (int e = 0; e < 4; ++e) {
           const float2 f = unpack16(u[e], a.f16);
           mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+          finite = finite && fabsf(f.x) < INFINITY && fabsf(f.y) < INFINITY;
         }
       }
       const int be = (int)(__float_as_uint(mx) >> 23);
@@ -856,11 +862,12 @@ __device__ __forceinline__ void pr_softmax(const AttnArgs& a, PrShared& sh, uint
       const float down =
           a.scale_log2 == 0.f ? 0.f : (a.scale_log2 < 0.f ? -pow2f(-shift) : pow2f(-shift));
       fac = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2) * pow2f(shift);
+      poison = !finite;
       if (PAIR || t == 0) {
 #pragma unroll
         for (int k = 0; k < D / 8; ++k) {
           uint4 w = make_uint4(0, 0, 0, 0);
-          if (real) w = *reinterpret_cast<const uint4*>(q + 8 * k);
+          if (real && finite) w = *reinterpret_cast<const uint4*>(q + 8 * k);
           const float2 f0 = unpack16(w.x, a.f16), f1 = unpack16(w.y, a.f16),
                        f2 = unpack16(w.z, a.f16), f3 = unpack16(w.w, a.f16);
           *reinterpret_cast<uint4*>(dst + k * S::QGROUP) = make_uint4(
@@ -1013,7 +1020,7 @@ __device__ __forceinline__ void pr_softmax(const AttnArgs& a, PrShared& sh, uint
     }
     __syncwarp();
     tc_fence_after();
-    if (*(volatile int*)&sh.dead) l = __int_as_float(0x7FFFFFFF);
+    if (*(volatile int*)&sh.dead || (poison && l > 0.f)) l = __int_as_float(0x7FFFFFFF);
     if (PAIR || t == 0) {
       const float inv = attn_inverse(l);
       const long long tok = c.w.tok + i;

@@ -145,3 +145,18 @@ def test_scales_over_the_whole_range(rows):
         c = base.Case([(200, 1), (90, 6), (600, 2)], 16, 2, 128, 16, seed=8, v_exp=v_exp)
         out, lse = _run(c, rows, scale=0.02)
         base.check(c, out, lse, c.expect(0.02), v_exp)
+
+
+@every_kernel
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+def test_a_query_that_sees_only_blocks_outside_the_cache_gives_zero(bad, rows):
+    """... whatever the query holds; and one that sees some keys is as without the others."""
+    c = base.Case([(31, 1), (100, 3), (20, 40)], 8, 2, 128, 32, seed=4)
+    c.table[0] = -1
+    c.table[1, :2] = c.n_blocks
+    q = c.q.clone()
+    q[0, 2] = bad
+    q[0, 5, 7] = -bad
+    out, lse = _run(c, rows, q=q)
+    base.check(c, out, lse, c.expect(128 ** -0.5))
+    assert not out[0].any() and torch.isneginf(lse[0]).all()
