@@ -309,8 +309,9 @@ int moe_kv_attention(void* stream, const moe_kv_cache_t* cache, const moe_kv_att
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   a.arrived = static_cast<unsigned*>(t.workspace);
   a.partial = reinterpret_cast<float*>(static_cast<char*>(t.workspace) + arrived_bytes(dev->n_sm));
-  return cache->head_dim == 64 ? launch_attention<64>(a, dev->n_sm, t.max_q, st)
-                               : launch_attention<128>(a, dev->n_sm, t.max_q, st);
+  const int max_q = std::max(t.max_q, 1);   // a hint, whatever it says
+  return cache->head_dim == 64 ? launch_attention<64>(a, dev->n_sm, max_q, st)
+                               : launch_attention<128>(a, dev->n_sm, max_q, st);
 }
 
 int moe_route(void* stream, const moe_route_t* cfg, const void* logits, int dtype,

@@ -160,3 +160,15 @@ def test_a_query_that_sees_only_blocks_outside_the_cache_gives_zero(bad, rows):
     out, lse = _run(c, rows, q=q)
     base.check(c, out, lse, c.expect(128 ** -0.5))
     assert not out[0].any() and torch.isneginf(lse[0]).all()
+
+
+# ---------------------------------------------------------------------------
+# Attention: what the host announces
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("max_q", [-2 ** 31, -1000, 0, 10 ** 6, 2 ** 31 - 1])
+@pytest.mark.parametrize("window", [0, 9])
+def test_any_announced_length_gives_the_same_result(max_q, window):
+    c = base.Case([(100, 1)] * 64 + [(40, 3)], 16, 8, 64, 16, seed=5)
+    c.max_q = max_q
+    out, lse = c.run(window=window)
+    base.check(c, out, lse, c.expect(64 ** -0.5, window=window))
