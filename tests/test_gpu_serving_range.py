@@ -172,3 +172,25 @@ def test_any_announced_length_gives_the_same_result(max_q, window):
     c.max_q = max_q
     out, lse = c.run(window=window)
     base.check(c, out, lse, c.expect(64 ** -0.5, window=window))
+
+
+# ---------------------------------------------------------------------------
+# Block tables
+# ---------------------------------------------------------------------------
+PLAN_ROWS = """
+import sys
+sys.path[:0] = {path!r}
+import numpy as np, test_gpu_serving as base
+rows = {rows}
+base._plan_case(np.full(rows, 5), np.ones(rows, int), 16, 2, 3, rows)
+"""
+
+
+@pytest.mark.parametrize("rows", [6109, 6110, 6143, 6144])
+def test_plan_needs_no_larger_plan_before_it(rows):
+    """Rows at which the kernel's shared memory passes 48 KB, each as a process's first plan."""
+    import subprocess
+    import sys
+    p = subprocess.run([sys.executable, "-c", PLAN_ROWS.format(path=sys.path, rows=rows)],
+                       capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0, p.stderr[-2000:]
