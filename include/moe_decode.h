@@ -356,7 +356,8 @@ typedef struct {
  * its block_table row) and gets q_lens[r] new ones.  New blocks are taken in
  * row order from the top of the stack free_list[0 .. *n_free): the i-th new
  * block of the step is free_list[*n_free - 1 - i].  A row is served when its
- * blocks fit max_blocks, its tokens (if any) fit n_slots and the stack still holds all
+ * blocks fit max_blocks and its length an int32, its tokens (if any) fit n_slots
+ * and the stack still holds all
  * the new blocks it needs (once the stack is short, later rows that need
  * none are still served); a negative length leaves a row unserved, with no
  * tokens.  Writes, with q_start[r] the sum of the q_lens before r:

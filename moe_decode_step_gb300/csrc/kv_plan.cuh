@@ -91,7 +91,8 @@ __device__ __forceinline__ PlanRow plan_row(const PlanArgs& p, int r) {
   } else {
     w.have = (w.ctx + up) >> p.bs_log2;
     const long long total = ((long long)w.ctx + w.q + up) >> p.bs_log2;
-    w.need = total <= p.max_blocks ? total - w.have : -1;
+    // (positions are 32-bit below: a table may have room for more tokens)
+    w.need = total <= p.max_blocks && (long long)w.ctx + w.q <= INT32_MAX ? total - w.have : -1;
   }
   return w;
 }

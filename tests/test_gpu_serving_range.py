@@ -194,3 +194,15 @@ def test_plan_needs_no_larger_plan_before_it(rows):
     p = subprocess.run([sys.executable, "-c", PLAN_ROWS.format(path=sys.path, rows=rows)],
                        capture_output=True, text=True, timeout=300)
     assert p.returncode == 0, p.stderr[-2000:]
+
+
+def test_plan_lengths_past_31_bits_are_not_served():
+    """A table wide enough for them: the row keeps its length, its tokens go nowhere."""
+    bs, mb = 128, 2 ** 24 + 8
+    table = torch.zeros(2, mb, dtype=torch.int32, device=DEV)
+    ctx = base._dev([2 ** 31 - 100, 5])
+    p = M.kv_plan(ctx, base._dev([200, 1]), table, base._dev([3, 4]), base._dev([2]), bs, 300)
+    assert base._np(p.seq_lens).tolist() == [2 ** 31 - 100, 6] and int(p.n_unserved) == 1
+    slots = base._np(p.slot_map)
+    assert (slots[:200] == -1).all() and slots[200] == 5 and (slots[201:] == -1).all()
+    assert int(p.n_free) == 2
