@@ -366,7 +366,8 @@ typedef struct {
  *  - q_start [n_rows + 1],
  *  - slot_map [n_slots]: token i of row r goes to slot
  *    block * block_size + offset, at q_start[r] + i; -1 for the tokens of
- *    unserved rows and past the last row,
+ *    unserved rows, past the last row, and where a block id that the table
+ *    holds is negative or gives no int32,
  *  - *n_free_out: blocks left on the stack, *n_unserved: rows not served.
  * Outputs must not overlap inputs (n_free_out is not n_free).  Rows of
  * block_table are table_stride entries apart.  *n_free is read as at most

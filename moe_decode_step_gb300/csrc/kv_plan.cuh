@@ -164,7 +164,8 @@ static __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const Plan
         const int have = (int)(((long long)ctx + bs - 1) >> p.bs_log2), b = pos >> p.bs_log2;
         const int id = b < have ? p.table[lo * p.tstride + b]
                                 : p.free_list[n_free - 1 - (s_blk[lo] + b - have)];
-        slot = id * bs + (pos & (bs - 1));
+        const long long at = (long long)id * bs + (pos & (bs - 1));
+        slot = at >= 0 && at <= INT32_MAX ? (int)at : -1;
       }
     }
     p.slot[i] = slot;

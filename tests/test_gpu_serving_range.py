@@ -206,3 +206,11 @@ def test_plan_lengths_past_31_bits_are_not_served():
     slots = base._np(p.slot_map)
     assert (slots[:200] == -1).all() and slots[200] == 5 and (slots[201:] == -1).all()
     assert int(p.n_free) == 2
+
+
+def test_plan_block_ids_whose_slots_pass_31_bits_map_nowhere():
+    ids = [2 ** 27, 2 ** 27 + 1, -2 ** 28, 2 ** 31 - 1, -2 ** 31, 2 ** 27 - 1]
+    p = M.kv_plan(base._dev([3] * 6), base._dev([1] * 6), base._dev(ids)[:, None], base._dev([0]),
+                  base._dev([0]), 16, 6)
+    slots = base._np(p.slot_map).astype(np.int64)
+    assert (slots[:5] < 0).all() and slots[5] == (2 ** 27 - 1) * 16 + 3
