@@ -150,7 +150,8 @@ static __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const Plan
   const int bs = 1 << p.bs_log2;
   const int stride = gridDim.x * kPlanThreads;
   // slots: the row by bisection of the first tokens
-  for (int i = blockIdx.x * kPlanThreads + t; i < p.n_slots; i += stride) {
+  for (long long at = blockIdx.x * kPlanThreads + t; at < p.n_slots; at += stride) {
+    const int i = (int)at;
     int slot = -1;
     if (i < s_tok[p.rows]) {
       int lo = 0, hi = p.rows;
@@ -164,8 +165,8 @@ static __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const Plan
         const int have = (int)(((long long)ctx + bs - 1) >> p.bs_log2), b = pos >> p.bs_log2;
         const int id = b < have ? p.table[lo * p.tstride + b]
                                 : p.free_list[n_free - 1 - (s_blk[lo] + b - have)];
-        const long long at = (long long)id * bs + (pos & (bs - 1));
-        slot = at >= 0 && at <= INT32_MAX ? (int)at : -1;
+        const long long wide = (long long)id * bs + (pos & (bs - 1));
+        slot = wide >= 0 && wide <= INT32_MAX ? (int)wide : -1;
       }
     }
     p.slot[i] = slot;

@@ -214,3 +214,11 @@ def test_plan_block_ids_whose_slots_pass_31_bits_map_nowhere():
                   base._dev([0]), 16, 6)
     slots = base._np(p.slot_map).astype(np.int64)
     assert (slots[:5] < 0).all() and slots[5] == (2 ** 27 - 1) * 16 + 3
+
+
+def test_plan_fills_a_slot_map_of_any_length():
+    n = 2 ** 31 - 1
+    p = M.kv_plan(base._dev([3]), base._dev([2]), base._dev([[7]]), base._dev([0]), base._dev([0]), 16, n)
+    assert base._np(p.slot_map[:3]).tolist() == [115, 116, -1]
+    tail = p.slot_map[2:]
+    assert all(int(x.max()) == -1 and int(x.min()) == -1 for x in tail.split(2 ** 29))
