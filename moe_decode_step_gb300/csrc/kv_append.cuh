@@ -139,12 +139,12 @@ static __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) kv_append_
   // where the slot after each lane's begins another block
   unsigned long long leaders = 0, ends = 0;
   for (int k = 0; k < a.chunk; k += 32) {
-    const int t = c0 + k + lane;
     int b = -1, prev = -1, next = -1;
-    if (k + lane < a.chunk && t < a.n_tokens) {
+    if (k + lane < min(a.chunk, a.n_tokens - c0)) {
+      const int t = c0 + k + lane;
       b = append_block_of(a, __ldg(a.slot + t));
       if (t > 0) prev = append_block_of(a, __ldg(a.slot + t - 1));
-      if (t + 1 < a.n_tokens) next = append_block_of(a, __ldg(a.slot + t + 1));
+      if (t < a.n_tokens - 1) next = append_block_of(a, __ldg(a.slot + t + 1));
     }
     leaders |= (unsigned long long)__ballot_sync(0xffffffffu, b >= 0 && b != prev) << k;
     ends |= (unsigned long long)__ballot_sync(0xffffffffu, b != next) << k;

@@ -222,3 +222,14 @@ def test_plan_fills_a_slot_map_of_any_length():
     assert base._np(p.slot_map[:3]).tolist() == [115, 116, -1]
     tail = p.slot_map[2:]
     assert all(int(x.max()) == -1 and int(x.min()) == -1 for x in tail.split(2 ** 29))
+
+
+def test_append_of_as_many_tokens_as_32_bits_count():
+    n = 2 ** 31 - 1
+    slots = torch.full((n,), -1, dtype=torch.int32, device=DEV)
+    slots[-1] = 17
+    x = torch.ones(1, 1, 64, dtype=torch.bfloat16, device=DEV).expand(n, 1, 64)
+    k, v = (torch.zeros(2, 1, 16, 64, dtype=torch.uint8, device=DEV) for _ in range(2))
+    ks, vs = (torch.full((2, 1), 127, dtype=torch.uint8, device=DEV) for _ in range(2))
+    M.KVCache(k, v, ks, vs).append(x, x, slots)
+    assert not k[0].any() and not k[1, 0, 2:].any() and k[1, 0, 1].all()
