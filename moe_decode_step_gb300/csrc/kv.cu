@@ -174,8 +174,8 @@ int moe_kv_plan(void* stream, const int32_t* ctx_lens, const int32_t* q_lens, in
                 const int32_t* free_list, int free_cap, const int32_t* n_free, int block_size,
                 int32_t* seq_lens, int32_t* q_start, int32_t* slot_map, int n_slots,
                 int32_t* n_free_out, int32_t* n_unserved) {
-  if (!ctx_lens || !q_lens || !block_table || !free_list || !n_free || !seq_lens || !q_start ||
-      (!slot_map && n_slots > 0) || !n_free_out || !n_unserved)
+  if (!ctx_lens || !q_lens || !block_table || (!free_list && free_cap > 0) || !n_free ||
+      !seq_lens || !q_start || (!slot_map && n_slots > 0) || !n_free_out || !n_unserved)
     return MOE_ERR_INVALID_ARG;
   const int bl = block_log2(block_size);
   if (n_rows < 1 || max_blocks < 1 || table_stride < max_blocks || free_cap < 0 || n_slots < 0 ||
@@ -203,7 +203,8 @@ int moe_kv_release(void* stream, const uint8_t* finished, int n_rows, int32_t* s
                    const int32_t* block_table, int64_t table_stride, int max_blocks,
                    int32_t* free_list, int free_cap, const int32_t* n_free, int block_size,
                    int32_t* n_free_out) {
-  if (!finished || !seq_lens || !block_table || !free_list || !n_free || !n_free_out)
+  if (!finished || !seq_lens || !block_table || (!free_list && free_cap > 0) || !n_free ||
+      !n_free_out)
     return MOE_ERR_INVALID_ARG;
   const int bl = block_log2(block_size);
   if (n_rows < 1 || max_blocks < 1 || table_stride < max_blocks || free_cap < 0 || bl < 0)

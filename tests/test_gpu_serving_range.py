@@ -233,3 +233,13 @@ def test_append_of_as_many_tokens_as_32_bits_count():
     ks, vs = (torch.full((2, 1), 127, dtype=torch.uint8, device=DEV) for _ in range(2))
     M.KVCache(k, v, ks, vs).append(x, x, slots)
     assert not k[0].any() and not k[1, 0, 2:].any() and k[1, 0, 1].all()
+
+
+def test_an_empty_free_list_serves_rows_that_need_no_block():
+    none = torch.empty(0, dtype=torch.int32, device=DEV)
+    table = base._dev([[4], [9]])
+    p = M.kv_plan(base._dev([3, 16]), base._dev([2, 1]), table, none, base._dev([0]), 16, 3)
+    assert base._np(p.slot_map).tolist() == [67, 68, -1] and int(p.n_unserved) == 1
+    seq, n = base._dev([3, 16]), base._dev([0])
+    M.kv_release(torch.tensor([True, False], device=DEV), seq, table, none, n, 16)
+    assert base._np(seq).tolist() == [0, 16] and int(n) == 0
