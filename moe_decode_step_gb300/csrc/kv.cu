@@ -185,11 +185,13 @@ int moe_kv_plan(void* stream, const int32_t* ctx_lens, const int32_t* q_lens, in
   const Device* dev;
   int rc = begin(&dev);
   if (rc) return rc;
-  // (the kernel's static shared memory counts towards the 48 KB too)
+  // (past 48 KB with the kernel's static shared memory, for which there is room)
   const int smem = (2 * n_rows + 1) * 4;
-  const cudaError_t e = cudaFuncSetAttribute(
-      kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (2 * kPlanMaxRows + 1) * 4);
-  if (e != cudaSuccess) return cuda_fail(e);
+  if (smem > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (2 * kPlanMaxRows + 1) * 4);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
   PlanArgs p{ctx_lens, q_lens,   n_rows,  block_table, table_stride, max_blocks, free_list, free_cap,
              n_free,   bl,       seq_lens, q_start,    slot_map,     n_slots,    n_free_out, n_unserved};
   // entries to write per thread: one slot, or one row's table entries per warp
