@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "kv_append.cuh"
@@ -25,8 +26,9 @@ using moe_internal::cuda_fail;
 constexpr int kMaxDevices = 64;
 
 struct Device {
-  bool known = false, sm103 = false;
-  int n_sm = 0;
+  std::atomic<bool> known{false};   // set after the others
+  std::atomic<bool> sm103{false};
+  std::atomic<int> n_sm{0};
 };
 
 // The current device's properties, asked for once per device: a host-side
@@ -38,15 +40,16 @@ int this_device(const Device** out) {
   if (e != cudaSuccess) return cuda_fail(e);
   if (dev < 0 || dev >= kMaxDevices) return MOE_ERR_UNSUPPORTED;
   Device& d = devices[dev];
-  if (!d.known) {
+  if (!d.known.load(std::memory_order_acquire)) {
     int major = 0, minor = 0, n_sm = 0;
     if ((e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev)) ||
         (e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev)) ||
         (e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev)))
       return cuda_fail(e);
-    d.sm103 = major == 10 && minor == 3;
-    d.n_sm = std::min(n_sm, kDecMaxCtas);
-    d.known = true;   // concurrent first calls write the same values
+    // threads whose first calls meet store the same values
+    d.sm103.store(major == 10 && minor == 3, std::memory_order_relaxed);
+    d.n_sm.store(std::min(n_sm, kDecMaxCtas), std::memory_order_relaxed);
+    d.known.store(true, std::memory_order_release);
   }
   *out = &d;
   return d.sm103 ? MOE_OK : MOE_ERR_UNSUPPORTED;

@@ -243,3 +243,33 @@ def test_an_empty_free_list_serves_rows_that_need_no_block():
     seq, n = base._dev([3, 16]), base._dev([0])
     M.kv_release(torch.tensor([True, False], device=DEV), seq, table, none, n, 16)
     assert base._np(seq).tolist() == [0, 16] and int(n) == 0
+
+
+# ---------------------------------------------------------------------------
+# First calls
+# ---------------------------------------------------------------------------
+FIRST_CALLS = """
+import sys
+sys.path[:0] = {path!r}
+import threading, torch
+import moe_decode_step_gb300 as M
+torch.cuda.init()
+lib, n = M.lib(), 16
+gate, got = threading.Barrier(n), [None] * n
+def first(i):
+    torch.cuda.set_device(0)
+    gate.wait()
+    got[i] = lib.moe_kv_attention_workspace(128)
+threads = [threading.Thread(target=first, args=(i,)) for i in range(n)]
+[t.start() for t in threads]
+[t.join() for t in threads]
+assert min(got) > 0 and len(set(got)) == 1, got
+"""
+
+
+def test_first_calls_of_many_threads_agree():
+    import subprocess
+    import sys
+    p = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(path=sys.path)],
+                       capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0, p.stderr[-2000:]
