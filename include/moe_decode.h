@@ -388,6 +388,19 @@ int moe_kv_release(void* stream, const uint8_t* finished, int n_rows, int32_t* s
                    int32_t* free_list, int free_cap, const int32_t* n_free, int block_size,
                    int32_t* n_free_out);
 
+/* The same for rows that keep a part: a row that is not finished and has 0 <=
+ * keep_lens[r] < seq_lens[r] gives back the blocks from entry
+ * ceil(keep_lens[r] / block_size) of its block_table row on, and seq_lens[r]
+ * becomes keep_lens[r]; a keep_lens[r] below 0 or not below seq_lens[r] leaves
+ * the row as it is.  finished or keep_lens may be NULL, not both.  This is how
+ * a row gets shorter (rejected drafts): moe_kv_plan takes a row to hold the
+ * blocks of its ctx_lens and no more, so that a length lowered without this
+ * call loses the blocks past it. */
+int moe_kv_release_past(void* stream, const uint8_t* finished, const int32_t* keep_lens,
+                        int n_rows, int32_t* seq_lens, const int32_t* block_table,
+                        int64_t table_stride, int max_blocks, int32_t* free_list, int free_cap,
+                        const int32_t* n_free, int block_size, int32_t* n_free_out);
+
 /* Write the keys and values of n_tokens new tokens into the cache.  k, v
  * device [n_tokens][n_kv_heads][head_dim] of `dtype` (BF16 or F16), token and
  * head strides in elements (multiples of 8; pointers 16-byte aligned), rows

@@ -92,6 +92,8 @@ _PROTOS = {
                                    _P]),
     "moe_kv_release": (ctypes.c_int, [_P, _P, ctypes.c_int, _P, _P, ctypes.c_int64, ctypes.c_int,
                                       _P, ctypes.c_int, _P, ctypes.c_int, _P]),
+    "moe_kv_release_past": (ctypes.c_int, [_P, _P, _P, ctypes.c_int, _P, _P, ctypes.c_int64,
+                                           ctypes.c_int, _P, ctypes.c_int, _P, ctypes.c_int, _P]),
     "moe_kv_append": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int, ctypes.c_int64, ctypes.c_int64,
                                      ctypes.c_int64, ctypes.c_int64, _P, ctypes.c_int]),
     "moe_kv_attention": (ctypes.c_int, [_P, _P, _P]),

@@ -208,8 +208,17 @@ int moe_kv_release(void* stream, const uint8_t* finished, int n_rows, int32_t* s
                    const int32_t* block_table, int64_t table_stride, int max_blocks,
                    int32_t* free_list, int free_cap, const int32_t* n_free, int block_size,
                    int32_t* n_free_out) {
-  if (!finished || !seq_lens || !block_table || (!free_list && free_cap > 0) || !n_free ||
-      !n_free_out)
+  if (!finished) return MOE_ERR_INVALID_ARG;
+  return moe_kv_release_past(stream, finished, nullptr, n_rows, seq_lens, block_table, table_stride,
+                             max_blocks, free_list, free_cap, n_free, block_size, n_free_out);
+}
+
+int moe_kv_release_past(void* stream, const uint8_t* finished, const int32_t* keep_lens,
+                        int n_rows, int32_t* seq_lens, const int32_t* block_table,
+                        int64_t table_stride, int max_blocks, int32_t* free_list, int free_cap,
+                        const int32_t* n_free, int block_size, int32_t* n_free_out) {
+  if ((!finished && !keep_lens) || !seq_lens || !block_table || (!free_list && free_cap > 0) ||
+      !n_free || !n_free_out)
     return MOE_ERR_INVALID_ARG;
   const int bl = block_log2(block_size);
   if (n_rows < 1 || max_blocks < 1 || table_stride < max_blocks || free_cap < 0 || bl < 0)
@@ -218,8 +227,8 @@ int moe_kv_release(void* stream, const uint8_t* finished, int n_rows, int32_t* s
   const Device* dev;
   int rc = begin(&dev);
   if (rc) return rc;
-  ReleaseArgs p{finished,  n_rows,   seq_lens, block_table, table_stride, max_blocks,
-                free_list, free_cap, n_free,   bl,          n_free_out};
+  ReleaseArgs p{finished,   keep_lens, n_rows,   seq_lens, block_table, table_stride,
+                max_blocks, free_list, free_cap, n_free,   bl,          n_free_out};
   kv_release_kernel<<<1, kPlanThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
   return end();
 }

@@ -182,7 +182,8 @@ static __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const Plan
 }
 
 struct ReleaseArgs {
-  const uint8_t* finished;
+  const uint8_t* finished;   // or null
+  const int* keep;           // or null
   int rows;
   int* seq;
   const int* table;
@@ -195,20 +196,28 @@ struct ReleaseArgs {
   int* n_free_out;
 };
 
-// One CTA: the pushes are few and the stack's height is one word.
+// One CTA: the pushes are few and the stack's height is one word.  A row gives
+// the blocks from entry s_entry on back, those past the length it keeps.
 static __global__ void __launch_bounds__(kPlanThreads) kv_release_kernel(const ReleaseArgs p) {
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int n_free = min(max(*p.n_free, 0), p.free_cap);
   __shared__ long long s_first[kPlanThreads];
-  __shared__ int s_blocks[kPlanThreads];
+  __shared__ int s_blocks[kPlanThreads], s_entry[kPlanThreads];
+  const long long up = (1 << p.bs_log2) - 1;
   long long base = n_free;
   for (int r0 = 0; r0 < p.rows; r0 += kPlanThreads) {
     const int r = r0 + t;
     long long n = 0, unused = 0, total, tu;
-    if (r < p.rows && p.finished[r]) {
-      n = ((long long)max(p.seq[r], 0) + (1 << p.bs_log2) - 1) >> p.bs_log2;
-      n = min(n, (long long)p.max_blocks);
-      p.seq[r] = 0;
+    if (r < p.rows) {
+      const int seq = max(p.seq[r], 0);
+      const bool all = p.finished && p.finished[r];
+      const int keep = all ? 0 : p.keep ? p.keep[r] : -1;
+      const long long entry = min((keep + up) >> p.bs_log2, (long long)p.max_blocks);
+      if (all || (keep >= 0 && keep < seq)) {
+        n = min((seq + up) >> p.bs_log2, (long long)p.max_blocks) - entry;
+        p.seq[r] = keep;
+      }
+      s_entry[t] = (int)entry;
     }
     s_blocks[t] = (int)n;
     plan_scan2(n, unused, total, tu);
@@ -217,7 +226,7 @@ static __global__ void __launch_bounds__(kPlanThreads) kv_release_kernel(const R
     for (int w = warp; w < kPlanThreads; w += kPlanThreads / 32)
       for (int j = lane; j < s_blocks[w]; j += 32)
         if (s_first[w] + j < p.free_cap)
-          p.free_list[s_first[w] + j] = p.table[(r0 + w) * p.tstride + j];
+          p.free_list[s_first[w] + j] = p.table[(r0 + w) * p.tstride + s_entry[w] + j];
     base += total;
     __syncthreads();
   }

@@ -77,7 +77,9 @@ def kv_plan(ctx_lens, q_lens, block_table, free_list, n_free, block_size, n_slot
     extends block_table in place and returns a KVPlan.  ctx_lens, q_lens int32
     [rows]; block_table int32 [rows, max_blocks]; free_list int32 [n], n_free
     int32 [1]: a stack of free block ids and its height; n_slots: entries of
-    the slot map, at least the new tokens the step may have."""
+    the slot map, at least the new tokens the step may have.  A row is taken
+    to hold the blocks of its ctx_lens: one that got shorter gives the others
+    back by kv_release's keep_lens first."""
     dev = ctx_lens.device
     _want(ctx_lens.is_cuda, "ctx_lens", "a CUDA tensor", ctx_lens)
     rows = ctx_lens.shape[0]
@@ -105,23 +107,30 @@ def kv_plan(ctx_lens, q_lens, block_table, free_list, n_free, block_size, n_slot
     return KVPlan(lens, start, slots, left, unserved)
 
 
-def kv_release(finished, seq_lens, block_table, free_list, n_free, block_size, stream=None):
+def kv_release(finished, seq_lens, block_table, free_list, n_free, block_size, stream=None,
+               keep_lens=None):
     """Give the finished rows' blocks back (moe_kv_release): finished bool or
     uint8 [rows]; pushes onto free_list, zeroes their seq_lens and updates
-    n_free, all in place."""
+    n_free, all in place.  With keep_lens (int32 [rows]) the other rows give
+    back what lies past that many tokens, and it becomes their length
+    (moe_kv_release_past): a row whose drafts were rejected is shortened this
+    way before the next kv_plan."""
     dev = seq_lens.device
     _want(seq_lens.is_cuda, "seq_lens", "a CUDA tensor", seq_lens)
     rows = seq_lens.shape[0]
     _vector(seq_lens, rows, torch.int32, "seq_lens", dev)
     _vector(finished, rows, torch.bool if finished.dtype == torch.bool else torch.uint8,
             "finished", dev)
+    if keep_lens is not None:
+        _vector(keep_lens, rows, torch.int32, "keep_lens", dev)
     _vector(free_list, None, torch.int32, "free_list", dev)
     _vector(n_free, 1, torch.int32, "n_free", dev)
     stride = _table(block_table, rows, dev)
-    check(lib().moe_kv_release(_raw_stream(stream, dev), finished.data_ptr(), rows,
-                               seq_lens.data_ptr(), block_table.data_ptr(), stride,
-                               block_table.shape[1], free_list.data_ptr(), free_list.shape[0],
-                               n_free.data_ptr(), int(block_size), n_free.data_ptr()),
+    check(lib().moe_kv_release_past(_raw_stream(stream, dev), finished.data_ptr(),
+                                    None if keep_lens is None else keep_lens.data_ptr(), rows,
+                                    seq_lens.data_ptr(), block_table.data_ptr(), stride,
+                                    block_table.shape[1], free_list.data_ptr(), free_list.shape[0],
+                                    n_free.data_ptr(), int(block_size), n_free.data_ptr()),
           "moe_kv_release")
 
 

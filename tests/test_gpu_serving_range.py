@@ -273,3 +273,66 @@ def test_first_calls_of_many_threads_agree():
     p = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(path=sys.path)],
                        capture_output=True, text=True, timeout=300)
     assert p.returncode == 0, p.stderr[-2000:]
+
+
+# ---------------------------------------------------------------------------
+# Rows that shrink
+# ---------------------------------------------------------------------------
+def _conserved(table, seq, free, n, bs, n_blocks):
+    """Every block is held by one row or free, once."""
+    held = [int(b) for r in range(len(seq)) for b in table[r, :-(-int(seq[r]) // bs)]]
+    ids = held + [int(b) for b in free[:n]]
+    assert sorted(ids) == list(range(n_blocks))
+
+
+def test_rejected_drafts_give_their_blocks_back():
+    """Steps of eight drafts of which some are accepted, for as many steps as would use up a
+    stack that lost a block in each."""
+    bs, rows, n_blocks, mb = 16, 5, 40, 8
+    rng = np.random.default_rng(0)
+    table = torch.zeros(rows, mb, dtype=torch.int32, device=DEV)
+    free = torch.arange(n_blocks, dtype=torch.int32, device=DEV)
+    n, ctx = base._dev([n_blocks]), torch.zeros(rows, dtype=torch.int32, device=DEV)
+    q = torch.full((rows,), 8, dtype=torch.int32, device=DEV)
+    done = torch.zeros(rows, dtype=torch.bool, device=DEV)
+    for step in range(60):
+        p = M.kv_plan(ctx, q, table, free, n, bs, 8 * rows)
+        assert int(p.n_unserved) == 0
+        n.copy_(p.n_free)
+        keep = base._dev(base._np(ctx) + rng.integers(1, 9, rows))
+        if step % 12 == 11:
+            done[step // 12] = True
+        M.kv_release(done, p.seq_lens, table, free, n, bs, keep_lens=keep)
+        want = np.where(base._np(done), 0, base._np(keep))
+        assert np.array_equal(base._np(p.seq_lens), want)
+        _conserved(base._np(table), want, base._np(free), int(n), bs, n_blocks)
+        ctx = torch.where(done | (p.seq_lens > 110), 0, p.seq_lens).to(torch.int32)
+        if (p.seq_lens > 110).any():      # finished
+            M.kv_release(p.seq_lens > 110, p.seq_lens, table, free, n, bs)
+        done[:] = False
+
+
+@pytest.mark.parametrize("rows", [1, 7, 600, 3000])
+def test_release_past_kept_lengths_matches_row_by_row(rows):
+    rng = np.random.default_rng(rows)
+    bs, mb = 16, 6
+    seq = rng.integers(0, bs * mb + 1, rows)
+    keep = np.where(rng.random(rows) < 0.7, seq - rng.integers(0, 40, rows), rng.integers(-5, 200, rows))
+    fin = rng.random(rows) < 0.2
+    table = rng.permutation(rows * mb).reshape(rows, mb)
+    free = np.concatenate([[7, 8, 9], np.full(rows * mb, -1)])
+    want, lens = [7, 8, 9], seq.copy()
+    for r in range(rows):
+        k = 0 if fin[r] else int(keep[r])
+        if k < 0 or k >= seq[r]:          # nothing past it
+            continue
+        want += table[r, -(-k // bs):-(-int(seq[r]) // bs)].tolist()
+        lens[r] = k
+    t_seq, t_free, t_n = base._dev(seq), base._dev(free), base._dev([3])
+    M.kv_release(torch.from_numpy(fin).to(DEV), t_seq, base._dev(table), t_free, t_n, bs,
+                 keep_lens=base._dev(keep))
+    assert np.array_equal(base._np(t_seq), lens)
+    assert int(t_n) == len(want) and base._np(t_free)[:len(want)].tolist() == want
+    with pytest.raises(ValueError, match="keep_lens"):
+        M.kv_release(torch.from_numpy(fin).to(DEV), t_seq, base._dev(table), t_free, t_n, bs,
+                     keep_lens=base._dev(keep).long())
