@@ -468,8 +468,8 @@ size_t moe_kv_attention_workspace(int head_dim);
 
 /* Expert routing from logits, for any number of rows.  Per row: score s_e =
  * sigmoid(l_e) or softmax(l)_e in fp32 (all of a softmax row at -infinity:
- * scores 0); experts are compared by s_e + bias_e (bias NULL: s_e), the s_e
- * of this comparison within 3e-7 of themselves.  With
+ * scores 0); experts are compared by s_e + bias_e (bias NULL: s_e), the sum
+ * rounded to fp32, with the very s_e that the weights are made of.  With
  * n_groups > 1 the experts form n_groups equal consecutive groups, a group
  * counts with the sum of its group_top (1 or 2) best, and only the experts of
  * the topk_groups best groups are left.  The top_k best are written in

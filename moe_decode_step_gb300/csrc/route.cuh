@@ -7,15 +7,15 @@
 // of these only its two best in order: a selection is then the warp's largest
 // head (redux) and the lowest expert among equals (redux), after which one lane
 // moves up; a lane whose two are gone looks through the rest again, once a row
-// or so.  Selection compares the scores of the fast exponential and reciprocal
-// (errors of 3e-7); the k weights are computed again with the full ones.
-// Groups whose size is a power of two find their two best by shuffles, others
-// through shared memory.
-// Measured: 32,768 rows of 256 experts, 8 of the 4 best of 8 groups: 30.5 us,
-// 1.2 TB/s; ALU slots bound it (some 800 instructions a row).  Before the keys
-// were merged as integers and a lane looked again by itself 35 us, with one
-// best a lane and groups through shared memory 74.  64 rows of 896, 16 best:
-// 13 us, most of it the host's time for the call.
+// or so.  Selection compares the scores that are written: the k of them are
+// computed again, by the same operations, from the logits (the layer's own
+// router does the same, so both pick the same experts).  Groups whose size is
+// a power of two find their two best by shuffles, others through shared memory.
+// Measured: 32,768 rows of 256 experts, 8 of the 4 best of 8 groups: 32.8 us,
+// 1.1 TB/s; ALU slots bound it (some 900 instructions a row; with approximate
+// exponentials and reciprocals 30.2 us, but neighbours changed places where
+// their scores differ by less than a few 1e-7).  64 rows of 896, 16 best: 14 to
+// 17 us a call, most of it the host's time.
 #pragma once
 
 #include "kv_cache.cuh"
@@ -46,26 +46,6 @@ __device__ __forceinline__ float route_load(const RouteArgs& a, long long row, i
   if (a.dtype == MOE_DTYPE_F32) return __ldg(static_cast<const float*>(a.logits) + i);
   const uint16_t u = __ldg(static_cast<const uint16_t*>(a.logits) + i);
   return a.dtype == MOE_DTYPE_F16 ? f16_lo(u) : bf16_bits_to_f32(u);
-}
-
-// e^x and 1 / x, approximate (subnormal results are kept: scores that small
-// are still compared).
-__device__ __forceinline__ float route_exp(float x) {
-  float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
-  return y;
-}
-__device__ __forceinline__ float route_rcp(float x) {
-  float y;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// 1 / (1 + e^-x): an e^-x that is subnormal does not count beside 1.
-__device__ __forceinline__ float route_sigmoid(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * -1.4426950408889634f));
-  return route_rcp(1.f + y);
 }
 
 // The two best of (a1, a2) and (b1, b2).
@@ -115,8 +95,9 @@ static __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Ro
       for (int v = 0; v < V; ++v) s[V * c + v] = e + v < a.E ? route_load(a, row, e + v) : -INFINITY;
     }
   }
-  float m = 0.f, z = 0.f;
+  float m = 0.f, inv = 0.f;
   if (a.softmax) {
+    float z = 0.f;
     m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < N; ++i) m = fmaxf(m, s[i]);
@@ -124,16 +105,16 @@ static __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Ro
     if (m == -INFINITY) m = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      s[i] = route_exp(s[i] - m);
+      s[i] = expf(s[i] - m);
       z += s[i];
     }
     z = warp_sum(z);
-    const float inv = z == 0.f ? 0.f : route_rcp(z);
+    inv = z == 0.f ? 0.f : 1.f / z;
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i] *= inv;
+    for (int i = 0; i < N; ++i) s[i] = __fmul_rn(s[i], inv);   // rounded, as it is written
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = route_sigmoid(s[i]);
+    for (int i = 0; i < N; ++i) s[i] = topk_score(s[i]);
   }
   if (a.bias) {
 #pragma unroll
@@ -262,12 +243,12 @@ static __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Ro
   float v = 0.f;
   if (lane < a.k) {
     const float x = route_load(a, row, mine);
-    v = a.softmax ? (z == 0.f ? 0.f : expf(x - m) / z) : topk_score(x);
+    v = a.softmax ? __fmul_rn(expf(x - m), inv) : topk_score(x);
   }
   const float sum = warp_sum(v);
   if (lane < a.k) {
     a.idx[row * a.k + lane] = mine;
-    a.w[row * a.k + lane] = a.scale * (a.renorm ? (sum == 0.f ? 0.f : __fdividef(v, sum)) : v);
+    a.w[row * a.k + lane] = a.scale * (a.renorm ? (sum == 0.f ? 0.f : v / sum) : v);
   }
 }
 

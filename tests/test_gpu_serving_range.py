@@ -246,6 +246,39 @@ def test_an_empty_free_list_serves_rows_that_need_no_block():
 
 
 # ---------------------------------------------------------------------------
+# Routing
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("around", [-60.0, -40.0, -20.0, -14.0, -9.0])
+@pytest.mark.parametrize("experts,k", [(256, 32), (60, 32), (896, 16)])
+def test_route_orders_neighbouring_logits(experts, k, around, scoring):
+    """Consecutive fp32 logits, whose scores differ by 8 of their own last places or more: more
+    than the exponentials (2 each) and the reciprocals (1 each) may be off together."""
+    step = np.spacing(np.float32(abs(around)))
+    rng = np.random.default_rng(experts)
+    x = np.float32(around) + np.arange(experts) * np.float64(step)
+    x = rng.permuted(np.tile(x, (50, 1)), axis=1).astype(np.float32)
+    assert len(np.unique(x[0])) == experts
+    if scoring == "softmax":
+        x[:, 0] = 0.0                               # the row's largest: the others subtract exactly
+    want_i, _ = ref.route(x.astype(np.float64), None, k, scoring, 1, 1, 1, True, 1.0)
+    idx, w = M.moe_route(base._dev(x, torch.float32), k, scoring=scoring)
+    assert np.array_equal(base._np(idx), want_i)
+    assert (w[:, :-1] >= w[:, 1:]).all()
+
+
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+def test_route_writes_the_scores_it_compared(scoring):
+    """Without a bias the written scores descend, equal ones by ascending expert."""
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.randn(20000, 896, generator=g, device=DEV) * 4
+    idx, w = M.moe_route(x, 32, scoring=scoring, renormalize=False)
+    a, b = w[:, :-1], w[:, 1:]
+    assert (a >= b).all()
+    assert (idx[:, :-1] < idx[:, 1:])[a == b].all()
+
+
+# ---------------------------------------------------------------------------
 # First calls
 # ---------------------------------------------------------------------------
 FIRST_CALLS = """
