@@ -406,9 +406,11 @@ int moe_kv_release_past(void* stream, const uint8_t* finished, const int32_t* ke
  * head strides in elements (multiples of 8; pointers 16-byte aligned), rows
  * contiguous.  slot_map device [n_tokens]: block * block_size + offset per
  * token; -1 (or any slot outside the cache) skips the token.  The tokens a
- * step writes into one block are consecutive in the slot map, at consecutive
- * ascending offsets, and the block holds the sequence's earlier tokens below
- * them (what moe_kv_plan makes).  Per block, head and side: e is the smallest
+ * step writes into one block follow one another in the slot map at consecutive
+ * ascending offsets, with nothing but skipped tokens between them (then the
+ * offsets need only ascend) and within block_size entries, and the block holds
+ * the sequence's earlier tokens below them (what moe_kv_plan makes).  Per
+ * block, head and side: e is the smallest
  * integer with max |finite value| <= 448 * 2^e, at least -60, at most 60; a
  * block that already held tokens keeps its exponent if that is larger, and
  * otherwise has their codes rounded to the new one.  Codes are value / 2^e

@@ -2,7 +2,8 @@
 //
 // The tokens a step writes into one block share its scale, so the unit of
 // work is a group: the consecutive tokens of one block, found at its first
-// token (the leader: the slot before it lies in another block).  Of a group of
+// token (the leader: the slot before it lies in another block).  Tokens that
+// are skipped may stand between those of a block: a path of its own.  Of a group of
 // one head and one side: the largest magnitude, the exponent, then the codes;
 // where the block held tokens and its exponent grows, their codes are rounded
 // to the new scale first.
@@ -11,7 +12,7 @@
 // batch, a token each) go a warp each; few (a prompt, whole blocks) one after
 // the other to all eight warps, which hold a group's values in registers
 // between the maximum and the codes, so that they are read once.  Measured: 16
-// prompts of 517 to 1,531 tokens, 8 heads of 128, blocks of 64: 32 us, 3.1 TB/s
+// prompts of 517 to 1,531 tokens, 8 heads of 128, blocks of 64: 33.5 us, 3.0 TB/s
 // (74 us with a warp a group; five CTAs an SM hide each other's chain of slot,
 // values, maximum and codes, with two 55 us).  64 rows' one token each: 7.5 us,
 // the host's time for the call.
@@ -59,6 +60,25 @@ __device__ __forceinline__ uint2 append_codes(const uint4& w, int f16, float inv
                         f32x2_to_e4m3x2(f1.x * inv, f1.y * inv) << 16,
                     f32x2_to_e4m3x2(f2.x * inv, f2.y * inv) |
                         f32x2_to_e4m3x2(f3.x * inv, f3.y * inv) << 16);
+}
+
+// The codes of tokens [sub, sub + step, ..) below off, LPT threads a token, to
+// an exponent that is `down` higher.
+__device__ __forceinline__ void append_round_again(uint8_t* dst, long long tstride, int sub,
+                                                   int step, int off, float down) {
+  for (int i = sub; i < off; i += step) {
+    uint2* p = reinterpret_cast<uint2*>(dst + i * tstride);
+    uint2 v = *p;
+    uint32_t r[2] = {v.x, v.y};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      uint32_t lo, hi;
+      e4m3x4_to_f16x2(r[j], lo, hi);
+      r[j] = f32x2_to_e4m3x2(f16_lo(lo) * down, f16_hi(lo) * down) |
+             f32x2_to_e4m3x2(f16_lo(hi) * down, f16_hi(hi) * down) << 16;
+    }
+    *p = make_uint2(r[0], r[1]);
+  }
 }
 
 // Tokens [t0, t0 + n) of head h, side s (0 K, 1 V) into block b from offset
@@ -129,8 +149,62 @@ __device__ __forceinline__ void append_group(const AppendArgs& a, int s, int h, 
         __ldg(reinterpret_cast<const uint4*>(src + i * a.ts[s])), a.f16, inv);
 }
 
+// The block of the last token before t that is not skipped, less than a block's
+// tokens away; -1: none.
+__device__ __forceinline__ int append_block_before(const AppendArgs& a, int t) {
+  const int far = min((1 << a.c.bs_log2) - 1, t);
+  int b = -1;
+  for (int j = 1; j <= far && b < 0; ++j) b = append_block_of(a, __ldg(a.slot + t - j));
+  return b;
+}
+
+// Groups with skipped tokens among or beside them, a warp each, values read
+// twice: rare, so its code and registers stay out of the others'.  Those of the
+// chunk whose leaders are in `own`, or (own all ones) dealt round the warps.  A
+// group's tokens lie in as many entries of the slot map as a block has tokens.
 template <int D>
-static __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) kv_append_kernel(const AppendArgs a) {
+__device__ __noinline__ void append_sparse(const AppendArgs& a, unsigned long long own) {
+  constexpr int LPT = D / 8, TPP = 32 / LPT;
+  const int lane = threadIdx.x & 31, sub = lane / LPT, part = lane % LPT;
+  const int h = blockIdx.y >> 1, s = blockIdx.y & 1, c0 = blockIdx.x * a.chunk;
+  unsigned long long leaders = 0;
+  for (int k = 0; k < a.chunk; k += 32) {
+    int b = -1;
+    if (k + lane < min(a.chunk, a.n_tokens - c0)) b = append_block_of(a, __ldg(a.slot + c0 + k + lane));
+    const bool leads = b >= 0 && b != append_block_before(a, c0 + k + lane);
+    leaders |= (unsigned long long)__ballot_sync(0xffffffffu, leads) << k;
+  }
+  for (int k = 0; leaders; ++k, leaders &= leaders - 1) {
+    if (own == ~0ull ? k % kAppendWarps != (int)(threadIdx.x >> 5) : !(own & leaders & -leaders)) continue;
+    const int t0 = c0 + __ffsll((long long)leaders) - 1, first = __ldg(a.slot + t0);
+    const int b = first >> a.c.bs_log2, mask = (1 << a.c.bs_log2) - 1, off = first & mask;
+    const int n = min(mask + 1, a.n_tokens - t0);
+    const uint16_t* src = a.src[s] + t0 * a.ts[s] + h * a.hs[s] + part * 8;
+    uint8_t* dst = (s ? a.c.v : a.c.k) + b * a.c.bstride + h * a.c.hstride + part * 8;
+    uint8_t* sp = (s ? a.c.vs : a.c.ks) + b * a.c.sstride + h;
+    const int old = off > 0 ? kv_exp(*sp) : kKvExpMin;
+    float amax = 0.f;
+    for (int i = sub; i < n; i += TPP)
+      if (append_block_of(a, __ldg(a.slot + t0 + i)) == b)
+        amax = append_max(__ldg(reinterpret_cast<const uint4*>(src + i * a.ts[s])), a.f16, amax);
+    amax = warp_max(amax);
+    __syncwarp();
+    const int e = max(kv_block_exp(amax), old);
+    if (off > 0 && old < e) append_round_again(dst, a.c.tstride, sub, TPP, off, pow2f(old - e));
+    if (lane == 0) *sp = (uint8_t)(e + 127);
+    const float inv = pow2f(-e);
+    for (int i = sub; i < n; i += TPP) {
+      const int slot = __ldg(a.slot + t0 + i);
+      if (append_block_of(a, slot) == b)
+        *reinterpret_cast<uint2*>(dst + (slot & mask) * a.c.tstride) = append_codes(
+            __ldg(reinterpret_cast<const uint4*>(src + i * a.ts[s])), a.f16, inv);
+    }
+    __syncwarp();
+  }
+}
+
+template <int D>
+static __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) kv_append_kernel(const __grid_constant__ AppendArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c0 = blockIdx.x * a.chunk;
   const int h = blockIdx.y >> 1, s = blockIdx.y & 1;
@@ -138,6 +212,7 @@ static __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) kv_append_
   // leaders among this chunk's slots (every warp finds them for itself), and
   // where the slot after each lane's begins another block
   unsigned long long leaders = 0, ends = 0;
+  bool beside = false;   // a skipped token
   for (int k = 0; k < a.chunk; k += 32) {
     int b = -1, prev = -1, next = -1;
     if (k + lane < min(a.chunk, a.n_tokens - c0)) {
@@ -148,7 +223,13 @@ static __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) kv_append_
     }
     leaders |= (unsigned long long)__ballot_sync(0xffffffffu, b >= 0 && b != prev) << k;
     ends |= (unsigned long long)__ballot_sync(0xffffffffu, b != next) << k;
+    beside |= b >= 0 && ((prev < 0 && c0 + k + lane > 0) || (next < 0 && c0 + k + lane < a.n_tokens - 1));
   }
+  if (__any_sync(0xffffffffu, beside)) {
+    append_sparse<D>(a, ~0ull);
+    return;
+  }
+  unsigned long long sparse = 0;   // groups that meet one past the chunk, a warp each
   const bool few = __popcll(leaders) <= kAppendFew;
   for (int k = 0; leaders; ++k, leaders &= leaders - 1) {
     if (!few && k % kAppendWarps != warp) continue;
@@ -162,17 +243,24 @@ static __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) kv_append_
     if (e) {
       n = min(__ffsll((long long)e), room);
     } else {
-      while (n < room) {
-        const bool in = n + lane < room && append_block_of(a, __ldg(a.slot + t0 + n + lane)) == b;
-        const unsigned m = __ballot_sync(0xffffffffu, in);
-        n += m == 0xffffffffu ? 32 : __ffs(~m) - 1;
-        if (m != 0xffffffffu) break;
+      for (unsigned m = ~0u; m == ~0u;) {
+        const int i = n + lane;
+        const int at = i <= room && i < a.n_tokens - t0 ? append_block_of(a, __ldg(a.slot + t0 + i)) : b;
+        m = __ballot_sync(0xffffffffu, at == b && i < room);
+        const unsigned skipped = __ballot_sync(0xffffffffu, at < 0);
+        const int in = m == ~0u ? 32 : __ffs(~m) - 1;
+        n += in;
+        if (in < 32 && ((skipped >> in) & 1u)) n = 0;
       }
-      n = min(n, room);
+      if (n == 0) {
+        if (k % kAppendWarps == warp) sparse |= leaders & -leaders;
+        continue;
+      }
     }
     if (few) append_group<D, kAppendThreads>(a, s, h, b, off, t0, n);
     else append_group<D, 32>(a, s, h, b, off, t0, n);
   }
+  if (sparse) append_sparse<D>(a, sparse);
 }
 
 }  // namespace moe

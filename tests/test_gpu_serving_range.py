@@ -369,3 +369,61 @@ def test_release_past_kept_lengths_matches_row_by_row(rows):
     with pytest.raises(ValueError, match="keep_lens"):
         M.kv_release(torch.from_numpy(fin).to(DEV), t_seq, base._dev(table), t_free, t_n, bs,
                      keep_lens=base._dev(keep).long())
+
+
+# ---------------------------------------------------------------------------
+# Append: skipped tokens
+# ---------------------------------------------------------------------------
+def _expect_append(codes, scale, new, slots, bs):
+    """As moe_kv_append states it: the tokens of a block are those among the slot map's entries,
+    whatever skipped ones lie between."""
+    codes, scale = codes.copy(), scale.copy()
+    n_blocks, hkv = scale.shape
+    for b in dict.fromkeys(int(s) // bs for s in slots if 0 <= s < n_blocks * bs):
+        ts = [t for t, s in enumerate(slots) if s >= 0 and s // bs == b]
+        offs = [int(slots[t]) % bs for t in ts]
+        for h in range(hkv):
+            e = ref.block_exp(np.abs(new[ts, h]).max())
+            if offs[0]:
+                old = int(np.clip(int(scale[b, h]) - 127, -60, 60))
+                if old < e:
+                    codes[b, h, :offs[0]] = ref.e4m3_round(
+                        ref.e4m3_table()[codes[b, h, :offs[0]]] * 2.0 ** (old - e))
+                e = max(e, old)
+            scale[b, h] = e + 127
+            codes[b, h, offs] = ref.e4m3_round(new[ts, h] * 2.0 ** -e)
+    return codes, scale
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("bs", [16, 64, 128])
+def test_append_with_skipped_tokens_inside_blocks(bs, many):
+    """Tokens that go nowhere between those of one block, few and long runs of them, at chunks'
+    ends and at the map's: still one scale a block, whatever order the GPU works in."""
+    rng = np.random.default_rng(bs + many)
+    lens = [(0, 3 * bs), (bs - 3, 40), (7, 1), (0, 1), (5, 2), (bs // 2, 2 * bs + 9), (1, bs - 1)]
+    lens = lens * (5 if many else 1) + ([(3, 1500)] if many else [])
+    need = [-(-(c + n) // bs) for c, n in lens]
+    n_blocks, d, hkv = sum(need) + 1, 128, 2
+    ids = rng.permutation(n_blocks)
+    slots, at = [], 0
+    for (c, n), k in zip(lens, need):
+        slots += [int(ids[at + p // bs]) * bs + p % bs for p in range(c, c + n)]
+        at += k
+    slots = np.array(slots)
+    skip = rng.random(len(slots)) < 0.2
+    for a, n in ((3, 2), (bs + 1, bs - 3), (60, 10), (len(slots) - 2, 2)):
+        skip[a:a + n] = True
+    slots[skip] = rng.choice([-1, n_blocks * bs, 2 ** 31 - 1], int(skip.sum()))
+    codes = rng.integers(0, 127, (2, n_blocks, hkv, bs, d)).astype(np.uint8)
+    scale = rng.integers(127 - 14, 127 - 3, (2, n_blocks, hkv)).astype(np.uint8)
+    new = rng.standard_normal((2, len(slots), hkv, d)) * 2.0 ** rng.integers(-6, 4, (2, len(slots), 1, 1))
+    t = [torch.from_numpy(x).to(torch.bfloat16).to(DEV) for x in new]
+    for _ in range(3):
+        k, v = torch.from_numpy(codes).to(DEV)
+        ks, vs = torch.from_numpy(scale).to(DEV)
+        M.KVCache(k, v, ks, vs).append(t[0], t[1], base._dev(slots))
+        for s, (c, sc) in enumerate(((k, ks), (v, vs))):
+            wc, ws = _expect_append(codes[s], scale[s], base._np(t[s].double()), slots, bs)
+            assert np.array_equal(base._np(sc), ws), s
+            assert np.array_equal(base._np(c), wc), s
