@@ -139,22 +139,28 @@ int launch_tensor(const AttnArgs& a, int n_sm, cudaStream_t st) {
 }
 
 // The kernel by the rows (queries times heads) of a KV head in the longest batch
-// row, as far as the host knows.  Measured, 64 heads over 8 of 128, 8 batch rows
-// of 4,090 to 8,185 tokens:
-//  - up to 8 rows, one n-tile a warp; to 32, two: 81 us at 32 rows, 92 on
-//    tcgen05; at 48 rows 106 against 96.  Where a row has few tokens the
-//    tcgen05 kernel's start counts: to 64 rows with 500 to 900 tokens 28 us
-//    against 52, with 1,000 to 2,000 65 against 60.
-//  - then one row tile whose streams share its keys: 219 us at 384 rows against
-//    267 in pairs of row tiles, 271 against 270 at 512, 484 against 441 at
-//    1,024; with 32 heads of 64 and 600 rows 192 against 224.
+// row, as far as the host knows.  Measured on the device (us), 64 heads over 8
+// of 128, 8 batch rows of 4,090 to 8,185 tokens where nothing else is said:
+//  - up to 8 rows, one n-tile a warp: 47, two 52; to 32, two: 81 at 32 rows, on
+//    tcgen05 89 (32 batch rows of 1,000 to 4,000 tokens 119 against 134); at 48
+//    102 against 89.  Where the table says that rows are short the tcgen05
+//    kernel's start counts, to 64 rows: with 500 to 900 tokens 44 against 53 at
+//    48 rows, 49 against 56 at 64.
+//  - then one row tile whose streams share its keys: 96 at 128 rows against 111
+//    in pairs of row tiles.  Above that pairs, if the batch's rows fill them on
+//    average and are enough for the SMs: 116 against 147 at 256 rows, 194 against
+//    188 at 384, 198 against 231 at 512 (32 heads of 64: 103 against 116, 154
+//    against 175); of one batch row the pairs are few: 118 against 73 at 256,
+//    102 against 92 at 768, 106 against 109 at 1,024, 134 against 161 at 2,048.
 template <int D>
 int launch_attention(const AttnArgs& a, int n_sm, int max_q, cudaStream_t st) {
   const long long rows = (long long)max_q * a.group;
   const long long tokens = (long long)a.max_blocks << a.c.bs_log2;
   if (rows <= 8) return launch_decode<D, 1>(a, n_sm, max_q, st);
   if (rows <= 32 || (rows <= 64 && tokens <= 1024)) return launch_decode<D, 2>(a, n_sm, max_q, st);
-  if (rows <= 65536 / D) return launch_tensor<D, false>(a, n_sm, st);
+  const long long pairs = (long long)a.rows * a.c.heads * ((rows + 255) / 256);
+  const bool filled = (long long)a.n_tokens * a.group > 128ll * a.rows && pairs > n_sm / 4;
+  if (rows <= 128 || (rows <= 65536 / D && !filled)) return launch_tensor<D, false>(a, n_sm, st);
   return launch_tensor<D, true>(a, n_sm, st);
 }
 
