@@ -379,6 +379,7 @@ struct PrShared {
   // second stream may wait for a tile while the one before is not there yet)
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2];
   uint64_t sfull[2], ofull[2];                   // products of each stream
+  uint64_t drained[2];                           // all of them, where a wait ran out
   uint32_t tmem;
   int dead;                 // a wait ran out
   int nan[8];               // by segment: a NaN value in a masked tile
@@ -693,6 +694,16 @@ __device__ __forceinline__ void pr_values(PrShared& sh, uint32_t base, int t, in
     if (n & 1) pr_values_of<D, PAIR, 1, 1>(sh, base, add);
     else pr_values_of<D, PAIR, 1, 0>(sh, base, add);
   }
+}
+
+// A dead CTA's products in flight, before their memory is given back (a stream's
+// first warp; a tenth of a second at most).
+__device__ __noinline__ void pr_drain(PrShared& sh, int t) {
+  __syncwarp();
+  if (elect_one()) umma_commit(&sh.drained[t]);
+  for (int i = 0; i < 100 && !pr_try_wait(&sh.drained[t], 0); ++i) {
+  }
+  __syncwarp();
 }
 
 // ---------------------------------------------------------------------------
@@ -1101,6 +1112,7 @@ static __global__ void __launch_bounds__(kPrThreads, 1) kv_attention_tc(const At
       mbar_init(&sh.vempty[s], PAIR ? 2 : 1);
       mbar_init(&sh.sfull[s], 1);
       mbar_init(&sh.ofull[s], 1);
+      mbar_init(&sh.drained[s], 1);
       sh.open[s] = 0;
     }
     for (int s = 0; s < 8; ++s) sh.nan[s] = 0;
@@ -1116,8 +1128,12 @@ static __global__ void __launch_bounds__(kPrThreads, 1) kv_attention_tc(const At
   tc_fence_after();
 
   if (threadIdx.x == 0 && sh.tmem != 0) sh.dead = 1;   // never: all of it was allocated
-  if (warp < 8) pr_softmax<D, PAIR>(a, sh, pr_smem, cur, n_units);
-  else pr_convert<D, PAIR>(a, sh, pr_smem, cur, n_units);
+  if (warp < 8) {
+    pr_softmax<D, PAIR>(a, sh, pr_smem, cur, n_units);
+    if (*(volatile int*)&sh.dead && (warp & 3) == 0) pr_drain(sh, warp >> 2);
+  } else {
+    pr_convert<D, PAIR>(a, sh, pr_smem, cur, n_units);
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
