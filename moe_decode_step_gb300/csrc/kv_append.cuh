@@ -7,8 +7,8 @@
 // one head and one side: the largest magnitude, the exponent, then the codes;
 // where the block held tokens and its exponent grows, their codes are rounded
 // to the new scale first.
-// HBM bounds long calls (2 bytes read, 1 written an element), latency short
-// ones.  A CTA looks after the leaders among `chunk` slots: many (a decode
+// HBM would bound long calls (2 bytes read, 1 written an element); issue slots do
+// (73% busy).  Latency bounds short ones.  A CTA looks after the leaders among `chunk` slots: many (a decode
 // batch, a token each) go a warp each; few (a prompt, whole blocks) one after
 // the other to all eight warps, which hold a group's values in registers
 // between the maximum and the codes, so that they are read once.  Measured: 16

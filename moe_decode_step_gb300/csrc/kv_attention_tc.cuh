@@ -32,11 +32,11 @@
 // row tile, KV head, keys).
 //
 // Measured at D = 128: prompts of 2,049 to 4,096 tokens behind 4,097 to 8,191,
-// 32 heads over 8: 960 us, 895 TFLOP/s, 47% of the dense rate: 5,000 cycles a
+// 32 heads over 8: 939 us, 915 TFLOP/s, 48% of the dense rate: 4,900 cycles a
 // tile of 256 x 128, of which the products take 2,100; no unit is busy more
 // than 40% of the time, the chain scores, softmax, values of two streams is
 // (a softmax 2,400 cycles beside the other stream and the converters).  8 rows
-// of 8 queries, 64 heads over 8, 4,090 to 8,185 tokens: 77 us, of which 11 before
+// of 8 queries, 64 heads over 8, 4,090 to 8,185 tokens: 78 us, of which 11 before
 // the first scores, 1.6 a tile of 128 x 128 (the converters'), 15 for the joins.
 #pragma once
 

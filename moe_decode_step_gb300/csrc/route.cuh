@@ -12,7 +12,7 @@
 // router does the same, so both pick the same experts).  Groups whose size is
 // a power of two find their two best by shuffles, others through shared memory.
 // Measured: 32,768 rows of 256 experts, 8 of the 4 best of 8 groups: 32.8 us,
-// 1.1 TB/s; ALU slots bound it (some 900 instructions a row; with approximate
+// 1.1 TB/s; issue slots bound it (85% busy, 951 instructions a row; approximate
 // exponentials and reciprocals 30.2 us, but neighbours changed places where
 // their scores differ by less than a few 1e-7).  64 rows of 896, 16 best: 14 to
 // 17 us a call, most of it the host's time.
