@@ -353,7 +353,8 @@ typedef struct {
 
 /* Block tables and slot maps of one step, from request lengths.  Row r holds
  * ctx_lens[r] cached tokens (in the first ceil(ctx / block_size) entries of
- * its block_table row) and gets q_lens[r] new ones.  New blocks are taken in
+ * its block_table row, which are all it holds: a row that got shorter gives the
+ * others back first, by moe_kv_release_past) and gets q_lens[r] new ones.  New blocks are taken in
  * row order from the top of the stack free_list[0 .. *n_free): the i-th new
  * block of the step is free_list[*n_free - 1 - i].  A row is served when its
  * blocks fit max_blocks and its length an int32, its tokens (if any) fit n_slots
