@@ -325,11 +325,11 @@ int moe_router_topk_noalloc_status(int* device_status);
  * and nothing is launched.  Limits: 16,384 rows (requests) per call; device
  * sm_103, else UNSUPPORTED. */
 
-/* Element type of queries, new keys and values, outputs and logits. */
+/* Element types: BF16 and F16, of moe_route's logits F32 too. */
 typedef enum {
   MOE_DTYPE_BF16 = 0,
   MOE_DTYPE_F16 = 1,
-  MOE_DTYPE_F32 = 2    /* logits of moe_route only */
+  MOE_DTYPE_F32 = 2    /* only where a call says so */
 } moe_dtype;
 
 /* A paged KV cache in 8 bits.  Tokens live in blocks of block_size (16, 32,
@@ -493,6 +493,139 @@ typedef struct {
  * fp32 [n_rows][top_k].  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 int moe_route(void* stream, const moe_route_t* cfg, const void* logits, int dtype,
               int64_t row_stride, int64_t n_rows, const float* bias, int32_t* idx, float* w);
+
+/* ---- 8-bit products, norms and the experts of any number of rows ----
+ * What a prompt, or more than the layer's 64 rows, needs around the routing:
+ * the norm with the residual's addition, 8-bit activations, products with
+ * 8-bit or MXFP4 weights, dense or by expert, and the sorting of tokens by
+ * expert and the weighted sum that go with them (no counterpart in the pages;
+ * the formulas are stated at each call).  The rules of the serving operators
+ * hold: no handle, asynchronous on `stream`, nothing allocated, no host
+ * synchronisation, capturable; what the host can see is checked, values read
+ * on the device are bounded there.  None of them needs a workspace.
+ *
+ * 8-bit activations are E4M3 codes [rows][d] with one E8M0 scale per (row, 128
+ * columns), [rows][ceil(d / 128)]: code * 2^(scale - 127).  They are made so: e
+ * is the smallest integer with max |finite value| <= 448 * 2^e over the 128, at
+ * least -126 and at most 120 (an all-zero block: -126); a code is value / 2^e
+ * rounded to the nearest E4M3 (ties to even), infinities to 448; NaN stays NaN.
+ * 8-bit weights [n][k] have one scale per (128 rows, 128 columns).  The sums of
+ * products are in fp32. */
+
+/* More types, of outputs here only. */
+enum { MOE_DTYPE_E4M3 = 3 };
+
+/* Norm of rows, with a residual's addition: z = x + residual (fp32; x alone
+ * where residual is NULL), residual <- z rounded to dtype, y = z / sqrt(mean(z^2)
+ * + eps) * gamma from the unrounded z; out <- y rounded to dtype, codes and
+ * scales <- y in 8 bits.  out may be NULL, or codes and scales, not all; out may
+ * be x. */
+typedef struct {
+  const void* x;            /* device [n_rows][d] */
+  int64_t x_stride;         /* elements, as all strides here; multiples of 8 */
+  void* residual;           /* device [n_rows][d], read and written, or NULL */
+  int64_t residual_stride;
+  const void* gamma;        /* device [d] */
+  void* out;                /* device [n_rows][d], or NULL */
+  int64_t out_stride;
+  uint8_t* codes;           /* device [n_rows][d], or NULL */
+  int64_t codes_stride;
+  uint8_t* scales;          /* device [n_rows][ceil(d / 128)] */
+  int64_t scales_stride;    /* any */
+  int64_t n_rows;
+  int32_t d;                /* a multiple of 8, <= 16384 */
+  int32_t dtype;            /* of x, residual and out: BF16, F16 or F32 */
+  int32_t gamma_dtype;      /* BF16, F16 or F32 */
+  float eps;
+} moe_rms_norm_t;
+
+/* Pointers 16-byte aligned (codes 8, scales any).  Errors: INVALID_ARG,
+ * UNSUPPORTED, CUDA. */
+int moe_rms_norm(void* stream, const moe_rms_norm_t* args);
+
+/* The 8-bit form of x device [n_rows][d] of dtype BF16, F16 or F32. */
+int moe_fp8_quantize(void* stream, const void* x, int dtype, int64_t x_stride, int64_t n_rows,
+                     int d, uint8_t* codes, int64_t codes_stride, uint8_t* scales,
+                     int64_t scales_stride);
+
+/* The 8-bit form of weights: n_mat matrices w device [n][k] of dtype BF16, F16
+ * or F32, back to back -> codes [n_mat][n][k], scales [n_mat][ceil(n / 128)]
+ * [ceil(k / 128)], by the activations' rule over 128 x 128. */
+int moe_fp8_pack(void* stream, const void* w, int dtype, int64_t n_mat, int64_t n, int64_t k,
+                 uint8_t* codes, uint8_t* scales);
+
+typedef enum {
+  MOE_WEIGHTS_E4M3 = 0,     /* codes [n][k], scales [ceil(n / 128)][ceil(k / 128)] */
+  MOE_WEIGHTS_MXFP4 = 1     /* canonical (layout 0): q [n][k / 2], scales [n][k / 32] */
+} moe_weight_format;
+
+typedef enum {
+  MOE_ACT_NONE = 0,         /* out[., j] = p[., j] */
+  MOE_ACT_SWIGLU = 1        /* out[., j] = silu(p[., j]) * p[., n / 2 + j]: gates, then ups */
+} moe_activation;
+
+/* Products of 8-bit activations with 8-bit or MXFP4 weights: p[i, j] = sum_k
+ * x[src(i), k] w[j, k].  With offsets NULL there is one matrix, n_experts is 1
+ * and src(i) = i, or rows[i].  With offsets, output rows offsets[e] ..
+ * offsets[e + 1) go through matrix e (a moe_dispatch's offsets); output rows
+ * outside these are left alone, and offsets are read as within [0, n_rows], an
+ * end below its start as the start.  rows[i], the row of x that output row i
+ * reads, is read as within [0, x_rows).  out_dtype E4M3 (SWIGLU only) writes
+ * the 8-bit form of the result: codes in out, scales in out_scales.  The
+ * kernel's waits between its warps are bounded: one that runs out (none does on
+ * a device that works) leaves NaN in the tile it was for. */
+typedef struct {
+  const uint8_t* x;         /* device [x_rows][k], 16-byte aligned */
+  int64_t x_stride;         /* a multiple of 16 */
+  const uint8_t* x_scales;
+  int64_t x_scales_stride;
+  const uint8_t* w;         /* device [n_experts][n][k or k / 2], 16- (MXFP4: 32-) byte aligned */
+  int64_t w_stride, w_expert_stride;   /* bytes, multiples of 16 (MXFP4: 32) */
+  const uint8_t* w_scales;
+  int64_t w_scales_stride, w_scales_expert_stride;
+  const int32_t* offsets;   /* device [n_experts + 1], or NULL */
+  const int32_t* rows;      /* device [n_rows], or NULL */
+  void* out;                /* device [n_rows][n, or n / 2 with SWIGLU] */
+  int64_t out_stride;       /* elements */
+  uint8_t* out_scales;      /* E4M3: device [n_rows][ceil(n / 2 / 128)] */
+  int64_t out_scales_stride;
+  int32_t n_rows, x_rows, n, k;   /* k a multiple of 16 (MXFP4: 128) */
+  int32_t n_experts;        /* <= 1024 */
+  int32_t w_format, activation, out_dtype;   /* BF16, F16, F32 or E4M3 */
+} moe_fp8_product_t;
+
+/* Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+int moe_fp8_product(void* stream, const moe_fp8_product_t* args);
+
+/* Tokens by expert, from the choices idx device [n_tokens][top_k]: choice (t, j)
+ * of an expert in [0, n_experts) is one entry; entries are ordered by expert,
+ * and by t, then j, within one.  offsets [n_experts + 1]: each expert's first
+ * entry; rows [n_tokens * top_k]: the token of each entry, -1 past the last;
+ * slots [n_tokens][top_k]: the entry of each choice, -1 where idx names no
+ * expert.  n_experts <= 1024, n_tokens * top_k <= 2^24.  Errors: INVALID_ARG,
+ * UNSUPPORTED, CUDA. */
+int moe_dispatch(void* stream, const int32_t* idx, int n_tokens, int top_k, int n_experts,
+                 int32_t* offsets, int32_t* rows, int32_t* slots);
+
+/* Weighted sums of the experts' rows: out[t] = residual[t] + sum_j w[t, j]
+ * y[slots[t, j]], in fp32 in the order of j and rounded once; residual may be
+ * NULL (0) or out; slots outside [0, y_rows) count 0.  y [y_rows][d], residual
+ * and out [n_tokens][d] of dtype BF16, F16 or F32, 16-byte aligned, strides in
+ * elements, multiples of 8, as is d; w fp32 and slots [n_tokens][top_k], top_k
+ * <= 32.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+typedef struct {
+  const void* y;
+  int64_t y_stride;
+  const float* w;
+  const int32_t* slots;
+  const void* residual;
+  int64_t residual_stride;
+  void* out;
+  int64_t out_stride;
+  int32_t n_tokens, top_k, y_rows, d, dtype;
+} moe_combine_t;
+
+int moe_combine(void* stream, const moe_combine_t* args);
 
 /* Human-readable name of a status code (static string). */
 const char* moe_status_string(int status);

@@ -1,7 +1,8 @@
 """GB300-native (sm_103a) MoE decode layer: router + biased top-k, MXFP4 routed
 SwiGLU experts with weighted combine, bf16 shared expert, residual + RMSNorm;
 beside it the serving operators of a decode step (serving.py): block tables and
-slot maps, an 8-bit KV cache with its attention, expert routing from logits.
+slot maps, an 8-bit KV cache with its attention, expert routing from logits; and
+for prompts, or any number of rows, the 8-bit products, norms and experts (fp8.py).
 
 The compute path is the CUDA library `libmoe_decode.so` behind the C ABI in
 include/moe_decode.h; this package only marshals arguments (PyTorch tensors
@@ -15,9 +16,12 @@ from ._binding import (MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR
                        MOE_ERR_ALLOC, MOE_ERR_TIMEOUT, MoEDims, MoEError, MoEWeights, check, lib,
                        status_string)
 
+from .fp8 import (MoEDispatch, Quantized, RMSNormed, expert_linear, fp8_linear, fp8_pack,
+                  fp8_quantize, moe_combine, moe_dispatch, rms_norm)
 from .serving import KVCache, KVPlan, kv_plan, kv_release, moe_route
 
-__all__ = ["KVCache", "KVPlan", "kv_plan", "kv_release", "moe_route", "MoELayer", "MoEDims", "MoEWeights", "MoEError", "mxfp4_pack", "mxfp4_pack_device",
+__all__ = ["MoEDispatch", "Quantized", "RMSNormed", "expert_linear", "fp8_linear", "fp8_pack",
+           "fp8_quantize", "moe_combine", "moe_dispatch", "rms_norm", "KVCache", "KVPlan", "kv_plan", "kv_release", "moe_route", "MoELayer", "MoEDims", "MoEWeights", "MoEError", "mxfp4_pack", "mxfp4_pack_device",
            "mxfp4_repack", "mxfp4_retile_device",
            "mxfp4_packed_bytes", "status_string", "lib", "MOE_OK", "MOE_ERR_INVALID_ARG",
            "MOE_ERR_UNSUPPORTED", "MOE_ERR_CUDA", "MOE_ERR_ALLOC", "MOE_ERR_TIMEOUT"]

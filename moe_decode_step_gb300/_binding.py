@@ -39,8 +39,12 @@ class MoEWeights(ctypes.Structure):
 KV_CACHE = struct.Struct("4P4q4i")
 KV_ATTENTION = struct.Struct("P2qP2q2Pq3PN8if4x")
 ROUTE = struct.Struct("7if")
+# moe_rms_norm_t, moe_fp8_product_t and moe_combine_t
+RMS_NORM = struct.Struct("PqPq2PqPqP2q3if")
+FP8_PRODUCT = struct.Struct("PqPqP2qP2q3PqPq8i")
+COMBINE = struct.Struct("Pq3PqPq5i4x")
 
-DTYPE_BF16, DTYPE_F16, DTYPE_F32 = 0, 1, 2
+DTYPE_BF16, DTYPE_F16, DTYPE_F32, DTYPE_E4M3 = 0, 1, 2, 3
 
 
 class MoEError(RuntimeError):
@@ -100,6 +104,15 @@ _PROTOS = {
     "moe_kv_attention_workspace": (ctypes.c_size_t, [ctypes.c_int]),
     "moe_route": (ctypes.c_int, [_P, _P, _P, ctypes.c_int, ctypes.c_int64, ctypes.c_int64, _P, _P,
                                  _P]),
+    "moe_rms_norm": (ctypes.c_int, [_P, _P]),
+    "moe_fp8_quantize": (ctypes.c_int, [_P, _P, ctypes.c_int, ctypes.c_int64, ctypes.c_int64,
+                                        ctypes.c_int, _P, ctypes.c_int64, _P, ctypes.c_int64]),
+    "moe_fp8_pack": (ctypes.c_int, [_P, _P, ctypes.c_int, ctypes.c_int64, ctypes.c_int64,
+                                    ctypes.c_int64, _P, _P]),
+    "moe_fp8_product": (ctypes.c_int, [_P, _P]),
+    "moe_dispatch": (ctypes.c_int, [_P, _P, ctypes.c_int, ctypes.c_int, ctypes.c_int, _P, _P,
+                                    _P]),
+    "moe_combine": (ctypes.c_int, [_P, _P]),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "moe_last_cuda_error": (ctypes.c_int, []),
 }

@@ -1,0 +1,283 @@
+// C ABI of the 8-bit products, norms and the experts of any number of rows.
+#include <cuda.h>
+
+#include "fp8_product.cuh"
+#include "fp8_rows.cuh"
+#include "host.cuh"
+#include "moe_decode.h"
+#include "moe_rows.cuh"
+
+using namespace moe;
+
+namespace {
+
+bool dtype16or32(int t) { return t == MOE_DTYPE_BF16 || t == MOE_DTYPE_F16 || t == MOE_DTYPE_F32; }
+
+template <int T, int NV>
+void launch_norm(const NormArgs& a, bool f32, cudaStream_t st) {
+  constexpr int THREADS = T < 256 ? 256 : T, ROWS = THREADS / T;
+  const unsigned grid = (unsigned)((a.rows + ROWS - 1) / ROWS);
+  if (a.gamma) {
+    if (f32) rms_norm_kernel<T, NV, true, true><<<grid, THREADS, 0, st>>>(a);
+    else rms_norm_kernel<T, NV, false, true><<<grid, THREADS, 0, st>>>(a);
+  } else {
+    if (f32) rms_norm_kernel<T, NV, true, false><<<grid, THREADS, 0, st>>>(a);
+    else rms_norm_kernel<T, NV, false, false><<<grid, THREADS, 0, st>>>(a);
+  }
+}
+
+int run_norm(const NormArgs& a, int dtype, void* stream) {
+  if (a.rows == 0) return MOE_OK;
+  if (a.rows > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  const Device* dev;
+  const int rc = begin(&dev);
+  if (rc) return rc;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool f32 = dtype == MOE_DTYPE_F32;
+  if (a.d <= 1024) launch_norm<32, 4>(a, f32, st);
+  else if (a.d <= 4096) launch_norm<128, 4>(a, f32, st);
+  else if (a.d <= 8192) launch_norm<256, 4>(a, f32, st);
+  else launch_norm<512, 4>(a, f32, st);
+  return end();
+}
+
+// Tensor map of bytes (or of E2M1 nibbles that become 16 bytes each 16) with
+// 128-byte-swizzled boxes of 128 columns.
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                            const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                            CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                            CUtensorMapFloatOOBfill);
+
+int encoder(Encode* out) {
+  static std::atomic<void*> known{nullptr};   // a symbol of the driver: the same for every caller
+  void* fn = known.load(std::memory_order_acquire);
+  if (!fn) {
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess || !fn) {
+      cudaGetLastError();
+      return MOE_ERR_UNSUPPORTED;
+    }
+    known.store(fn, std::memory_order_release);
+  }
+  *out = reinterpret_cast<Encode>(fn);
+  return MOE_OK;
+}
+
+int encode_map(Encode fn, CUtensorMap* map, bool nibbles, const void* p, uint64_t cols,
+               uint64_t rows, uint64_t mats, uint64_t stride, uint64_t mat_stride, int box_rows) {
+  const cuuint64_t dims[3] = {cols, rows, mats};
+  const cuuint64_t strides[2] = {stride, mat_stride};
+  const cuuint32_t box[3] = {kGemmK, (cuuint32_t)box_rows, 1};
+  const cuuint32_t one[3] = {1, 1, 1};
+  const CUresult r = fn(map, nibbles ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B
+                                     : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                        mats ? 3 : 2, const_cast<void*>(p), dims, strides, box, one,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+
+template <bool W4, bool SWIGLU>
+int launch_product(const GemmArgs& a, const CUtensorMap& xt, const CUtensorMap& xg,
+                   const CUtensorMap& wm, int n_sm, cudaStream_t st) {
+  const cudaError_t e = cudaFuncSetAttribute(fp8_product_kernel<W4, SWIGLU>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             GemmShape::SMEM);
+  if (e != cudaSuccess) return cuda_fail(e);
+  // tiles the call can have at most, as far as the host knows; any grid is right
+  constexpr int COLS = SWIGLU ? kGemmN / 2 : kGemmN;
+  const long long m = a.offsets ? (long long)a.rows / kGemmM + std::min(a.experts, a.rows)
+                                : ((long long)a.rows + kGemmM - 1) / kGemmM;
+  const long long tiles = m * ((a.n + COLS - 1) / COLS);
+  const int grid = (int)std::min<long long>(n_sm, tiles);
+  fp8_product_kernel<W4, SWIGLU><<<grid, kGemmThreads, GemmShape::SMEM, st>>>(a, xt, xg, wm);
+  return end();
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_rms_norm(void* stream, const moe_rms_norm_t* args) {
+  if (!args) return MOE_ERR_INVALID_ARG;
+  const moe_rms_norm_t& t = *args;
+  if (t.n_rows < 0 || t.d < 1 || !dtype16or32(t.dtype) || !dtype16or32(t.gamma_dtype) ||
+      !(t.eps >= 0.f))
+    return MOE_ERR_INVALID_ARG;
+  if (t.n_rows == 0) return MOE_OK;
+  if (!t.x || !t.gamma || (!t.out && !t.codes) || !t.codes != !t.scales)
+    return MOE_ERR_INVALID_ARG;
+  if (t.d % 8 || t.d > 16384 || misaligned(t.x, 16) || misaligned(t.residual, 16) ||
+      misaligned(t.gamma, 16) || misaligned(t.out, 16) || misaligned(t.codes, 8) ||
+      ((t.x_stride | (t.residual ? t.residual_stride : 0) | (t.out ? t.out_stride : 0) |
+        (t.codes ? t.codes_stride : 0)) & 7))
+    return MOE_ERR_UNSUPPORTED;
+  NormArgs a{t.x,     t.x_stride,     t.residual, t.residual_stride, t.gamma,  t.out, t.out_stride,
+             t.codes, t.codes_stride, t.scales,   t.scales_stride,   t.n_rows, t.d,
+             t.dtype == MOE_DTYPE_F16, t.gamma_dtype, t.eps};
+  return run_norm(a, t.dtype, stream);
+}
+
+int moe_fp8_quantize(void* stream, const void* x, int dtype, int64_t x_stride, int64_t n_rows,
+                     int d, uint8_t* codes, int64_t codes_stride, uint8_t* scales,
+                     int64_t scales_stride) {
+  if (n_rows < 0 || d < 1 || !dtype16or32(dtype)) return MOE_ERR_INVALID_ARG;
+  if (n_rows == 0) return MOE_OK;
+  if (!x || !codes || !scales) return MOE_ERR_INVALID_ARG;
+  if (d % 8 || d > 16384 || misaligned(x, 16) || misaligned(codes, 8) ||
+      ((x_stride | codes_stride) & 7))
+    return MOE_ERR_UNSUPPORTED;
+  NormArgs a{};
+  a.x = x;
+  a.xs = x_stride;
+  a.codes = codes;
+  a.cs = codes_stride;
+  a.scales = scales;
+  a.ss = scales_stride;
+  a.rows = n_rows;
+  a.d = d;
+  a.f16 = dtype == MOE_DTYPE_F16;
+  return run_norm(a, dtype, stream);
+}
+
+int moe_fp8_pack(void* stream, const void* w, int dtype, int64_t n_mat, int64_t n, int64_t k,
+                 uint8_t* codes, uint8_t* scales) {
+  if (n_mat < 0 || n < 1 || k < 1 || !dtype16or32(dtype)) return MOE_ERR_INVALID_ARG;
+  if (n_mat == 0) return MOE_OK;
+  if (!w || !codes || !scales) return MOE_ERR_INVALID_ARG;
+  if (n > INT32_MAX || k > INT32_MAX || n_mat > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  const long long blocks = (n + 127) / 128 * ((k + 127) / 128);
+  if (blocks > INT32_MAX / n_mat || misaligned(w, dtype == MOE_DTYPE_F32 ? 4 : 2))
+    return MOE_ERR_UNSUPPORTED;
+  const Device* dev;
+  const int rc = begin(&dev);
+  if (rc) return rc;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const unsigned grid = (unsigned)(blocks * n_mat);
+  if (dtype == MOE_DTYPE_F32) fp8_pack_kernel<MOE_DTYPE_F32><<<grid, 256, 0, st>>>(w, n, k, codes, scales);
+  else if (dtype == MOE_DTYPE_F16) fp8_pack_kernel<MOE_DTYPE_F16><<<grid, 256, 0, st>>>(w, n, k, codes, scales);
+  else fp8_pack_kernel<MOE_DTYPE_BF16><<<grid, 256, 0, st>>>(w, n, k, codes, scales);
+  return end();
+}
+
+int moe_fp8_product(void* stream, const moe_fp8_product_t* args) {
+  if (!args) return MOE_ERR_INVALID_ARG;
+  const moe_fp8_product_t& t = *args;
+  const bool w4 = t.w_format == MOE_WEIGHTS_MXFP4, swiglu = t.activation == MOE_ACT_SWIGLU;
+  const bool codes = t.out_dtype == MOE_DTYPE_E4M3;
+  if ((!w4 && t.w_format != MOE_WEIGHTS_E4M3) || (!swiglu && t.activation != MOE_ACT_NONE) ||
+      (!codes && !dtype16or32(t.out_dtype)) || t.n_rows < 0 || t.x_rows < 0 || t.n < 1 || t.k < 1 ||
+      t.n_experts < 1 || (!t.offsets && t.n_experts != 1) || (codes && !swiglu) ||
+      (swiglu && t.n % 2) || (!t.rows && t.x_rows != t.n_rows))
+    return MOE_ERR_INVALID_ARG;
+  if (t.n_rows == 0) return MOE_OK;
+  if (!t.x || !t.x_scales || !t.w || !t.w_scales || !t.out || (codes && !t.out_scales) ||
+      t.x_rows == 0 || t.x_stride < t.k ||
+      t.w_stride < (w4 ? t.k / 2 : t.k))
+    return MOE_ERR_INVALID_ARG;
+  const int unit = w4 ? 32 : 16, size = codes ? 1 : t.out_dtype == MOE_DTYPE_F32 ? 4 : 2;
+  if (t.k % (w4 ? 128 : 16) || t.n_experts > kGemmMaxExperts || misaligned(t.x, 16) ||
+      (t.x_stride & 15) || misaligned(t.w, unit) || ((t.w_stride | t.w_expert_stride) & (unit - 1)) ||
+      t.n_rows > INT32_MAX - kGemmM || t.n > INT32_MAX - kGemmN || t.k > INT32_MAX - kGemmK ||
+      misaligned(t.out, size))
+    return MOE_ERR_UNSUPPORTED;
+  const Device* dev;
+  int rc = begin(&dev);
+  if (rc) return rc;
+  Encode fn;
+  if ((rc = encoder(&fn))) return rc;
+  CUtensorMap xt, xg, wm;
+  if ((rc = encode_map(fn, &xt, false, t.x, t.k, t.x_rows, 0, t.x_stride, 0, kGemmM)) ||
+      (rc = encode_map(fn, &xg, false, t.x, t.k, t.x_rows, 0, t.x_stride, 0, 1)) ||
+      (rc = encode_map(fn, &wm, w4, t.w, t.k, t.n, t.n_experts, t.w_stride,
+                       t.n_experts > 1 ? t.w_expert_stride : (uint64_t)t.w_stride * t.n, kGemmN / 2)))
+    return rc;
+  GemmArgs a{};
+  a.K = t.k;
+  a.kb = (t.k + kGemmK - 1) / kGemmK;
+  a.wide = t.n;
+  a.n = swiglu ? t.n / 2 : t.n;
+  a.rows = t.n_rows;
+  a.x_rows = t.x_rows;
+  a.experts = t.n_experts;
+  a.offsets = t.offsets;
+  a.src = t.rows;
+  a.xs = t.x_scales;
+  a.xs_stride = t.x_scales_stride;
+  a.ws = t.w_scales;
+  a.ws_stride = t.w_scales_stride;
+  a.ws_expert = t.w_scales_expert_stride;
+  a.out = static_cast<char*>(t.out);
+  a.out_stride = t.out_stride * size;
+  a.os = t.out_scales;
+  a.os_stride = t.out_scales_stride;
+  a.out_dtype = t.out_dtype;
+  a.vec = !misaligned(t.out, 16) && a.out_stride % 16 == 0;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (w4) return swiglu ? launch_product<true, true>(a, xt, xg, wm, dev->n_sm, st)
+                        : launch_product<true, false>(a, xt, xg, wm, dev->n_sm, st);
+  return swiglu ? launch_product<false, true>(a, xt, xg, wm, dev->n_sm, st)
+                : launch_product<false, false>(a, xt, xg, wm, dev->n_sm, st);
+}
+
+int moe_dispatch(void* stream, const int32_t* idx, int n_tokens, int top_k, int n_experts,
+                 int32_t* offsets, int32_t* rows, int32_t* slots) {
+  if (n_tokens < 0 || top_k < 1 || n_experts < 1 || !offsets) return MOE_ERR_INVALID_ARG;
+  const long long n = (long long)n_tokens * top_k;
+  if (n > 0 && (!idx || !rows || !slots)) return MOE_ERR_INVALID_ARG;
+  if (n_experts > kDispMaxExperts || n > 1 << 24) return MOE_ERR_UNSUPPORTED;
+  const Device* dev;
+  const int rc = begin(&dev);
+  if (rc) return rc;
+  const int smem = kDispWarps * n_experts * 2;
+  cudaError_t e = cudaFuncSetAttribute(dispatch_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kDispWarps * kDispMaxExperts * 2);
+  if (e != cudaSuccess) return cuda_fail(e);
+  int ctas = 1;
+  while (ctas < kDispMaxCtas && n > 4096ll * ctas) ctas *= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kDispThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = ctas;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  const DispatchArgs a{idx, (int)n, top_k, n_experts, offsets, rows, slots};
+  e = cudaLaunchKernelEx(&cfg, dispatch_kernel, a);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return cuda_fail(e);
+  }
+  return end();
+}
+
+int moe_combine(void* stream, const moe_combine_t* args) {
+  if (!args) return MOE_ERR_INVALID_ARG;
+  const moe_combine_t& t = *args;
+  if (t.n_tokens < 0 || t.top_k < 1 || t.y_rows < 0 || t.d < 1 || !dtype16or32(t.dtype))
+    return MOE_ERR_INVALID_ARG;
+  if (t.n_tokens == 0) return MOE_OK;
+  if ((!t.y && t.y_rows > 0) || !t.w || !t.slots || !t.out) return MOE_ERR_INVALID_ARG;
+  if (t.d % 8 || t.top_k > 32 || misaligned(t.y, 16) || misaligned(t.residual, 16) ||
+      misaligned(t.out, 16) ||
+      ((t.y_stride | (t.residual ? t.residual_stride : 0) | t.out_stride) & 7))
+    return MOE_ERR_UNSUPPORTED;
+  const Device* dev;
+  const int rc = begin(&dev);
+  if (rc) return rc;
+  const CombineArgs a{t.y, t.y_stride, t.w, t.slots, t.residual, t.residual_stride, t.out,
+                      t.out_stride, t.n_tokens, t.top_k, t.y_rows, t.d, t.dtype == MOE_DTYPE_F16};
+  const dim3 grid((t.d / 8 + kCombThreads - 1) / kCombThreads, std::min(t.n_tokens, 65535));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (t.dtype == MOE_DTYPE_F32) combine_kernel<true><<<grid, kCombThreads, 0, st>>>(a);
+  else combine_kernel<false><<<grid, kCombThreads, 0, st>>>(a);
+  return end();
+}
+
+}  // extern "C"

@@ -1,11 +1,6 @@
 // The serving operators' C ABI: block tables, the 8-bit KV cache, expert
 // routing from logits.
-#include <cuda_runtime.h>
-
-#include <algorithm>
-#include <atomic>
-#include <cstdint>
-
+#include "host.cuh"
 #include "kv_append.cuh"
 #include "kv_attention.cuh"
 #include "kv_attention_tc.cuh"
@@ -15,60 +10,10 @@
 
 using namespace moe;
 
-namespace moe_internal {
-int cuda_fail(cudaError_t e);
-}
-
 namespace {
 
-using moe_internal::cuda_fail;
-
-constexpr int kMaxDevices = 64;
-
-struct Device {
-  std::atomic<bool> known{false};   // set after the others
-  std::atomic<bool> sm103{false};
-  std::atomic<int> n_sm{0};
-};
-
-// The current device's properties, asked for once per device: a host-side
-// query whose answer cannot change.
-int this_device(const Device** out) {
-  static Device devices[kMaxDevices];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_fail(e);
-  if (dev < 0 || dev >= kMaxDevices) return MOE_ERR_UNSUPPORTED;
-  Device& d = devices[dev];
-  if (!d.known.load(std::memory_order_acquire)) {
-    int major = 0, minor = 0, n_sm = 0;
-    if ((e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev)) ||
-        (e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev)) ||
-        (e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev)))
-      return cuda_fail(e);
-    // threads whose first calls meet store the same values
-    d.sm103.store(major == 10 && minor == 3, std::memory_order_relaxed);
-    d.n_sm.store(std::min(n_sm, kDecMaxCtas), std::memory_order_relaxed);
-    d.known.store(true, std::memory_order_release);
-  }
-  *out = &d;
-  return d.sm103 ? MOE_OK : MOE_ERR_UNSUPPORTED;
-}
-
-// What every call starts with: an error left pending by earlier work is
-// reported as it is, not blamed on this call's launches.
-int begin(const Device** dev) {
-  const cudaError_t e = cudaPeekAtLastError();
-  if (e != cudaSuccess) return cuda_fail(e);
-  return this_device(dev);
-}
-
-int end() {
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? MOE_OK : cuda_fail(e);
-}
-
-inline bool misaligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) != 0; }
+// SMs that the attention kernels' joins and workspace count on.
+int attention_sms(const Device* dev) { return std::min((int)dev->n_sm, kDecMaxCtas); }
 
 int block_log2(int bs) {
   for (int l = 4; l <= 7; ++l)
@@ -280,7 +225,8 @@ size_t moe_kv_attention_workspace(int head_dim) {
   if (head_dim != 64 && head_dim != 128) return 0;
   const Device* dev;
   if (this_device(&dev)) return 0;
-  return arrived_bytes(dev->n_sm) + (size_t)dev->n_sm * dec_floats(head_dim) * 4;
+  const int n_sm = attention_sms(dev);
+  return arrived_bytes(n_sm) + (size_t)n_sm * dec_floats(head_dim) * 4;
 }
 
 int moe_kv_attention(void* stream, const moe_kv_cache_t* cache, const moe_kv_attention_t* args) {
@@ -328,10 +274,11 @@ int moe_kv_attention(void* stream, const moe_kv_cache_t* cache, const moe_kv_att
   a.scale_log2 = t.scale * 1.4426950408889634f;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   a.arrived = static_cast<unsigned*>(t.workspace);
-  a.partial = reinterpret_cast<float*>(static_cast<char*>(t.workspace) + arrived_bytes(dev->n_sm));
+  const int n_sm = attention_sms(dev);
+  a.partial = reinterpret_cast<float*>(static_cast<char*>(t.workspace) + arrived_bytes(n_sm));
   const int max_q = std::max(t.max_q, 1);   // a hint, whatever it says
-  return cache->head_dim == 64 ? launch_attention<64>(a, dev->n_sm, max_q, st)
-                               : launch_attention<128>(a, dev->n_sm, max_q, st);
+  return cache->head_dim == 64 ? launch_attention<64>(a, n_sm, max_q, st)
+                               : launch_attention<128>(a, n_sm, max_q, st);
 }
 
 int moe_route(void* stream, const moe_route_t* cfg, const void* logits, int dtype,

@@ -80,21 +80,6 @@ struct PrShape {
   static constexpr int OCOL = 256;   // tensor memory: S at 0 and 128, O at OCOL + D t
 };
 
-// ---- tensor memory, 32 lanes x 32 columns a warp ----
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
@@ -147,10 +132,6 @@ __device__ __forceinline__ constexpr uint32_t umma_idesc_f16(uint32_t N) {
   return (1u << 4) | ((N >> 3) << 17) | ((128u >> 4) << 24);
 }
 constexpr uint32_t kUmmaTransposeB = 1u << 16;   // B is MN-major
-// Generic writes to shared memory become visible to the tensor cores.
-__device__ __forceinline__ void fence_async_shared() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
 
 // ---------------------------------------------------------------------------
 // Items and schedule
@@ -396,23 +377,11 @@ struct PrShared {
 };
 
 // Waits for a phase, two seconds at most; then marks the CTA dead, whose waits
-// all end at once and whose results become NaN.  The hint lets the hardware
-// suspend the thread: threads that poll take issue slots and shared-memory
-// cycles from the ones that work (a tile took 1.5 times as long).
-__device__ __forceinline__ bool pr_try_wait(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity), "r"(1000000u)
-      : "memory");
-  return ok != 0;
-}
+// all end at once and whose results become NaN.
 __device__ __forceinline__ void pr_wait(uint64_t* bar, uint32_t parity, PrShared& sh) {
-  if (pr_try_wait(bar, parity)) return;
+  if (mbar_try_wait_long(bar, parity)) return;
   const unsigned long long t0 = global_ns();
-  while (!pr_try_wait(bar, parity)) {
+  while (!mbar_try_wait_long(bar, parity)) {
     if (*(volatile int*)&sh.dead) return;
     if (global_ns() - t0 > kWaitLimitNs) {
       *(volatile int*)&sh.dead = 1;
@@ -701,7 +670,7 @@ __device__ __forceinline__ void pr_values(PrShared& sh, uint32_t base, int t, in
 __device__ __noinline__ void pr_drain(PrShared& sh, int t) {
   __syncwarp();
   if (elect_one()) umma_commit(&sh.drained[t]);
-  for (int i = 0; i < 100 && !pr_try_wait(&sh.drained[t], 0); ++i) {
+  for (int i = 0; i < 100 && !mbar_try_wait_long(&sh.drained[t], 0); ++i) {
   }
   __syncwarp();
 }

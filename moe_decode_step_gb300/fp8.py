@@ -1,0 +1,254 @@
+"""8-bit products, norms and the experts of any number of rows: the norm with
+the residual's addition, 8-bit activations and weights, products dense or by
+expert, the sorting of tokens by expert and the weighted sum of their results.
+
+Argument marshalling only, as in serving.py: every call checks its tensors, then
+makes one call of the C ABI (include/moe_decode.h states the formulas and the
+rules).  All of it is asynchronous on `stream` (default: the current stream);
+tensors made here are allocated on that stream.
+
+8-bit activations are E4M3 codes (float8_e4m3fn or uint8) [rows, d] with E8M0
+scales (float8_e8m0fnu or uint8) [rows, ceil(d / 128)]; 8-bit weights codes [n, k]
+with scales [ceil(n / 128), ceil(k / 128)]; MXFP4 weights the layer's canonical
+layout, uint8 [n, k / 2] with scales [n, k / 32].
+"""
+from typing import NamedTuple, Optional
+
+import torch
+
+from ._binding import COMBINE, DTYPE_E4M3, FP8_PRODUCT, RMS_NORM, check, lib
+from .serving import _CODES, _DTYPE, _SCALES, _empty, _raw_stream, _vector, _want
+
+_ACTIVATION = {None: 0, "swiglu": 1}
+
+
+class Quantized(NamedTuple):
+    codes: torch.Tensor     # float8_e4m3fn
+    scales: torch.Tensor    # float8_e8m0fnu
+
+
+class RMSNormed(NamedTuple):
+    out: Optional[torch.Tensor]      # 16- or 32-bit, as x
+    codes: Optional[torch.Tensor]    # float8_e4m3fn
+    scales: Optional[torch.Tensor]   # float8_e8m0fnu
+
+
+class MoEDispatch(NamedTuple):
+    """What moe_dispatch writes: the choices sorted by expert."""
+    offsets: torch.Tensor   # int32 [n_experts + 1]: first entry of each expert
+    rows: torch.Tensor      # int32 [tokens * top_k]: token of each entry
+    slots: torch.Tensor     # int32 [tokens, top_k]: entry of each choice
+
+
+def _blocks(n):
+    return (n + 127) // 128
+
+
+def _matrix(t, name, dtypes, device=None):
+    """Rows with a contiguous last dimension, on `device` (None: any CUDA device);
+    returns the row stride, of one row its length rounded up to 16."""
+    if (t.dim() != 2 or t.dtype not in dtypes or not t.is_cuda
+            or (device is not None and t.device != device)
+            or (t.shape[1] > 1 and t.stride(1) != 1)):
+        _want(False, name, f"{' or '.join(map(str, dtypes))} [rows, columns] with a contiguous "
+              f"last dimension on {device or 'a CUDA device'}", t)
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
+
+
+def _new_codes(stream, dev, rows, d):
+    return (_empty(stream, torch.float8_e4m3fn, dev, rows, d),
+            _empty(stream, torch.float8_e8m0fnu, dev, rows, _blocks(d)))
+
+
+def rms_norm(x, gamma, residual=None, eps=1e-6, out=True, quantize=False, stream=None):
+    """Norm of rows with the residual's addition (moe_rms_norm): x bfloat16,
+    float16 or float32 [rows, d], residual the same (updated in place) or None,
+    gamma [d].  Returns an RMSNormed: out in x's type (out=True, or a tensor to
+    write; None where out=False), and with quantize the 8-bit form of the same
+    unrounded values."""
+    dev = x.device
+    xs = _matrix(x, "x", tuple(_DTYPE))
+    rows, d = x.shape
+    rs = 0
+    if residual is not None:
+        rs = _matrix(residual, "residual", (x.dtype,), dev)
+        _want(residual.shape == x.shape, "residual", f"the shape of x, {tuple(x.shape)}", residual)
+    _vector(gamma, d, gamma.dtype if gamma.dtype in _DTYPE else torch.float32, "gamma", dev)
+    raw = _raw_stream(stream, dev)
+    os = 0
+    if out is True:
+        out = _empty(stream, x.dtype, dev, rows, d)
+    if out is False or out is None:
+        out = None
+        _want(quantize, "out", "an output: out or quantize", out)
+    else:
+        os = _matrix(out, "out", (x.dtype,), dev)
+        _want(out.shape == x.shape, "out", f"the shape of x, {tuple(x.shape)}", out)
+    codes = scales = None
+    if quantize:
+        codes, scales = _new_codes(stream, dev, rows, d)
+    args = RMS_NORM.pack(
+        x.data_ptr(), xs, residual.data_ptr() if residual is not None else 0, rs,
+        gamma.data_ptr(), out.data_ptr() if out is not None else 0, os,
+        codes.data_ptr() if quantize else 0, d, scales.data_ptr() if quantize else 0, _blocks(d),
+        rows, d, _DTYPE[x.dtype], _DTYPE[gamma.dtype], eps)
+    check(lib().moe_rms_norm(raw, args), "moe_rms_norm")
+    return RMSNormed(out, codes, scales)
+
+
+def fp8_quantize(x, stream=None):
+    """The 8-bit form of activations x bfloat16, float16 or float32 [rows, d]
+    (moe_fp8_quantize): Quantized(codes, scales)."""
+    xs = _matrix(x, "x", tuple(_DTYPE))
+    rows, d = x.shape
+    raw = _raw_stream(stream, x.device)
+    codes, scales = _new_codes(stream, x.device, rows, d)
+    check(lib().moe_fp8_quantize(raw, x.data_ptr(), _DTYPE[x.dtype], xs, rows, d, codes.data_ptr(),
+                                 d, scales.data_ptr(), _blocks(d)), "moe_fp8_quantize")
+    return Quantized(codes, scales)
+
+
+def fp8_pack(w, stream=None):
+    """The 8-bit form of weights w bfloat16, float16 or float32 [..., n, k],
+    contiguous (moe_fp8_pack): Quantized(codes [..., n, k], scales [...,
+    ceil(n / 128), ceil(k / 128)])."""
+    if w.dim() < 2 or w.dtype not in _DTYPE or not w.is_cuda or not w.is_contiguous():
+        _want(False, "w", "bfloat16, float16 or float32 [..., n, k] contiguous on a CUDA device", w)
+    n, k = w.shape[-2:]
+    raw = _raw_stream(stream, w.device)
+    codes = _empty(stream, torch.float8_e4m3fn, w.device, *w.shape)
+    scales = _empty(stream, torch.float8_e8m0fnu, w.device, *w.shape[:-2], _blocks(n), _blocks(k))
+    check(lib().moe_fp8_pack(raw, w.data_ptr(), _DTYPE[w.dtype], w.numel() // max(n * k, 1), n, k,
+                             codes.data_ptr(), scales.data_ptr()), "moe_fp8_pack")
+    return Quantized(codes, scales)
+
+
+def _product(what, x, x_scales, w, w_scales, offsets, rows, activation, quantize, out_dtype, out,
+             stream):
+    """fp8_linear and expert_linear; w [experts, n, k or k / 2]."""
+    dev = x.device
+    xs = _matrix(x, "x", _CODES)
+    x_rows, k = x.shape
+    ss = _matrix(x_scales, "x_scales", _SCALES, dev)
+    if tuple(x_scales.shape) != (x_rows, _blocks(k)):
+        _want(False, "x_scales", f"E8M0 scales {(x_rows, _blocks(k))}", x_scales)
+    experts, n = w.shape[:2]
+    mx = w.dtype == torch.uint8 and w.shape[2] * 2 == k
+    if ((not mx and (w.dtype not in _CODES or w.shape[2] != k)) or w.device != dev
+            or w.stride(2) != 1):
+        _want(False, "w", f"E4M3 codes [..., n, {k}] or MXFP4 bytes [..., n, {k // 2}], rows "
+              f"contiguous on {dev}", w)
+    want = (experts, n, k // 32) if mx else (experts, _blocks(n), _blocks(k))
+    if (tuple(w_scales.shape) != want or w_scales.dtype not in _SCALES or w_scales.device != dev
+            or (want[2] > 1 and w_scales.stride(2) != 1)):
+        _want(False, "w_scales", f"E8M0 scales {want[1:]} for each matrix, rows contiguous on "
+              f"{dev}", w_scales)
+    _want(activation in _ACTIVATION, "activation", "None or 'swiglu'", activation)
+    _want(activation is None or n % 2 == 0, "w", "gates and ups: an even number of rows", w)
+    _want(not quantize or activation is not None, "quantize", "an activation", quantize)
+    if offsets is not None:
+        _vector(offsets, experts + 1, torch.int32, "offsets", dev)
+    if rows is not None:
+        _vector(rows, None, torch.int32, "rows", dev)
+    n_rows = x_rows if rows is None else rows.shape[0]
+    cols = n // 2 if activation else n
+    raw = _raw_stream(stream, dev)
+    scales = None
+    if quantize:
+        out, scales = _new_codes(stream, dev, n_rows, cols)
+        kind, os = DTYPE_E4M3, cols
+    elif out is None:
+        _want(out_dtype in _DTYPE, "out_dtype", "bfloat16, float16 or float32", out_dtype)
+        out = _empty(stream, out_dtype, dev, n_rows, cols)
+        kind, os = _DTYPE[out_dtype], cols
+    else:
+        os = _matrix(out, "out", tuple(_DTYPE), dev)
+        _want(tuple(out.shape) == (n_rows, cols), "out", f"[{n_rows}, {cols}]", out)
+        kind = _DTYPE[out.dtype]
+    row = w.stride(1) if n > 1 else (w.shape[2] + 31) // 32 * 32
+    args = FP8_PRODUCT.pack(
+        x.data_ptr(), xs, x_scales.data_ptr(), ss, w.data_ptr(), row, w.stride(0),
+        w_scales.data_ptr(), w_scales.stride(1), w_scales.stride(0),
+        offsets.data_ptr() if offsets is not None else 0, rows.data_ptr() if rows is not None else 0,
+        out.data_ptr(), os, scales.data_ptr() if quantize else 0, _blocks(cols), n_rows, x_rows, n,
+        k, experts, int(mx), _ACTIVATION[activation], kind)
+    check(lib().moe_fp8_product(raw, args), what)
+    return Quantized(out, scales) if quantize else out
+
+
+def fp8_linear(x, x_scales, w, w_scales, activation=None, quantize=False,
+               out_dtype=torch.bfloat16, out=None, stream=None):
+    """x W^T of 8-bit activations x [rows, k] with 8-bit weights w [n, k] or MXFP4
+    weights w uint8 [n, k / 2] (moe_fp8_product).  activation 'swiglu' takes w as
+    n / 2 gate rows and n / 2 up rows and returns silu(gate) * up.  Returns out
+    [rows, n or n / 2] in out_dtype (or the given out), or with quantize (and an
+    activation) its 8-bit form, Quantized(codes, scales)."""
+    _want(w.dim() == 2, "w", "a matrix", w)
+    _want(w_scales.dim() == 2, "w_scales", "a matrix", w_scales)
+    return _product("fp8_linear", x, x_scales, w.unsqueeze(0), w_scales.unsqueeze(0), None, None,
+                    activation, quantize, out_dtype, out, stream)
+
+
+def expert_linear(x, x_scales, w, w_scales, offsets, rows=None, activation=None, quantize=False,
+                  out_dtype=torch.bfloat16, out=None, stream=None):
+    """fp8_linear by expert: w [experts, n, k or k / 2]; output rows offsets[e] ..
+    offsets[e + 1) (int32 [experts + 1], a dispatch's) go through matrix e, output
+    row i reading row rows[i] of x (int32, a dispatch's rows; None: row i).  Rows
+    of no expert are left as they are."""
+    _want(w.dim() == 3, "w", "a matrix for each expert", w)
+    _want(w_scales.dim() == 3, "w_scales", "a matrix for each expert", w_scales)
+    return _product("expert_linear", x, x_scales, w, w_scales, offsets, rows, activation, quantize,
+                    out_dtype, out, stream)
+
+
+def moe_dispatch(idx, n_experts, stream=None):
+    """Tokens by expert (moe_dispatch) from moe_route's idx, int32 [tokens, top_k]
+    contiguous: a MoEDispatch.  Choices outside [0, n_experts) are left out."""
+    if idx.dim() != 2 or idx.dtype != torch.int32 or not idx.is_cuda or not idx.is_contiguous():
+        _want(False, "idx", "torch.int32 [tokens, top_k] contiguous on a CUDA device", idx)
+    tokens, k = idx.shape
+    dev = idx.device
+    n_experts = int(n_experts)
+    _want(n_experts >= 1, "n_experts", "at least 1", n_experts)
+    raw = _raw_stream(stream, dev)
+    # one allocation, cut as kv_plan's
+    buf = _empty(stream, torch.int32, dev, 2 * tokens * k + n_experts + 1)
+    rows, slots, offsets = torch.unsafe_split_with_sizes(
+        buf, [tokens * k, tokens * k, n_experts + 1])
+    at = buf.data_ptr()
+    check(lib().moe_dispatch(raw, idx.data_ptr(), tokens, k, n_experts, at + 8 * tokens * k, at,
+                             at + 4 * tokens * k), "moe_dispatch")
+    return MoEDispatch(offsets, rows, slots.view(tokens, k))
+
+
+def moe_combine(y, w, slots, residual=None, out=None, stream=None):
+    """Weighted sums of the experts' rows (moe_combine): y bfloat16, float16 or
+    float32 [entries, d], w float32 and slots int32 [tokens, top_k] (moe_route's
+    weights, a dispatch's slots), residual [tokens, d] in y's type or None.
+    Returns out [tokens, d]; out may be residual."""
+    dev = y.device
+    ys = _matrix(y, "y", tuple(_DTYPE))
+    d = y.shape[1]
+    if (slots.dim() != 2 or slots.dtype != torch.int32 or slots.device != dev
+            or not slots.is_contiguous()):
+        _want(False, "slots", f"torch.int32 [tokens, top_k] contiguous on {dev}", slots)
+    tokens, k = slots.shape
+    if (w.dtype != torch.float32 or w.shape != slots.shape or w.device != dev
+            or not w.is_contiguous()):
+        _want(False, "w", f"torch.float32 {(tokens, k)} contiguous on {dev}", w)
+    rs = 0
+    if residual is not None:
+        rs = _matrix(residual, "residual", (y.dtype,), dev)
+        _want(tuple(residual.shape) == (tokens, d), "residual", f"[{tokens}, {d}]", residual)
+    raw = _raw_stream(stream, dev)
+    if out is None:
+        out = _empty(stream, y.dtype, dev, tokens, d)
+        os = d
+    else:
+        os = _matrix(out, "out", (y.dtype,), dev)
+        _want(tuple(out.shape) == (tokens, d), "out", f"[{tokens}, {d}]", out)
+    args = COMBINE.pack(y.data_ptr(), ys, w.data_ptr(), slots.data_ptr(),
+                        residual.data_ptr() if residual is not None else 0, rs, out.data_ptr(), os,
+                        tokens, k, y.shape[0], d, _DTYPE[y.dtype])
+    check(lib().moe_combine(raw, args), "moe_combine")
+    return out
