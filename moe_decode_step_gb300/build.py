@@ -11,7 +11,7 @@ HEADERS = ["csrc/common.cuh", "csrc/mxfp4.cuh", "csrc/planes.cuh", "csrc/stream.
            "csrc/tc.cuh", "csrc/tcgen05.cuh", "csrc/topk.cuh", "csrc/tail.cuh", "csrc/kv_cache.cuh",
            "csrc/kv_plan.cuh", "csrc/kv_append.cuh", "csrc/kv_attention.cuh",
            "csrc/kv_attention_tc.cuh", "csrc/route.cuh", "csrc/host.cuh", "csrc/fp8_rows.cuh",
-           "csrc/fp8_product.cuh", "csrc/moe_rows.cuh"]
+           "csrc/fp8_product.cuh", "csrc/moe_rows.cuh", "csrc/cluster.cuh"]
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-shared", "--threads", "4"]
 

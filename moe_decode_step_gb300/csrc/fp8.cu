@@ -79,20 +79,44 @@ int encode_map(Encode fn, CUtensorMap* map, bool nibbles, const void* p, uint64_
   return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
 
+// Token tiles and weight tiles of a call at most, as far as the host knows.
+long long tiles_at_most(const GemmArgs& a, bool swiglu) {
+  const int cols = swiglu ? kGemmRows : 2 * kGemmRows;
+  const long long m = a.offsets ? (long long)a.rows / a.tokens + std::min(a.experts, a.rows)
+                                : ((long long)a.rows + a.tokens - 1) / a.tokens;
+  return m * ((a.n + cols - 1) / cols);
+}
+
 template <bool W4, bool SWIGLU>
-int launch_product(const GemmArgs& a, const CUtensorMap& xt, const CUtensorMap& xg,
-                   const CUtensorMap& wm, int n_sm, cudaStream_t st) {
-  const cudaError_t e = cudaFuncSetAttribute(fp8_product_kernel<W4, SWIGLU>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             GemmShape::SMEM);
+int launch_product(GemmArgs a, const CUtensorMap& xt, const CUtensorMap& xg, const CUtensorMap& wm,
+                   int n_sm, cudaStream_t st) {
+  a.stages = GemmShape::stages(a.tokens);
+  const int smem = GemmShape::smem(a.tokens);
+  cudaError_t e = cudaFuncSetAttribute(fp8_product_kernel<W4, SWIGLU>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_fail(e);
-  // tiles the call can have at most, as far as the host knows; any grid is right
-  constexpr int COLS = SWIGLU ? kGemmN / 2 : kGemmN;
-  const long long m = a.offsets ? (long long)a.rows / kGemmM + std::min(a.experts, a.rows)
-                                : ((long long)a.rows + kGemmM - 1) / kGemmM;
-  const long long tiles = m * ((a.n + COLS - 1) / COLS);
-  const int grid = (int)std::min<long long>(n_sm, tiles);
-  fp8_product_kernel<W4, SWIGLU><<<grid, kGemmThreads, GemmShape::SMEM, st>>>(a, xt, xg, wm);
+  const long long tiles = tiles_at_most(a, SWIGLU);
+  const int pairs = n_sm / 2, groups = (a.kb + 3) / 4;
+  a.splits = 1;
+  while (a.splits < kGemmMaxSplits && 2 * a.splits * tiles <= pairs && 2 * a.splits <= groups)
+    a.splits *= 2;
+  const int grid = 2 * a.splits * (int)std::min<long long>(pairs / a.splits, tiles);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kGemmThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = 2 * a.splits;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, fp8_product_kernel<W4, SWIGLU>, a, xt, xg, wm);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return cuda_fail(e);
+  }
   return end();
 }
 
@@ -180,7 +204,7 @@ int moe_fp8_product(void* stream, const moe_fp8_product_t* args) {
   const int unit = w4 ? 32 : 16, size = codes ? 1 : t.out_dtype == MOE_DTYPE_F32 ? 4 : 2;
   if (t.k % (w4 ? 128 : 16) || t.n_experts > kGemmMaxExperts || misaligned(t.x, 16) ||
       (t.x_stride & 15) || misaligned(t.w, unit) || ((t.w_stride | t.w_expert_stride) & (unit - 1)) ||
-      t.n_rows > INT32_MAX - kGemmM || t.n > INT32_MAX - kGemmN || t.k > INT32_MAX - kGemmK ||
+      t.n_rows > INT32_MAX - 256 || t.n > INT32_MAX - 256 || t.k > INT32_MAX - kGemmK ||
       misaligned(t.out, size))
     return MOE_ERR_UNSUPPORTED;
   const Device* dev;
@@ -188,18 +212,23 @@ int moe_fp8_product(void* stream, const moe_fp8_product_t* args) {
   if (rc) return rc;
   Encode fn;
   if ((rc = encoder(&fn))) return rc;
+  // tokens of a tile: whole ones where there are many, of experts three times their
+  // average (a smaller ring stage holds more of the weights in flight)
+  const long long many = t.offsets ? 3 * (((long long)t.n_rows + t.n_experts - 1) / t.n_experts)
+                                   : t.n_rows;
+  const int tokens = (int)std::min<long long>(kGemmTokens, (std::max(many, 32ll) + 15) / 16 * 16);
   CUtensorMap xt, xg, wm;
-  if ((rc = encode_map(fn, &xt, false, t.x, t.k, t.x_rows, 0, t.x_stride, 0, kGemmM)) ||
+  if ((rc = encode_map(fn, &xt, false, t.x, t.k, t.x_rows, 0, t.x_stride, 0, tokens / 2)) ||
       (rc = encode_map(fn, &xg, false, t.x, t.k, t.x_rows, 0, t.x_stride, 0, 1)) ||
       (rc = encode_map(fn, &wm, w4, t.w, t.k, t.n, t.n_experts, t.w_stride,
-                       t.n_experts > 1 ? t.w_expert_stride : (uint64_t)t.w_stride * t.n, kGemmN / 2)))
+                       t.n_experts > 1 ? t.w_expert_stride : (uint64_t)t.w_stride * t.n, swiglu ? 16 : kGemmRows)))
     return rc;
   GemmArgs a{};
-  a.K = t.k;
   a.kb = (t.k + kGemmK - 1) / kGemmK;
   a.wide = t.n;
   a.n = swiglu ? t.n / 2 : t.n;
   a.rows = t.n_rows;
+  a.tokens = tokens;
   a.x_rows = t.x_rows;
   a.experts = t.n_experts;
   a.offsets = t.offsets;
@@ -214,7 +243,7 @@ int moe_fp8_product(void* stream, const moe_fp8_product_t* args) {
   a.os = t.out_scales;
   a.os_stride = t.out_scales_stride;
   a.out_dtype = t.out_dtype;
-  a.vec = !misaligned(t.out, 16) && a.out_stride % 16 == 0;
+  a.vec = !misaligned(t.out, 4) && a.out_stride % 4 == 0;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (w4) return swiglu ? launch_product<true, true>(a, xt, xg, wm, dev->n_sm, st)
                         : launch_product<true, false>(a, xt, xg, wm, dev->n_sm, st);
