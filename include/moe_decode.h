@@ -568,8 +568,8 @@ typedef enum {
  * x[src(i), k] w[j, k].  With offsets NULL there is one matrix, n_experts is 1
  * and src(i) = i, or rows[i].  With offsets, output rows offsets[e] ..
  * offsets[e + 1) go through matrix e (a moe_dispatch's offsets); output rows
- * outside these are left alone, and offsets are read as within [0, n_rows], an
- * end below its start as the start.  rows[i], the row of x that output row i
+ * outside these are left alone, and offsets are read as within [0, n_rows], one
+ * below an earlier one as that one.  rows[i], the row of x that output row i
  * reads, is read as within [0, x_rows).  out_dtype E4M3 (SWIGLU only) writes
  * the 8-bit form of the result: codes in out, scales in out_scales.  The
  * kernel's waits between its warps are bounded: one that runs out (none does on

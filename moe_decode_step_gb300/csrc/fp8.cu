@@ -65,18 +65,37 @@ int encoder(Encode* out) {
   return MOE_OK;
 }
 
-int encode_map(Encode fn, CUtensorMap* map, bool nibbles, const void* p, uint64_t cols,
-               uint64_t rows, uint64_t mats, uint64_t stride, uint64_t mat_stride, int box_rows) {
-  const cuuint64_t dims[3] = {cols, rows, mats};
-  const cuuint64_t strides[2] = {stride, mat_stride};
-  const cuuint32_t box[3] = {kGemmK, (cuuint32_t)box_rows, 1};
-  const cuuint32_t one[3] = {1, 1, 1};
+int encode_map(Encode fn, CUtensorMap* map, bool nibbles, const void* p, int rank,
+               const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
+  const cuuint32_t one[5] = {1, 1, 1, 1, 1};
   const CUresult r = fn(map, nibbles ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B
                                      : CU_TENSOR_MAP_DATA_TYPE_UINT8,
-                        mats ? 3 : 2, const_cast<void*>(p), dims, strides, box, one,
+                        rank, const_cast<void*>(p), dims, strides, box, one,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+int encode_rows(Encode fn, CUtensorMap* map, const moe_fp8_product_t& t, int box_rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)t.k, (cuuint64_t)t.x_rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)t.x_stride};
+  const cuuint32_t box[2] = {kGemmK, (cuuint32_t)box_rows};
+  return encode_map(fn, map, false, t.x, 2, dims, strides, box);
+}
+int encode_weights(Encode fn, CUtensorMap* map, const moe_fp8_product_t& t, bool swiglu,
+                   bool interleaved) {
+  const bool w4 = t.w_format == MOE_WEIGHTS_MXFP4;
+  const cuuint64_t k = t.k, n = t.n, e = t.n_experts, row = t.w_stride;
+  const cuuint64_t mat = e > 1 ? (cuuint64_t)t.w_expert_stride : row * n;
+  if (interleaved) {
+    const cuuint64_t dims[5] = {k, 16, 2, n / 32, e};
+    const cuuint64_t strides[4] = {row, row * (n / 2), row * 16, mat};
+    const cuuint32_t box[5] = {kGemmK, 16, 2, 4, 1};
+    return encode_map(fn, map, w4, t.w, 5, dims, strides, box);
+  }
+  const cuuint64_t dims[3] = {k, n, e};
+  const cuuint64_t strides[2] = {row, mat};
+  const cuuint32_t box[3] = {kGemmK, swiglu ? 16u : (cuuint32_t)kGemmRows, 1};
+  return encode_map(fn, map, w4, t.w, 3, dims, strides, box);
 }
 
 // Token tiles and weight tiles of a call at most, as far as the host knows.
@@ -88,14 +107,14 @@ long long tiles_at_most(const GemmArgs& a, bool swiglu) {
 }
 
 template <bool W4, bool SWIGLU>
-int launch_product(GemmArgs a, const CUtensorMap& xt, const CUtensorMap& xg, const CUtensorMap& wm,
-                   int n_sm, cudaStream_t st) {
+int launch_product(GemmArgs a, const GemmMaps& maps, int n_sm, cudaStream_t st) {
   a.stages = GemmShape::stages(a.tokens);
   const int smem = GemmShape::smem(a.tokens);
   cudaError_t e = cudaFuncSetAttribute(fp8_product_kernel<W4, SWIGLU>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_fail(e);
   const long long tiles = tiles_at_most(a, SWIGLU);
+  if (tiles > INT32_MAX - 65536) return MOE_ERR_UNSUPPORTED;
   const int pairs = n_sm / 2, groups = (a.kb + 3) / 4;
   a.splits = 1;
   while (a.splits < kGemmMaxSplits && 2 * a.splits * tiles <= pairs && 2 * a.splits <= groups)
@@ -112,7 +131,7 @@ int launch_product(GemmArgs a, const CUtensorMap& xt, const CUtensorMap& xg, con
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, fp8_product_kernel<W4, SWIGLU>, a, xt, xg, wm);
+  e = cudaLaunchKernelEx(&cfg, fp8_product_kernel<W4, SWIGLU>, a, maps);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return cuda_fail(e);
@@ -217,12 +236,16 @@ int moe_fp8_product(void* stream, const moe_fp8_product_t* args) {
   const long long many = t.offsets ? 3 * (((long long)t.n_rows + t.n_experts - 1) / t.n_experts)
                                    : t.n_rows;
   const int tokens = (int)std::min<long long>(kGemmTokens, (std::max(many, 32ll) + 15) / 16 * 16);
-  CUtensorMap xt, xg, wm;
-  if ((rc = encode_map(fn, &xt, false, t.x, t.k, t.x_rows, 0, t.x_stride, 0, tokens / 2)) ||
-      (rc = encode_map(fn, &xg, false, t.x, t.k, t.x_rows, 0, t.x_stride, 0, 1)) ||
-      (rc = encode_map(fn, &wm, w4, t.w, t.k, t.n, t.n_experts, t.w_stride,
-                       t.n_experts > 1 ? t.w_expert_stride : (uint64_t)t.w_stride * t.n, swiglu ? 16 : kGemmRows)))
+  // many rows by index come through warps of their own
+  const bool loaders = t.rows && tokens > 32, interleaved = swiglu && t.n % 32 == 0;
+  GemmMaps maps;
+  if (!t.rows) {
+    for (int i = 0; i < 4; ++i)
+      if (tokens / 2 >= 64 >> i && (rc = encode_rows(fn, &maps.x[i], t, 64 >> i))) return rc;
+  } else if (!loaders && (rc = encode_rows(fn, &maps.gather, t, 1))) {
     return rc;
+  }
+  if ((rc = encode_weights(fn, &maps.w, t, swiglu, interleaved))) return rc;
   GemmArgs a{};
   a.kb = (t.k + kGemmK - 1) / kGemmK;
   a.wide = t.n;
@@ -233,6 +256,11 @@ int moe_fp8_product(void* stream, const moe_fp8_product_t* args) {
   a.experts = t.n_experts;
   a.offsets = t.offsets;
   a.src = t.rows;
+  a.loaders = loaders;
+  a.interleaved = interleaved;
+  a.x = t.x;
+  a.x_stride = t.x_stride;
+  a.k = t.k;
   a.xs = t.x_scales;
   a.xs_stride = t.x_scales_stride;
   a.ws = t.w_scales;
@@ -243,12 +271,15 @@ int moe_fp8_product(void* stream, const moe_fp8_product_t* args) {
   a.os = t.out_scales;
   a.os_stride = t.out_scales_stride;
   a.out_dtype = t.out_dtype;
-  a.vec = !misaligned(t.out, 4) && a.out_stride % 4 == 0;
+  const int piece = codes ? 4 : 16;   // what a lane stores at a time
+  a.vec = !misaligned(t.out, piece) && a.out_stride % piece == 0;
+  a.xs_words = !misaligned(t.x_scales, 4) && a.xs_stride % 4 == 0;
+  a.ws_words = !misaligned(t.w_scales, 4) && ((a.ws_stride | a.ws_expert) & 3) == 0;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (w4) return swiglu ? launch_product<true, true>(a, xt, xg, wm, dev->n_sm, st)
-                        : launch_product<true, false>(a, xt, xg, wm, dev->n_sm, st);
-  return swiglu ? launch_product<false, true>(a, xt, xg, wm, dev->n_sm, st)
-                : launch_product<false, false>(a, xt, xg, wm, dev->n_sm, st);
+  if (w4) return swiglu ? launch_product<true, true>(a, maps, dev->n_sm, st)
+                        : launch_product<true, false>(a, maps, dev->n_sm, st);
+  return swiglu ? launch_product<false, true>(a, maps, dev->n_sm, st)
+                : launch_product<false, false>(a, maps, dev->n_sm, st);
 }
 
 int moe_dispatch(void* stream, const int32_t* idx, int n_tokens, int top_k, int n_experts,

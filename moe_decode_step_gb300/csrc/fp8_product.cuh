@@ -14,9 +14,10 @@
 // accumulators (480 columns) and the scales of two steps fit tensor memory, and
 // one accumulator is stored while the next one is summed.
 //
-// Roles (8 warps a CTA): 0 copies tiles (rows of x by index through gather4, four
-// a copy), 1 issues the MMAs (of the pair's first CTA), 2 and 3 lay the scales of
-// the weights and the tokens out, 4..7 the results, a thread a weight row.  Pairs
+// Roles (16 warps a CTA): 0 copies tiles, 1 issues the MMAs (of the pair's first
+// CTA), 2 and 3 lay the scales of the weights and the tokens out, 4..11 the results,
+// a thread a weight row, in two groups that take tokens in turn, 12..15 bring rows of
+// x by index.  Pairs
 // take tiles in the order (expert, 16 token tiles, weight rows, token tile): pairs
 // next to one another read the same weights.  Calls with fewer tiles than pairs
 // split K over `splits` pairs of a cluster, which add up through distributed
@@ -33,7 +34,7 @@
 
 namespace moe {
 
-constexpr int kGemmThreads = 256;
+constexpr int kGemmThreads = 512;
 constexpr int kGemmK = 128;
 constexpr int kGemmRows = 128;      // weight rows of a CTA's part of a tile
 constexpr int kGemmTokens = 240;    // tokens of a tile at most
@@ -44,19 +45,20 @@ constexpr int kGemmMaxSplits = 4;   // pairs of a cluster (8 CTAs)
 
 struct GemmShape {
   static constexpr int ABYTES = kGemmRows * kGemmK;
-  static constexpr int SFA = 512, SFB = 1024;   // scales of a stage
+  // scales of four blocks of K: 4 bytes a row, of MXFP4 weights 4 a row and block
+  static constexpr int SFA = 512, SFB = 1024, SFSLOT = 4 * SFA + SFB, SFSLOTS = 3;
   static constexpr int SFCOL = 480;             // tensor memory: accumulators at 0 and 240, scales
   // the ring of a call whose tiles have at most `tokens`: tiles, then scales
   __host__ __device__ static constexpr int stage(int tokens) {
     return ABYTES + tokens / 2 * kGemmK;   // multiples of 1,024, the swizzle's pattern
   }
-  static constexpr int LIMIT = 227 * 1024 - 12 * 1024;   // beside the static part
+  static constexpr int LIMIT = 227 * 1024 - 18 * 1024;   // beside the static part
   static constexpr int stages(int tokens) {
-    const int n = (LIMIT - 1024) / (stage(tokens) + SFA + SFB);
+    const int n = (LIMIT - 1024 - SFSLOTS * SFSLOT) / stage(tokens);
     return n < kGemmMaxStages ? n : kGemmMaxStages;
   }
   static constexpr int smem(int tokens) {
-    return stages(tokens) * (stage(tokens) + SFA + SFB) + 1024;   // (1,024: alignment)
+    return stages(tokens) * stage(tokens) + SFSLOTS * SFSLOT + 1024;   // (1,024: alignment)
   }
 };
 
@@ -68,6 +70,11 @@ struct GemmArgs {
   int stages, splits;
   const int* offsets;        // or null
   const int* src;            // or null
+  int loaders;               // rows by index come through warps 12..15
+  int interleaved;           // SwiGLU: gates and ups in one copy
+  const uint8_t* x;
+  long long x_stride;
+  int k;
   const uint8_t* xs;
   long long xs_stride;
   const uint8_t* ws;
@@ -76,50 +83,55 @@ struct GemmArgs {
   long long out_stride;      // bytes
   uint8_t* os;
   long long os_stride;
-  int out_dtype, vec;        // vec: rows of out are 4-byte aligned
+  int out_dtype, vec;        // vec: rows of out are aligned to 16 bytes, of codes to 4
+  int xs_words, ws_words;    // scales of a row can be read as words
+};
+
+struct GemmMaps {
+  CUtensorMap x[4];          // boxes of 64, 32, 16 and 8 rows
+  CUtensorMap gather, w;
 };
 
 struct GemmShared {
   uint64_t full[kGemmMaxStages], empty[kGemmMaxStages];
-  uint64_t acc_full[2], acc_empty[2], amax_full, drained;
+  uint64_t sf_full[GemmShape::SFSLOTS], sf_empty[GemmShape::SFSLOTS];
+  uint64_t acc_full[2], acc_empty[2], amax_full[2], drained;
   uint32_t tmem;
   int dead;                           // a wait ran out
+  int first[kGemmMaxExperts + 1];     // output row of each expert
   int tiles[kGemmMaxExperts + 1];     // token tiles before each expert
-  int warp_sum[kGemmThreads / 32];
-  unsigned amax[3][256];              // of a token's 128 results, by tile
+  int warp_scan[kGemmThreads / 32];
+  // 8-bit results, by group of warps: of 64 tokens the largest result of each of the
+  // pair's eight warps, in turn in two places, and the scales' reciprocals
+  float amax[2][2][8][64], inv[2][64];
 };
 
 // ---- barriers between the CTAs of a pair ----
-__device__ __forceinline__ bool gemm_try_wait(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, "
-      "%3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity), "r"(1000000u)
-      : "memory");
-  return ok != 0;
-}
-// Waits for a phase, two seconds at most; then the CTA is dead: its waits all
-// end at once and its results become NaN.
+// Waits for a phase, two seconds at most; then the CTA is dead: its waits end
+// with false and its results become NaN.
 __device__ __forceinline__ bool gemm_dead(GemmShared& sh) { return *(volatile int*)&sh.dead != 0; }
-__device__ __forceinline__ void gemm_wait(uint64_t* bar, uint32_t parity, GemmShared& sh) {
-  if (gemm_try_wait(bar, parity)) return;
+__device__ __forceinline__ bool gemm_wait(uint64_t* bar, uint32_t parity, GemmShared& sh) {
+  if (mbar_try_wait_long(bar, parity)) return true;
   const unsigned long long t0 = global_ns();
-  while (!gemm_try_wait(bar, parity)) {
-    if (gemm_dead(sh)) return;
+  while (!mbar_try_wait_long(bar, parity)) {
+    if (gemm_dead(sh)) return false;
     if (global_ns() - t0 > kWaitLimitNs) {
       *(volatile int*)&sh.dead = 1;
-      return;
+      return false;
     }
   }
+  return true;
 }
-// `addr`: from cluster_map.
+// The same for a whole warp, whose lanes go on, or give up, together.
+__device__ __forceinline__ bool gemm_wait_warp(uint64_t* bar, uint32_t parity, GemmShared& sh) {
+  return __all_sync(0xffffffffu, gemm_wait(bar, parity, sh));
+}
+// `addr`: from cluster_map.  (Without a release to the cluster, which waits for the
+// thread's loads and stores too: what is handed over lies in this CTA, whose own
+// tensor cores read it, or is no data at all.)
 __device__ __forceinline__ void gemm_arrive(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
-               : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
-
 // ---- TMA; `bar` may be the other CTA's of the pair ----
 __device__ __forceinline__ void tma_tile_2d(uint32_t dst, const CUtensorMap* map, int c, int r,
                                             uint32_t bar) {
@@ -135,6 +147,16 @@ __device__ __forceinline__ void tma_tile_3d(uint32_t dst, const CUtensorMap* map
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       ".cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(map), "r"(c), "r"(r), "r"(e), "r"(bar)
+      : "memory");
+}
+// Gates and ups interleaved: the map's dimensions are (column, row of 16, gate or up,
+// 16 rows, matrix), its box (128, 16, 2, 4, 1).
+__device__ __forceinline__ void tma_tile_5d(uint32_t dst, const CUtensorMap* map, int c, int r16,
+                                            int e, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".cta_group::2 [%0], [%1, {%2, %6, %6, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(c), "r"(r16), "r"(e), "r"(bar), "r"(0)
       : "memory");
 }
 // Four rows of a map whose box is one row.
@@ -207,69 +229,117 @@ __device__ __forceinline__ int gemm_start(const GemmArgs& a, int e) {
   return min(max(__ldg(a.offsets + e), 0), a.rows);
 }
 
-// Token tiles before each expert; every thread calls.
+// Inclusive scan over the block's threads.
+template <class Op>
+__device__ __forceinline__ int gemm_scan(int v, GemmShared& sh, Op op) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v = op(v, x);
+  }
+  __syncthreads();
+  if (lane == 31) sh.warp_scan[warp] = v;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) v = op(v, sh.warp_scan[w]);
+  return v;
+}
+
+// First rows of the experts (none below an earlier one's: so no two experts have a
+// row in common, whatever the offsets hold) and token tiles before each; every
+// thread calls.
 __device__ __forceinline__ void gemm_prefix(const GemmArgs& a, GemmShared& sh) {
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  constexpr int PER = kGemmMaxExperts / kGemmThreads;
+  constexpr int PER = (kGemmMaxExperts + kGemmThreads) / kGemmThreads;
+  const int e0 = threadIdx.x * PER;
+  int first[PER], top = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (e0 + i <= a.experts) top = max(top, gemm_start(a, e0 + i));
+    first[i] = top;
+  }
+  const int upto = gemm_scan(top, sh, [](int x, int y) { return max(x, y); });
+  // (the maximum before this thread's: a scan of maxima one thread on)
+  int* scan = reinterpret_cast<int*>(sh.amax);   // (not in use yet)
+  if (threadIdx.x + 1 < kGemmThreads) scan[threadIdx.x + 1] = upto;
+  if (threadIdx.x == 0) scan[0] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (e0 + i <= a.experts) sh.first[e0 + i] = max(first[i], scan[threadIdx.x]);
+  __syncthreads();
   int v[PER], sum = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int e = t * PER + i;
-    v[i] = 0;
-    if (e < a.experts) {
-      const int s = gemm_start(a, e);
-      v[i] = (max(gemm_start(a, e + 1) - s, 0) + a.tokens - 1) / a.tokens;
-    }
+    const int e = e0 + i;
+    v[i] = e < a.experts ? (sh.first[e + 1] - sh.first[e] + a.tokens - 1) / a.tokens : 0;
     sum += v[i];
   }
-  int inc = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += x;
-  }
-  if (lane == 31) sh.warp_sum[warp] = inc;
-  __syncthreads();
-  int before = inc - sum;
-  for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
+  int before = gemm_scan(sum, sh, [](int x, int y) { return x + y; }) - sum;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int e = t * PER + i;
-    if (e < a.experts) sh.tiles[e] = before;
+    if (e0 + i <= a.experts) sh.tiles[e0 + i] = before;
     before += v[i];
-    if (e == a.experts - 1) sh.tiles[a.experts] = before;
   }
   __syncthreads();
 }
 
+// Walks a pair's tiles and each one's blocks of K: all of them, or (splits) this
+// pair's part, whole groups of four.  Whole warps call.
 template <bool SWIGLU>
-__device__ __forceinline__ GemmTile gemm_tile(const GemmArgs& a, const GemmShared& sh, int nt,
-                                              long long t) {
-  int lo = 0, hi = a.experts;   // tiles[lo] * nt <= t < tiles[hi] * nt
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if ((long long)sh.tiles[mid] * nt <= t) lo = mid;
-    else hi = mid;
+struct GemmWalk {
+  unsigned t, tiles, step;   // (the host has seen that they are fewer than 2^31)
+  int nt, k0, k1, expert;
+
+  __device__ __forceinline__ GemmWalk(const GemmArgs& a, const GemmShared& sh) {
+    constexpr int COLS = SWIGLU ? kGemmRows : 2 * kGemmRows;
+    nt = (a.n + COLS - 1) / COLS;
+    tiles = (unsigned)sh.tiles[a.experts] * nt;
+    const int pair = blockIdx.x / 2, split = pair % a.splits;
+    t = pair / a.splits;
+    step = gridDim.x / 2 / a.splits;
+    const int groups = (a.kb + 3) / 4;
+    k0 = 4 * (int)((long long)groups * split / a.splits);
+    k1 = min(a.kb, 4 * (int)((long long)groups * (split + 1) / a.splits));
+    expert = 0;
   }
-  // (experts without rows: lo is the last with this many tiles before it)
-  const int mt = sh.tiles[lo + 1] - sh.tiles[lo];
-  const long long l = t - (long long)sh.tiles[lo] * nt;
-  const int g = (int)(l / ((long long)kGemmGroup * nt));
-  const int gm = min(kGemmGroup, mt - g * kGemmGroup);
-  const int in = (int)(l - (long long)g * kGemmGroup * nt);
-  const int m = g * kGemmGroup + in % gm;
-  const int s = gemm_start(a, lo), end = max(gemm_start(a, lo + 1), s);
-  // an expert's tokens in equal parts, none of them empty: (mt - 1) * size <=
-  // (mt - 1) * a.tokens < end - s
-  const int size = ((end - s + mt - 1) / mt + 15) & ~15;
-  GemmTile r;
-  r.expert = lo;
-  r.row0 = s + m * size;
-  r.rows = min(size, end - r.row0);
-  r.N = (r.rows + 15) & ~15;
-  r.n0 = in / gm * (SWIGLU ? kGemmRows : 2 * kGemmRows);
-  return r;
-}
+
+  __device__ __forceinline__ GemmTile tile(const GemmArgs& a, const GemmShared& sh) {
+    // the expert with tiles[expert] * nt <= t < tiles[expert + 1] * nt, from the last on
+    const int lane = threadIdx.x & 31;
+    for (;;) {
+      const int e = expert + 1 + lane;
+      const unsigned past =
+          __ballot_sync(0xffffffffu, e >= a.experts || (unsigned)sh.tiles[e] * nt > t);
+      if (past) {
+        expert += __ffs(past) - 1;
+        break;
+      }
+      expert += 32;
+    }
+    const int mt = sh.tiles[expert + 1] - sh.tiles[expert];
+    unsigned in = t - (unsigned)sh.tiles[expert] * nt;
+    int g = 0, gm = mt;
+    if (mt > kGemmGroup) {
+      const unsigned pass = kGemmGroup * nt;
+      g = in / pass;
+      in -= g * pass;
+      gm = min(kGemmGroup, mt - g * kGemmGroup);
+    }
+    const unsigned n = in / (unsigned)gm;
+    const int m = g * kGemmGroup + (int)(in - n * gm);
+    // an expert's tokens in equal parts, none of them empty: (mt - 1) * size <=
+    // (mt - 1) * a.tokens < rows
+    const int s = sh.first[expert], rows = sh.first[expert + 1] - s;
+    const int size = (int)(((unsigned)(rows + mt - 1) / (unsigned)mt + 15) & ~15u);
+    GemmTile r;
+    r.expert = expert;
+    r.row0 = s + m * size;
+    r.rows = min(size, rows - m * size);
+    r.N = (r.rows + 15) & ~15;
+    r.n0 = n * (SWIGLU ? kGemmRows : 2 * kGemmRows);
+    return r;
+  }
+};
 
 // The row of x behind token r of the tile (tokens past the tile: its last).
 __device__ __forceinline__ int gemm_source(const GemmArgs& a, const GemmTile& w, int r) {
@@ -278,30 +348,10 @@ __device__ __forceinline__ int gemm_source(const GemmArgs& a, const GemmTile& w,
   return min(max(s, 0), a.x_rows - 1);
 }
 
-// Walks a pair's tiles and each one's blocks of K: all of them, or (splits) this
-// pair's part, whole groups of four.
-template <bool SWIGLU>
-struct GemmWalk {
-  long long t, tiles, step;
-  int nt, k0, k1;
-
-  __device__ __forceinline__ GemmWalk(const GemmArgs& a, const GemmShared& sh) {
-    constexpr int COLS = SWIGLU ? kGemmRows : 2 * kGemmRows;
-    nt = (a.n + COLS - 1) / COLS;
-    tiles = (long long)sh.tiles[a.experts] * nt;
-    const int pair = blockIdx.x / 2, split = pair % a.splits;
-    t = pair / a.splits;
-    step = gridDim.x / 2 / a.splits;
-    const int groups = (a.kb + 3) / 4;
-    k0 = 4 * (int)((long long)groups * split / a.splits);
-    k1 = min(a.kb, 4 * (int)((long long)groups * (split + 1) / a.splits));
-  }
-};
-
 struct GemmRing {
   uint32_t stage = 0, phase = 0;
-  __device__ __forceinline__ void next(const GemmArgs& a) {
-    if (++stage == (uint32_t)a.stages) {
+  __device__ __forceinline__ void next(uint32_t stages) {
+    if (++stage == stages) {
       stage = 0;
       phase ^= 1;
     }
@@ -313,164 +363,233 @@ struct GemmRing {
 // ---------------------------------------------------------------------------
 template <bool W4, bool SWIGLU>
 __device__ __forceinline__ void gemm_copy(const GemmArgs& a, GemmShared& sh, uint32_t base,
-                                          const CUtensorMap* xt, const CUtensorMap* xg,
-                                          const CUtensorMap* wm, uint32_t rank) {
+                                          const GemmMaps& maps, uint32_t rank) {
   using S = GemmShape;
   const int lane = threadIdx.x & 31, half = rank & 1;
   const uint32_t stage_bytes = S::stage(a.tokens);
+  const uint32_t full = cluster_map(smem_addr(sh.full), rank & ~1u);
   GemmRing ring;
-  uint32_t issued = 0;
   for (GemmWalk<SWIGLU> k(a, sh); k.t < k.tiles; k.t += k.step) {
-    const GemmTile w = gemm_tile<SWIGLU>(a, sh, k.nt, k.t);
-    // whole tiles of consecutive rows in one copy, others four rows a copy
-    const bool gather = a.src || w.N != a.tokens;
-    const bool mine = gather && 4 * lane < w.N / 2;
+    const GemmTile w = k.tile(a, sh);
+    // consecutive rows in boxes of 64, 32, 16 and 8 of them; rows by index four a
+    // copy where they are few (the loaders bring many)
+    const bool mine = a.src && !a.loaders && 4 * lane < w.N / 2;
     int r[4];
     if (mine) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) r[i] = gemm_source(a, w, half * (w.N / 2) + 4 * lane + i);
     }
     // the pair's bytes (nibbles count as the bytes they are read as)
-    const uint32_t bytes = (W4 ? S::ABYTES : 2 * S::ABYTES) + w.N * kGemmK;
-    for (int kb = k.k0; kb < k.k1; ++kb, ring.next(a), ++issued) {
-      gemm_wait(&sh.empty[ring.stage], ring.phase ^ 1, sh);
-      if (gemm_dead(sh)) return;
-      const uint32_t bar = cluster_map(smem_addr(&sh.full[ring.stage]), rank & ~1u);
-      const uint32_t at = base + ring.stage * stage_bytes;
+    const uint32_t bytes =
+        (W4 ? S::ABYTES : 2 * S::ABYTES) + (a.loaders ? 0u : (uint32_t)w.N * kGemmK);
+    for (int kb = k.k0; kb < k.k1; ++kb, ring.next(a.stages)) {
+      if (!gemm_wait_warp(&sh.empty[ring.stage], ring.phase ^ 1, sh)) return;
+      const uint32_t bar = full + ring.stage * 8, at = base + ring.stage * stage_bytes;
       if (half == 0 && lane == 0) mbar_arrive_expect_tx(&sh.full[ring.stage], bytes);
       __syncwarp();
-      if (SWIGLU) {
+      if (!SWIGLU) {
+        if (lane == 0)
+          tma_tile_3d(at, &maps.w, kb * kGemmK, w.n0 + half * kGemmRows, w.expert, bar);
+      } else if (a.interleaved) {
         // 16 gate rows and 16 up rows in turn: a warp's lanes
-        if (lane < 8)
-          tma_tile_3d(at + lane * 16 * kGemmK, wm, kb * kGemmK,
-                      (lane & 1 ? a.n : 0) + w.n0 + half * 64 + (lane >> 1) * 16, w.expert, bar);
-      } else if (lane == 0) {
-        tma_tile_3d(at, wm, kb * kGemmK, w.n0 + half * kGemmRows, w.expert, bar);
+        if (lane == 0)
+          tma_tile_5d(at, &maps.w, kb * kGemmK, (w.n0 + half * 64) >> 4, w.expert, bar);
+      } else if (lane < 8) {
+        tma_tile_3d(at + lane * 16 * kGemmK, &maps.w, kb * kGemmK,
+                    (lane & 1 ? a.n : 0) + w.n0 + half * 64 + (lane >> 1) * 16, w.expert, bar);
       }
-      if (!gather) {
-        if (lane == 8)
-          tma_tile_2d(at + S::ABYTES, xt, kb * kGemmK, w.row0 + half * (w.N / 2), bar);
+      if (!a.src) {
+        const int rows = w.N / 2, size = 64 >> (lane & 3), first = rows & ~(2 * size - 1);
+        if (lane >= 8 && lane < 12 && (rows & size))
+          tma_tile_2d(at + S::ABYTES + first * kGemmK, &maps.x[lane & 3], kb * kGemmK,
+                      w.row0 + half * rows + first, bar);
       } else if (mine) {
-        tma_gather4(at + S::ABYTES + lane * 4 * kGemmK, xg, kb * kGemmK, r, bar);
+        tma_gather4(at + S::ABYTES + lane * 4 * kGemmK, &maps.gather, kb * kGemmK, r, bar);
       }
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// Scales (warps 2, 3): for 128 rows at a time, 16 bytes a lane: one word for each
-// of the rows lane, lane + 32, lane + 64, lane + 96.  A word holds four bytes:
-// of MXFP4 weights those of a stage's four steps, of others those of four stages,
-// laid out with the first.  Read four stages at a time, one such group ahead.
+// Rows of x by index (warps 12..15): 16 rows of eight 16-byte pieces at a time, laid
+// out as the swizzle has them (piece c of row r at c ^ (r % 8)); columns past K
+// become zeros.  A gather4 takes the copy engine some 50 ns, four rows of 128
+// bytes: with 130 tokens a tile a block of K took 0.9 us.  Each thread's copies of
+// kLoadAhead blocks are under way while the block before them is handed over.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* p, int k, int kb) {
-  if (k + 4 <= kb && ((uintptr_t)(p + k) & 3) == 0)
-    return __ldg(reinterpret_cast<const uint32_t*>(p + k));
+constexpr int kLoadAhead = 4;
+
+template <bool SWIGLU>
+__device__ __forceinline__ void gemm_load_rows(const GemmArgs& a, GemmShared& sh, uint32_t base,
+                                               uint32_t rank) {
+  using S = GemmShape;
+  constexpr int PASSES = (kGemmTokens / 2 + 15) / 16;
+  const int t = threadIdx.x & 127, half = rank & 1, sub = t >> 3, c = t & 7;
+  const uint32_t stage_bytes = S::stage(a.tokens);
+  const uint32_t full = cluster_map(smem_addr(sh.full), rank & ~1u);
+  const uint32_t to = base + S::ABYTES + sub * kGemmK + ((c ^ (sub & 7)) << 4);
+  GemmRing ring, done;
+  int ahead = 0;
+  auto hand_over = [&]() {
+    fence_async_shared();   // the tensor cores read what these threads' copies wrote
+    __syncwarp();
+    if ((t & 31) == 0) gemm_arrive(full + done.stage * 8);
+    done.next(a.stages);
+  };
+  for (GemmWalk<SWIGLU> k(a, sh); k.t < k.tiles; k.t += k.step) {
+    const GemmTile w = k.tile(a, sh);
+    const int rows = w.N / 2;
+    const uint8_t* p[PASSES];
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i)
+      p[i] = a.x + gemm_source(a, w, half * rows + min(16 * i + sub, rows - 1)) * a.x_stride + c * 16;
+    for (int kb = k.k0; kb < k.k1; ++kb, ring.next(a.stages)) {
+      if (!gemm_wait_warp(&sh.empty[ring.stage], ring.phase ^ 1, sh)) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        return;
+      }
+      const uint32_t at = to + ring.stage * stage_bytes;
+      const int col = kb * kGemmK + c * 16;
+      const uint32_t size = col < a.k ? 16 : 0;   // (k is a multiple of 16)
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i)
+        if (16 * i + sub < rows)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at + i * 16 * kGemmK),
+                       "l"(p[i] + (size ? kb * kGemmK : 0)), "r"(size)
+                       : "memory");
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      if (++ahead > kLoadAhead) {
+        --ahead;
+        asm volatile("cp.async.wait_group %0;" ::"n"(kLoadAhead) : "memory");
+        hand_over();
+      }
+    }
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  for (; ahead > 0; --ahead) hand_over();
+}
+
+// ---------------------------------------------------------------------------
+// Scales (warps 2, 3): four blocks of K at a time, for 128 rows at a time, 16 bytes
+// a lane: one word for each of the rows lane, lane + 32, lane + 64, lane + 96.  A
+// word holds the bytes of the four blocks, or (MXFP4 weights) of a block's four
+// steps.  A ring of their own, whose three slots hide the loads of 16 blocks at a
+// time: the fence of each slot waits for every load under way, so that loading a
+// slot ahead took 0.4 us a block.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* p, int k, int end) {
   uint32_t v = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (k + i < kb) v |= (uint32_t)__ldg(p + k + i) << (8 * i);
+    if (k + i < end) v |= (uint32_t)__ldg(p + k + i) << (8 * i);
   return v;
 }
 
-// R rows a lane (4: weights, 8: tokens).  PERK: a word of its own for each block.
+// Words of R rows a lane (4: weights, 8: tokens) for blocks [k, k + 16), `per`
+// bytes each; rows are `end` bytes, as words where `aligned`.
 template <int R, bool PERK>
-__device__ __forceinline__ void scales_load(const uint8_t* const (&p)[R], int k, int kb,
-                                            uint32_t (&v)[R * (PERK ? 4 : 1)]) {
+__device__ __forceinline__ void scales_load(const uint8_t* const (&p)[R], int k, int end,
+                                            bool aligned, uint32_t (&v)[R][PERK ? 16 : 4]) {
+  constexpr int W = PERK ? 16 : 4;
+  const int at = PERK ? 4 * k : k;
+  if (aligned && at + 4 * W <= end) {
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    if (!p[i]) continue;
-    if (!PERK) {
-      v[i] = scale_word(p[i], k, kb);
-    } else {
+    for (int i = 0; i < R; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (k + j < kb) v[4 * i + j] = scale_word(p[i], 4 * (k + j), 4 * kb);
-    }
+      for (int j = 0; j < W; ++j) v[i][j] = __ldg(reinterpret_cast<const uint32_t*>(p[i] + at) + j);
+  } else {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int j = 0; j < W; ++j) v[i][j] = scale_word(p[i], at + 4 * j, end);
   }
 }
 
 template <int R, bool PERK, bool SWIGLU, class Rows>
 __device__ __forceinline__ void gemm_scales(const GemmArgs& a, GemmShared& sh, uint8_t* dst,
-                                            uint32_t rank, Rows rows_of) {
-  constexpr int W = R * (PERK ? 4 : 1);
+                                            uint32_t rank, bool aligned, Rows rows_of) {
+  using S = GemmShape;
   const int lane = threadIdx.x & 31;
+  const uint32_t full = cluster_map(smem_addr(sh.sf_full), rank & ~1u);
   GemmRing ring;
   for (GemmWalk<SWIGLU> k(a, sh); k.t < k.tiles; k.t += k.step) {
     const uint8_t* p[R];
     rows_of(k, p);
-    uint32_t cur[W] = {}, next[W] = {};
-    scales_load<R, PERK>(p, k.k0, a.kb, next);
-    for (int k0 = k.k0; k0 < k.k1; k0 += 4) {
+    for (int k0 = k.k0; k0 < k.k1; k0 += 16) {
+      uint32_t v[R][PERK ? 16 : 4];
+      scales_load<R, PERK>(p, k0, PERK ? 4 * a.kb : a.kb, aligned, v);
 #pragma unroll
-      for (int i = 0; i < W; ++i) cur[i] = next[i];
-      if (k0 + 4 < k.k1) scales_load<R, PERK>(p, k0 + 4, a.kb, next);
+      for (int s = 0; s < 4; ++s) {
+        if (k0 + 4 * s >= k.k1) break;
+        if (!gemm_wait_warp(&sh.sf_empty[ring.stage], ring.phase ^ 1, sh)) return;
+        uint4* to = reinterpret_cast<uint4*>(dst + ring.stage * S::SFSLOT);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (k0 + j >= k.k1) break;
-        gemm_wait(&sh.empty[ring.stage], ring.phase ^ 1, sh);
-        if (gemm_dead(sh)) return;
-        if (PERK || j == 0) {
-          uint4* to = reinterpret_cast<uint4*>(
-              dst + ring.stage * (GemmShape::SFA + GemmShape::SFB));
+        for (int j = 0; j < (PERK ? 4 : 1); ++j)
 #pragma unroll
           for (int g = 0; g < R / 4; ++g) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w[i] = cur[(4 * g + i) * (PERK ? 4 : 1) + (PERK ? j : 0)];
-            to[32 * g + lane] = make_uint4(w[0], w[1], w[2], w[3]);
+            const int c = PERK ? 4 * s + j : s;
+            to[32 * (j + g) + lane] =
+                make_uint4(v[4 * g][c], v[4 * g + 1][c], v[4 * g + 2][c], v[4 * g + 3][c]);
           }
-          fence_async_shared();
-        }
+        fence_async_shared();
         __syncwarp();
-        if (lane == 0) gemm_arrive(cluster_map(smem_addr(&sh.full[ring.stage]), rank & ~1u));
-        ring.next(a);
+        if (lane == 0) gemm_arrive(full + ring.stage * 8);
+        ring.next(S::SFSLOTS);
       }
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// MMAs (warp 1 of the pair's first CTA, one lane)
+// MMAs (warp 1 of the pair's first CTA)
 // ---------------------------------------------------------------------------
+// The loop's own latency counts: a block's four MMAs take the tensor cores 480
+// cycles, and with a vote and an early test of the next barrier in it (and each wait
+// checking for a dead CTA) the loop took 640.  So nobody leaves it early: where a
+// wait ran out, the others end at once and what is issued is garbage of no effect.
 template <bool W4, bool SWIGLU>
 __device__ __forceinline__ void gemm_mma(const GemmArgs& a, GemmShared& sh, uint32_t base,
                                          uint32_t rank) {
   using S = GemmShape;
   const uint32_t stage_bytes = S::stage(a.tokens), sf = base + a.stages * stage_bytes;
   const uint16_t both = (uint16_t)(3u << (rank & ~1u));
-  GemmRing ring;
+  const uint64_t da0 = umma_desc_sw128(base), db0 = umma_desc_sw128(base + S::ABYTES);
+  const uint64_t ds0 = umma_desc(sf, 0, 128);
+  GemmRing ring, sr;
   const uint32_t tm = sh.tmem;
   uint32_t n = 0;
   for (GemmWalk<SWIGLU> k(a, sh); k.t < k.tiles; k.t += k.step, ++n) {
-    const GemmTile w = gemm_tile<SWIGLU>(a, sh, k.nt, k.t);
-    const uint32_t acc = tm + (n & 1) * kGemmTokens;
+    const GemmTile w = k.tile(a, sh);
+    const uint32_t acc = tm + (n & 1) * kGemmTokens, id = umma_idesc_mxf8(W4 ? 5 : 0, 0, 0, w.N);
     gemm_wait(&sh.acc_empty[n & 1], (n >> 1 & 1) ^ 1, sh);
-    tc_fence_after();
-    for (int kb = k.k0; kb < k.k1; ++kb, ring.next(a)) {
-      gemm_wait(&sh.full[ring.stage], ring.phase, sh);
-      if (gemm_dead(sh)) return;
-      tc_fence_after();
-      const uint32_t at = base + ring.stage * stage_bytes;
-      const uint32_t sc = sf + ring.stage * (S::SFA + S::SFB);
+    for (int kb = k.k0; kb < k.k1; ++kb) {
       const uint32_t kq = kb & 3, j4 = kb >> 2 & 1;
-      // scales of this step (MXFP4 weights) or these four in turn in two places
-      const uint32_t sfa = tm + S::SFCOL + 4 * (W4 ? kb & 1 : j4), sfb = tm + S::SFCOL + 8 + 8 * j4;
-      if (W4 || kq == 0) umma_sf_copy_pair(sfa, umma_desc(sc, 0, 128));
-      if (kq == 0) {
-        umma_sf_copy_pair(sfb, umma_desc(sc + S::SFA, 0, 128));
-        if (w.N > 128) umma_sf_copy_pair(sfb + 4, umma_desc(sc + S::SFA + 512, 0, 128));
-      }
-      const uint64_t da = umma_desc_sw128(at), db = umma_desc_sw128(at + S::ABYTES);
+      const bool last = kb + 1 == k.k1;
+      if (kq == 0) gemm_wait(&sh.sf_full[sr.stage], sr.phase, sh);
+      gemm_wait(&sh.full[ring.stage], ring.phase, sh);
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t off = ring.stage * (stage_bytes >> 4);
+        const uint64_t ds = ds0 + sr.stage * (S::SFSLOT >> 4);
+        // scales of this block (MXFP4 weights) or these four, in turn in two places
+        const uint32_t sfa = tm + S::SFCOL + 4 * (W4 ? kb & 1 : j4);
+        const uint32_t sfb = tm + S::SFCOL + 8 + 8 * j4;
+        if (kq == 0) {
+          umma_sf_copy_pair(sfb, ds + (4 * S::SFA >> 4));
+          if (w.N > 128) umma_sf_copy_pair(sfb + 4, ds + ((4 * S::SFA + 512) >> 4));
+        }
+        if (W4 || kq == 0) umma_sf_copy_pair(sfa, ds + (W4 ? kq : 0) * (S::SFA >> 4));
 #pragma unroll
-      for (uint32_t j = 0; j < 4; ++j)
-        umma_mxf8_pair(acc, da + 2 * j, db + 2 * j,
-                       umma_idesc_mxf8(W4 ? 5 : 0, W4 ? j : kq, kq, w.N), sfa, sfb,
-                       (kb > k.k0) || j > 0);
-      umma_commit_pair(&sh.empty[ring.stage], both);
+        for (uint32_t j = 0; j < 4; ++j)
+          umma_mxf8_pair(acc, da0 + off + 2 * j, db0 + off + 2 * j,
+                         id | (W4 ? j : kq) << 29 | kq << 4, sfa, sfb, (kb > k.k0) || j > 0);
+        umma_commit_pair(&sh.empty[ring.stage], both);
+        if (kq == 3 || last) umma_commit_pair(&sh.sf_empty[sr.stage], both);
+        if (last) umma_commit_pair(&sh.acc_full[n & 1], both);
+      }
+      if (kq == 3 || last) sr.next(S::SFSLOTS);
+      ring.next(a.stages);
     }
-    umma_commit_pair(&sh.acc_full[n & 1], both);
   }
 }
 
@@ -509,21 +628,44 @@ __device__ __forceinline__ void gemm_store(const GemmArgs& a, const GemmTile& w,
       if (c + i < w.rows) *reinterpret_cast<float*>(p) = v[i];
     return;
   }
+  // eight tokens of eight lanes' columns are turned among the lanes, so that each
+  // stores eight columns of one token (16 bytes; by 4 bytes a lane the stores
+  // took as long as a tile of K = 2,048: 692 us for 408 without them)
   const int f16 = a.out_dtype == MOE_DTYPE_F16;
-  // two tokens at a time: even lanes take the first one's pair of columns, odd
-  // lanes the second's
-  const int odd = lane & 1, col2 = col - odd;
-  char* p = a.out + (long long)(w.row0 + c + odd) * a.out_stride + (long long)col2 * 2;
+  const int b0 = lane & 1, b1 = lane >> 1 & 1, b2 = lane >> 2 & 1, col8 = col & ~7;
+  char* p = a.out + (long long)(w.row0 + c + (lane & 7)) * a.out_stride + (long long)col8 * 2;
 #pragma unroll
-  for (int i = 0; i < 32; i += 2, p += 2 * a.out_stride) {
-    const float x = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
-    const uint32_t u = odd ? pack16(x, v[i + 1], f16) : pack16(v[i], x, f16);
-    if (c + i + odd >= w.rows) continue;
-    if (a.vec && col2 + 1 < a.n) {
-      *reinterpret_cast<uint32_t*>(p) = u;
+  for (int i = 0; i < 32; i += 8, p += 8 * a.out_stride) {
+    // columns (col & ~1, + 1) of token 2 j + b0
+    uint32_t u[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float lo = v[i + 2 * j], hi = v[i + 2 * j + 1];
+      const float x = __shfl_xor_sync(0xffffffffu, b0 ? lo : hi, 1);
+      u[j] = b0 ? pack16(x, hi, f16) : pack16(lo, x, f16);
+    }
+    // columns col & ~3 .. + 3 of token 4 j + 2 b1 + b0: words (2 j, 2 j + 1)
+    uint32_t s[4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t lo = u[2 * j], hi = u[2 * j + 1];
+      const uint32_t x = __shfl_xor_sync(0xffffffffu, b1 ? lo : hi, 2);
+      s[2 * j] = b1 ? x : lo;
+      s[2 * j + 1] = b1 ? hi : x;
+    }
+    // all eight of token 4 b2 + 2 b1 + b0
+    const uint32_t x0 = __shfl_xor_sync(0xffffffffu, b2 ? s[0] : s[2], 4);
+    const uint32_t x1 = __shfl_xor_sync(0xffffffffu, b2 ? s[1] : s[3], 4);
+    const uint4 o = b2 ? make_uint4(x0, x1, s[2], s[3]) : make_uint4(s[0], s[1], x0, x1);
+    if (c + i + (lane & 7) >= w.rows) continue;
+    if (a.vec && col8 + 7 < a.n) {
+      *reinterpret_cast<uint4*>(p) = o;
     } else {
-      if (col2 < a.n) *reinterpret_cast<uint16_t*>(p) = (uint16_t)u;
-      if (col2 + 1 < a.n) *reinterpret_cast<uint16_t*>(p + 2) = (uint16_t)(u >> 16);
+      const uint32_t t[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (col8 + j < a.n)
+          reinterpret_cast<uint16_t*>(p)[j] = (uint16_t)(t[j >> 1] >> (16 * (j & 1)));
     }
   }
 }
@@ -561,151 +703,148 @@ template <bool SWIGLU>
 __device__ __forceinline__ void gemm_results(const GemmArgs& a, GemmShared& sh, uint8_t* smem,
                                              uint32_t rank) {
   const int lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3, half = rank & 1;
+  const int group = (threadIdx.x >> 7) - 1, gt = threadIdx.x & 127;
   const uint32_t tm = sh.tmem + ((uint32_t)(q * 32) << 16);
-  const uint32_t part = smem_addr(smem) + (threadIdx.x & 127) * 4;
+  const uint32_t part = smem_addr(smem) + gt * 4;
   const int split = (blockIdx.x / 2) % a.splits;
   const float nan = __int_as_float(0x7FFFFFFF);
-  uint32_t n = 0;
+  const uint32_t acc_empty = cluster_map(smem_addr(sh.acc_empty), rank & ~1u);
+  uint32_t n = 0, batch = 0;
   for (GemmWalk<SWIGLU> k(a, sh); k.t < k.tiles; k.t += k.step, ++n) {
-    const GemmTile w = gemm_tile<SWIGLU>(a, sh, k.nt, k.t);
-    if (!gemm_dead(sh)) gemm_wait(&sh.acc_full[n & 1], n >> 1 & 1, sh);
+    const GemmTile w = k.tile(a, sh);
+    if (!gemm_dead(sh)) gemm_wait(&sh.acc_full[n & 1], n >> 1 & 1, sh);   // (dead: NaN)
     tc_fence_after();
     const uint32_t acc = tm + (n & 1) * kGemmTokens;
+    // tokens go to splits and groups in turn, `unit` at a time
+    int unit = 32, c0 = 32 * (group * a.splits + split);
+    if (SWIGLU && a.out_dtype == MOE_DTYPE_E4M3) unit = 64, c0 *= 2;
+    const int step = 2 * unit * a.splits;
     if (a.splits > 1) {
       // this pair's part of K to shared memory (the ring is idle: every copy was
       // waited for and every product is done), then the tokens are shared out
-      for (int c = 0; c < w.N; c += 32) {
+      for (int c = 32 * group; c < w.N; c += 64) {
         float v[32];
         tmem_ld32(acc + c, v);
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-          if (c + i < w.N)
-            *reinterpret_cast<float*>(smem + (c + i) * 512 + (threadIdx.x & 127) * 4) = v[i];
+          if (c + i < w.N) *reinterpret_cast<float*>(smem + (c + i) * 512 + gt * 4) = v[i];
       }
       cluster_sync();
     }
     const bool dead = gemm_dead(sh);
-    auto mine = [&](int c) { return c < w.N && (a.splits == 1 || (c >> 5) % a.splits == split); };
     auto release = [&]() {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) gemm_arrive(cluster_map(smem_addr(&sh.acc_empty[n & 1]), rank & ~1u));
+      if (lane == 0) gemm_arrive(acc_empty + (n & 1) * 8);
     };
+    if (c0 >= w.N) release();
     if (!SWIGLU) {
       const int col = w.n0 + half * kGemmRows + q * 32 + lane;
 #pragma unroll 1
-      for (int c = 0; c < w.N; c += 32) {
-        if (!mine(c)) continue;
+      for (int c = c0; c < w.N; c += step) {
         float v[32];
         gemm_sums(a, acc, part, rank, c, v);
+        if (c + step >= w.N) release();
         if (dead) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = nan;
         }
-        if (c + 32 >= w.N) release();
         gemm_store(a, w, c, col, v);
       }
-    } else {
-      const int col = w.n0 + half * 64 + q * 16 + (lane & 15), late = lane >> 4;
-      if (a.out_dtype != MOE_DTYPE_E4M3) {
+      continue;
+    }
+    const int col = w.n0 + half * 64 + q * 16 + (lane & 15), late = lane >> 4;
+    if (a.out_dtype != MOE_DTYPE_E4M3) {
 #pragma unroll 1
-        for (int c = 0; c < w.N; c += 32) {
-          if (!mine(c)) continue;
-          float v[32], h[16];
-          gemm_sums(a, acc, part, rank, c, v);
-          if (c + 32 >= w.N) release();
-          gemm_swiglu(v, h);
-          const int f16 = a.out_dtype == MOE_DTYPE_F16;
+      for (int c = c0; c < w.N; c += step) {
+        float v[32], h[16];
+        gemm_sums(a, acc, part, rank, c, v);
+        if (c + step >= w.N) release();
+        gemm_swiglu(v, h);
+        const int f16 = a.out_dtype == MOE_DTYPE_F16;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int t = c + 2 * i + late;
-            if (t >= w.rows || col >= a.n) continue;
-            const float x = dead ? nan : h[i];
-            char* p = a.out + (long long)(w.row0 + t) * a.out_stride;
-            if (a.out_dtype == MOE_DTYPE_F32) reinterpret_cast<float*>(p)[col] = x;
-            else reinterpret_cast<uint16_t*>(p)[col] = (uint16_t)pack16(x, 0.f, f16);
-          }
-        }
-      } else {
-        // a token's 128 results lie in both CTAs: each warp's maxima go to both.
-        // A tile's buffer is cleared two tiles after its last reader.
-        unsigned* clear = sh.amax[(n + 1) % 3] + q * 64;
-        clear[lane] = clear[lane + 32] = 0;
-        const uint32_t am = smem_addr(sh.amax[n % 3]);
-        const uint32_t here = cluster_map(am, rank), there = cluster_map(am, rank ^ 1);
-        float h[kGemmTokens / 2 + 8];
-#pragma unroll
-        for (int c = 0; c < kGemmTokens; c += 32) {
-          if (!mine(c)) continue;
-          float v[32], m[16];
-          gemm_sums(a, acc, part, rank, c, v);
-          gemm_swiglu(v, h + c / 2);
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            m[i] = col < a.n ? fp8_finite_max(0.f, h[c / 2 + i]) : 0.f;
-          const unsigned top = __float_as_uint(gemm_max16(m));
-          const int t = c + 2 * (lane & 15) + late;
-          max_cluster_u32(here + t * 4, top);
-          max_cluster_u32(there + t * 4, top);
-        }
-        release();
-        if (lane == 0) {
-          const uint32_t bar = smem_addr(&sh.amax_full);
-          gemm_arrive(cluster_map(bar, rank));
-          gemm_arrive(cluster_map(bar, rank ^ 1));
-        }
-        if (!gemm_dead(sh)) gemm_wait(&sh.amax_full, n & 1, sh);
-        const unsigned* amax = sh.amax[n % 3];
-        const bool lost = gemm_dead(sh);
-#pragma unroll
-        for (int c = 0; c < kGemmTokens; c += 32) {
-          if (!mine(c)) continue;
-#pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            // four tokens' codes of this column, turned among four lanes into four
-            // columns' codes of one token
-            uint32_t u = 0;
-#pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-              const int t = c + 2 * (i + j) + late;
-              const float e0 = pow2f(-fp8_block_exp(__uint_as_float(amax[t])));
-              const float e1 = pow2f(-fp8_block_exp(__uint_as_float(amax[t + 2])));
-              u |= f32x2_to_e4m3x2(h[c / 2 + i + j] * e0, h[c / 2 + i + j + 1] * e1) << (8 * j);
-            }
-            if (lost) u = 0x7F7F7F7Fu;
-            const uint32_t x = __shfl_xor_sync(0xffffffffu, u, 1);
-            u = lane & 1 ? __byte_perm(u, x, 0x3715) : __byte_perm(u, x, 0x6240);
-            const uint32_t y = __shfl_xor_sync(0xffffffffu, u, 2);
-            u = lane & 2 ? __byte_perm(u, y, 0x3276) : __byte_perm(u, y, 0x5410);
-            const int t = c + 2 * (i + (lane & 3)) + late, at = col & ~3;
-            if (t >= w.rows) continue;
-            char* p = a.out + (long long)(w.row0 + t) * a.out_stride + at;
-            if (a.vec && at + 3 < a.n) {
-              *reinterpret_cast<uint32_t*>(p) = u;
-            } else {
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                if (at + j < a.n) p[j] = (char)(u >> (8 * j));
-            }
-          }
-        }
-        if (half == 0) {
-          for (int t = threadIdx.x & 127; t < w.rows; t += 128)
-            if (mine(t & ~31))
-              a.os[(long long)(w.row0 + t) * a.os_stride + (w.n0 >> 7)] =
-                  (uint8_t)(fp8_block_exp(__uint_as_float(amax[t])) + 127);
+        for (int i = 0; i < 16; ++i) {
+          const int t = c + 2 * i + late;
+          if (t >= w.rows || col >= a.n) continue;
+          const float x = dead ? nan : h[i];
+          char* p = a.out + (long long)(w.row0 + t) * a.out_stride;
+          if (a.out_dtype == MOE_DTYPE_F32) reinterpret_cast<float*>(p)[col] = x;
+          else reinterpret_cast<uint16_t*>(p)[col] = (uint16_t)pack16(x, 0.f, f16);
         }
       }
+      continue;
+    }
+    // 8 bits.  A token's 128 results lie in both CTAs: each warp sends its largest
+    // to both, 64 tokens at a time, whose results stay in registers.  A place is
+    // written again two batches later, which this CTA's warps let the other's
+    // begin only when all have read it (the barrier below).
+#pragma unroll 1
+    for (int c1 = c0; c1 < w.N; c1 += step, ++batch) {
+      uint64_t* bar = &sh.amax_full[group];
+      const uint32_t slot = smem_addr(sh.amax[group][batch & 1][half * 4 + q]);
+      const uint32_t here = cluster_map(slot, rank), there = cluster_map(slot, rank ^ 1);
+      const uint32_t bar_here = cluster_map(smem_addr(bar), rank);
+      const uint32_t bar_there = cluster_map(smem_addr(bar), rank ^ 1);
+      if (gt == 0) mbar_arrive_expect_tx(bar, 8 * 64 * 4);
+      float h[32];
+#pragma unroll
+      for (int c = 0; c < 64; c += 32) {
+        float v[32], m[16];
+        gemm_sums(a, acc, part, rank, c1 + c, v);   // (past N: nobody's)
+        gemm_swiglu(v, h + c / 2);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m[i] = col < a.n ? fp8_finite_max(0.f, h[c / 2 + i]) : 0.f;
+        const float top = gemm_max16(m);
+        const int t = c + 2 * (lane & 15) + late;
+        st_async_f32(here + t * 4, top, bar_here);
+        st_async_f32(there + t * 4, top, bar_there);
+      }
+      if (c1 + step >= w.N) release();
+      const bool lost = !gemm_wait(bar, batch & 1, sh) || dead;
+      if (gt < 64) {
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, sh.amax[group][batch & 1][i][gt]);
+        const int e = fp8_block_exp(amax);
+        sh.inv[group][gt] = pow2f(-e);
+        if (half == 0 && c1 + gt < w.rows)
+          a.os[(long long)(w.row0 + c1 + gt) * a.os_stride + (w.n0 >> 7)] = (uint8_t)(e + 127);
+      }
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
+      const float* inv = sh.inv[group];
+#pragma unroll
+      for (int i = 0; i < 32; i += 4) {
+        // four tokens' codes of this column, turned among four lanes into four
+        // columns' codes of one token
+        const int t0 = 2 * i + late;
+        uint32_t u = f32x2_to_e4m3x2(h[i] * inv[t0], h[i + 1] * inv[t0 + 2]) |
+                     f32x2_to_e4m3x2(h[i + 2] * inv[t0 + 4], h[i + 3] * inv[t0 + 6]) << 16;
+        if (lost) u = 0x7F7F7F7Fu;
+        const uint32_t x = __shfl_xor_sync(0xffffffffu, u, 1);
+        u = lane & 1 ? __byte_perm(u, x, 0x3715) : __byte_perm(u, x, 0x6240);
+        const uint32_t y = __shfl_xor_sync(0xffffffffu, u, 2);
+        u = lane & 2 ? __byte_perm(u, y, 0x3276) : __byte_perm(u, y, 0x5410);
+        const int t = c1 + t0 + 2 * (lane & 3), at = col & ~3;
+        if (t >= w.rows) continue;
+        char* p = a.out + (long long)(w.row0 + t) * a.out_stride + at;
+        if (a.vec && at + 3 < a.n) {
+          *reinterpret_cast<uint32_t*>(p) = u;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (at + j < a.n) p[j] = (char)(u >> (8 * j));
+        }
+      }
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");   // (inv is read)
     }
   }
 }
 
 template <bool W4, bool SWIGLU>
 static __global__ void __launch_bounds__(kGemmThreads, 1)
-    fp8_product_kernel(const __grid_constant__ GemmArgs a, const __grid_constant__ CUtensorMap xt,
-                       const __grid_constant__ CUtensorMap xg,
-                       const __grid_constant__ CUtensorMap wm) {
+    fp8_product_kernel(const __grid_constant__ GemmArgs a,
+                       const __grid_constant__ GemmMaps maps) {
   using S = GemmShape;
   extern __shared__ uint8_t gemm_raw[];
   __shared__ GemmShared sh;
@@ -714,19 +853,22 @@ static __global__ void __launch_bounds__(kGemmThreads, 1)
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
-      mbar_init(&sh.full[s], 5);    // the copies' bytes, two warps' scales of both CTAs
+      mbar_init(&sh.full[s], a.loaders ? 9 : 1);   // the copies, the pair's loaders
       mbar_init(&sh.empty[s], 1);
+    }
+    for (int s = 0; s < S::SFSLOTS; ++s) {
+      mbar_init(&sh.sf_full[s], 4);   // two warps of both CTAs
+      mbar_init(&sh.sf_empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sh.acc_full[s], 1);
-      mbar_init(&sh.acc_empty[s], 8);   // four warps of both CTAs
+      mbar_init(&sh.acc_empty[s], 16);   // eight warps of both CTAs
+      mbar_init(&sh.amax_full[s], 1);
     }
-    mbar_init(&sh.amax_full, 8);
     mbar_init(&sh.drained, 1);
     sh.dead = 0;
     fence_barrier_init();
   }
-  sh.amax[0][threadIdx.x] = 0;
   if (warp == 1) tmem_alloc_pair(&sh.tmem);
   gemm_prefix(a, sh);
   tc_fence_before();
@@ -735,14 +877,14 @@ static __global__ void __launch_bounds__(kGemmThreads, 1)
   tc_fence_after();
 
   if (warp == 0) {
-    gemm_copy<W4, SWIGLU>(a, sh, base, &xt, &xg, &wm, rank);
+    gemm_copy<W4, SWIGLU>(a, sh, base, maps, rank);
   } else if (warp == 1) {
-    if ((rank & 1) == 0 && (threadIdx.x & 31) == 0) gemm_mma<W4, SWIGLU>(a, sh, base, rank);
+    if ((rank & 1) == 0) gemm_mma<W4, SWIGLU>(a, sh, base, rank);
   } else if (warp == 2) {
     gemm_scales<4, W4, SWIGLU>(
-        a, sh, smem + a.stages * S::stage(a.tokens), rank,
-        [&](const GemmWalk<SWIGLU>& k, const uint8_t* (&p)[4]) {
-          const GemmTile w = gemm_tile<SWIGLU>(a, sh, k.nt, k.t);
+        a, sh, smem + a.stages * S::stage(a.tokens), rank, a.ws_words != 0,
+        [&](GemmWalk<SWIGLU>& k, const uint8_t* (&p)[4]) {
+          const GemmTile w = k.tile(a, sh);
           const int lane = threadIdx.x & 31, half = rank & 1;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -754,29 +896,31 @@ static __global__ void __launch_bounds__(kGemmThreads, 1)
         });
   } else if (warp == 3) {
     gemm_scales<8, false, SWIGLU>(
-        a, sh, smem + a.stages * S::stage(a.tokens) + S::SFA, rank,
-        [&](const GemmWalk<SWIGLU>& k, const uint8_t* (&p)[8]) {
-          const GemmTile w = gemm_tile<SWIGLU>(a, sh, k.nt, k.t);
+        a, sh, smem + a.stages * S::stage(a.tokens) + 4 * S::SFA, rank, a.xs_words != 0,
+        [&](GemmWalk<SWIGLU>& k, const uint8_t* (&p)[8]) {
+          const GemmTile w = k.tile(a, sh);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int r = (threadIdx.x & 31) + 32 * i;
-            p[i] = 32 * i < w.N ? a.xs + gemm_source(a, w, r) * a.xs_stride : nullptr;
+            p[i] = a.xs + gemm_source(a, w, r) * a.xs_stride;
           }
         });
-  } else {
+  } else if (warp < 12) {
     gemm_results<SWIGLU>(a, sh, smem, rank);
+  } else if (a.loaders) {
+    gemm_load_rows<SWIGLU>(a, sh, base, rank);
   }
   __syncwarp();
-  if (a.splits > 1 && warp < 4) {   // the results' warps' one, where the cluster has a tile
+  if (a.splits > 1 && (warp < 4 || warp >= 12)) {   // the results' warps' one, where the cluster has a tile
     const GemmWalk<SWIGLU> k(a, sh);
     if (k.t < k.tiles) cluster_sync();
   }
   if (gemm_dead(sh) && warp == 1) {
     // products and copies in flight, before their memory is given back: bounded too
-    if ((threadIdx.x & 31) == 0) {
+    if (elect_one()) {
       if ((rank & 1) == 0) {
         umma_commit_pair(&sh.drained, (uint16_t)(1u << rank));
-        for (int i = 0; i < 100 && !gemm_try_wait(&sh.drained, 0); ++i) {
+        for (int i = 0; i < 100 && !mbar_try_wait_long(&sh.drained, 0); ++i) {
         }
       }
       const unsigned long long t0 = global_ns();

@@ -593,14 +593,6 @@ __device__ __forceinline__ void pr_convert(const AttnArgs& a, PrShared& sh, uint
 // every operand of an MMA is a constant of the code.  (Built in one thread's
 // registers, the operands of an MMA cost 145 cycles to issue, more than twice
 // its time on the tensor cores.)
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r));
-  return r != 0;
-}
-
 __device__ __forceinline__ void pr_wait_keys(PrShared& sh, int n) {
   pr_wait(&sh.kfull[n & 1], (n >> 1) & 1, sh);
 }

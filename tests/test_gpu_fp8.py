@@ -268,7 +268,7 @@ def test_experts(counts, mode, gather, mx):
 
 
 def test_experts_values_out_of_range_are_bounded():
-    """Offsets outside the rows, ends below their starts, sources outside x."""
+    """Offsets outside the rows or below earlier ones, sources outside x."""
     rng = np.random.default_rng(8)
     w, ws = _experts(rng, [0] * 4, 256, 128, False)
     x, xs = ref.random_x(rng, 10, 128)
@@ -278,14 +278,30 @@ def test_experts_values_out_of_range_are_bounded():
                           _dev(np.array([-4, 6, 2, 9, 1000]), torch.int32),
                           rows=_dev(rows, torch.int32), out=out)
     xv = ref.row_values(x, xs)[np.clip(rows, 0, 9)]
-    for e, (a, b) in enumerate(((0, 6), (6, 6), (2, 9), (9, 20))):
-        if e == 0:
-            b = 2       # rows 2..5 belong to two experts here: either's result
-        p, tol = ref.product(xv[a:b], ref.weight_values(w[e], ws[e], False))
-        if e == 2:
-            p, tol, a = p[4:], tol[4:], 6
+    for e, (a, b) in enumerate(((0, 6), (6, 6), (6, 9), (9, 20))):
         if a < b:
+            p, tol = ref.product(xv[a:b], ref.weight_values(w[e], ws[e], False))
             _check_product(got[a:b], p, tol, False, False, torch.float32, e)
+
+
+@pytest.mark.parametrize("experts", [511, 512, 513, 1023, 1024])
+def test_many_experts(experts):
+    """Few rows spread over many experts, most of which have none."""
+    rng = np.random.default_rng(experts)
+    counts = np.zeros(experts, int)
+    counts[rng.choice(experts, 9, replace=False)] = rng.integers(1, 40, 9)
+    counts[-1] = 2
+    total = counts.sum()
+    w, ws = ref.random_w(rng, 128, 128, False)
+    x, xs = ref.random_x(rng, total, 128)
+    sign = rng.integers(0, 2, experts) * 128        # experts differ in their weights' signs
+    we = torch.from_numpy(w)[None] ^ torch.from_numpy(sign.astype(np.uint8))[:, None, None]
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    got = M.expert_linear(_codes(x), _scales(xs), we.to(DEV).view(torch.float8_e4m3fn),
+                          _scales(ws)[None].expand(experts, -1, -1), _dev(offsets, torch.int32))
+    p, tol = ref.product(ref.row_values(x, xs), ref.weight_values(w, ws, False))
+    flip = np.repeat(np.where(sign, -1.0, 1.0), counts)[:, None]
+    _check_product(got, p * flip, tol, False, False, torch.bfloat16, experts)
 
 
 # ---------------------------------------------------------------------------
