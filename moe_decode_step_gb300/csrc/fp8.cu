@@ -222,7 +222,7 @@ int moe_fp8_product(void* stream, const moe_fp8_product_t* args) {
     return MOE_ERR_INVALID_ARG;
   const int unit = w4 ? 32 : 16, size = codes ? 1 : t.out_dtype == MOE_DTYPE_F32 ? 4 : 2;
   if (t.k % (w4 ? 128 : 16) || t.n_experts > kGemmMaxExperts || misaligned(t.x, 16) ||
-      (t.x_stride & 15) || misaligned(t.w, unit) || ((t.w_stride | t.w_expert_stride) & (unit - 1)) ||
+      (t.x_stride & 15) || t.x_stride > INT32_MAX || misaligned(t.w, unit) || ((t.w_stride | t.w_expert_stride) & (unit - 1)) ||
       t.n_rows > INT32_MAX - 256 || t.n > INT32_MAX - 256 || t.k > INT32_MAX - kGemmK ||
       misaligned(t.out, size))
     return MOE_ERR_UNSUPPORTED;
@@ -236,14 +236,17 @@ int moe_fp8_product(void* stream, const moe_fp8_product_t* args) {
   const long long many = t.offsets ? 3 * (((long long)t.n_rows + t.n_experts - 1) / t.n_experts)
                                    : t.n_rows;
   const int tokens = (int)std::min<long long>(kGemmTokens, (std::max(many, 32ll) + 15) / 16 * 16);
-  // many rows by index come through warps of their own
-  const bool loaders = t.rows && tokens > 32, interleaved = swiglu && t.n % 32 == 0;
+  const bool interleaved = swiglu && t.n % 32 == 0;
   GemmMaps maps;
   if (!t.rows) {
-    for (int i = 0; i < 4; ++i)
-      if (tokens / 2 >= 64 >> i && (rc = encode_rows(fn, &maps.x[i], t, 64 >> i))) return rc;
-  } else if (!loaders && (rc = encode_rows(fn, &maps.gather, t, 1))) {
-    return rc;
+    // tiles of a dense call have one size, but for the last; an expert's any
+    const int tiles = (t.n_rows + tokens - 1) / tokens;
+    const int size = ((t.n_rows + tiles - 1) / tiles + 15) / 16 * 16;
+    const int last = (t.n_rows - (tiles - 1) * size + 15) / 16 * 16;
+    for (int n = 16; n <= tokens; n += 16)
+      if ((t.offsets || n == size || n == last) &&
+          (rc = encode_rows(fn, &maps.x[n / 16 - 1], t, n / 2)))
+        return rc;
   }
   if ((rc = encode_weights(fn, &maps.w, t, swiglu, interleaved))) return rc;
   GemmArgs a{};
@@ -256,7 +259,6 @@ int moe_fp8_product(void* stream, const moe_fp8_product_t* args) {
   a.experts = t.n_experts;
   a.offsets = t.offsets;
   a.src = t.rows;
-  a.loaders = loaders;
   a.interleaved = interleaved;
   a.x = t.x;
   a.x_stride = t.x_stride;

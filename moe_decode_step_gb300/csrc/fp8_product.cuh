@@ -70,7 +70,6 @@ struct GemmArgs {
   int stages, splits;
   const int* offsets;        // or null
   const int* src;            // or null
-  int loaders;               // rows by index come through warps 12..15
   int interleaved;           // SwiGLU: gates and ups in one copy
   const uint8_t* x;
   long long x_stride;
@@ -88,12 +87,12 @@ struct GemmArgs {
 };
 
 struct GemmMaps {
-  CUtensorMap x[4];          // boxes of 64, 32, 16 and 8 rows
-  CUtensorMap gather, w;
+  CUtensorMap w;
+  CUtensorMap x[kGemmTokens / 16];   // boxes of 8, 16, .. rows: a CTA's part of a tile's tokens
 };
 
 struct GemmShared {
-  uint64_t full[kGemmMaxStages], empty[kGemmMaxStages];
+  uint64_t full[kGemmMaxStages], empty[kGemmMaxStages], loaded[kGemmMaxStages];
   uint64_t sf_full[GemmShape::SFSLOTS], sf_empty[GemmShape::SFSLOTS];
   uint64_t acc_full[2], acc_empty[2], amax_full[2], drained;
   uint32_t tmem;
@@ -125,6 +124,16 @@ __device__ __forceinline__ bool gemm_wait(uint64_t* bar, uint32_t parity, GemmSh
 // The same for a whole warp, whose lanes go on, or give up, together.
 __device__ __forceinline__ bool gemm_wait_warp(uint64_t* bar, uint32_t parity, GemmShared& sh) {
   return __all_sync(0xffffffffu, gemm_wait(bar, parity, sh));
+}
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 // `addr`: from cluster_map.  (Without a release to the cluster, which waits for the
 // thread's loads and stores too: what is handed over lies in this CTA, whose own
@@ -159,16 +168,6 @@ __device__ __forceinline__ void tma_tile_5d(uint32_t dst, const CUtensorMap* map
       "l"(map), "r"(c), "r"(r16), "r"(e), "r"(bar), "r"(0)
       : "memory");
 }
-// Four rows of a map whose box is one row.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int c,
-                                            const int (&r)[4], uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      ".cta_group::2 [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-      "l"(map), "r"(c), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar)
-      : "memory");
-}
-
 // ---- MMAs of a pair: both CTAs' shared and tensor memory, at the same places ----
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -371,17 +370,10 @@ __device__ __forceinline__ void gemm_copy(const GemmArgs& a, GemmShared& sh, uin
   GemmRing ring;
   for (GemmWalk<SWIGLU> k(a, sh); k.t < k.tiles; k.t += k.step) {
     const GemmTile w = k.tile(a, sh);
-    // consecutive rows in boxes of 64, 32, 16 and 8 of them; rows by index four a
-    // copy where they are few (the loaders bring many)
-    const bool mine = a.src && !a.loaders && 4 * lane < w.N / 2;
-    int r[4];
-    if (mine) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) r[i] = gemm_source(a, w, half * (w.N / 2) + 4 * lane + i);
-    }
     // the pair's bytes (nibbles count as the bytes they are read as)
     const uint32_t bytes =
-        (W4 ? S::ABYTES : 2 * S::ABYTES) + (a.loaders ? 0u : (uint32_t)w.N * kGemmK);
+        (W4 ? S::ABYTES : 2 * S::ABYTES) + (a.src ? 0u : (uint32_t)w.N * kGemmK);
+    const CUtensorMap* xm = &maps.x[w.N / 16 - 1];
     for (int kb = k.k0; kb < k.k1; ++kb, ring.next(a.stages)) {
       if (!gemm_wait_warp(&sh.empty[ring.stage], ring.phase ^ 1, sh)) return;
       const uint32_t bar = full + ring.stage * 8, at = base + ring.stage * stage_bytes;
@@ -398,75 +390,92 @@ __device__ __forceinline__ void gemm_copy(const GemmArgs& a, GemmShared& sh, uin
         tma_tile_3d(at + lane * 16 * kGemmK, &maps.w, kb * kGemmK,
                     (lane & 1 ? a.n : 0) + w.n0 + half * 64 + (lane >> 1) * 16, w.expert, bar);
       }
-      if (!a.src) {
-        const int rows = w.N / 2, size = 64 >> (lane & 3), first = rows & ~(2 * size - 1);
-        if (lane >= 8 && lane < 12 && (rows & size))
-          tma_tile_2d(at + S::ABYTES + first * kGemmK, &maps.x[lane & 3], kb * kGemmK,
-                      w.row0 + half * rows + first, bar);
-      } else if (mine) {
-        tma_gather4(at + S::ABYTES + lane * 4 * kGemmK, &maps.gather, kb * kGemmK, r, bar);
-      }
+      if (!a.src && lane == 8)
+        tma_tile_2d(at + S::ABYTES, xm, kb * kGemmK, w.row0 + half * (w.N / 2), bar);
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// Rows of x by index (warps 12..15): 16 rows of eight 16-byte pieces at a time, laid
-// out as the swizzle has them (piece c of row r at c ^ (r % 8)); columns past K
-// become zeros.  A gather4 takes the copy engine some 50 ns, four rows of 128
-// bytes: with 130 tokens a tile a block of K took 0.9 us.  Each thread's copies of
-// kLoadAhead blocks are under way while the block before them is handed over.
+// Rows of x by index (warps 12..14, a block of K each in turn): 4 rows of eight
+// 16-byte pieces at a time, laid out as the swizzle has them (piece c of row r at c ^
+// (r % 8)).  Columns past K become zeros.  (The copy engine's gather takes it some
+// 50 ns for four rows of 128 bytes: with 130 tokens a tile a block took 0.9 us, and
+// with 8 a CTA 0.3 instead of 0.2.)  Warp 15 hands the blocks over to the tensor
+// cores: the fence that this takes waits for every copy that its thread has under
+// way, so the threads that copy must not need it (a block then took 0.45 us, however
+// few its rows).
 // ---------------------------------------------------------------------------
-constexpr int kLoadAhead = 4;
+constexpr int kGemmLoaders = 3;   // warps
 
 template <bool SWIGLU>
 __device__ __forceinline__ void gemm_load_rows(const GemmArgs& a, GemmShared& sh, uint32_t base,
                                                uint32_t rank) {
   using S = GemmShape;
-  constexpr int PASSES = (kGemmTokens / 2 + 15) / 16;
-  const int t = threadIdx.x & 127, half = rank & 1, sub = t >> 3, c = t & 7;
+  const int lane = threadIdx.x & 31, half = rank & 1, sub = lane >> 3, c = lane & 7;
   const uint32_t stage_bytes = S::stage(a.tokens);
-  const uint32_t full = cluster_map(smem_addr(sh.full), rank & ~1u);
-  const uint32_t to = base + S::ABYTES + sub * kGemmK + ((c ^ (sub & 7)) << 4);
-  GemmRing ring, done;
-  int ahead = 0;
-  auto hand_over = [&]() {
-    fence_async_shared();   // the tensor cores read what these threads' copies wrote
-    __syncwarp();
-    if ((t & 31) == 0) gemm_arrive(full + done.stage * 8);
-    done.next(a.stages);
-  };
+  // even passes' rows are 0..3 of 8, odd ones' 4..7
+  const uint32_t to0 = base + S::ABYTES + sub * kGemmK + ((c ^ sub) << 4);
+  const uint32_t to1 = base + S::ABYTES + (4 + sub) * kGemmK + ((c ^ (4 + sub)) << 4);
+  GemmRing ring;
+  int turn = (int)(threadIdx.x >> 5) - 12;   // blocks until this warp's next one
   for (GemmWalk<SWIGLU> k(a, sh); k.t < k.tiles; k.t += k.step) {
     const GemmTile w = k.tile(a, sh);
-    const int rows = w.N / 2;
-    const uint8_t* p[PASSES];
+    const int rows = w.N / 2;   // a multiple of 8
+    unsigned src[kGemmTokens / 8];
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i)
-      p[i] = a.x + gemm_source(a, w, half * rows + min(16 * i + sub, rows - 1)) * a.x_stride + c * 16;
+    for (int i = 0; i < kGemmTokens / 8; ++i)
+      if (4 * i < rows) src[i] = gemm_source(a, w, half * rows + 4 * i + sub);
     for (int kb = k.k0; kb < k.k1; ++kb, ring.next(a.stages)) {
+      if (turn-- > 0) continue;
+      turn = kGemmLoaders - 1;
       if (!gemm_wait_warp(&sh.empty[ring.stage], ring.phase ^ 1, sh)) {
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        asm volatile("cp.async.wait_all;" ::: "memory");
         return;
       }
-      const uint32_t at = to + ring.stage * stage_bytes;
-      const int col = kb * kGemmK + c * 16;
-      const uint32_t size = col < a.k ? 16 : 0;   // (k is a multiple of 16)
+      const uint32_t at = ring.stage * stage_bytes;
+      const bool in = kb * kGemmK + c * 16 < a.k;   // (k is a multiple of 16)
+      const uint8_t* x = a.x + (in ? kb * kGemmK + c * 16 : 0);
+      const uint32_t size = in ? 16 : 0;
 #pragma unroll
-      for (int i = 0; i < PASSES; ++i)
-        if (16 * i + sub < rows)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at + i * 16 * kGemmK),
-                       "l"(p[i] + (size ? kb * kGemmK : 0)), "r"(size)
-                       : "memory");
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      if (++ahead > kLoadAhead) {
-        --ahead;
-        asm volatile("cp.async.wait_group %0;" ::"n"(kLoadAhead) : "memory");
-        hand_over();
+      for (int i = 0; i < kGemmTokens / 8; i += 2) {
+        if (4 * i >= rows) break;
+        const uint32_t to = at + i / 2 * 8 * kGemmK;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to0 + to),
+                     "l"(x + (uint64_t)src[i] * (uint32_t)a.x_stride), "r"(size)
+                     : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to1 + to),
+                     "l"(x + (uint64_t)src[i + 1] * (uint32_t)a.x_stride), "r"(size)
+                     : "memory");
       }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                       smem_addr(&sh.loaded[ring.stage]))
+                   : "memory");
     }
   }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
-  for (; ahead > 0; --ahead) hand_over();
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// All blocks of K that have arrived, up to four, behind one fence.
+template <bool SWIGLU>
+__device__ __forceinline__ void gemm_hand_over(const GemmArgs& a, GemmShared& sh, uint32_t rank) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t full = cluster_map(smem_addr(sh.full), rank & ~1u);
+  const GemmWalk<SWIGLU> k(a, sh);
+  long long left = k.t < k.tiles ? (long long)((k.tiles - 1 - k.t) / k.step + 1) * (k.k1 - k.k0) : 0;
+  GemmRing ring;
+  while (left > 0) {
+    if (!gemm_wait_warp(&sh.loaded[ring.stage], ring.phase, sh)) return;
+    uint32_t mine = ring.stage;   // lane l's stage
+    int n = 1;
+    for (ring.next(a.stages); n < 4 && n < left; ++n, ring.next(a.stages)) {
+      if (!__all_sync(0xffffffffu, mbar_test_wait(&sh.loaded[ring.stage], ring.phase))) break;
+      if (lane == n) mine = ring.stage;
+    }
+    fence_async_shared();
+    if (lane < n) gemm_arrive(full + mine * 8);
+    left -= n;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -544,9 +553,10 @@ __device__ __forceinline__ void gemm_scales(const GemmArgs& a, GemmShared& sh, u
 // MMAs (warp 1 of the pair's first CTA)
 // ---------------------------------------------------------------------------
 // The loop's own latency counts: a block's four MMAs take the tensor cores 480
-// cycles, and with a vote and an early test of the next barrier in it (and each wait
-// checking for a dead CTA) the loop took 640.  So nobody leaves it early: where a
-// wait ran out, the others end at once and what is issued is garbage of no effect.
+// cycles at most, and with a vote and an early test of the next barrier in it (and
+// each wait checking for a dead CTA) the loop took 640, a block at a time without
+// these 490.  So two blocks at a time, and nobody leaves it early: where a wait ran
+// out, the others end at once and what is issued is garbage of no effect.
 template <bool W4, bool SWIGLU>
 __device__ __forceinline__ void gemm_mma(const GemmArgs& a, GemmShared& sh, uint32_t base,
                                          uint32_t rank) {
@@ -562,33 +572,43 @@ __device__ __forceinline__ void gemm_mma(const GemmArgs& a, GemmShared& sh, uint
     const GemmTile w = k.tile(a, sh);
     const uint32_t acc = tm + (n & 1) * kGemmTokens, id = umma_idesc_mxf8(W4 ? 5 : 0, 0, 0, w.N);
     gemm_wait(&sh.acc_empty[n & 1], (n >> 1 & 1) ^ 1, sh);
-    for (int kb = k.k0; kb < k.k1; ++kb) {
+    for (int kb = k.k0; kb < k.k1; kb += 2) {
       const uint32_t kq = kb & 3, j4 = kb >> 2 & 1;
-      const bool last = kb + 1 == k.k1;
+      const bool two = kb + 1 < k.k1, last = kb + 2 >= k.k1;
+      const GemmRing one = ring;
+      ring.next(a.stages);
       if (kq == 0) gemm_wait(&sh.sf_full[sr.stage], sr.phase, sh);
-      gemm_wait(&sh.full[ring.stage], ring.phase, sh);
+      gemm_wait(&sh.full[one.stage], one.phase, sh);
+      if (two) gemm_wait(&sh.full[ring.stage], ring.phase, sh);
       tc_fence_after();
       if (elect_one()) {
-        const uint64_t off = ring.stage * (stage_bytes >> 4);
         const uint64_t ds = ds0 + sr.stage * (S::SFSLOT >> 4);
-        // scales of this block (MXFP4 weights) or these four, in turn in two places
-        const uint32_t sfa = tm + S::SFCOL + 4 * (W4 ? kb & 1 : j4);
         const uint32_t sfb = tm + S::SFCOL + 8 + 8 * j4;
         if (kq == 0) {
           umma_sf_copy_pair(sfb, ds + (4 * S::SFA >> 4));
           if (w.N > 128) umma_sf_copy_pair(sfb + 4, ds + ((4 * S::SFA + 512) >> 4));
         }
-        if (W4 || kq == 0) umma_sf_copy_pair(sfa, ds + (W4 ? kq : 0) * (S::SFA >> 4));
 #pragma unroll
-        for (uint32_t j = 0; j < 4; ++j)
-          umma_mxf8_pair(acc, da0 + off + 2 * j, db0 + off + 2 * j,
-                         id | (W4 ? j : kq) << 29 | kq << 4, sfa, sfb, (kb > k.k0) || j > 0);
-        umma_commit_pair(&sh.empty[ring.stage], both);
-        if (kq == 3 || last) umma_commit_pair(&sh.sf_empty[sr.stage], both);
+        for (uint32_t b = 0; b < 2; ++b) {
+          if (b == 1 && !two) break;
+          const uint32_t stage = b ? ring.stage : one.stage;
+          const uint64_t off = stage * (stage_bytes >> 4);
+          // scales of this block (MXFP4 weights) or these four, in turn in two places
+          const uint32_t sfa = tm + S::SFCOL + 4 * (W4 ? b : j4);
+          if (W4 || (b == 0 && kq == 0))
+            umma_sf_copy_pair(sfa, ds + (W4 ? kq + b : 0) * (S::SFA >> 4));
+#pragma unroll
+          for (uint32_t j = 0; j < 4; ++j)
+            umma_mxf8_pair(acc, da0 + off + 2 * j, db0 + off + 2 * j,
+                           id | (W4 ? j : kq + b) << 29 | (kq + b) << 4, sfa, sfb,
+                           (kb > k.k0) || b > 0 || j > 0);
+          umma_commit_pair(&sh.empty[stage], both);
+        }
+        if (kq == 2 || last) umma_commit_pair(&sh.sf_empty[sr.stage], both);
         if (last) umma_commit_pair(&sh.acc_full[n & 1], both);
       }
-      if (kq == 3 || last) sr.next(S::SFSLOTS);
-      ring.next(a.stages);
+      if (kq == 2 || last) sr.next(S::SFSLOTS);
+      if (two) ring.next(a.stages);
     }
   }
 }
@@ -853,7 +873,8 @@ static __global__ void __launch_bounds__(kGemmThreads, 1)
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
-      mbar_init(&sh.full[s], a.loaders ? 9 : 1);   // the copies, the pair's loaders
+      mbar_init(&sh.full[s], a.src ? 3 : 1);   // the copies, what the pair's loaders brought
+      mbar_init(&sh.loaded[s], 32);
       mbar_init(&sh.empty[s], 1);
     }
     for (int s = 0; s < S::SFSLOTS; ++s) {
@@ -907,8 +928,9 @@ static __global__ void __launch_bounds__(kGemmThreads, 1)
         });
   } else if (warp < 12) {
     gemm_results<SWIGLU>(a, sh, smem, rank);
-  } else if (a.loaders) {
-    gemm_load_rows<SWIGLU>(a, sh, base, rank);
+  } else if (a.src) {
+    if (warp < 15) gemm_load_rows<SWIGLU>(a, sh, base, rank);
+    else gemm_hand_over<SWIGLU>(a, sh, rank);
   }
   __syncwarp();
   if (a.splits > 1 && (warp < 4 || warp >= 12)) {   // the results' warps' one, where the cluster has a tile
