@@ -139,6 +139,34 @@ int launch_product(GemmArgs a, const GemmMaps& maps, int n_sm, cudaStream_t st) 
   return end();
 }
 
+template <int ITER>
+int launch_dispatch(const DispatchArgs& a, int ctas, cudaStream_t st) {
+  const int smem = disp_smem<ITER>(a.experts);
+  cudaError_t e = cudaFuncSetAttribute(dispatch_kernel<ITER>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       disp_smem<ITER>(kDispMaxExperts));
+  if (e == cudaSuccess && ctas > 8)
+    e = cudaFuncSetAttribute(dispatch_kernel<ITER>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return cuda_fail(e);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kDispThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = ctas;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, dispatch_kernel<ITER>, a);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return cuda_fail(e);
+  }
+  return end();
+}
+
 }  // namespace
 
 extern "C" {
@@ -293,30 +321,13 @@ int moe_dispatch(void* stream, const int32_t* idx, int n_tokens, int top_k, int 
   const Device* dev;
   const int rc = begin(&dev);
   if (rc) return rc;
-  const int smem = kDispWarps * n_experts * 2;
-  cudaError_t e = cudaFuncSetAttribute(dispatch_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kDispWarps * kDispMaxExperts * 2);
-  if (e != cudaSuccess) return cuda_fail(e);
+  // few choices (a decode batch's) to one CTA; 4,096 a CTA, then 16,384, up to 16 CTAs
+  const DispatchArgs a{idx, (int)n, top_k, n_experts, offsets, rows, slots};
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (n <= 1024) return launch_dispatch<1>(a, 1, st);
   int ctas = 1;
   while (ctas < kDispMaxCtas && n > 4096ll * ctas) ctas *= 2;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kDispThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = ctas;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  const DispatchArgs a{idx, (int)n, top_k, n_experts, offsets, rows, slots};
-  e = cudaLaunchKernelEx(&cfg, dispatch_kernel, a);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return cuda_fail(e);
-  }
-  return end();
+  return n <= 4096ll * ctas ? launch_dispatch<4>(a, ctas, st) : launch_dispatch<16>(a, ctas, st);
 }
 
 int moe_combine(void* stream, const moe_combine_t* args) {

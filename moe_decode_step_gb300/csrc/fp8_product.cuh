@@ -4,7 +4,9 @@
 // E4M3 rows of 128 columns brought by TMA into 128-byte-swizzled tiles, E2M1
 // weights unpacked on the way in (8 bytes of nibbles in every 16), and their
 // E8M0 scales in tensor memory, so no product is scaled or converted by a
-// thread.
+// thread.  Products are exact and summed in fp32; the additions of each 32 columns
+// cut rather than round (3e-7 of the rms at K = 4,096,
+// where a product in fp32 is 1e-7 off).
 //
 // The weights are the M side and the rows of x ("tokens") the N side: a tile is
 // 256 weight rows of a pair of CTAs (cta_group::2, 128 rows each) times up to 240
@@ -690,7 +692,9 @@ __device__ __forceinline__ void gemm_store(const GemmArgs& a, const GemmTile& w,
   }
 }
 
-// silu(gate) * up of 32 tokens: lanes below 16 hold gates, the others the ups of
+// silu(gate) * up of 32 tokens (in fast functions: their errors are below those of the
+// sums, 3e-7 of their rms at K = 4,096, and no result differs more with exact ones,
+// which took a prompt's gates and ups from 502 to 676 us): lanes below 16 hold gates, the others the ups of
 // the same columns; lane l gets the results of column l & 15, of the tokens 2 i (below
 // 16) or 2 i + 1.
 __device__ __forceinline__ void gemm_swiglu(const float (&v)[32], float* h) {

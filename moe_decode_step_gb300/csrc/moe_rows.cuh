@@ -10,18 +10,22 @@
 namespace moe {
 
 // ---------------------------------------------------------------------------
-// Dispatch: a stable counting sort of the choices by expert, in one launch of
-// one cluster, whose CTAs take consecutive runs of the choices: each counts its
-// run, they add up one another's counts through distributed shared memory, and
-// each places its own entries, 256 a warp at a time, ranked among equals by a
-// match over the warp's lanes and the counts of the warps before.  No workspace
-// and no order that could change.
+// Dispatch: a stable counting sort of the choices by expert, in one launch of one
+// cluster, whose CTAs take consecutive runs of the choices and add up one another's
+// counts through distributed shared memory.  A CTA takes 1,024 x ITER choices a
+// round, 32 x ITER a warp: a choice's place among its warp's is found by ballots over
+// the bits of the expert (a match of the lanes takes an SM 60 cycles: 16 us of a long
+// prompt's 27) and a count a warp and expert; the round's entries are put in order in
+// shared memory first, so that an expert's go out side by side.  Mostly one round,
+// whose counts are the CTA's.  No workspace, and no order that could change.
 // ---------------------------------------------------------------------------
 constexpr int kDispThreads = 1024, kDispWarps = 32;
 constexpr int kDispMaxExperts = 1024;
-constexpr int kDispIter = 8;                                   // times 32 choices a warp and round
-constexpr int kDispRound = kDispWarps * kDispIter * 32;        // choices a CTA places at a time
-constexpr int kDispMaxCtas = 8;
+constexpr int kDispMaxCtas = 16;
+template <int ITER>
+constexpr int disp_smem(int experts) {
+  return kDispWarps * experts * 2 + kDispThreads * ITER * (4 + 2);
+}
 
 struct DispatchArgs {
   const int* idx;
@@ -39,6 +43,7 @@ __device__ __forceinline__ int disp_scan(int v, int* s_warp) {
     const int x = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += x;
   }
+  __syncthreads();
   if (lane == 31) s_warp[warp] = v;
   __syncthreads();
   int w = s_warp[lane];
@@ -50,32 +55,92 @@ __device__ __forceinline__ int disp_scan(int v, int* s_warp) {
   return v + (warp ? __shfl_sync(0xffffffffu, w, warp - 1) : 0);
 }
 
-// Dynamic shared memory: uint16 counts [kDispWarps][experts].
+// Dynamic shared memory: uint16 counts [kDispWarps][experts], then a round's tokens
+// (int) and experts (uint16) in order.
+template <int ITER>
 static __global__ void __launch_bounds__(kDispThreads)
     dispatch_kernel(const __grid_constant__ DispatchArgs a) {
   extern __shared__ __align__(16) uint16_t disp_counts[];
   __shared__ int s_total[kDispMaxExperts];   // this CTA's choices of each expert
   __shared__ int s_next[kDispMaxExperts];    // where its next one goes
+  __shared__ int s_base[kDispMaxExperts];    // the same less its place in the round
   __shared__ int s_warp[kDispWarps];
   __shared__ int s_end;
+  constexpr int ROUND = kDispThreads * ITER;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, E = a.experts;
+  int* s_token = reinterpret_cast<int*>(disp_counts + kDispWarps * E);
+  uint16_t* s_expert = reinterpret_cast<uint16_t*>(s_token + ROUND);
+  uint16_t* mine = disp_counts + warp * E;
   const int ctas = (int)cluster_size(), rank = (int)cluster_rank();
   const int per = ((a.n + ctas - 1) / ctas + 31) / 32 * 32;
   const int i0 = min(a.n, rank * per), i1 = min(a.n, i0 + per);
-  s_total[t] = 0;
-  __syncthreads();
-  for (int i = i0 + t; i < i1; i += kDispThreads) {
-    const int e = __ldg(a.idx + i);
-    if ((unsigned)e < (unsigned)E) atomicAdd(&s_total[e], 1);
+  const int bits = 32 - __clz(E);   // of E and below
+  const bool once = per <= ROUND;   // (alike in every CTA)
+  int expert[ITER], at[ITER];
+
+  // this round's choices: their places among their warp's of the same expert, and
+  // what the warps before have of each; the round's totals to s_total
+  auto rank_round = [&](int r0) {
+    const int w0 = r0 + warp * (ITER * 32);
+#pragma unroll
+    for (int k = 0; k < ITER; ++k) {
+      const int i = w0 + 32 * k + lane;
+      expert[k] = i < i1 ? __ldg(a.idx + i) : E;
+      if ((unsigned)expert[k] >= (unsigned)E) expert[k] = E;   // none
+    }
+    for (int e = lane; e < E; e += 32) mine[e] = 0;
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < ITER; ++k) {
+      unsigned same = 0xffffffffu;
+      for (int b = 0; b < bits; ++b) {
+        const bool one = (expert[k] >> b) & 1;
+        const unsigned ones = __ballot_sync(0xffffffffu, one);
+        same &= one ? ones : ~ones;
+      }
+      const int before = __popc(same & ((1u << lane) - 1));
+      int seen = 0;
+      if (expert[k] < E) seen = mine[expert[k]];
+      __syncwarp();
+      if (expert[k] < E && before == 0) mine[expert[k]] = (uint16_t)(seen + __popc(same));
+      __syncwarp();
+      at[k] = seen + before;
+    }
+    __syncthreads();
+    if (t < E) {
+      int sum = 0;
+#pragma unroll 8
+      for (int w = 0; w < kDispWarps; ++w) {
+        const int v = disp_counts[w * E + t];
+        disp_counts[w * E + t] = (uint16_t)sum;
+        sum += v;
+      }
+      s_total[t] = sum;
+    }
+  };
+
+  if (once) {
+    rank_round(i0);
+  } else {
+    s_total[t] = 0;
+    __syncthreads();
+    for (int i = i0 + t; i < i1; i += kDispThreads) {
+      const int e = __ldg(a.idx + i);
+      if ((unsigned)e < (unsigned)E) atomicAdd(&s_total[e], 1);
+    }
   }
   cluster_sync();
   int all = 0, before = 0;
   if (t < E) {
-    const uint32_t mine = smem_addr(&s_total[t]);
-    for (int c = 0; c < ctas; ++c) {
-      const int v = ld_cluster_s32(cluster_map(mine, c));
-      if (c < rank) before += v;
-      all += v;
+    const uint32_t here = smem_addr(&s_total[t]);
+    int v[kDispMaxCtas];
+#pragma unroll
+    for (int c = 0; c < kDispMaxCtas; ++c)
+      v[c] = c < ctas ? ld_cluster_s32(cluster_map(here, c)) : 0;
+#pragma unroll
+    for (int c = 0; c < kDispMaxCtas; ++c) {
+      if (c < rank) before += v[c];
+      all += v[c];
     }
   }
   const int end = disp_scan(all, s_warp);
@@ -85,61 +150,39 @@ static __global__ void __launch_bounds__(kDispThreads)
     if (t == E - 1) a.offsets[E] = end;
   }
   if (t == E - 1) s_end = end;
-  __syncthreads();
+  cluster_sync();   // every CTA has read the counts (and s_end, s_next are written)
   // past the last entry, where choices name no expert
   for (int i = s_end + rank * kDispThreads + t; i < a.n; i += ctas * kDispThreads) a.rows[i] = -1;
 
-  uint16_t* mine = disp_counts + warp * E;
-  for (int r0 = i0; r0 < i1; r0 += kDispRound) {
-    for (int e = lane; e < E; e += 32) mine[e] = 0;
-    __syncwarp();
-    const int w0 = r0 + warp * (kDispIter * 32);
-    int expert[kDispIter], at[kDispIter];
-#pragma unroll
-    for (int k = 0; k < kDispIter; ++k) {
-      const int i = w0 + 32 * k + lane;
-      expert[k] = i < i1 ? __ldg(a.idx + i) : -1;
-      if ((unsigned)expert[k] >= (unsigned)E) expert[k] = -1;
-    }
-#pragma unroll
-    for (int k = 0; k < kDispIter; ++k) {
-      const unsigned same = __match_any_sync(0xffffffffu, expert[k]);
-      const int before_me = __popc(same & ((1u << lane) - 1));
-      int seen = 0;
-      if (expert[k] >= 0) seen = mine[expert[k]];
-      __syncwarp();
-      if (expert[k] >= 0 && before_me == 0) mine[expert[k]] = (uint16_t)(seen + __popc(same));
-      __syncwarp();
-      at[k] = seen + before_me;
-    }
-    __syncthreads();
-    // the warps' counts to where each warp's first one goes, relative to s_next
+  for (int r0 = i0; r0 < i1; r0 += ROUND) {
+    if (!once) rank_round(r0);
+    const int own = t < E ? s_total[t] : 0;
+    const int first = disp_scan(own, s_warp) - own;   // its place in the round
     if (t < E) {
-      int sum = 0;
-      for (int w = 0; w < kDispWarps; ++w) {
-        const int v = disp_counts[w * E + t];
-        disp_counts[w * E + t] = (uint16_t)sum;
-        sum += v;
-      }
-      s_total[t] = sum;
+      s_base[t] = s_next[t] - first;
+#pragma unroll 8
+      for (int w = 0; w < kDispWarps; ++w) disp_counts[w * E + t] += (uint16_t)first;
     }
+    if (t == E - 1) s_end = first + own;   // entries of this round
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kDispIter; ++k) {
-      const int i = w0 + 32 * k + lane;
+    for (int k = 0; k < ITER; ++k) {
+      const int i = r0 + warp * (ITER * 32) + 32 * k + lane;
       if (i >= i1) continue;
       int slot = -1;
-      if (expert[k] >= 0) {
-        slot = s_next[expert[k]] + mine[expert[k]] + at[k];
-        a.rows[slot] = i / a.top_k;
+      if (expert[k] < E) {
+        const int p = mine[expert[k]] + at[k];
+        slot = s_base[expert[k]] + p;
+        s_token[p] = (int)((unsigned)i / (unsigned)a.top_k);
+        s_expert[p] = (uint16_t)expert[k];
       }
       a.slots[i] = slot;
     }
     __syncthreads();
-    if (t < E) s_next[t] += s_total[t];
+    for (int p = t; p < s_end; p += kDispThreads) a.rows[s_base[s_expert[p]] + p] = s_token[p];
+    if (t < E) s_next[t] += own;
     __syncthreads();
   }
-  cluster_sync();   // no CTA leaves while another may still read its counts
 }
 
 // ---------------------------------------------------------------------------

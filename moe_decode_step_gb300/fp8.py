@@ -12,12 +12,14 @@ scales (float8_e8m0fnu or uint8) [rows, ceil(d / 128)]; 8-bit weights codes [n, 
 with scales [ceil(n / 128), ceil(k / 128)]; MXFP4 weights the layer's canonical
 layout, uint8 [n, k / 2] with scales [n, k / 32].
 """
+import math
 from typing import NamedTuple, Optional
 
 import torch
+from torch._C._dynamo.guards import _empty_strided_cuda
 
 from ._binding import COMBINE, DTYPE_E4M3, FP8_PRODUCT, RMS_NORM, check, lib
-from .serving import _CODES, _DTYPE, _SCALES, _empty, _raw_stream, _vector, _want
+from .serving import _CODES, _DTYPE, _SCALES, _raw_stream, _vector, _want
 
 _ACTIVATION = {None: 0, "swiglu": 1}
 
@@ -38,6 +40,20 @@ class MoEDispatch(NamedTuple):
     offsets: torch.Tensor   # int32 [n_experts + 1]: first entry of each expert
     rows: torch.Tensor      # int32 [tokens * top_k]: token of each entry
     slots: torch.Tensor     # int32 [tokens, top_k]: entry of each choice
+
+
+def _empty(stream, dtype, device, *shape):
+    """A new tensor on the current device whose memory belongs to the stream the call
+    runs on (what torch.empty does, at a third of its time: behind a launch three of
+    its calls cost the host 7 us, these 1.6)."""
+    if len(shape) == 2:
+        strides = (max(shape[1], 1), 1)
+    else:
+        strides = tuple(math.prod(max(d, 1) for d in shape[i + 1:]) for i in range(len(shape)))
+    if stream is None:
+        return _empty_strided_cuda(shape, strides, dtype)
+    with torch.cuda.stream(stream):
+        return _empty_strided_cuda(shape, strides, dtype)
 
 
 def _blocks(n):
@@ -66,32 +82,33 @@ def rms_norm(x, gamma, residual=None, eps=1e-6, out=True, quantize=False, stream
     gamma [d].  Returns an RMSNormed: out in x's type (out=True, or a tensor to
     write; None where out=False), and with quantize the 8-bit form of the same
     unrounded values."""
-    dev = x.device
-    xs = _matrix(x, "x", tuple(_DTYPE))
+    dev, dtype = x.device, x.dtype
+    xs = _matrix(x, "x", _DTYPE)
     rows, d = x.shape
-    rs = 0
+    rs = os = 0
     if residual is not None:
-        rs = _matrix(residual, "residual", (x.dtype,), dev)
-        _want(residual.shape == x.shape, "residual", f"the shape of x, {tuple(x.shape)}", residual)
+        rs = _matrix(residual, "residual", (dtype,), dev)
+        if residual.shape != x.shape:
+            _want(False, "residual", f"the shape of x, {tuple(x.shape)}", residual)
     _vector(gamma, d, gamma.dtype if gamma.dtype in _DTYPE else torch.float32, "gamma", dev)
     raw = _raw_stream(stream, dev)
-    os = 0
     if out is True:
-        out = _empty(stream, x.dtype, dev, rows, d)
-    if out is False or out is None:
+        out, os = _empty(stream, dtype, dev, rows, d), d
+    elif out is False or out is None:
         out = None
         _want(quantize, "out", "an output: out or quantize", out)
     else:
-        os = _matrix(out, "out", (x.dtype,), dev)
-        _want(out.shape == x.shape, "out", f"the shape of x, {tuple(x.shape)}", out)
+        os = _matrix(out, "out", (dtype,), dev)
+        if out.shape != x.shape:
+            _want(False, "out", f"the shape of x, {tuple(x.shape)}", out)
     codes = scales = None
     if quantize:
         codes, scales = _new_codes(stream, dev, rows, d)
     args = RMS_NORM.pack(
-        x.data_ptr(), xs, residual.data_ptr() if residual is not None else 0, rs,
-        gamma.data_ptr(), out.data_ptr() if out is not None else 0, os,
-        codes.data_ptr() if quantize else 0, d, scales.data_ptr() if quantize else 0, _blocks(d),
-        rows, d, _DTYPE[x.dtype], _DTYPE[gamma.dtype], eps)
+        x.data_ptr(), xs, residual.data_ptr() if rs else 0, rs, gamma.data_ptr(),
+        out.data_ptr() if os else 0, os, codes.data_ptr() if quantize else 0, d,
+        scales.data_ptr() if quantize else 0, _blocks(d), rows, d, _DTYPE[dtype],
+        _DTYPE[gamma.dtype], eps)
     check(lib().moe_rms_norm(raw, args), "moe_rms_norm")
     return RMSNormed(out, codes, scales)
 
@@ -99,7 +116,7 @@ def rms_norm(x, gamma, residual=None, eps=1e-6, out=True, quantize=False, stream
 def fp8_quantize(x, stream=None):
     """The 8-bit form of activations x bfloat16, float16 or float32 [rows, d]
     (moe_fp8_quantize): Quantized(codes, scales)."""
-    xs = _matrix(x, "x", tuple(_DTYPE))
+    xs = _matrix(x, "x", _DTYPE)
     rows, d = x.shape
     raw = _raw_stream(stream, x.device)
     codes, scales = _new_codes(stream, x.device, rows, d)
@@ -123,55 +140,64 @@ def fp8_pack(w, stream=None):
     return Quantized(codes, scales)
 
 
-def _product(what, x, x_scales, w, w_scales, offsets, rows, activation, quantize, out_dtype, out,
-             stream):
-    """fp8_linear and expert_linear; w [experts, n, k or k / 2]."""
+def _product(what, x, x_scales, w, w_scales, experts, offsets, rows, activation, quantize,
+             out_dtype, out, stream):
+    """fp8_linear (experts 0) and expert_linear."""
     dev = x.device
     xs = _matrix(x, "x", _CODES)
     x_rows, k = x.shape
+    kb = (k + 127) // 128
     ss = _matrix(x_scales, "x_scales", _SCALES, dev)
-    if tuple(x_scales.shape) != (x_rows, _blocks(k)):
-        _want(False, "x_scales", f"E8M0 scales {(x_rows, _blocks(k))}", x_scales)
-    experts, n = w.shape[:2]
-    mx = w.dtype == torch.uint8 and w.shape[2] * 2 == k
-    if ((not mx and (w.dtype not in _CODES or w.shape[2] != k)) or w.device != dev
-            or w.stride(2) != 1):
+    if x_scales.shape != (x_rows, kb):
+        _want(False, "x_scales", f"E8M0 scales {(x_rows, kb)}", x_scales)
+    shape = w.shape
+    n, width = shape[-2:]
+    mx = w.dtype == torch.uint8 and 2 * width == k
+    if ((not mx and (w.dtype not in _CODES or width != k)) or w.device != dev
+            or (width > 1 and w.stride(-1) != 1)):
         _want(False, "w", f"E4M3 codes [..., n, {k}] or MXFP4 bytes [..., n, {k // 2}], rows "
               f"contiguous on {dev}", w)
-    want = (experts, n, k // 32) if mx else (experts, _blocks(n), _blocks(k))
-    if (tuple(w_scales.shape) != want or w_scales.dtype not in _SCALES or w_scales.device != dev
-            or (want[2] > 1 and w_scales.stride(2) != 1)):
-        _want(False, "w_scales", f"E8M0 scales {want[1:]} for each matrix, rows contiguous on "
-              f"{dev}", w_scales)
+    want = (n, k // 32) if mx else ((n + 127) // 128, kb)
+    if (w_scales.shape != (shape[:-2] + want) or w_scales.dtype not in _SCALES
+            or w_scales.device != dev or (want[1] > 1 and w_scales.stride(-1) != 1)):
+        _want(False, "w_scales", f"E8M0 scales {want} for each matrix, rows contiguous on {dev}",
+              w_scales)
     _want(activation in _ACTIVATION, "activation", "None or 'swiglu'", activation)
-    _want(activation is None or n % 2 == 0, "w", "gates and ups: an even number of rows", w)
-    _want(not quantize or activation is not None, "quantize", "an activation", quantize)
-    if offsets is not None:
+    cols = n
+    if activation:
+        _want(n % 2 == 0, "w", "gates and ups: an even number of rows", w)
+        cols = n // 2
+    else:
+        _want(not quantize, "quantize", "an activation", activation)
+    n_rows = x_rows
+    at_offsets = at_rows = w_expert = ws_expert = 0
+    if experts:
         _vector(offsets, experts + 1, torch.int32, "offsets", dev)
-    if rows is not None:
-        _vector(rows, None, torch.int32, "rows", dev)
-    n_rows = x_rows if rows is None else rows.shape[0]
-    cols = n // 2 if activation else n
+        at_offsets = offsets.data_ptr()
+        if rows is not None:
+            _vector(rows, None, torch.int32, "rows", dev)
+            n_rows, at_rows = rows.shape[0], rows.data_ptr()
+        if experts > 1:
+            w_expert, ws_expert = w.stride(0), w_scales.stride(0)
     raw = _raw_stream(stream, dev)
-    scales = None
+    scales, at_scales, os = None, 0, cols
     if quantize:
         out, scales = _new_codes(stream, dev, n_rows, cols)
-        kind, os = DTYPE_E4M3, cols
+        kind, at_scales = DTYPE_E4M3, scales.data_ptr()
     elif out is None:
-        _want(out_dtype in _DTYPE, "out_dtype", "bfloat16, float16 or float32", out_dtype)
-        out = _empty(stream, out_dtype, dev, n_rows, cols)
-        kind, os = _DTYPE[out_dtype], cols
+        if out_dtype not in _DTYPE:
+            _want(False, "out_dtype", "bfloat16, float16 or float32", out_dtype)
+        out, kind = _empty(stream, out_dtype, dev, n_rows, cols), _DTYPE[out_dtype]
     else:
-        os = _matrix(out, "out", tuple(_DTYPE), dev)
-        _want(tuple(out.shape) == (n_rows, cols), "out", f"[{n_rows}, {cols}]", out)
+        os = _matrix(out, "out", _DTYPE, dev)
+        if out.shape != (n_rows, cols):
+            _want(False, "out", f"[{n_rows}, {cols}]", out)
         kind = _DTYPE[out.dtype]
-    row = w.stride(1) if n > 1 else (w.shape[2] + 31) // 32 * 32
     args = FP8_PRODUCT.pack(
-        x.data_ptr(), xs, x_scales.data_ptr(), ss, w.data_ptr(), row, w.stride(0),
-        w_scales.data_ptr(), w_scales.stride(1), w_scales.stride(0),
-        offsets.data_ptr() if offsets is not None else 0, rows.data_ptr() if rows is not None else 0,
-        out.data_ptr(), os, scales.data_ptr() if quantize else 0, _blocks(cols), n_rows, x_rows, n,
-        k, experts, int(mx), _ACTIVATION[activation], kind)
+        x.data_ptr(), xs, x_scales.data_ptr(), ss, w.data_ptr(),
+        w.stride(-2) if n > 1 else (width + 31) // 32 * 32, w_expert, w_scales.data_ptr(),
+        w_scales.stride(-2), ws_expert, at_offsets, at_rows, out.data_ptr(), os, at_scales,
+        _blocks(cols), n_rows, x_rows, n, k, experts or 1, mx, _ACTIVATION[activation], kind)
     check(lib().moe_fp8_product(raw, args), what)
     return Quantized(out, scales) if quantize else out
 
@@ -183,10 +209,10 @@ def fp8_linear(x, x_scales, w, w_scales, activation=None, quantize=False,
     n / 2 gate rows and n / 2 up rows and returns silu(gate) * up.  Returns out
     [rows, n or n / 2] in out_dtype (or the given out), or with quantize (and an
     activation) its 8-bit form, Quantized(codes, scales)."""
-    _want(w.dim() == 2, "w", "a matrix", w)
-    _want(w_scales.dim() == 2, "w_scales", "a matrix", w_scales)
-    return _product("fp8_linear", x, x_scales, w.unsqueeze(0), w_scales.unsqueeze(0), None, None,
-                    activation, quantize, out_dtype, out, stream)
+    if w.dim() != 2:
+        _want(False, "w", "a matrix", w)
+    return _product("fp8_linear", x, x_scales, w, w_scales, 0, None, None, activation, quantize,
+                    out_dtype, out, stream)
 
 
 def expert_linear(x, x_scales, w, w_scales, offsets, rows=None, activation=None, quantize=False,
@@ -195,10 +221,10 @@ def expert_linear(x, x_scales, w, w_scales, offsets, rows=None, activation=None,
     offsets[e + 1) (int32 [experts + 1], a dispatch's) go through matrix e, output
     row i reading row rows[i] of x (int32, a dispatch's rows; None: row i).  Rows
     of no expert are left as they are."""
-    _want(w.dim() == 3, "w", "a matrix for each expert", w)
-    _want(w_scales.dim() == 3, "w_scales", "a matrix for each expert", w_scales)
-    return _product("expert_linear", x, x_scales, w, w_scales, offsets, rows, activation, quantize,
-                    out_dtype, out, stream)
+    if w.dim() != 3 or w.shape[0] < 1:
+        _want(False, "w", "a matrix for each expert", w)
+    return _product("expert_linear", x, x_scales, w, w_scales, w.shape[0], offsets, rows,
+                    activation, quantize, out_dtype, out, stream)
 
 
 def moe_dispatch(idx, n_experts, stream=None):
@@ -211,14 +237,12 @@ def moe_dispatch(idx, n_experts, stream=None):
     n_experts = int(n_experts)
     _want(n_experts >= 1, "n_experts", "at least 1", n_experts)
     raw = _raw_stream(stream, dev)
-    # one allocation, cut as kv_plan's
-    buf = _empty(stream, torch.int32, dev, 2 * tokens * k + n_experts + 1)
-    rows, slots, offsets = torch.unsafe_split_with_sizes(
-        buf, [tokens * k, tokens * k, n_experts + 1])
-    at = buf.data_ptr()
-    check(lib().moe_dispatch(raw, idx.data_ptr(), tokens, k, n_experts, at + 8 * tokens * k, at,
-                             at + 4 * tokens * k), "moe_dispatch")
-    return MoEDispatch(offsets, rows, slots.view(tokens, k))
+    offsets = _empty(stream, torch.int32, dev, n_experts + 1)
+    rows = _empty(stream, torch.int32, dev, tokens * k)
+    slots = _empty(stream, torch.int32, dev, tokens, k)
+    check(lib().moe_dispatch(raw, idx.data_ptr(), tokens, k, n_experts, offsets.data_ptr(),
+                             rows.data_ptr(), slots.data_ptr()), "moe_dispatch")
+    return MoEDispatch(offsets, rows, slots)
 
 
 def moe_combine(y, w, slots, residual=None, out=None, stream=None):
@@ -227,7 +251,7 @@ def moe_combine(y, w, slots, residual=None, out=None, stream=None):
     weights, a dispatch's slots), residual [tokens, d] in y's type or None.
     Returns out [tokens, d]; out may be residual."""
     dev = y.device
-    ys = _matrix(y, "y", tuple(_DTYPE))
+    ys = _matrix(y, "y", _DTYPE)
     d = y.shape[1]
     if (slots.dim() != 2 or slots.dtype != torch.int32 or slots.device != dev
             or not slots.is_contiguous()):
@@ -239,16 +263,18 @@ def moe_combine(y, w, slots, residual=None, out=None, stream=None):
     rs = 0
     if residual is not None:
         rs = _matrix(residual, "residual", (y.dtype,), dev)
-        _want(tuple(residual.shape) == (tokens, d), "residual", f"[{tokens}, {d}]", residual)
+        if residual.shape != (tokens, d):
+            _want(False, "residual", f"[{tokens}, {d}]", residual)
     raw = _raw_stream(stream, dev)
     if out is None:
         out = _empty(stream, y.dtype, dev, tokens, d)
         os = d
     else:
         os = _matrix(out, "out", (y.dtype,), dev)
-        _want(tuple(out.shape) == (tokens, d), "out", f"[{tokens}, {d}]", out)
+        if out.shape != (tokens, d):
+            _want(False, "out", f"[{tokens}, {d}]", out)
     args = COMBINE.pack(y.data_ptr(), ys, w.data_ptr(), slots.data_ptr(),
-                        residual.data_ptr() if residual is not None else 0, rs, out.data_ptr(), os,
+                        residual.data_ptr() if rs else 0, rs, out.data_ptr(), os,
                         tokens, k, y.shape[0], d, _DTYPE[y.dtype])
     check(lib().moe_combine(raw, args), "moe_combine")
     return out

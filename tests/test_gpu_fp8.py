@@ -309,7 +309,8 @@ def test_many_experts(experts):
 # ---------------------------------------------------------------------------
 @pytest.mark.parametrize("tokens,k,experts", [(1, 1, 1), (1, 16, 896), (64, 16, 896), (33, 4, 60),
                                               (700, 8, 256), (3000, 8, 8), (4097, 2, 1024),
-                                              (20000, 8, 128), (33000, 2, 3)])
+                                              (20000, 8, 128), (33000, 2, 3), (1025, 4, 1024),
+                                              (70000, 4, 100), (300000, 2, 17)])
 @pytest.mark.parametrize("holes", [False, True])
 def test_dispatch(tokens, k, experts, holes):
     rng = np.random.default_rng(tokens + k)
