@@ -303,8 +303,12 @@ int moe_fp8_product(void* stream, const moe_fp8_product_t* args) {
   a.out_dtype = t.out_dtype;
   const int piece = codes ? 4 : 16;   // what a lane stores at a time
   a.vec = !misaligned(t.out, piece) && a.out_stride % piece == 0;
-  a.xs_words = !misaligned(t.x_scales, 4) && a.xs_stride % 4 == 0;
-  a.ws_words = !misaligned(t.w_scales, 4) && ((a.ws_stride | a.ws_expert) & 3) == 0;
+  auto align = [](const void* q, int64_t s) {
+    const uintptr_t b = (uintptr_t)q | (uintptr_t)s;
+    return b % 16 == 0 ? 16 : b % 8 == 0 ? 8 : b % 4 == 0 ? 4 : 1;
+  };
+  a.xs_align = align(t.x_scales, a.xs_stride);
+  a.ws_align = align(t.w_scales, a.ws_stride | a.ws_expert);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (w4) return swiglu ? launch_product<true, true>(a, maps, dev->n_sm, st)
                         : launch_product<true, false>(a, maps, dev->n_sm, st);

@@ -85,7 +85,7 @@ struct GemmArgs {
   uint8_t* os;
   long long os_stride;
   int out_dtype, vec;        // vec: rows of out are aligned to 16 bytes, of codes to 4
-  int xs_words, ws_words;    // scales of a row can be read as words
+  int xs_align, ws_align;    // of the scales' rows: 16, 8, 4 or 1
 };
 
 struct GemmMaps {
@@ -407,6 +407,10 @@ __device__ __forceinline__ void gemm_copy(const GemmArgs& a, GemmShared& sh, uin
 // cores: the fence that this takes waits for every copy that its thread has under
 // way, so the threads that copy must not need it (a block then took 0.45 us, however
 // few its rows).
+// A warp waits for a stage's barrier every third use of it only.  It cannot take a
+// phase for the one two before: its last block, three before this one, was let in
+// after all blocks up to the ring's length before that one were done with, and this
+// stage's use two before is among them (rings have more than three stages).
 // ---------------------------------------------------------------------------
 constexpr int kGemmLoaders = 3;   // warps
 
@@ -443,6 +447,7 @@ __device__ __forceinline__ void gemm_load_rows(const GemmArgs& a, GemmShared& sh
       for (int i = 0; i < kGemmTokens / 8; i += 2) {
         if (4 * i >= rows) break;
         const uint32_t to = at + i / 2 * 8 * kGemmK;
+        asm volatile("" : "+r"(src[i]), "+r"(src[i + 1]));   // (offsets are not kept: registers)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to0 + to),
                      "l"(x + (uint64_t)src[i] * (uint32_t)a.x_stride), "r"(size)
                      : "memory");
@@ -484,53 +489,75 @@ __device__ __forceinline__ void gemm_hand_over(const GemmArgs& a, GemmShared& sh
 // Scales (warps 2, 3): four blocks of K at a time, for 128 rows at a time, 16 bytes
 // a lane: one word for each of the rows lane, lane + 32, lane + 64, lane + 96.  A
 // word holds the bytes of the four blocks, or (MXFP4 weights) of a block's four
-// steps.  A ring of their own, whose three slots hide the loads of 16 blocks at a
-// time: the fence of each slot waits for every load under way, so that loading a
-// slot ahead took 0.4 us a block.
+// steps.  A ring of their own, read a batch of 8 blocks ahead.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* p, int k, int end) {
-  uint32_t v = 0;
+// Words of R rows a lane (4: weights, 8: tokens) from byte `at` on, of rows of
+// `end` bytes; `align`: what every row's start is a multiple of (16, 8, 4 or 1); `at` is a
+// multiple of 4 (splits begin at groups of four blocks).
+template <int R, int W>
+__device__ __forceinline__ void scales_load(const uint8_t* const (&p)[R], int at, int end,
+                                            int align, uint32_t (&v)[R][W]) {
+  if (W == 2 && align >= 8 && (at & 7) == 0 && at + 8 <= end) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (k + i < end) v |= (uint32_t)__ldg(p + k + i) << (8 * i);
-  return v;
-}
-
-// Words of R rows a lane (4: weights, 8: tokens) for blocks [k, k + 16), `per`
-// bytes each; rows are `end` bytes, as words where `aligned`.
-template <int R, bool PERK>
-__device__ __forceinline__ void scales_load(const uint8_t* const (&p)[R], int k, int end,
-                                            bool aligned, uint32_t (&v)[R][PERK ? 16 : 4]) {
-  constexpr int W = PERK ? 16 : 4;
-  const int at = PERK ? 4 * k : k;
-  if (aligned && at + 4 * W <= end) {
+    for (int i = 0; i < R; ++i) {
+      const uint2 u = __ldg(reinterpret_cast<const uint2*>(p[i] + at));
+      v[i][0] = u.x;
+      v[i][1] = u.y;
+    }
+  } else if (W % 4 == 0 && align == 16 && (at & 15) == 0 && at + 4 * W <= end) {
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
-      for (int j = 0; j < W; ++j) v[i][j] = __ldg(reinterpret_cast<const uint32_t*>(p[i] + at) + j);
+      for (int j = 0; j + 3 < W; j += 4) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(p[i] + at + 4 * j));
+        v[i][j] = u.x;
+        v[i][j + 1] = u.y;
+        v[i][j + 2] = u.z;
+        v[i][j + 3] = u.w;
+      }
+  } else if (align >= 4 && (at + 4 * W <= end || (end & 3) == 0)) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int j = 0; j < W; ++j)
+        if (at + 4 * j < end) v[i][j] = __ldg(reinterpret_cast<const uint32_t*>(p[i] + at) + j);
   } else {
+#pragma unroll 1
+    for (int j = 0; j < W; ++j)
+      for (int b = 0; b < 4; ++b) {
+        if (at + 4 * j + b >= end) break;
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+        for (int i = 0; i < R; ++i) {
+          const uint32_t u = (uint32_t)__ldg(p[i] + at + 4 * j + b) << (8 * b);
 #pragma unroll
-      for (int j = 0; j < W; ++j) v[i][j] = scale_word(p[i], at + 4 * j, end);
+          for (int k = 0; k < W; ++k)   // (no indexed registers)
+            if (k == j) v[i][k] = b ? v[i][k] | u : u;
+        }
+      }
   }
 }
 
 template <int R, bool PERK, bool SWIGLU, class Rows>
 __device__ __forceinline__ void gemm_scales(const GemmArgs& a, GemmShared& sh, uint8_t* dst,
-                                            uint32_t rank, bool aligned, Rows rows_of) {
+                                            uint32_t rank, int align, Rows rows_of) {
   using S = GemmShape;
+  constexpr int BATCH = 8, W = PERK ? 8 : 2, BYTES = PERK ? 4 : 1;   // a block
   const int lane = threadIdx.x & 31;
   const uint32_t full = cluster_map(smem_addr(sh.sf_full), rank & ~1u);
   GemmRing ring;
   for (GemmWalk<SWIGLU> k(a, sh); k.t < k.tiles; k.t += k.step) {
     const uint8_t* p[R];
     rows_of(k, p);
-    for (int k0 = k.k0; k0 < k.k1; k0 += 16) {
-      uint32_t v[R][PERK ? 16 : 4];
-      scales_load<R, PERK>(p, k0, PERK ? 4 * a.kb : a.kb, aligned, v);
+    uint32_t cur[R][W], next[R][W] = {};
+    scales_load(p, BYTES * k.k0, BYTES * a.kb, align, next);
+    for (int k0 = k.k0; k0 < k.k1; k0 += BATCH) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < W; ++j) cur[i][j] = next[i][j];
+      if (k0 + BATCH < k.k1) scales_load(p, BYTES * (k0 + BATCH), BYTES * a.kb, align, next);
+#pragma unroll
+      for (int s = 0; s < BATCH / 4; ++s) {
         if (k0 + 4 * s >= k.k1) break;
         if (!gemm_wait_warp(&sh.sf_empty[ring.stage], ring.phase ^ 1, sh)) return;
         uint4* to = reinterpret_cast<uint4*>(dst + ring.stage * S::SFSLOT);
@@ -539,8 +566,8 @@ __device__ __forceinline__ void gemm_scales(const GemmArgs& a, GemmShared& sh, u
 #pragma unroll
           for (int g = 0; g < R / 4; ++g) {
             const int c = PERK ? 4 * s + j : s;
-            to[32 * (j + g) + lane] =
-                make_uint4(v[4 * g][c], v[4 * g + 1][c], v[4 * g + 2][c], v[4 * g + 3][c]);
+            to[32 * (j + g) + lane] = make_uint4(cur[4 * g][c], cur[4 * g + 1][c],
+                                                 cur[4 * g + 2][c], cur[4 * g + 3][c]);
           }
         fence_async_shared();
         __syncwarp();
@@ -554,11 +581,11 @@ __device__ __forceinline__ void gemm_scales(const GemmArgs& a, GemmShared& sh, u
 // ---------------------------------------------------------------------------
 // MMAs (warp 1 of the pair's first CTA)
 // ---------------------------------------------------------------------------
-// The loop's own latency counts: a block's four MMAs take the tensor cores 480
-// cycles at most, and with a vote and an early test of the next barrier in it (and
-// each wait checking for a dead CTA) the loop took 640, a block at a time without
-// these 490.  So two blocks at a time, and nobody leaves it early: where a wait ran
-// out, the others end at once and what is issued is garbage of no effect.
+// One thread, chosen once a tile: the loop's own latency counts.  A block's four MMAs
+// take the tensor cores 480 cycles at most; with the whole warp in the loop (a
+// choice of the lane, a vote on every wait, an early test of the next barrier a
+// block) it took 640, without the last two 490, so 230.  Where a wait ran out, the
+// others end at once and what is issued is garbage of no effect.
 template <bool W4, bool SWIGLU>
 __device__ __forceinline__ void gemm_mma(const GemmArgs& a, GemmShared& sh, uint32_t base,
                                          uint32_t rank) {
@@ -574,44 +601,38 @@ __device__ __forceinline__ void gemm_mma(const GemmArgs& a, GemmShared& sh, uint
     const GemmTile w = k.tile(a, sh);
     const uint32_t acc = tm + (n & 1) * kGemmTokens, id = umma_idesc_mxf8(W4 ? 5 : 0, 0, 0, w.N);
     gemm_wait(&sh.acc_empty[n & 1], (n >> 1 & 1) ^ 1, sh);
-    for (int kb = k.k0; kb < k.k1; kb += 2) {
-      const uint32_t kq = kb & 3, j4 = kb >> 2 & 1;
-      const bool two = kb + 1 < k.k1, last = kb + 2 >= k.k1;
-      const GemmRing one = ring;
-      ring.next(a.stages);
-      if (kq == 0) gemm_wait(&sh.sf_full[sr.stage], sr.phase, sh);
-      gemm_wait(&sh.full[one.stage], one.phase, sh);
-      if (two) gemm_wait(&sh.full[ring.stage], ring.phase, sh);
-      tc_fence_after();
-      if (elect_one()) {
+    if (elect_one()) {
+      for (int kb = k.k0; kb < k.k1; kb += 4) {
+        const uint32_t j4 = kb >> 2 & 1, sfb = tm + S::SFCOL + 8 + 8 * j4;
         const uint64_t ds = ds0 + sr.stage * (S::SFSLOT >> 4);
-        const uint32_t sfb = tm + S::SFCOL + 8 + 8 * j4;
-        if (kq == 0) {
-          umma_sf_copy_pair(sfb, ds + (4 * S::SFA >> 4));
-          if (w.N > 128) umma_sf_copy_pair(sfb + 4, ds + ((4 * S::SFA + 512) >> 4));
-        }
+        gemm_wait(&sh.sf_full[sr.stage], sr.phase, sh);
+        tc_fence_after();
+        umma_sf_copy_pair(sfb, ds + (4 * S::SFA >> 4));
+        if (w.N > 128) umma_sf_copy_pair(sfb + 4, ds + ((4 * S::SFA + 512) >> 4));
+        if (!W4) umma_sf_copy_pair(tm + S::SFCOL + 4 * j4, ds);
 #pragma unroll
-        for (uint32_t b = 0; b < 2; ++b) {
-          if (b == 1 && !two) break;
-          const uint32_t stage = b ? ring.stage : one.stage;
-          const uint64_t off = stage * (stage_bytes >> 4);
+        for (uint32_t b = 0; b < 4; ++b) {
+          if (kb + (int)b >= k.k1) break;
           // scales of this block (MXFP4 weights) or these four, in turn in two places
-          const uint32_t sfa = tm + S::SFCOL + 4 * (W4 ? b : j4);
-          if (W4 || (b == 0 && kq == 0))
-            umma_sf_copy_pair(sfa, ds + (W4 ? kq + b : 0) * (S::SFA >> 4));
+          const uint32_t sfa = tm + S::SFCOL + 4 * (W4 ? b & 1 : j4);
+          const uint64_t off = ring.stage * (stage_bytes >> 4);
+          gemm_wait(&sh.full[ring.stage], ring.phase, sh);
+          tc_fence_after();
+          if (W4) umma_sf_copy_pair(sfa, ds + b * (S::SFA >> 4));
 #pragma unroll
           for (uint32_t j = 0; j < 4; ++j)
             umma_mxf8_pair(acc, da0 + off + 2 * j, db0 + off + 2 * j,
-                           id | (W4 ? j : kq + b) << 29 | (kq + b) << 4, sfa, sfb,
+                           id | (W4 ? j : b) << 29 | b << 4, sfa, sfb,
                            (kb > k.k0) || b > 0 || j > 0);
-          umma_commit_pair(&sh.empty[stage], both);
+          umma_commit_pair(&sh.empty[ring.stage], both);
+          ring.next(a.stages);
         }
-        if (kq == 2 || last) umma_commit_pair(&sh.sf_empty[sr.stage], both);
-        if (last) umma_commit_pair(&sh.acc_full[n & 1], both);
+        umma_commit_pair(&sh.sf_empty[sr.stage], both);
+        sr.next(S::SFSLOTS);
       }
-      if (kq == 2 || last) sr.next(S::SFSLOTS);
-      if (two) ring.next(a.stages);
+      umma_commit_pair(&sh.acc_full[n & 1], both);
     }
+    __syncwarp();
   }
 }
 
@@ -907,7 +928,7 @@ static __global__ void __launch_bounds__(kGemmThreads, 1)
     if ((rank & 1) == 0) gemm_mma<W4, SWIGLU>(a, sh, base, rank);
   } else if (warp == 2) {
     gemm_scales<4, W4, SWIGLU>(
-        a, sh, smem + a.stages * S::stage(a.tokens), rank, a.ws_words != 0,
+        a, sh, smem + a.stages * S::stage(a.tokens), rank, a.ws_align,
         [&](GemmWalk<SWIGLU>& k, const uint8_t* (&p)[4]) {
           const GemmTile w = k.tile(a, sh);
           const int lane = threadIdx.x & 31, half = rank & 1;
@@ -921,7 +942,7 @@ static __global__ void __launch_bounds__(kGemmThreads, 1)
         });
   } else if (warp == 3) {
     gemm_scales<8, false, SWIGLU>(
-        a, sh, smem + a.stages * S::stage(a.tokens) + 4 * S::SFA, rank, a.xs_words != 0,
+        a, sh, smem + a.stages * S::stage(a.tokens) + 4 * S::SFA, rank, a.xs_align,
         [&](GemmWalk<SWIGLU>& k, const uint8_t* (&p)[8]) {
           const GemmTile w = k.tile(a, sh);
 #pragma unroll
