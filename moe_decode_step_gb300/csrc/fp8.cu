@@ -11,19 +11,43 @@ using namespace moe;
 
 namespace {
 
+// A launch that may begin while the one before it in the stream ends: every kernel
+// here waits for that before it touches memory (decode steps are chains of such
+// calls, whose starts take as long as their work).  cluster: CTAs of one.
+template <class... Args>
+int launch(void (*kernel)(Args...), unsigned grid_x, unsigned grid_y, int threads, int smem,
+           int cluster, cudaStream_t st, const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid_x, grid_y);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2] = {};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return cuda_fail(e);
+  }
+  return end();
+}
+
 bool dtype16or32(int t) { return t == MOE_DTYPE_BF16 || t == MOE_DTYPE_F16 || t == MOE_DTYPE_F32; }
 
 template <int T, int NV>
-void launch_norm(const NormArgs& a, bool f32, cudaStream_t st) {
+int launch_norm(const NormArgs& a, bool f32, cudaStream_t st) {
   constexpr int THREADS = T < 256 ? 256 : T, ROWS = THREADS / T;
   const unsigned grid = (unsigned)((a.rows + ROWS - 1) / ROWS);
-  if (a.gamma) {
-    if (f32) rms_norm_kernel<T, NV, true, true><<<grid, THREADS, 0, st>>>(a);
-    else rms_norm_kernel<T, NV, false, true><<<grid, THREADS, 0, st>>>(a);
-  } else {
-    if (f32) rms_norm_kernel<T, NV, true, false><<<grid, THREADS, 0, st>>>(a);
-    else rms_norm_kernel<T, NV, false, false><<<grid, THREADS, 0, st>>>(a);
-  }
+  void (*kernel)(NormArgs) =
+      a.gamma ? (f32 ? rms_norm_kernel<T, NV, true, true> : rms_norm_kernel<T, NV, false, true>)
+              : (f32 ? rms_norm_kernel<T, NV, true, false> : rms_norm_kernel<T, NV, false, false>);
+  return launch(kernel, grid, 1, THREADS, 0, 1, st, a);
 }
 
 int run_norm(const NormArgs& a, int dtype, void* stream) {
@@ -34,11 +58,10 @@ int run_norm(const NormArgs& a, int dtype, void* stream) {
   if (rc) return rc;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool f32 = dtype == MOE_DTYPE_F32;
-  if (a.d <= 1024) launch_norm<32, 4>(a, f32, st);
-  else if (a.d <= 4096) launch_norm<128, 4>(a, f32, st);
-  else if (a.d <= 8192) launch_norm<256, 4>(a, f32, st);
-  else launch_norm<512, 4>(a, f32, st);
-  return end();
+  if (a.d <= 1024) return launch_norm<32, 4>(a, f32, st);
+  if (a.d <= 4096) return launch_norm<128, 4>(a, f32, st);
+  if (a.d <= 8192) return launch_norm<256, 4>(a, f32, st);
+  return launch_norm<512, 4>(a, f32, st);
 }
 
 // Tensor map of bytes (or of E2M1 nibbles that become 16 bytes each 16) with
@@ -110,8 +133,10 @@ template <bool W4, bool SWIGLU>
 int launch_product(GemmArgs a, const GemmMaps& maps, int n_sm, cudaStream_t st) {
   a.stages = GemmShape::stages(a.tokens);
   const int smem = GemmShape::smem(a.tokens);
-  cudaError_t e = cudaFuncSetAttribute(fp8_product_kernel<W4, SWIGLU>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // (the most any call asks for: calls of other threads may come between)
+  const cudaError_t e = cudaFuncSetAttribute(fp8_product_kernel<W4, SWIGLU>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             GemmShape::LIMIT);
   if (e != cudaSuccess) return cuda_fail(e);
   const long long tiles = tiles_at_most(a, SWIGLU);
   if (tiles > INT32_MAX - 65536) return MOE_ERR_UNSUPPORTED;
@@ -120,23 +145,8 @@ int launch_product(GemmArgs a, const GemmMaps& maps, int n_sm, cudaStream_t st) 
   while (a.splits < kGemmMaxSplits && 2 * a.splits * tiles <= pairs && 2 * a.splits <= groups)
     a.splits *= 2;
   const int grid = 2 * a.splits * (int)std::min<long long>(pairs / a.splits, tiles);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kGemmThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = 2 * a.splits;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, fp8_product_kernel<W4, SWIGLU>, a, maps);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return cuda_fail(e);
-  }
-  return end();
+  return launch(fp8_product_kernel<W4, SWIGLU>, grid, 1, kGemmThreads, smem, 2 * a.splits, st, a,
+                maps);
 }
 
 template <int ITER>
@@ -148,23 +158,7 @@ int launch_dispatch(const DispatchArgs& a, int ctas, cudaStream_t st) {
   if (e == cudaSuccess && ctas > 8)
     e = cudaFuncSetAttribute(dispatch_kernel<ITER>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return cuda_fail(e);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kDispThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = ctas;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, dispatch_kernel<ITER>, a);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return cuda_fail(e);
-  }
-  return end();
+  return launch(dispatch_kernel<ITER>, ctas, 1, kDispThreads, smem, ctas, st, a);
 }
 
 }  // namespace
@@ -350,11 +344,10 @@ int moe_combine(void* stream, const moe_combine_t* args) {
   if (rc) return rc;
   const CombineArgs a{t.y, t.y_stride, t.w, t.slots, t.residual, t.residual_stride, t.out,
                       t.out_stride, t.n_tokens, t.top_k, t.y_rows, t.d, t.dtype == MOE_DTYPE_F16};
-  const dim3 grid((t.d / 8 + kCombThreads - 1) / kCombThreads, std::min(t.n_tokens, 65535));
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (t.dtype == MOE_DTYPE_F32) combine_kernel<true><<<grid, kCombThreads, 0, st>>>(a);
-  else combine_kernel<false><<<grid, kCombThreads, 0, st>>>(a);
-  return end();
+  const unsigned pieces = (t.d / 8 + kCombThreads - 1) / kCombThreads;
+  return launch(t.dtype == MOE_DTYPE_F32 ? combine_kernel<true> : combine_kernel<false>, pieces,
+                std::min(t.n_tokens, 65535), kCombThreads, 0, 1, static_cast<cudaStream_t>(stream),
+                a);
 }
 
 }  // extern "C"

@@ -226,7 +226,6 @@ struct GemmTile {
 };
 
 __device__ __forceinline__ int gemm_start(const GemmArgs& a, int e) {
-  if (!a.offsets) return e ? a.rows : 0;
   return min(max(__ldg(a.offsets + e), 0), a.rows);
 }
 
@@ -250,6 +249,14 @@ __device__ __forceinline__ int gemm_scan(int v, GemmShared& sh, Op op) {
 // row in common, whatever the offsets hold) and token tiles before each; every
 // thread calls.
 __device__ __forceinline__ void gemm_prefix(const GemmArgs& a, GemmShared& sh) {
+  if (!a.offsets) {   // one matrix: no scans (they take 1.4 us)
+    if (threadIdx.x < 2) {
+      sh.first[threadIdx.x] = threadIdx.x * a.rows;
+      sh.tiles[threadIdx.x] = threadIdx.x * ((a.rows + a.tokens - 1) / a.tokens);
+    }
+    __syncthreads();
+    return;
+  }
   constexpr int PER = (kGemmMaxExperts + kGemmThreads) / kGemmThreads;
   const int e0 = threadIdx.x * PER;
   int first[PER], top = 0;
@@ -896,26 +903,31 @@ static __global__ void __launch_bounds__(kGemmThreads, 1)
   uint8_t* smem = gemm_raw + ((1024 - (smem_addr(gemm_raw) & 1023)) & 1023);
   const uint32_t base = smem_addr(smem), rank = cluster_rank();
   const int warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < a.stages; ++s) {
+  if (warp == 0) {
+    const int s = threadIdx.x;
+    if (s < a.stages) {
       mbar_init(&sh.full[s], a.src ? 3 : 1);   // the copies, what the pair's loaders brought
       mbar_init(&sh.loaded[s], 32);
       mbar_init(&sh.empty[s], 1);
     }
-    for (int s = 0; s < S::SFSLOTS; ++s) {
+    if (s < S::SFSLOTS) {
       mbar_init(&sh.sf_full[s], 4);   // two warps of both CTAs
       mbar_init(&sh.sf_empty[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
+    if (s < 2) {
       mbar_init(&sh.acc_full[s], 1);
       mbar_init(&sh.acc_empty[s], 16);   // eight warps of both CTAs
       mbar_init(&sh.amax_full[s], 1);
     }
-    mbar_init(&sh.drained, 1);
-    sh.dead = 0;
+    if (s == 0) {
+      mbar_init(&sh.drained, 1);
+      sh.dead = 0;
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.w) : "memory");
+    }
     fence_barrier_init();
   }
   if (warp == 1) tmem_alloc_pair(&sh.tmem);
+  pdl_wait_prerequisites();   // (the launch before may still be running up to here)
   gemm_prefix(a, sh);
   tc_fence_before();
   __syncthreads();
@@ -957,6 +969,7 @@ static __global__ void __launch_bounds__(kGemmThreads, 1)
     if (warp < 15) gemm_load_rows<SWIGLU>(a, sh, base, rank);
     else gemm_hand_over<SWIGLU>(a, sh, rank);
   }
+  pdl_launch_dependents();
   __syncwarp();
   if (a.splits > 1 && (warp < 4 || warp >= 12)) {   // the results' warps' one, where the cluster has a tile
     const GemmWalk<SWIGLU> k(a, sh);

@@ -115,6 +115,8 @@ static __global__ void __launch_bounds__(T < 256 ? 256 : T)
     rms_norm_kernel(const __grid_constant__ NormArgs a) {
   constexpr int THREADS = T < 256 ? 256 : T, ROWS = THREADS / T, WARPS = T / 32;
   __shared__ float s_sum[THREADS / 32];
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
   const int t = threadIdx.x % T, sub = threadIdx.x / T;
   const long long row = (long long)blockIdx.x * ROWS + sub;
   const bool there = row < a.rows;

@@ -71,6 +71,8 @@ static __global__ void __launch_bounds__(kDispThreads)
   int* s_token = reinterpret_cast<int*>(disp_counts + kDispWarps * E);
   uint16_t* s_expert = reinterpret_cast<uint16_t*>(s_token + ROUND);
   uint16_t* mine = disp_counts + warp * E;
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
   const int ctas = (int)cluster_size(), rank = (int)cluster_rank();
   const int per = ((a.n + ctas - 1) / ctas + 31) / 32 * 32;
   const int i0 = min(a.n, rank * per), i1 = min(a.n, i0 + per);
@@ -206,6 +208,8 @@ struct CombineArgs {
 template <bool F32>
 static __global__ void __launch_bounds__(kCombThreads)
     combine_kernel(const __grid_constant__ CombineArgs a) {
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
   const int c = 8 * (blockIdx.x * kCombThreads + threadIdx.x);
   if (c >= a.d) return;
   for (int t = blockIdx.y; t < a.tokens; t += gridDim.y) {
