@@ -38,6 +38,9 @@ int launch(void (*kernel)(Args...), unsigned grid_x, unsigned grid_y, int thread
   return end();
 }
 
+// Rows that are written lie apart.
+bool overlap(long long rows, int64_t stride, int64_t d) { return rows > 1 && stride < d; }
+
 bool dtype16or32(int t) { return t == MOE_DTYPE_BF16 || t == MOE_DTYPE_F16 || t == MOE_DTYPE_F32; }
 
 template <int T, int NV>
@@ -149,16 +152,17 @@ int launch_product(GemmArgs a, const GemmMaps& maps, int n_sm, cudaStream_t st) 
                 maps);
 }
 
-template <int ITER>
-int launch_dispatch(const DispatchArgs& a, int ctas, cudaStream_t st) {
-  const int smem = disp_smem<ITER>(a.experts);
-  cudaError_t e = cudaFuncSetAttribute(dispatch_kernel<ITER>,
+template <int WARPS, int ITER>
+int launch_dispatch(const DispatchArgs& a, int ctas, int clusters, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(dispatch_kernel<WARPS, ITER>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       disp_smem<ITER>(kDispMaxExperts));
+                                       disp_smem<WARPS, ITER>(kDispMaxExperts));
   if (e == cudaSuccess && ctas > 8)
-    e = cudaFuncSetAttribute(dispatch_kernel<ITER>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    e = cudaFuncSetAttribute(dispatch_kernel<WARPS, ITER>,
+                             cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return cuda_fail(e);
-  return launch(dispatch_kernel<ITER>, ctas, 1, kDispThreads, smem, ctas, st, a);
+  return launch(dispatch_kernel<WARPS, ITER>, ctas * clusters, 1, kDispThreads,
+                disp_smem<WARPS, ITER>(a.experts), ctas, st, a);
 }
 
 }  // namespace
@@ -172,7 +176,11 @@ int moe_rms_norm(void* stream, const moe_rms_norm_t* args) {
       !(t.eps >= 0.f))
     return MOE_ERR_INVALID_ARG;
   if (t.n_rows == 0) return MOE_OK;
-  if (!t.x || !t.gamma || (!t.out && !t.codes) || !t.codes != !t.scales)
+  if (!t.x || !t.gamma || (!t.out && !t.codes) || !t.codes != !t.scales ||
+      (t.residual && overlap(t.n_rows, t.residual_stride, t.d)) ||
+      (t.out && overlap(t.n_rows, t.out_stride, t.d)) ||
+      (t.codes && (overlap(t.n_rows, t.codes_stride, t.d) ||
+                   overlap(t.n_rows, t.scales_stride, (t.d + 127) / 128))))
     return MOE_ERR_INVALID_ARG;
   if (t.d % 8 || t.d > 16384 || misaligned(t.x, 16) || misaligned(t.residual, 16) ||
       misaligned(t.gamma, 16) || misaligned(t.out, 16) || misaligned(t.codes, 8) ||
@@ -190,7 +198,9 @@ int moe_fp8_quantize(void* stream, const void* x, int dtype, int64_t x_stride, i
                      int64_t scales_stride) {
   if (n_rows < 0 || d < 1 || !dtype16or32(dtype)) return MOE_ERR_INVALID_ARG;
   if (n_rows == 0) return MOE_OK;
-  if (!x || !codes || !scales) return MOE_ERR_INVALID_ARG;
+  if (!x || !codes || !scales || overlap(n_rows, codes_stride, d) ||
+      overlap(n_rows, scales_stride, (d + 127) / 128))
+    return MOE_ERR_INVALID_ARG;
   if (d % 8 || d > 16384 || misaligned(x, 16) || misaligned(codes, 8) ||
       ((x_stride | codes_stride) & 7))
     return MOE_ERR_UNSUPPORTED;
@@ -240,7 +250,8 @@ int moe_fp8_product(void* stream, const moe_fp8_product_t* args) {
   if (t.n_rows == 0) return MOE_OK;
   if (!t.x || !t.x_scales || !t.w || !t.w_scales || !t.out || (codes && !t.out_scales) ||
       t.x_rows == 0 || t.x_stride < t.k ||
-      t.w_stride < (w4 ? t.k / 2 : t.k))
+      t.w_stride < (w4 ? t.k / 2 : t.k) || overlap(t.n_rows, t.out_stride, swiglu ? t.n / 2 : t.n) ||
+      (codes && overlap(t.n_rows, t.out_scales_stride, (t.n / 2 + 127) / 128)))
     return MOE_ERR_INVALID_ARG;
   const int unit = w4 ? 32 : 16, size = codes ? 1 : t.out_dtype == MOE_DTYPE_F32 ? 4 : 2;
   if (t.k % (w4 ? 128 : 16) || t.n_experts > kGemmMaxExperts || misaligned(t.x, 16) ||
@@ -319,13 +330,16 @@ int moe_dispatch(void* stream, const int32_t* idx, int n_tokens, int top_k, int 
   const Device* dev;
   const int rc = begin(&dev);
   if (rc) return rc;
-  // few choices (a decode batch's) to one CTA; 4,096 a CTA, then 16,384, up to 16 CTAs
+  // few choices (a decode batch's) to eight warps of one CTA (fewer counts to clear
+  // and add); then 4,096 a CTA, up to 16 CTAs; then clusters of 16 with as many a
+  // round, whose parts are 2,048 a CTA and up
   const DispatchArgs a{idx, (int)n, top_k, n_experts, offsets, rows, slots};
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (n <= 1024) return launch_dispatch<1>(a, 1, st);
+  if (n <= 1024) return launch_dispatch<8, 4>(a, 1, 1, st);
   int ctas = 1;
   while (ctas < kDispMaxCtas && n > 4096ll * ctas) ctas *= 2;
-  return n <= 4096ll * ctas ? launch_dispatch<4>(a, ctas, st) : launch_dispatch<16>(a, ctas, st);
+  const int clusters = n <= 65536 ? 1 : (int)std::min<long long>(kDispMaxClusters, n / 32768);
+  return launch_dispatch<32, 4>(a, ctas, clusters, st);
 }
 
 int moe_combine(void* stream, const moe_combine_t* args) {
@@ -334,7 +348,9 @@ int moe_combine(void* stream, const moe_combine_t* args) {
   if (t.n_tokens < 0 || t.top_k < 1 || t.y_rows < 0 || t.d < 1 || !dtype16or32(t.dtype))
     return MOE_ERR_INVALID_ARG;
   if (t.n_tokens == 0) return MOE_OK;
-  if ((!t.y && t.y_rows > 0) || !t.w || !t.slots || !t.out) return MOE_ERR_INVALID_ARG;
+  if ((!t.y && t.y_rows > 0) || !t.w || !t.slots || !t.out ||
+      overlap(t.n_tokens, t.out_stride, t.d))
+    return MOE_ERR_INVALID_ARG;
   if (t.d % 8 || t.top_k > 32 || misaligned(t.y, 16) || misaligned(t.residual, 16) ||
       misaligned(t.out, 16) ||
       ((t.y_stride | (t.residual ? t.residual_stride : 0) | t.out_stride) & 7))

@@ -12,7 +12,6 @@ scales (float8_e8m0fnu or uint8) [rows, ceil(d / 128)]; 8-bit weights codes [n, 
 with scales [ceil(n / 128), ceil(k / 128)]; MXFP4 weights the layer's canonical
 layout, uint8 [n, k / 2] with scales [n, k / 32].
 """
-import math
 from typing import NamedTuple, Optional
 
 import torch
@@ -20,6 +19,7 @@ from torch._C._dynamo.guards import _empty_strided_cuda
 
 from ._binding import COMBINE, DTYPE_E4M3, FP8_PRODUCT, RMS_NORM, check, lib
 from .serving import _CODES, _DTYPE, _SCALES, _raw_stream, _vector, _want
+from .serving import _empty as _empty_on
 
 _ACTIVATION = {None: 0, "swiglu": 1}
 
@@ -42,18 +42,25 @@ class MoEDispatch(NamedTuple):
     slots: torch.Tensor     # int32 [tokens, top_k]: entry of each choice
 
 
-def _empty(stream, dtype, device, *shape):
+def _empty(stream, dtype, shape, strides):
     """A new tensor on the current device whose memory belongs to the stream the call
-    runs on (what torch.empty does, at a third of its time: behind a launch three of
-    its calls cost the host 7 us, these 1.6)."""
-    if len(shape) == 2:
-        strides = (max(shape[1], 1), 1)
-    else:
-        strides = tuple(math.prod(max(d, 1) for d in shape[i + 1:]) for i in range(len(shape)))
+    runs on (what torch.empty_strided does, at a third of its time: behind a launch
+    three of its calls cost the host 7 us, these 1.6)."""
     if stream is None:
         return _empty_strided_cuda(shape, strides, dtype)
     with torch.cuda.stream(stream):
         return _empty_strided_cuda(shape, strides, dtype)
+
+
+def _rows(stream, dtype, rows, d):
+    return _empty(stream, dtype, (rows, d), (max(d, 1), 1))
+
+
+def _stream(stream, device):
+    """cudaStream_t of the call (see _raw_stream, which has the checks)."""
+    if stream is None and device.index == torch._C._cuda_getDevice():
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return _raw_stream(stream, device)
 
 
 def _blocks(n):
@@ -61,19 +68,29 @@ def _blocks(n):
 
 
 def _matrix(t, name, dtypes, device=None):
-    """Rows with a contiguous last dimension, on `device` (None: any CUDA device);
-    returns the row stride, of one row its length rounded up to 16."""
-    if (t.dim() != 2 or t.dtype not in dtypes or not t.is_cuda
-            or (device is not None and t.device != device)
-            or (t.shape[1] > 1 and t.stride(1) != 1)):
-        _want(False, name, f"{' or '.join(map(str, dtypes))} [rows, columns] with a contiguous "
-              f"last dimension on {device or 'a CUDA device'}", t)
-    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
+    """Rows with a contiguous last dimension, on `device` (None: any CUDA device):
+    how many, how long, and their stride (of one row its length rounded up to 16)."""
+    if t.dtype in dtypes and t.is_cuda and t.dim() == 2 and (device is None or t.device == device):
+        rows, d = t.shape
+        s0, s1 = t.stride()
+        if s1 == 1 or d <= 1:
+            return rows, d, s0 if rows > 1 else (d + 15) // 16 * 16
+    _want(False, name, f"{' or '.join(map(str, dtypes))} [rows, columns] with a contiguous last "
+          f"dimension on {device or 'a CUDA device'}", t)
 
 
-def _new_codes(stream, dev, rows, d):
-    return (_empty(stream, torch.float8_e4m3fn, dev, rows, d),
-            _empty(stream, torch.float8_e8m0fnu, dev, rows, _blocks(d)))
+def _alike(t, name, dtype, rows, d, device, written=True):
+    """The row stride of a matrix [rows, d]; of one that is written, rows apart."""
+    r, c, stride = _matrix(t, name, (dtype,), device)
+    if r != rows or c != d or (written and stride < d):
+        _want(False, name, f"[{rows}, {d}]{', rows apart' if written else ''}", t)
+    return stride
+
+
+def _new_codes(stream, rows, d):
+    b = (d + 127) // 128
+    return (_empty(stream, torch.float8_e4m3fn, (rows, d), (max(d, 1), 1)),
+            _empty(stream, torch.float8_e8m0fnu, (rows, b), (max(b, 1), 1)))
 
 
 def rms_norm(x, gamma, residual=None, eps=1e-6, out=True, quantize=False, stream=None):
@@ -83,30 +100,25 @@ def rms_norm(x, gamma, residual=None, eps=1e-6, out=True, quantize=False, stream
     write; None where out=False), and with quantize the 8-bit form of the same
     unrounded values."""
     dev, dtype = x.device, x.dtype
-    xs = _matrix(x, "x", _DTYPE)
-    rows, d = x.shape
+    rows, d, xs = _matrix(x, "x", _DTYPE)
     rs = os = 0
     if residual is not None:
-        rs = _matrix(residual, "residual", (dtype,), dev)
-        if residual.shape != x.shape:
-            _want(False, "residual", f"the shape of x, {tuple(x.shape)}", residual)
+        rs = _alike(residual, "residual", dtype, rows, d, dev)
     _vector(gamma, d, gamma.dtype if gamma.dtype in _DTYPE else torch.float32, "gamma", dev)
-    raw = _raw_stream(stream, dev)
+    raw = _stream(stream, dev)
     if out is True:
-        out, os = _empty(stream, dtype, dev, rows, d), d
+        out, os = _rows(stream, dtype, rows, d), d
     elif out is False or out is None:
         out = None
         _want(quantize, "out", "an output: out or quantize", out)
     else:
-        os = _matrix(out, "out", (dtype,), dev)
-        if out.shape != x.shape:
-            _want(False, "out", f"the shape of x, {tuple(x.shape)}", out)
+        os = _alike(out, "out", dtype, rows, d, dev)
     codes = scales = None
     if quantize:
-        codes, scales = _new_codes(stream, dev, rows, d)
+        codes, scales = _new_codes(stream, rows, d)
     args = RMS_NORM.pack(
-        x.data_ptr(), xs, residual.data_ptr() if rs else 0, rs, gamma.data_ptr(),
-        out.data_ptr() if os else 0, os, codes.data_ptr() if quantize else 0, d,
+        x.data_ptr(), xs, residual.data_ptr() if residual is not None else 0, rs,
+        gamma.data_ptr(), out.data_ptr() if out is not None else 0, os, codes.data_ptr() if quantize else 0, d,
         scales.data_ptr() if quantize else 0, _blocks(d), rows, d, _DTYPE[dtype],
         _DTYPE[gamma.dtype], eps)
     check(lib().moe_rms_norm(raw, args), "moe_rms_norm")
@@ -116,10 +128,9 @@ def rms_norm(x, gamma, residual=None, eps=1e-6, out=True, quantize=False, stream
 def fp8_quantize(x, stream=None):
     """The 8-bit form of activations x bfloat16, float16 or float32 [rows, d]
     (moe_fp8_quantize): Quantized(codes, scales)."""
-    xs = _matrix(x, "x", _DTYPE)
-    rows, d = x.shape
-    raw = _raw_stream(stream, x.device)
-    codes, scales = _new_codes(stream, x.device, rows, d)
+    rows, d, xs = _matrix(x, "x", _DTYPE)
+    raw = _stream(stream, x.device)
+    codes, scales = _new_codes(stream, rows, d)
     check(lib().moe_fp8_quantize(raw, x.data_ptr(), _DTYPE[x.dtype], xs, rows, d, codes.data_ptr(),
                                  d, scales.data_ptr(), _blocks(d)), "moe_fp8_quantize")
     return Quantized(codes, scales)
@@ -132,9 +143,10 @@ def fp8_pack(w, stream=None):
     if w.dim() < 2 or w.dtype not in _DTYPE or not w.is_cuda or not w.is_contiguous():
         _want(False, "w", "bfloat16, float16 or float32 [..., n, k] contiguous on a CUDA device", w)
     n, k = w.shape[-2:]
-    raw = _raw_stream(stream, w.device)
-    codes = _empty(stream, torch.float8_e4m3fn, w.device, *w.shape)
-    scales = _empty(stream, torch.float8_e8m0fnu, w.device, *w.shape[:-2], _blocks(n), _blocks(k))
+    raw = _stream(stream, w.device)
+    codes = _empty_on(stream, torch.float8_e4m3fn, w.device, *w.shape)
+    scales = _empty_on(stream, torch.float8_e8m0fnu, w.device, *w.shape[:-2], _blocks(n),
+                       _blocks(k))
     check(lib().moe_fp8_pack(raw, w.data_ptr(), _DTYPE[w.dtype], w.numel() // max(n * k, 1), n, k,
                              codes.data_ptr(), scales.data_ptr()), "moe_fp8_pack")
     return Quantized(codes, scales)
@@ -144,11 +156,10 @@ def _product(what, x, x_scales, w, w_scales, experts, offsets, rows, activation,
              out_dtype, out, stream):
     """fp8_linear (experts 0) and expert_linear."""
     dev = x.device
-    xs = _matrix(x, "x", _CODES)
-    x_rows, k = x.shape
+    x_rows, k, xs = _matrix(x, "x", _CODES)
     kb = (k + 127) // 128
-    ss = _matrix(x_scales, "x_scales", _SCALES, dev)
-    if x_scales.shape != (x_rows, kb):
+    sr, sc, ss = _matrix(x_scales, "x_scales", _SCALES, dev)
+    if sr != x_rows or sc != kb:
         _want(False, "x_scales", f"E8M0 scales {(x_rows, kb)}", x_scales)
     shape = w.shape
     n, width = shape[-2:]
@@ -179,19 +190,18 @@ def _product(what, x, x_scales, w, w_scales, experts, offsets, rows, activation,
             n_rows, at_rows = rows.shape[0], rows.data_ptr()
         if experts > 1:
             w_expert, ws_expert = w.stride(0), w_scales.stride(0)
-    raw = _raw_stream(stream, dev)
+    raw = _stream(stream, dev)
     scales, at_scales, os = None, 0, cols
     if quantize:
-        out, scales = _new_codes(stream, dev, n_rows, cols)
+        out, scales = _new_codes(stream, n_rows, cols)
         kind, at_scales = DTYPE_E4M3, scales.data_ptr()
     elif out is None:
         if out_dtype not in _DTYPE:
             _want(False, "out_dtype", "bfloat16, float16 or float32", out_dtype)
-        out, kind = _empty(stream, out_dtype, dev, n_rows, cols), _DTYPE[out_dtype]
+        out, kind = _rows(stream, out_dtype, n_rows, cols), _DTYPE[out_dtype]
     else:
-        os = _matrix(out, "out", _DTYPE, dev)
-        if out.shape != (n_rows, cols):
-            _want(False, "out", f"[{n_rows}, {cols}]", out)
+        os = _alike(out, "out", out.dtype if out.dtype in _DTYPE else torch.bfloat16, n_rows, cols,
+                    dev)
         kind = _DTYPE[out.dtype]
     args = FP8_PRODUCT.pack(
         x.data_ptr(), xs, x_scales.data_ptr(), ss, w.data_ptr(),
@@ -236,10 +246,10 @@ def moe_dispatch(idx, n_experts, stream=None):
     dev = idx.device
     n_experts = int(n_experts)
     _want(n_experts >= 1, "n_experts", "at least 1", n_experts)
-    raw = _raw_stream(stream, dev)
-    offsets = _empty(stream, torch.int32, dev, n_experts + 1)
-    rows = _empty(stream, torch.int32, dev, tokens * k)
-    slots = _empty(stream, torch.int32, dev, tokens, k)
+    raw = _stream(stream, dev)
+    offsets = _empty(stream, torch.int32, (n_experts + 1,), (1,))
+    rows = _empty(stream, torch.int32, (tokens * k,), (1,))
+    slots = _rows(stream, torch.int32, tokens, k)
     check(lib().moe_dispatch(raw, idx.data_ptr(), tokens, k, n_experts, offsets.data_ptr(),
                              rows.data_ptr(), slots.data_ptr()), "moe_dispatch")
     return MoEDispatch(offsets, rows, slots)
@@ -251,8 +261,7 @@ def moe_combine(y, w, slots, residual=None, out=None, stream=None):
     weights, a dispatch's slots), residual [tokens, d] in y's type or None.
     Returns out [tokens, d]; out may be residual."""
     dev = y.device
-    ys = _matrix(y, "y", _DTYPE)
-    d = y.shape[1]
+    y_rows, d, ys = _matrix(y, "y", _DTYPE)
     if (slots.dim() != 2 or slots.dtype != torch.int32 or slots.device != dev
             or not slots.is_contiguous()):
         _want(False, "slots", f"torch.int32 [tokens, top_k] contiguous on {dev}", slots)
@@ -262,19 +271,14 @@ def moe_combine(y, w, slots, residual=None, out=None, stream=None):
         _want(False, "w", f"torch.float32 {(tokens, k)} contiguous on {dev}", w)
     rs = 0
     if residual is not None:
-        rs = _matrix(residual, "residual", (y.dtype,), dev)
-        if residual.shape != (tokens, d):
-            _want(False, "residual", f"[{tokens}, {d}]", residual)
-    raw = _raw_stream(stream, dev)
+        rs = _alike(residual, "residual", y.dtype, tokens, d, dev, written=False)
+    raw = _stream(stream, dev)
     if out is None:
-        out = _empty(stream, y.dtype, dev, tokens, d)
-        os = d
+        out, os = _rows(stream, y.dtype, tokens, d), d
     else:
-        os = _matrix(out, "out", (y.dtype,), dev)
-        if out.shape != (tokens, d):
-            _want(False, "out", f"[{tokens}, {d}]", out)
+        os = _alike(out, "out", y.dtype, tokens, d, dev)
     args = COMBINE.pack(y.data_ptr(), ys, w.data_ptr(), slots.data_ptr(),
-                        residual.data_ptr() if rs else 0, rs, out.data_ptr(), os,
-                        tokens, k, y.shape[0], d, _DTYPE[y.dtype])
+                        residual.data_ptr() if residual is not None else 0, rs, out.data_ptr(), os,
+                        tokens, k, y_rows, d, _DTYPE[y.dtype])
     check(lib().moe_combine(raw, args), "moe_combine")
     return out
