@@ -7,7 +7,8 @@ One step is kv_plan (blocks and slots for this step's tokens), the projections
 (torch), KVCache.append, KVCache.attention and MoELayer.forward.  Lengths,
 tables and the free stack stay on the device, so the decode step is captured
 into a CUDA graph once and replayed for every token; kv_release gives a
-finished request's blocks back.
+finished request's blocks back.  PromptLayer is the MoE layer for any number of
+rows, with 8-bit activations on the same expert weights.
 """
 import os
 import sys
@@ -93,6 +94,32 @@ class DecoderBlock:
                      self.cache.block_size)
 
 
+class PromptLayer:
+    """The MoE layer for any number of rows: its experts' MXFP4 weights in the canonical
+    layout, the shared expert's in 8 bits, 8-bit activations."""
+
+    def __init__(self, cfg):
+        self.cfg = cfg
+        self.weights = synthetic.make_weights(cfg, layout=0)
+        self.shared_gu = M.fp8_pack(self.weights["shared_gu"])
+        self.shared_d = M.fp8_pack(self.weights["shared_d"])
+
+    def forward(self, x, residual):
+        """x and residual bf16 [tokens, d], residual updated; returns the normalised
+        output, as MoELayer.forward."""
+        c, w = self.cfg, self.weights
+        logits = F.linear(x, w["router_w"])
+        idx, mix = M.moe_route(logits, c.top_k, bias=w["router_bias"], routed_scale=c.routed_scale)
+        by = M.moe_dispatch(idx, c.n_experts)
+        x8 = M.fp8_quantize(x)
+        h = M.expert_linear(*x8, w["w_gu_q"], w["w_gu_s"], by.offsets, rows=by.rows,
+                            activation="swiglu", quantize=True)
+        y = M.expert_linear(*h, w["w_d_q"], w["w_d_s"], by.offsets)
+        hs = M.fp8_linear(*x8, *self.shared_gu, activation="swiglu", quantize=True)
+        z = M.moe_combine(y, mix, by.slots, residual=M.fp8_linear(*hs, *self.shared_d))
+        return M.rms_norm(z, w["rms_gamma"], residual=residual, eps=c.rms_eps).out
+
+
 def generate(block, prompts, steps, graph=True):
     """Prefill, then `steps` decode steps; the outputs [steps, rows, d] and the
     prompts' expert load."""
@@ -129,6 +156,10 @@ def main():
           f"contexts {block.ctx_lens.tolist()}, {used} blocks in use")
     print(f"output rms {out.float().square().mean().sqrt():.3f}; the prompts' busiest experts "
           f"{torch.topk(load, 4).indices.tolist()}")
+    tokens = torch.cat(prompts)
+    out = PromptLayer(cfg).forward(tokens, torch.zeros_like(tokens))
+    print(f"all {tokens.shape[0]} prompt tokens through the MoE layer: output rms "
+          f"{out.float().square().mean().sqrt():.3f}")
     block.release(torch.ones(rows, dtype=torch.bool, device="cuda"))
     print(f"released: {int(block.n_free)} of {block.free_list.shape[0]} blocks free, "
           f"{int(block.unserved)} unserved rows")
