@@ -403,6 +403,9 @@ __device__ __forceinline__ void gemm_copy(const GemmArgs& a, GemmShared& sh, uin
         tma_tile_2d(at + S::ABYTES, xm, kb * kGemmK, w.row0 + half * (w.N / 2), bar);
     }
   }
+  // the last arrivals from the pair's first CTA are in before this one may leave
+  for (int i = 0; i < a.stages; ++i, ring.next(a.stages))
+    if (!gemm_wait_warp(&sh.empty[ring.stage], ring.phase ^ 1, sh)) return;
 }
 
 // ---------------------------------------------------------------------------
@@ -583,6 +586,8 @@ __device__ __forceinline__ void gemm_scales(const GemmArgs& a, GemmShared& sh, u
       }
     }
   }
+  for (int i = 0; i < S::SFSLOTS; ++i, ring.next(S::SFSLOTS))   // (as the copies' end)
+    if (!gemm_wait_warp(&sh.sf_empty[ring.stage], ring.phase ^ 1, sh)) return;
 }
 
 // ---------------------------------------------------------------------------

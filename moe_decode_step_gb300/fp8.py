@@ -193,6 +193,7 @@ def _product(what, x, x_scales, w, w_scales, experts, offsets, rows, activation,
     raw = _stream(stream, dev)
     scales, at_scales, os = None, 0, cols
     if quantize:
+        _want(out is None, "out", "None with quantize", out)
         out, scales = _new_codes(stream, n_rows, cols)
         kind, at_scales = DTYPE_E4M3, scales.data_ptr()
     elif out is None:

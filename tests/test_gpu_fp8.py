@@ -180,7 +180,8 @@ def test_linear_short_and_odd_k(k):
 @pytest.mark.parametrize("mx", [False, True])
 @pytest.mark.parametrize("quantize", [False, True])
 @pytest.mark.parametrize("rows,f,k", [(1, 128, 128), (130, 256, 512), (33, 200, 256), (7, 1, 128),
-                                      (64, 1408, 1024), (260, 129, 384)])
+                                      (64, 1408, 1024), (260, 129, 384), (5, 256, 2048),
+                                      (200, 144, 2304)])
 def test_swiglu(rows, f, k, quantize, mx):
     rng = np.random.default_rng(rows + f + k)
     x, xs = ref.random_x(rng, rows, k)
@@ -265,6 +266,135 @@ def test_experts(counts, mode, gather, mx):
         p, tol = ref.product(xv[a:b], ref.weight_values(w[e], ws[e], mx))
         part = (M.Quantized(got.codes[a:b], got.scales[a:b]) if kw["quantize"] else got[a:b])
         _check_product(part, p, tol, mode != "plain", kw["quantize"], torch.bfloat16, (e, c))
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("mode", ["plain", "swiglu", "quantize"])
+def test_few_rows_of_experts_split_k(mode, mx):
+    """Fewer tiles than the device has room for: K is split; some clusters have no tile."""
+    rng = np.random.default_rng(11)
+    counts, k, n = [0, 2, 0, 1, 0, 0], 2048, 272
+    w, ws = _experts(rng, counts, n, k, mx)
+    x, xs = ref.random_x(rng, 4, k)
+    rows = np.array([3, 1, 3])
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    kw = dict(activation=None if mode == "plain" else "swiglu", quantize=mode == "quantize",
+              out_dtype=torch.float16)
+    got = M.expert_linear(_codes(x), _scales(xs), _dev(w) if mx else _codes(w), _scales(ws),
+                          _dev(offsets, torch.int32), rows=_dev(rows, torch.int32), **kw)
+    xv = ref.row_values(x, xs)[rows]
+    for e, (a, b) in ((1, (0, 2)), (3, (2, 3))):
+        p, tol = ref.product(xv[a:b], ref.weight_values(w[e], ws[e], mx))
+        part = M.Quantized(got.codes[a:b], got.scales[a:b]) if kw["quantize"] else got[a:b]
+        _check_product(part, p, tol, mode != "plain", kw["quantize"], torch.float16, e)
+
+
+@pytest.mark.parametrize("k", [16, 144, 528])
+def test_rows_by_index_with_odd_k(k):
+    rng = np.random.default_rng(k)
+    counts = [70, 0, 9]
+    w, ws = _experts(rng, counts, 130, k, False)
+    x, xs = ref.random_x(rng, 30, k)
+    rows = rng.integers(0, 30, 79)
+    got = M.expert_linear(_codes(x), _scales(xs), _codes(w), _scales(ws),
+                          _dev(np.array([0, 70, 70, 79]), torch.int32), rows=_dev(rows, torch.int32))
+    xv = ref.row_values(x, xs)[rows]
+    for e, (a, b) in ((0, (0, 70)), (2, (70, 79))):
+        p, tol = ref.product(xv[a:b], ref.weight_values(w[e], ws[e], False))
+        _check_product(got[a:b], p, tol, False, False, torch.bfloat16, e)
+
+
+@pytest.mark.parametrize("shift", [1, 4, 8])
+def test_scales_of_any_alignment(shift):
+    rng = np.random.default_rng(shift)
+    x, xs = ref.random_x(rng, 40, 1024)
+    w, ws = ref.random_w(rng, 300, 1024, True)
+    p, tol = ref.product(ref.row_values(x, xs), ref.weight_values(w, ws, True))
+    wide = torch.zeros(300, 48, dtype=torch.uint8, device=DEV)
+    wide[:, shift:shift + 32] = _dev(ws)
+    xw = torch.zeros(40, 24, dtype=torch.uint8, device=DEV)
+    xw[:, shift:shift + 8] = _dev(xs)
+    got = M.fp8_linear(_codes(x), xw[:, shift:shift + 8], _dev(w), wide[:, shift:shift + 32],
+                       out_dtype=torch.float32)
+    _check_product(got, p, tol, False, False, torch.float32, shift)
+
+
+def test_rows_and_results_past_4_gib():
+    """Codes and results whose places pass 32 bits."""
+    rng = np.random.default_rng(9)
+    x, xs = ref.random_x(rng, 40, 8192)
+    big = torch.zeros(560000, 8192, dtype=torch.uint8, device=DEV)      # 4.6 GB
+    sc = torch.full((560000, 64), 127, dtype=torch.uint8, device=DEV)
+    big[-40:], sc[-40:] = _dev(x), _dev(xs)
+    w, ws = ref.random_w(rng, 256, 8192, False)
+    p, tol = ref.product(ref.row_values(x, xs), ref.weight_values(w, ws, False))
+    rows = torch.arange(560000 - 40, 560000, device=DEV, dtype=torch.int32)
+    offsets = torch.tensor([0, 40], dtype=torch.int32, device=DEV)
+    got = M.expert_linear(big, sc, _codes(w)[None], _scales(ws)[None], offsets, rows=rows)
+    _check_product(got, p, tol, False, False, torch.bfloat16, "rows")
+    one = M.fp8_linear(big, sc, _codes(w)[:64], _scales(ws)[:1])
+    _check_product(one[-40:], p[:, :64], tol[:, :64], False, False, torch.bfloat16, "all rows")
+    del big, sc, one
+    x, xs = ref.random_x(rng, 70000, 128)
+    w, ws = ref.random_w(rng, 16384, 128, False)
+    got = M.fp8_linear(_codes(x), _scales(xs), _codes(w), _scales(ws), out_dtype=torch.float32)
+    assert got.numel() * 4 > 2 ** 32
+    p, tol = ref.product(ref.row_values(x[-9:], xs[-9:]), ref.weight_values(w, ws, False))
+    _check_product(got[-9:], p, tol, False, False, torch.float32, "results")
+
+
+def test_refusals():
+    rng = np.random.default_rng(1)
+    x, xs = ref.random_x(rng, 4, 256)
+    w, ws = ref.random_w(rng, 64, 256, False)
+    x, xs, w, ws = _codes(x), _scales(xs), _codes(w), _scales(ws)
+    bad = [lambda: M.fp8_linear(x.float(), xs, w, ws), lambda: M.fp8_linear(x, xs[:3], w, ws),
+           lambda: M.fp8_linear(x, xs, w[None], ws), lambda: M.fp8_linear(x, xs, w[:, :128], ws),
+           lambda: M.fp8_linear(x, xs, w, ws[:, :1]), lambda: M.fp8_linear(x, xs, w.T, ws),
+           lambda: M.fp8_linear(x, xs, w, ws, activation="relu"),
+           lambda: M.fp8_linear(x, xs, w[:63], ws, activation="swiglu"),
+           lambda: M.fp8_linear(x, xs, w, ws, quantize=True),
+           lambda: M.fp8_linear(x, xs, w, ws, out_dtype=torch.int32),
+           lambda: M.fp8_linear(x, xs, w, ws, out=torch.empty(4, 63, device=DEV)),
+           lambda: M.fp8_linear(x, xs, w, ws, activation="swiglu", quantize=True,
+                                out=torch.empty(4, 32, device=DEV)),
+           lambda: M.fp8_linear(x.cpu(), xs, w, ws), lambda: M.fp8_linear(x, xs.cpu(), w, ws),
+           lambda: M.expert_linear(x, xs, w, ws, torch.zeros(2, dtype=torch.int32, device=DEV)),
+           lambda: M.expert_linear(x, xs, w[None], ws[None], torch.zeros(3, dtype=torch.int32,
+                                                                         device=DEV)),
+           lambda: M.expert_linear(x, xs, w[None], ws[None], torch.zeros(2, device=DEV)),
+           lambda: M.fp8_quantize(x), lambda: M.fp8_quantize(torch.zeros(8, device=DEV)),
+           lambda: M.fp8_pack(torch.zeros(8, 8, device=DEV).T[:, :4]),
+           lambda: M.rms_norm(torch.zeros(2, 8, device=DEV), torch.ones(9, device=DEV)),
+           lambda: M.rms_norm(torch.zeros(2, 8, device=DEV), torch.ones(8, device=DEV), out=False),
+           lambda: M.rms_norm(torch.zeros(2, 8, device=DEV), torch.ones(8, device=DEV),
+                              residual=torch.zeros(1, 8, device=DEV).expand(2, 8)),
+           lambda: M.rms_norm(torch.zeros(2, 8, device=DEV), torch.ones(8, device=DEV),
+                              residual=torch.zeros(2, 8, device=DEV).half()),
+           lambda: M.moe_dispatch(torch.zeros(4, device=DEV), 3),
+           lambda: M.moe_dispatch(torch.zeros(4, 2, dtype=torch.int32, device=DEV), 0),
+           lambda: M.moe_combine(torch.zeros(4, 8, device=DEV), torch.zeros(2, 2, device=DEV),
+                                 torch.zeros(2, 3, dtype=torch.int32, device=DEV))]
+    for i, f in enumerate(bad):
+        with pytest.raises(ValueError):
+            f()
+            pytest.fail(str(i))
+    for f in (lambda: M.rms_norm(torch.zeros(2, 12, device=DEV), torch.ones(12, device=DEV)),
+              lambda: M.fp8_quantize(torch.zeros(2, 16392, device=DEV)),
+              lambda: M.moe_dispatch(torch.zeros(4, 2, dtype=torch.int32, device=DEV), 1025),
+              lambda: M.fp8_linear(x[:, :248].contiguous(), xs, w[:, :248].contiguous(), ws)):
+        with pytest.raises(M.MoEError):
+            f()
+
+
+def test_combine_broadcast_residual():
+    rng = np.random.default_rng(2)
+    y = _rows(rng, 6, 64, torch.bfloat16)
+    r = _rows(rng, 1, 64, torch.bfloat16)
+    slots = torch.arange(6, dtype=torch.int32, device=DEV).view(3, 2)
+    w = torch.rand(3, 2, device=DEV)
+    assert torch.equal(M.moe_combine(y, w, slots, residual=r.expand(3, 64)),
+                       M.moe_combine(y, w, slots, residual=r.repeat(3, 1)))
 
 
 def test_experts_values_out_of_range_are_bounded():
