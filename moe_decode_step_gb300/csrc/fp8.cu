@@ -93,7 +93,7 @@ int encoder(Encode* out) {
 
 int encode_map(Encode fn, CUtensorMap* map, bool nibbles, const void* p, int rank,
                const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
-  const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+  const cuuint32_t one[4] = {1, 1, 1, 1};
   const CUresult r = fn(map, nibbles ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B
                                      : CU_TENSOR_MAP_DATA_TYPE_UINT8,
                         rank, const_cast<void*>(p), dims, strides, box, one,
@@ -107,20 +107,17 @@ int encode_rows(Encode fn, CUtensorMap* map, const moe_fp8_product_t& t, int box
   const cuuint32_t box[2] = {kGemmK, (cuuint32_t)box_rows};
   return encode_map(fn, map, false, t.x, 2, dims, strides, box);
 }
-int encode_weights(Encode fn, CUtensorMap* map, const moe_fp8_product_t& t, bool swiglu,
-                   bool interleaved) {
+int encode_weights(Encode fn, CUtensorMap* map, const moe_fp8_product_t& t, bool swiglu) {
   const bool w4 = t.w_format == MOE_WEIGHTS_MXFP4;
   const cuuint64_t k = t.k, n = t.n, e = t.n_experts, row = t.w_stride;
   const cuuint64_t mat = e > 1 ? (cuuint64_t)t.w_expert_stride : row * n;
-  if (interleaved) {
-    const cuuint64_t dims[5] = {k, 16, 2, n / 32, e};
-    const cuuint64_t strides[4] = {row, row * (n / 2), row * 16, mat};
-    const cuuint32_t box[5] = {kGemmK, 16, 2, 4, 1};
-    return encode_map(fn, map, w4, t.w, 5, dims, strides, box);
+  if (swiglu) {   // 64 gates and their ups
+    const cuuint64_t dims[4] = {k, n / 2, 2, e}, strides[3] = {row, row * (n / 2), mat};
+    const cuuint32_t box[4] = {kGemmK, kGemmRows / 2, 2, 1};
+    return encode_map(fn, map, w4, t.w, 4, dims, strides, box);
   }
-  const cuuint64_t dims[3] = {k, n, e};
-  const cuuint64_t strides[2] = {row, mat};
-  const cuuint32_t box[3] = {kGemmK, swiglu ? 16u : (cuuint32_t)kGemmRows, 1};
+  const cuuint64_t dims[3] = {k, n, e}, strides[2] = {row, mat};
+  const cuuint32_t box[3] = {kGemmK, kGemmRows, 1};
   return encode_map(fn, map, w4, t.w, 3, dims, strides, box);
 }
 
@@ -269,7 +266,6 @@ int moe_fp8_product(void* stream, const moe_fp8_product_t* args) {
   const long long many = t.offsets ? 3 * (((long long)t.n_rows + t.n_experts - 1) / t.n_experts)
                                    : t.n_rows;
   const int tokens = (int)std::min<long long>(kGemmTokens, (std::max(many, 32ll) + 15) / 16 * 16);
-  const bool interleaved = swiglu && t.n % 32 == 0;
   GemmMaps maps;
   if (!t.rows) {
     // tiles of a dense call have one size, but for the last; an expert's any
@@ -281,7 +277,7 @@ int moe_fp8_product(void* stream, const moe_fp8_product_t* args) {
           (rc = encode_rows(fn, &maps.x[n / 16 - 1], t, n / 2)))
         return rc;
   }
-  if ((rc = encode_weights(fn, &maps.w, t, swiglu, interleaved))) return rc;
+  if ((rc = encode_weights(fn, &maps.w, t, swiglu))) return rc;
   GemmArgs a{};
   a.kb = (t.k + kGemmK - 1) / kGemmK;
   a.wide = t.n;
@@ -292,7 +288,6 @@ int moe_fp8_product(void* stream, const moe_fp8_product_t* args) {
   a.experts = t.n_experts;
   a.offsets = t.offsets;
   a.src = t.rows;
-  a.interleaved = interleaved;
   a.x = t.x;
   a.x_stride = t.x_stride;
   a.k = t.k;

@@ -54,7 +54,7 @@ struct GemmShape {
   __host__ __device__ static constexpr int stage(int tokens) {
     return ABYTES + tokens / 2 * kGemmK;   // multiples of 1,024, the swizzle's pattern
   }
-  static constexpr int LIMIT = 227 * 1024 - 18 * 1024;   // beside the static part
+  static constexpr int LIMIT = 227 * 1024 - 22 * 1024;   // beside the static part
   static constexpr int stages(int tokens) {
     const int n = (LIMIT - 1024 - SFSLOTS * SFSLOT) / stage(tokens);
     return n < kGemmMaxStages ? n : kGemmMaxStages;
@@ -72,7 +72,6 @@ struct GemmArgs {
   int stages, splits;
   const int* offsets;        // or null
   const int* src;            // or null
-  int interleaved;           // SwiGLU: gates and ups in one copy
   const uint8_t* x;
   long long x_stride;
   int k;
@@ -102,9 +101,13 @@ struct GemmShared {
   int first[kGemmMaxExperts + 1];     // output row of each expert
   int tiles[kGemmMaxExperts + 1];     // token tiles before each expert
   int warp_scan[kGemmThreads / 32];
-  // 8-bit results, by group of warps: of 64 tokens the largest result of each of the
-  // pair's eight warps, in turn in two places, and the scales' reciprocals
-  float amax[2][2][8][64], inv[2][64];
+  // SwiGLU, by group of warps: four tokens' gates or ups on their way from each warp
+  // to the one that holds the others, in turn in two places;
+  float4 swap[2][4][2][32];
+  // 8 bits: of 64 tokens the largest result of each of the pair's warps that have
+  // them, in turn in two places, and the scales' reciprocals
+  float amax[2][2][4][64];
+  alignas(16) float inv[2][64];
 };
 
 // ---- barriers between the CTAs of a pair ----
@@ -160,16 +163,16 @@ __device__ __forceinline__ void tma_tile_3d(uint32_t dst, const CUtensorMap* map
       "l"(map), "r"(c), "r"(r), "r"(e), "r"(bar)
       : "memory");
 }
-// Gates and ups interleaved: the map's dimensions are (column, row of 16, gate or up,
-// 16 rows, matrix), its box (128, 16, 2, 4, 1).
-__device__ __forceinline__ void tma_tile_5d(uint32_t dst, const CUtensorMap* map, int c, int r16,
+// Gates and their ups: the map's dimensions are (column, row, gate or up, matrix).
+__device__ __forceinline__ void tma_tile_4d(uint32_t dst, const CUtensorMap* map, int c, int r,
                                             int e, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".cta_group::2 [%0], [%1, {%2, %6, %6, %3, %4}], [%5];" ::"r"(dst),
-      "l"(map), "r"(c), "r"(r16), "r"(e), "r"(bar), "r"(0)
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".cta_group::2 [%0], [%1, {%2, %3, %6, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(c), "r"(r), "r"(e), "r"(bar), "r"(0)
       : "memory");
 }
+
 // ---- MMAs of a pair: both CTAs' shared and tensor memory, at the same places ----
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -388,16 +391,10 @@ __device__ __forceinline__ void gemm_copy(const GemmArgs& a, GemmShared& sh, uin
       const uint32_t bar = full + ring.stage * 8, at = base + ring.stage * stage_bytes;
       if (half == 0 && lane == 0) mbar_arrive_expect_tx(&sh.full[ring.stage], bytes);
       __syncwarp();
-      if (!SWIGLU) {
-        if (lane == 0)
-          tma_tile_3d(at, &maps.w, kb * kGemmK, w.n0 + half * kGemmRows, w.expert, bar);
-      } else if (a.interleaved) {
-        // 16 gate rows and 16 up rows in turn: a warp's lanes
-        if (lane == 0)
-          tma_tile_5d(at, &maps.w, kb * kGemmK, (w.n0 + half * 64) >> 4, w.expert, bar);
-      } else if (lane < 8) {
-        tma_tile_3d(at + lane * 16 * kGemmK, &maps.w, kb * kGemmK,
-                    (lane & 1 ? a.n : 0) + w.n0 + half * 64 + (lane >> 1) * 16, w.expert, bar);
+      // (as few copies as can be: each takes the copy engine some 30 ns beside its rows)
+      if (lane == 0) {
+        if (SWIGLU) tma_tile_4d(at, &maps.w, kb * kGemmK, w.n0 + half * 64, w.expert, bar);
+        else tma_tile_3d(at, &maps.w, kb * kGemmK, w.n0 + half * kGemmRows, w.expert, bar);
       }
       if (!a.src && lane == 8)
         tma_tile_2d(at + S::ABYTES, xm, kb * kGemmK, w.row0 + half * (w.N / 2), bar);
@@ -671,15 +668,16 @@ __device__ __forceinline__ void gemm_sums(const GemmArgs& a, uint32_t taddr, uin
   }
 }
 
-// 32 tokens of this thread's output column to out.
+// T tokens of this thread's output column to out.
+template <int T>
 __device__ __forceinline__ void gemm_store(const GemmArgs& a, const GemmTile& w, int c, int col,
-                                           const float (&v)[32]) {
+                                           const float (&v)[T]) {
   const int lane = threadIdx.x & 31;
   if (a.out_dtype == MOE_DTYPE_F32) {
     if (col >= a.n) return;
     char* p = a.out + (long long)(w.row0 + c) * a.out_stride + (long long)col * 4;
 #pragma unroll
-    for (int i = 0; i < 32; ++i, p += a.out_stride)
+    for (int i = 0; i < T; ++i, p += a.out_stride)
       if (c + i < w.rows) *reinterpret_cast<float*>(p) = v[i];
     return;
   }
@@ -690,7 +688,7 @@ __device__ __forceinline__ void gemm_store(const GemmArgs& a, const GemmTile& w,
   const int b0 = lane & 1, b1 = lane >> 1 & 1, b2 = lane >> 2 & 1, col8 = col & ~7;
   char* p = a.out + (long long)(w.row0 + c + (lane & 7)) * a.out_stride + (long long)col8 * 2;
 #pragma unroll
-  for (int i = 0; i < 32; i += 8, p += 8 * a.out_stride) {
+  for (int i = 0; i < T; i += 8, p += 8 * a.out_stride) {
     // columns (col & ~1, + 1) of token 2 j + b0
     uint32_t u[4];
 #pragma unroll
@@ -725,22 +723,34 @@ __device__ __forceinline__ void gemm_store(const GemmArgs& a, const GemmTile& w,
   }
 }
 
-// silu(gate) * up of 32 tokens (in fast functions: their errors are below those of the
-// sums, 3e-7 of their rms at K = 4,096, and no result differs more with exact ones,
-// which took a prompt's gates and ups from 502 to 676 us): lanes below 16 hold gates, the others the ups of
-// the same columns; lane l gets the results of column l & 15, of the tokens 2 i (below
-// 16) or 2 i + 1.
-__device__ __forceinline__ void gemm_swiglu(const float (&v)[32], float* h) {
-  const bool up = (threadIdx.x & 16) != 0;
+// silu(gate) * up of 32 tokens: warps 0 and 1 of a group hold gates, 2 and 3 the ups of
+// the same columns.  The first two get the results of the first 16 tokens, the others
+// of the rest; what each needs of the other goes through shared memory, four tokens
+// at a time, in turn in two places: a warp writes a place again only behind the
+// barrier of the turn between, which the other passes when it has read it.  (Fast
+// functions: their errors are below those of the sums, and no result differs more
+// with exact ones, which took a prompt's gates and ups from 502 to 676 us.)
+__device__ __forceinline__ void gemm_swiglu(GemmShared& sh, int group, int q, const float (&v)[32],
+                                            float* h) {
+  const int lane = threadIdx.x & 31;
+  const bool up = q >= 2;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float x = __shfl_xor_sync(0xffffffffu, up ? v[2 * i] : v[2 * i + 1], 16);
-    const float g = up ? x : v[2 * i], u = up ? v[2 * i + 1] : x;
-    h[i] = __fdividef(g, 1.f + __expf(-g)) * u;
+  for (int i = 0; i < 16; i += 4) {
+    const int b = i >> 2 & 1;
+    sh.swap[group][q][b][lane] = up ? make_float4(v[i], v[i + 1], v[i + 2], v[i + 3])
+                                    : make_float4(v[i + 16], v[i + 17], v[i + 18], v[i + 19]);
+    asm volatile("bar.sync %0, 64;" ::"r"(3 + 2 * group + (q & 1)) : "memory");
+    const float4 o = sh.swap[group][q ^ 2][b][lane];
+    const float x[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float g = up ? x[j] : v[i + j], u = up ? v[i + j + 16] : x[j];
+      h[i + j] = __fdividef(g, 1.f + __expf(-g)) * u;
+    }
   }
 }
 
-// Maxima of 16 values each over 16 lanes: lane l gets value l & 15's.
+// Maxima of 16 values each over the warp: lane l gets value l & 15's.
 __device__ __forceinline__ float gemm_max16(float (&m)[16]) {
   const int lane = threadIdx.x;
 #pragma unroll
@@ -753,7 +763,7 @@ __device__ __forceinline__ float gemm_max16(float (&m)[16]) {
       m[i] = fmaxf(upper ? m[i + w] : m[i], x);
     }
   }
-  return m[0];
+  return fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], 16));
 }
 
 template <bool SWIGLU>
@@ -811,78 +821,74 @@ __device__ __forceinline__ void gemm_results(const GemmArgs& a, GemmShared& sh, 
       }
       continue;
     }
-    const int col = w.n0 + half * 64 + q * 16 + (lane & 15), late = lane >> 4;
+    // this warp's results: column col of the tokens from 16 on, or below (gemm_swiglu)
+    const int col = w.n0 + half * 64 + (q & 1) * 32 + lane, late = q >= 2 ? 16 : 0;
     if (a.out_dtype != MOE_DTYPE_E4M3) {
 #pragma unroll 1
       for (int c = c0; c < w.N; c += step) {
         float v[32], h[16];
         gemm_sums(a, acc, part, rank, c, v);
         if (c + step >= w.N) release();
-        gemm_swiglu(v, h);
-        const int f16 = a.out_dtype == MOE_DTYPE_F16;
+        gemm_swiglu(sh, group, q, v, h);
+        if (dead) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int t = c + 2 * i + late;
-          if (t >= w.rows || col >= a.n) continue;
-          const float x = dead ? nan : h[i];
-          char* p = a.out + (long long)(w.row0 + t) * a.out_stride;
-          if (a.out_dtype == MOE_DTYPE_F32) reinterpret_cast<float*>(p)[col] = x;
-          else reinterpret_cast<uint16_t*>(p)[col] = (uint16_t)pack16(x, 0.f, f16);
+          for (int i = 0; i < 16; ++i) h[i] = nan;
         }
+        gemm_store(a, w, c + late, col, h);
       }
       continue;
     }
-    // 8 bits.  A token's 128 results lie in both CTAs: each warp sends its largest
-    // to both, 64 tokens at a time, whose results stay in registers.  A place is
-    // written again two batches later, which this CTA's warps let the other's
-    // begin only when all have read it (the barrier below).
+    // 8 bits.  A token's 128 results lie in both CTAs, in two warps each: each warp
+    // sends its largest to both CTAs, 64 tokens at a time, whose results stay in
+    // registers.  A place is written again two batches later, which this CTA's warps
+    // let the other's begin only when all have read it (the barrier below).
 #pragma unroll 1
     for (int c1 = c0; c1 < w.N; c1 += step, ++batch) {
       uint64_t* bar = &sh.amax_full[group];
-      const uint32_t slot = smem_addr(sh.amax[group][batch & 1][half * 4 + q]);
+      const uint32_t slot = smem_addr(sh.amax[group][batch & 1][half * 2 + (q & 1)]);
       const uint32_t here = cluster_map(slot, rank), there = cluster_map(slot, rank ^ 1);
       const uint32_t bar_here = cluster_map(smem_addr(bar), rank);
       const uint32_t bar_there = cluster_map(smem_addr(bar), rank ^ 1);
-      if (gt == 0) mbar_arrive_expect_tx(bar, 8 * 64 * 4);
+      if (gt == 0) mbar_arrive_expect_tx(bar, 4 * 64 * 4);
       float h[32];
 #pragma unroll
       for (int c = 0; c < 64; c += 32) {
         float v[32], m[16];
         gemm_sums(a, acc, part, rank, c1 + c, v);   // (past N: nobody's)
-        gemm_swiglu(v, h + c / 2);
+        gemm_swiglu(sh, group, q, v, h + c / 2);
 #pragma unroll
         for (int i = 0; i < 16; ++i) m[i] = col < a.n ? fp8_finite_max(0.f, h[c / 2 + i]) : 0.f;
         const float top = gemm_max16(m);
-        const int t = c + 2 * (lane & 15) + late;
-        st_async_f32(here + t * 4, top, bar_here);
-        st_async_f32(there + t * 4, top, bar_there);
+        const int t = c + late + (lane & 15);
+        // (the lower lanes to this CTA, the others to its peer)
+        st_async_f32((lane < 16 ? here : there) + t * 4, top, lane < 16 ? bar_here : bar_there);
       }
       if (c1 + step >= w.N) release();
       const bool lost = !gemm_wait(bar, batch & 1, sh) || dead;
       if (gt < 64) {
         float amax = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, sh.amax[group][batch & 1][i][gt]);
+        for (int i = 0; i < 4; ++i) amax = fmaxf(amax, sh.amax[group][batch & 1][i][gt]);
         const int e = fp8_block_exp(amax);
         sh.inv[group][gt] = pow2f(-e);
         if (half == 0 && c1 + gt < w.rows)
           a.os[(long long)(w.row0 + c1 + gt) * a.os_stride + (w.n0 >> 7)] = (uint8_t)(e + 127);
       }
       asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
-      const float* inv = sh.inv[group];
 #pragma unroll
       for (int i = 0; i < 32; i += 4) {
         // four tokens' codes of this column, turned among four lanes into four
         // columns' codes of one token
-        const int t0 = 2 * i + late;
-        uint32_t u = f32x2_to_e4m3x2(h[i] * inv[t0], h[i + 1] * inv[t0 + 2]) |
-                     f32x2_to_e4m3x2(h[i + 2] * inv[t0 + 4], h[i + 3] * inv[t0 + 6]) << 16;
+        const int t0 = (i & 16) * 2 + late + (i & 15);
+        const float4 inv = *reinterpret_cast<const float4*>(&sh.inv[group][t0]);
+        uint32_t u = f32x2_to_e4m3x2(h[i] * inv.x, h[i + 1] * inv.y) |
+                     f32x2_to_e4m3x2(h[i + 2] * inv.z, h[i + 3] * inv.w) << 16;
         if (lost) u = 0x7F7F7F7Fu;
         const uint32_t x = __shfl_xor_sync(0xffffffffu, u, 1);
         u = lane & 1 ? __byte_perm(u, x, 0x3715) : __byte_perm(u, x, 0x6240);
         const uint32_t y = __shfl_xor_sync(0xffffffffu, u, 2);
         u = lane & 2 ? __byte_perm(u, y, 0x3276) : __byte_perm(u, y, 0x5410);
-        const int t = c1 + t0 + 2 * (lane & 3), at = col & ~3;
+        const int t = c1 + t0 + (lane & 3), at = col & ~3;
         if (t >= w.rows) continue;
         char* p = a.out + (long long)(w.row0 + t) * a.out_stride + at;
         if (a.vec && at + 3 < a.n) {
@@ -952,7 +958,7 @@ static __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             int r = w.n0 + half * kGemmRows + 32 * i + lane;
-            if (SWIGLU) r = (lane & 16 ? a.n : 0) + w.n0 + half * 64 + 16 * i + (lane & 15);
+            if (SWIGLU) r = (i < 2 ? 0 : a.n) + w.n0 + half * 64 + 32 * (i & 1) + lane;
             r = min(r, a.wide - 1);
             p[i] = a.ws + w.expert * a.ws_expert + (W4 ? r : r >> 7) * a.ws_stride;
           }
