@@ -93,7 +93,7 @@ int encoder(Encode* out) {
 
 int encode_map(Encode fn, CUtensorMap* map, bool nibbles, const void* p, int rank,
                const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
-  const cuuint32_t one[4] = {1, 1, 1, 1};
+  const cuuint32_t one[5] = {1, 1, 1, 1, 1};
   const CUresult r = fn(map, nibbles ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B
                                      : CU_TENSOR_MAP_DATA_TYPE_UINT8,
                         rank, const_cast<void*>(p), dims, strides, box, one,
@@ -101,23 +101,37 @@ int encode_map(Encode fn, CUtensorMap* map, bool nibbles, const void* p, int ran
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
-int encode_rows(Encode fn, CUtensorMap* map, const moe_fp8_product_t& t, int box_rows) {
-  const cuuint64_t dims[2] = {(cuuint64_t)t.k, (cuuint64_t)t.x_rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)t.x_stride};
+// Boxes of one block of 128 columns (zeros past their end), or of two: of K in whole
+// blocks, the block a dimension of its own.
+int encode_rows(Encode fn, CUtensorMap* map, const moe_fp8_product_t& t, int per, int box_rows) {
+  const cuuint64_t k = t.k, rows = t.x_rows, row = t.x_stride;
+  if (per == 2) {
+    const cuuint64_t dims[3] = {kGemmK, rows, k / kGemmK}, strides[2] = {row, kGemmK};
+    const cuuint32_t box[3] = {kGemmK, (cuuint32_t)box_rows, 2};
+    return encode_map(fn, map, false, t.x, 3, dims, strides, box);
+  }
+  const cuuint64_t dims[2] = {k, rows}, strides[1] = {row};
   const cuuint32_t box[2] = {kGemmK, (cuuint32_t)box_rows};
   return encode_map(fn, map, false, t.x, 2, dims, strides, box);
 }
-int encode_weights(Encode fn, CUtensorMap* map, const moe_fp8_product_t& t, bool swiglu) {
+int encode_weights(Encode fn, CUtensorMap* map, const moe_fp8_product_t& t, int per, bool swiglu) {
   const bool w4 = t.w_format == MOE_WEIGHTS_MXFP4;
-  const cuuint64_t k = t.k, n = t.n, e = t.n_experts, row = t.w_stride;
-  const cuuint64_t mat = e > 1 ? (cuuint64_t)t.w_expert_stride : row * n;
-  if (swiglu) {   // 64 gates and their ups
-    const cuuint64_t dims[4] = {k, n / 2, 2, e}, strides[3] = {row, row * (n / 2), mat};
-    const cuuint32_t box[4] = {kGemmK, kGemmRows / 2, 2, 1};
+  const cuuint64_t k = t.k, n = swiglu ? t.n / 2 : t.n, e = t.n_experts, row = t.w_stride;
+  const cuuint64_t mat = e > 1 ? (cuuint64_t)t.w_expert_stride : row * t.n;
+  const cuuint32_t rows = swiglu ? kGemmRows / 2 : kGemmRows, sides = swiglu ? 2 : 1;
+  if (per == 2) {
+    const cuuint64_t dims[5] = {kGemmK, n, sides, k / kGemmK, e};
+    const cuuint64_t strides[4] = {row, row * n, (cuuint64_t)(w4 ? kGemmK / 2 : kGemmK), mat};
+    const cuuint32_t box[5] = {kGemmK, rows, sides, 2, 1};
+    return encode_map(fn, map, w4, t.w, 5, dims, strides, box);
+  }
+  if (swiglu) {
+    const cuuint64_t dims[4] = {k, n, sides, e}, strides[3] = {row, row * n, mat};
+    const cuuint32_t box[4] = {kGemmK, rows, sides, 1};
     return encode_map(fn, map, w4, t.w, 4, dims, strides, box);
   }
   const cuuint64_t dims[3] = {k, n, e}, strides[2] = {row, mat};
-  const cuuint32_t box[3] = {kGemmK, kGemmRows, 1};
+  const cuuint32_t box[3] = {kGemmK, rows, 1};
   return encode_map(fn, map, w4, t.w, 3, dims, strides, box);
 }
 
@@ -129,12 +143,12 @@ long long tiles_at_most(const GemmArgs& a, bool swiglu) {
   return m * ((a.n + cols - 1) / cols);
 }
 
-template <bool W4, bool SWIGLU>
+template <bool W4, bool SWIGLU, int PER>
 int launch_product(GemmArgs a, const GemmMaps& maps, int n_sm, cudaStream_t st) {
-  a.stages = GemmShape::stages(a.tokens);
-  const int smem = GemmShape::smem(a.tokens);
+  a.stages = GemmShape::stages(a.tokens, PER);
+  const int smem = GemmShape::smem(a.tokens, PER);
   // (the most any call asks for: calls of other threads may come between)
-  const cudaError_t e = cudaFuncSetAttribute(fp8_product_kernel<W4, SWIGLU>,
+  const cudaError_t e = cudaFuncSetAttribute(fp8_product_kernel<W4, SWIGLU, PER>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              GemmShape::LIMIT);
   if (e != cudaSuccess) return cuda_fail(e);
@@ -145,7 +159,7 @@ int launch_product(GemmArgs a, const GemmMaps& maps, int n_sm, cudaStream_t st) 
   while (a.splits < kGemmMaxSplits && 2 * a.splits * tiles <= pairs && 2 * a.splits <= groups)
     a.splits *= 2;
   const int grid = 2 * a.splits * (int)std::min<long long>(pairs / a.splits, tiles);
-  return launch(fp8_product_kernel<W4, SWIGLU>, grid, 1, kGemmThreads, smem, 2 * a.splits, st, a,
+  return launch(fp8_product_kernel<W4, SWIGLU, PER>, grid, 1, kGemmThreads, smem, 2 * a.splits, st, a,
                 maps);
 }
 
@@ -266,6 +280,10 @@ int moe_fp8_product(void* stream, const moe_fp8_product_t* args) {
   const long long many = t.offsets ? 3 * (((long long)t.n_rows + t.n_experts - 1) / t.n_experts)
                                    : t.n_rows;
   const int tokens = (int)std::min<long long>(kGemmTokens, (std::max(many, 32ll) + 15) / 16 * 16);
+  // Two blocks a copy where the copy engine bounds: MXFP4 weights, whose rows are
+  // half as long, with few tokens (a verify step's experts 294 us, one by one 316);
+  // elsewhere the coarser ring costs more (a prompt's gates and ups 516 us for 481).
+  const int per = w4 && tokens <= 128 ? 2 : 1;
   GemmMaps maps;
   if (!t.rows) {
     // tiles of a dense call have one size, but for the last; an expert's any
@@ -274,10 +292,10 @@ int moe_fp8_product(void* stream, const moe_fp8_product_t* args) {
     const int last = (t.n_rows - (tiles - 1) * size + 15) / 16 * 16;
     for (int n = 16; n <= tokens; n += 16)
       if ((t.offsets || n == size || n == last) &&
-          (rc = encode_rows(fn, &maps.x[n / 16 - 1], t, n / 2)))
+          (rc = encode_rows(fn, &maps.x[n / 16 - 1], t, per, n / 2)))
         return rc;
   }
-  if ((rc = encode_weights(fn, &maps.w, t, swiglu))) return rc;
+  if ((rc = encode_weights(fn, &maps.w, t, per, swiglu))) return rc;
   GemmArgs a{};
   a.kb = (t.k + kGemmK - 1) / kGemmK;
   a.wide = t.n;
@@ -310,10 +328,13 @@ int moe_fp8_product(void* stream, const moe_fp8_product_t* args) {
   a.xs_align = align(t.x_scales, a.xs_stride);
   a.ws_align = align(t.w_scales, a.ws_stride | a.ws_expert);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (w4) return swiglu ? launch_product<true, true>(a, maps, dev->n_sm, st)
-                        : launch_product<true, false>(a, maps, dev->n_sm, st);
-  return swiglu ? launch_product<false, true>(a, maps, dev->n_sm, st)
-                : launch_product<false, false>(a, maps, dev->n_sm, st);
+  const int n_sm = dev->n_sm;
+  if (per == 2) return swiglu ? launch_product<true, true, 2>(a, maps, n_sm, st)
+                              : launch_product<true, false, 2>(a, maps, n_sm, st);
+  if (w4) return swiglu ? launch_product<true, true, 1>(a, maps, n_sm, st)
+                        : launch_product<true, false, 1>(a, maps, n_sm, st);
+  return swiglu ? launch_product<false, true, 1>(a, maps, n_sm, st)
+                : launch_product<false, false, 1>(a, maps, n_sm, st);
 }
 
 int moe_dispatch(void* stream, const int32_t* idx, int n_tokens, int top_k, int n_experts,

@@ -50,17 +50,19 @@ struct GemmShape {
   // scales of four blocks of K: 4 bytes a row, of MXFP4 weights 4 a row and block
   static constexpr int SFA = 512, SFB = 1024, SFSLOT = 4 * SFA + SFB, SFSLOTS = 3;
   static constexpr int SFCOL = 480;             // tensor memory: accumulators at 0 and 240, scales
-  // the ring of a call whose tiles have at most `tokens`: tiles, then scales
-  __host__ __device__ static constexpr int stage(int tokens) {
-    return ABYTES + tokens / 2 * kGemmK;   // multiples of 1,024, the swizzle's pattern
+  // the ring of a call whose tiles have at most `tokens`: stages of `per` blocks of K
+  // (weights, then tokens; all in multiples of 1,024, the swizzle's pattern), then
+  // the scales
+  __host__ __device__ static constexpr int stage(int tokens, int per) {
+    return per * (ABYTES + tokens / 2 * kGemmK);
   }
   static constexpr int LIMIT = 227 * 1024 - 22 * 1024;   // beside the static part
-  static constexpr int stages(int tokens) {
-    const int n = (LIMIT - 1024 - SFSLOTS * SFSLOT) / stage(tokens);
+  static constexpr int stages(int tokens, int per) {
+    const int n = (LIMIT - 1024 - SFSLOTS * SFSLOT) / stage(tokens, per);
     return n < kGemmMaxStages ? n : kGemmMaxStages;
   }
-  static constexpr int smem(int tokens) {
-    return stages(tokens) * stage(tokens) + SFSLOTS * SFSLOT + 1024;   // (1,024: alignment)
+  static constexpr int smem(int tokens, int per) {
+    return stages(tokens, per) * stage(tokens, per) + SFSLOTS * SFSLOT + 1024;   // (1,024: alignment)
   }
 };
 
@@ -147,15 +149,11 @@ __device__ __forceinline__ void gemm_arrive(uint32_t addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 // ---- TMA; `bar` may be the other CTA's of the pair ----
-__device__ __forceinline__ void tma_tile_2d(uint32_t dst, const CUtensorMap* map, int c, int r,
-                                            uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(map), "r"(c), "r"(r), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void tma_tile_3d(uint32_t dst, const CUtensorMap* map, int c, int r,
+// A block of K at column c: dimensions (column, row[, gate or up], matrix), of x
+// (column, row).  Two blocks from block b on: K is two dimensions, (column, row, gate
+// or up, block, matrix) and (column, row, block).  (No more dimensions than needed: a
+// block a copy with five took a prompt 322 us for 298.)
+__device__ __forceinline__ void tma_weights(uint32_t dst, const CUtensorMap* map, int c, int r,
                                             int e, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
@@ -163,13 +161,36 @@ __device__ __forceinline__ void tma_tile_3d(uint32_t dst, const CUtensorMap* map
       "l"(map), "r"(c), "r"(r), "r"(e), "r"(bar)
       : "memory");
 }
-// Gates and their ups: the map's dimensions are (column, row, gate or up, matrix).
-__device__ __forceinline__ void tma_tile_4d(uint32_t dst, const CUtensorMap* map, int c, int r,
-                                            int e, uint32_t bar) {
+__device__ __forceinline__ void tma_gates_ups(uint32_t dst, const CUtensorMap* map, int c, int r,
+                                              int e, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       ".cta_group::2 [%0], [%1, {%2, %3, %6, %4}], [%5];" ::"r"(dst),
       "l"(map), "r"(c), "r"(r), "r"(e), "r"(bar), "r"(0)
+      : "memory");
+}
+__device__ __forceinline__ void tma_tokens(uint32_t dst, const CUtensorMap* map, int c, int r,
+                                           uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(c), "r"(r), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_weights2(uint32_t dst, const CUtensorMap* map, int r, int b,
+                                             int e, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".cta_group::2 [%0], [%1, {%6, %2, %6, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(r), "r"(b), "r"(e), "r"(bar), "r"(0)
+      : "memory");
+}
+__device__ __forceinline__ void tma_tokens2(uint32_t dst, const CUtensorMap* map, int r, int b,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".cta_group::2 [%0], [%1, {%5, %2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(r), "r"(b), "r"(bar), "r"(0)
       : "memory");
 }
 
@@ -372,32 +393,38 @@ struct GemmRing {
 // ---------------------------------------------------------------------------
 // Copies (warp 0)
 // ---------------------------------------------------------------------------
-template <bool W4, bool SWIGLU>
+template <bool W4, bool SWIGLU, int PER>
 __device__ __forceinline__ void gemm_copy(const GemmArgs& a, GemmShared& sh, uint32_t base,
                                           const GemmMaps& maps, uint32_t rank) {
   using S = GemmShape;
   const int lane = threadIdx.x & 31, half = rank & 1;
-  const uint32_t stage_bytes = S::stage(a.tokens);
+  const uint32_t stage_bytes = S::stage(a.tokens, PER);
   const uint32_t full = cluster_map(smem_addr(sh.full), rank & ~1u);
   GemmRing ring;
   for (GemmWalk<SWIGLU> k(a, sh); k.t < k.tiles; k.t += k.step) {
     const GemmTile w = k.tile(a, sh);
-    // the pair's bytes (nibbles count as the bytes they are read as)
+    // the pair's bytes a block (nibbles count as the bytes they are read as; blocks
+    // past the last are zeros)
     const uint32_t bytes =
         (W4 ? S::ABYTES : 2 * S::ABYTES) + (a.src ? 0u : (uint32_t)w.N * kGemmK);
     const CUtensorMap* xm = &maps.x[w.N / 16 - 1];
-    for (int kb = k.k0; kb < k.k1; ++kb, ring.next(a.stages)) {
+    const int wr = w.n0 + half * (SWIGLU ? 64 : kGemmRows);
+    const int xr = w.row0 + half * (w.N / 2);
+    for (int kb = k.k0; kb < k.k1; kb += PER, ring.next(a.stages)) {
       if (!gemm_wait_warp(&sh.empty[ring.stage], ring.phase ^ 1, sh)) return;
       const uint32_t bar = full + ring.stage * 8, at = base + ring.stage * stage_bytes;
-      if (half == 0 && lane == 0) mbar_arrive_expect_tx(&sh.full[ring.stage], bytes);
+      if (half == 0 && lane == 0) mbar_arrive_expect_tx(&sh.full[ring.stage], PER * bytes);
       __syncwarp();
-      // (as few copies as can be: each takes the copy engine some 30 ns beside its rows)
+      // as few copies as can be: each takes the copy engine some 30 ns beside its rows
       if (lane == 0) {
-        if (SWIGLU) tma_tile_4d(at, &maps.w, kb * kGemmK, w.n0 + half * 64, w.expert, bar);
-        else tma_tile_3d(at, &maps.w, kb * kGemmK, w.n0 + half * kGemmRows, w.expert, bar);
+        if (PER == 2) tma_weights2(at, &maps.w, wr, kb, w.expert, bar);
+        else if (SWIGLU) tma_gates_ups(at, &maps.w, kb * kGemmK, wr, w.expert, bar);
+        else tma_weights(at, &maps.w, kb * kGemmK, wr, w.expert, bar);
       }
-      if (!a.src && lane == 8)
-        tma_tile_2d(at + S::ABYTES, xm, kb * kGemmK, w.row0 + half * (w.N / 2), bar);
+      if (lane == 8 && !a.src) {
+        if (PER == 2) tma_tokens2(at + PER * S::ABYTES, xm, xr, kb, bar);
+        else tma_tokens(at + PER * S::ABYTES, xm, kb * kGemmK, xr, bar);
+      }
     }
   }
   // the last arrivals from the pair's first CTA are in before this one may leave
@@ -406,7 +433,7 @@ __device__ __forceinline__ void gemm_copy(const GemmArgs& a, GemmShared& sh, uin
 }
 
 // ---------------------------------------------------------------------------
-// Rows of x by index (warps 12..14, a block of K each in turn): 4 rows of eight
+// Rows of x by index (warps 12..14, a stage each in turn): 4 rows of eight
 // 16-byte pieces at a time, laid out as the swizzle has them (piece c of row r at c ^
 // (r % 8)).  Columns past K become zeros.  (The copy engine's gather takes it some
 // 50 ns for four rows of 128 bytes: with 130 tokens a tile a block took 0.9 us, and
@@ -414,24 +441,24 @@ __device__ __forceinline__ void gemm_copy(const GemmArgs& a, GemmShared& sh, uin
 // cores: the fence that this takes waits for every copy that its thread has under
 // way, so the threads that copy must not need it (a block then took 0.45 us, however
 // few its rows).
-// A warp waits for a stage's barrier every third use of it only.  It cannot take a
-// phase for the one two before: its last block, three before this one, was let in
-// after all blocks up to the ring's length before that one were done with, and this
-// stage's use two before is among them (rings have more than three stages).
+// A warp may wait for a stage's barrier every third use of it only.  It cannot take a
+// phase for the one two before: its last fill, three before this one, was let in
+// after all fills up to the ring's length before that one were done with, and this
+// stage's use two before is among them (rings have three stages at least).
 // ---------------------------------------------------------------------------
 constexpr int kGemmLoaders = 3;   // warps
 
-template <bool SWIGLU>
+template <bool SWIGLU, int PER>
 __device__ __forceinline__ void gemm_load_rows(const GemmArgs& a, GemmShared& sh, uint32_t base,
                                                uint32_t rank) {
   using S = GemmShape;
   const int lane = threadIdx.x & 31, half = rank & 1, sub = lane >> 3, c = lane & 7;
-  const uint32_t stage_bytes = S::stage(a.tokens);
+  const uint32_t stage_bytes = S::stage(a.tokens, PER);
   // even passes' rows are 0..3 of 8, odd ones' 4..7
-  const uint32_t to0 = base + S::ABYTES + sub * kGemmK + ((c ^ sub) << 4);
-  const uint32_t to1 = base + S::ABYTES + (4 + sub) * kGemmK + ((c ^ (4 + sub)) << 4);
+  const uint32_t to0 = base + PER * S::ABYTES + sub * kGemmK + ((c ^ sub) << 4);
+  const uint32_t to1 = base + PER * S::ABYTES + (4 + sub) * kGemmK + ((c ^ (4 + sub)) << 4);
   GemmRing ring;
-  int turn = (int)(threadIdx.x >> 5) - 12;   // blocks until this warp's next one
+  int turn = (int)(threadIdx.x >> 5) - 12;   // fills until this warp's next one
   for (GemmWalk<SWIGLU> k(a, sh); k.t < k.tiles; k.t += k.step) {
     const GemmTile w = k.tile(a, sh);
     const int rows = w.N / 2;   // a multiple of 8
@@ -439,28 +466,31 @@ __device__ __forceinline__ void gemm_load_rows(const GemmArgs& a, GemmShared& sh
 #pragma unroll
     for (int i = 0; i < kGemmTokens / 8; ++i)
       if (4 * i < rows) src[i] = gemm_source(a, w, half * rows + 4 * i + sub);
-    for (int kb = k.k0; kb < k.k1; ++kb, ring.next(a.stages)) {
+    for (int kb = k.k0; kb < k.k1; kb += PER, ring.next(a.stages)) {
       if (turn-- > 0) continue;
       turn = kGemmLoaders - 1;
       if (!gemm_wait_warp(&sh.empty[ring.stage], ring.phase ^ 1, sh)) {
         asm volatile("cp.async.wait_all;" ::: "memory");
         return;
       }
-      const uint32_t at = ring.stage * stage_bytes;
-      const bool in = kb * kGemmK + c * 16 < a.k;   // (k is a multiple of 16)
-      const uint8_t* x = a.x + (in ? kb * kGemmK + c * 16 : 0);
-      const uint32_t size = in ? 16 : 0;
+#pragma unroll 1
+      for (int b = 0; b < PER && kb + b < k.k1; ++b) {
+        const uint32_t at = ring.stage * stage_bytes + b * (rows * kGemmK);
+        const bool in = (kb + b) * kGemmK + c * 16 < a.k;   // (k is a multiple of 16)
+        const uint8_t* x = a.x + (in ? (kb + b) * kGemmK + c * 16 : 0);
+        const uint32_t size = in ? 16 : 0;
 #pragma unroll
-      for (int i = 0; i < kGemmTokens / 8; i += 2) {
-        if (4 * i >= rows) break;
-        const uint32_t to = at + i / 2 * 8 * kGemmK;
-        asm volatile("" : "+r"(src[i]), "+r"(src[i + 1]));   // (offsets are not kept: registers)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to0 + to),
-                     "l"(x + (uint64_t)src[i] * (uint32_t)a.x_stride), "r"(size)
-                     : "memory");
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to1 + to),
-                     "l"(x + (uint64_t)src[i + 1] * (uint32_t)a.x_stride), "r"(size)
-                     : "memory");
+        for (int i = 0; i < kGemmTokens / 8; i += 2) {
+          if (4 * i >= rows) break;
+          const uint32_t to = at + i / 2 * 8 * kGemmK;
+          asm volatile("" : "+r"(src[i]), "+r"(src[i + 1]));   // (offsets are not kept: registers)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to0 + to),
+                       "l"(x + (uint64_t)src[i] * (uint32_t)a.x_stride), "r"(size)
+                       : "memory");
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to1 + to),
+                       "l"(x + (uint64_t)src[i + 1] * (uint32_t)a.x_stride), "r"(size)
+                       : "memory");
+        }
       }
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
                        smem_addr(&sh.loaded[ring.stage]))
@@ -470,13 +500,13 @@ __device__ __forceinline__ void gemm_load_rows(const GemmArgs& a, GemmShared& sh
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// All blocks of K that have arrived, up to four, behind one fence.
-template <bool SWIGLU>
+// All stages that have arrived, up to four, behind one fence.
+template <bool SWIGLU, int PER>
 __device__ __forceinline__ void gemm_hand_over(const GemmArgs& a, GemmShared& sh, uint32_t rank) {
   const int lane = threadIdx.x & 31;
   const uint32_t full = cluster_map(smem_addr(sh.full), rank & ~1u);
   const GemmWalk<SWIGLU> k(a, sh);
-  long long left = k.t < k.tiles ? (long long)((k.tiles - 1 - k.t) / k.step + 1) * (k.k1 - k.k0) : 0;
+  long long left = k.t < k.tiles ? (long long)((k.tiles - 1 - k.t) / k.step + 1) * ((k.k1 - k.k0 + PER - 1) / PER) : 0;
   GemmRing ring;
   while (left > 0) {
     if (!gemm_wait_warp(&sh.loaded[ring.stage], ring.phase, sh)) return;
@@ -595,13 +625,13 @@ __device__ __forceinline__ void gemm_scales(const GemmArgs& a, GemmShared& sh, u
 // choice of the lane, a vote on every wait, an early test of the next barrier a
 // block) it took 640, without the last two 490, so 230.  Where a wait ran out, the
 // others end at once and what is issued is garbage of no effect.
-template <bool W4, bool SWIGLU>
+template <bool W4, bool SWIGLU, int PER>
 __device__ __forceinline__ void gemm_mma(const GemmArgs& a, GemmShared& sh, uint32_t base,
                                          uint32_t rank) {
   using S = GemmShape;
-  const uint32_t stage_bytes = S::stage(a.tokens), sf = base + a.stages * stage_bytes;
+  const uint32_t stage_bytes = S::stage(a.tokens, PER), sf = base + a.stages * stage_bytes;
   const uint16_t both = (uint16_t)(3u << (rank & ~1u));
-  const uint64_t da0 = umma_desc_sw128(base), db0 = umma_desc_sw128(base + S::ABYTES);
+  const uint64_t da0 = umma_desc_sw128(base), db0 = umma_desc_sw128(base + PER * S::ABYTES);
   const uint64_t ds0 = umma_desc(sf, 0, 128);
   GemmRing ring, sr;
   const uint32_t tm = sh.tmem;
@@ -609,6 +639,7 @@ __device__ __forceinline__ void gemm_mma(const GemmArgs& a, GemmShared& sh, uint
   for (GemmWalk<SWIGLU> k(a, sh); k.t < k.tiles; k.t += k.step, ++n) {
     const GemmTile w = k.tile(a, sh);
     const uint32_t acc = tm + (n & 1) * kGemmTokens, id = umma_idesc_mxf8(W4 ? 5 : 0, 0, 0, w.N);
+    const uint64_t block_b = w.N / 2 * kGemmK >> 4;
     gemm_wait(&sh.acc_empty[n & 1], (n >> 1 & 1) ^ 1, sh);
     if (elect_one()) {
       for (int kb = k.k0; kb < k.k1; kb += 4) {
@@ -625,16 +656,21 @@ __device__ __forceinline__ void gemm_mma(const GemmArgs& a, GemmShared& sh, uint
           // scales of this block (MXFP4 weights) or these four, in turn in two places
           const uint32_t sfa = tm + S::SFCOL + 4 * (W4 ? b & 1 : j4);
           const uint64_t off = ring.stage * (stage_bytes >> 4);
-          gemm_wait(&sh.full[ring.stage], ring.phase, sh);
-          tc_fence_after();
+          const uint32_t in = b & (PER - 1);   // the block in its stage
+          const uint64_t da = da0 + off + in * (S::ABYTES >> 4), db = db0 + off + in * block_b;
+          if (in == 0) {
+            gemm_wait(&sh.full[ring.stage], ring.phase, sh);
+            tc_fence_after();
+          }
           if (W4) umma_sf_copy_pair(sfa, ds + b * (S::SFA >> 4));
 #pragma unroll
           for (uint32_t j = 0; j < 4; ++j)
-            umma_mxf8_pair(acc, da0 + off + 2 * j, db0 + off + 2 * j,
-                           id | (W4 ? j : b) << 29 | b << 4, sfa, sfb,
+            umma_mxf8_pair(acc, da + 2 * j, db + 2 * j, id | (W4 ? j : b) << 29 | b << 4, sfa, sfb,
                            (kb > k.k0) || b > 0 || j > 0);
-          umma_commit_pair(&sh.empty[ring.stage], both);
-          ring.next(a.stages);
+          if (in + 1 == PER || kb + (int)b + 1 >= k.k1) {
+            umma_commit_pair(&sh.empty[ring.stage], both);
+            ring.next(a.stages);
+          }
         }
         umma_commit_pair(&sh.sf_empty[sr.stage], both);
         sr.next(S::SFSLOTS);
@@ -904,7 +940,8 @@ __device__ __forceinline__ void gemm_results(const GemmArgs& a, GemmShared& sh, 
   }
 }
 
-template <bool W4, bool SWIGLU>
+// PER: blocks of K a stage.
+template <bool W4, bool SWIGLU, int PER>
 static __global__ void __launch_bounds__(kGemmThreads, 1)
     fp8_product_kernel(const __grid_constant__ GemmArgs a,
                        const __grid_constant__ GemmMaps maps) {
@@ -946,12 +983,12 @@ static __global__ void __launch_bounds__(kGemmThreads, 1)
   tc_fence_after();
 
   if (warp == 0) {
-    gemm_copy<W4, SWIGLU>(a, sh, base, maps, rank);
+    gemm_copy<W4, SWIGLU, PER>(a, sh, base, maps, rank);
   } else if (warp == 1) {
-    if ((rank & 1) == 0) gemm_mma<W4, SWIGLU>(a, sh, base, rank);
+    if ((rank & 1) == 0) gemm_mma<W4, SWIGLU, PER>(a, sh, base, rank);
   } else if (warp == 2) {
     gemm_scales<4, W4, SWIGLU>(
-        a, sh, smem + a.stages * S::stage(a.tokens), rank, a.ws_align,
+        a, sh, smem + a.stages * S::stage(a.tokens, PER), rank, a.ws_align,
         [&](GemmWalk<SWIGLU>& k, const uint8_t* (&p)[4]) {
           const GemmTile w = k.tile(a, sh);
           const int lane = threadIdx.x & 31, half = rank & 1;
@@ -965,7 +1002,7 @@ static __global__ void __launch_bounds__(kGemmThreads, 1)
         });
   } else if (warp == 3) {
     gemm_scales<8, false, SWIGLU>(
-        a, sh, smem + a.stages * S::stage(a.tokens) + 4 * S::SFA, rank, a.xs_align,
+        a, sh, smem + a.stages * S::stage(a.tokens, PER) + 4 * S::SFA, rank, a.xs_align,
         [&](GemmWalk<SWIGLU>& k, const uint8_t* (&p)[8]) {
           const GemmTile w = k.tile(a, sh);
 #pragma unroll
@@ -977,8 +1014,8 @@ static __global__ void __launch_bounds__(kGemmThreads, 1)
   } else if (warp < 12) {
     gemm_results<SWIGLU>(a, sh, smem, rank);
   } else if (a.src) {
-    if (warp < 15) gemm_load_rows<SWIGLU>(a, sh, base, rank);
-    else gemm_hand_over<SWIGLU>(a, sh, rank);
+    if (warp < 15) gemm_load_rows<SWIGLU, PER>(a, sh, base, rank);
+    else gemm_hand_over<SWIGLU, PER>(a, sh, rank);
   }
   pdl_launch_dependents();
   __syncwarp();
