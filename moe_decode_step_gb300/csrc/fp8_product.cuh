@@ -408,22 +408,24 @@ __device__ __forceinline__ void gemm_copy(const GemmArgs& a, GemmShared& sh, uin
     const uint32_t bytes =
         (W4 ? S::ABYTES : 2 * S::ABYTES) + (a.src ? 0u : (uint32_t)w.N * kGemmK);
     const CUtensorMap* xm = &maps.x[w.N / 16 - 1];
-    const int wr = w.n0 + half * (SWIGLU ? 64 : kGemmRows);
-    const int xr = w.row0 + half * (w.N / 2);
     for (int kb = k.k0; kb < k.k1; kb += PER, ring.next(a.stages)) {
       if (!gemm_wait_warp(&sh.empty[ring.stage], ring.phase ^ 1, sh)) return;
       const uint32_t bar = full + ring.stage * 8, at = base + ring.stage * stage_bytes;
       if (half == 0 && lane == 0) mbar_arrive_expect_tx(&sh.full[ring.stage], PER * bytes);
       __syncwarp();
       // as few copies as can be: each takes the copy engine some 30 ns beside its rows
-      if (lane == 0) {
-        if (PER == 2) tma_weights2(at, &maps.w, wr, kb, w.expert, bar);
-        else if (SWIGLU) tma_gates_ups(at, &maps.w, kb * kGemmK, wr, w.expert, bar);
-        else tma_weights(at, &maps.w, kb * kGemmK, wr, w.expert, bar);
-      }
-      if (lane == 8 && !a.src) {
-        if (PER == 2) tma_tokens2(at + PER * S::ABYTES, xm, xr, kb, bar);
-        else tma_tokens(at + PER * S::ABYTES, xm, kb * kGemmK, xr, bar);
+      if constexpr (PER == 2) {
+        if (lane == 0)
+          tma_weights2(at, &maps.w, w.n0 + half * (SWIGLU ? 64 : kGemmRows), kb, w.expert, bar);
+        if (lane == 8 && !a.src)
+          tma_tokens2(at + PER * S::ABYTES, xm, w.row0 + half * (w.N / 2), kb, bar);
+      } else {
+        if (lane == 0) {
+          if (SWIGLU) tma_gates_ups(at, &maps.w, kb * kGemmK, w.n0 + half * 64, w.expert, bar);
+          else tma_weights(at, &maps.w, kb * kGemmK, w.n0 + half * kGemmRows, w.expert, bar);
+        }
+        if (!a.src && lane == 8)
+          tma_tokens(at + S::ABYTES, xm, kb * kGemmK, w.row0 + half * (w.N / 2), bar);
       }
     }
   }
@@ -639,7 +641,6 @@ __device__ __forceinline__ void gemm_mma(const GemmArgs& a, GemmShared& sh, uint
   for (GemmWalk<SWIGLU> k(a, sh); k.t < k.tiles; k.t += k.step, ++n) {
     const GemmTile w = k.tile(a, sh);
     const uint32_t acc = tm + (n & 1) * kGemmTokens, id = umma_idesc_mxf8(W4 ? 5 : 0, 0, 0, w.N);
-    const uint64_t block_b = w.N / 2 * kGemmK >> 4;
     gemm_wait(&sh.acc_empty[n & 1], (n >> 1 & 1) ^ 1, sh);
     if (elect_one()) {
       for (int kb = k.k0; kb < k.k1; kb += 4) {
@@ -656,9 +657,12 @@ __device__ __forceinline__ void gemm_mma(const GemmArgs& a, GemmShared& sh, uint
           // scales of this block (MXFP4 weights) or these four, in turn in two places
           const uint32_t sfa = tm + S::SFCOL + 4 * (W4 ? b & 1 : j4);
           const uint64_t off = ring.stage * (stage_bytes >> 4);
-          const uint32_t in = b & (PER - 1);   // the block in its stage
-          const uint64_t da = da0 + off + in * (S::ABYTES >> 4), db = db0 + off + in * block_b;
-          if (in == 0) {
+          uint64_t da = da0 + off, db = db0 + off;
+          if constexpr (PER == 2) {   // the second block of a stage
+            da += (b & 1) * (S::ABYTES >> 4);
+            db += (b & 1) * (w.N / 2 * kGemmK >> 4);
+          }
+          if (PER == 1 || (b & 1) == 0) {
             gemm_wait(&sh.full[ring.stage], ring.phase, sh);
             tc_fence_after();
           }
@@ -667,7 +671,7 @@ __device__ __forceinline__ void gemm_mma(const GemmArgs& a, GemmShared& sh, uint
           for (uint32_t j = 0; j < 4; ++j)
             umma_mxf8_pair(acc, da + 2 * j, db + 2 * j, id | (W4 ? j : b) << 29 | b << 4, sfa, sfb,
                            (kb > k.k0) || b > 0 || j > 0);
-          if (in + 1 == PER || kb + (int)b + 1 >= k.k1) {
+          if (PER == 1 || (b & 1) || kb + (int)b + 1 >= k.k1) {
             umma_commit_pair(&sh.empty[ring.stage], both);
             ring.next(a.stages);
           }
