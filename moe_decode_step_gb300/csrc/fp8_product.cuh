@@ -398,8 +398,6 @@ __device__ __forceinline__ void gemm_copy(const GemmArgs& a, GemmShared& sh, uin
                                           const GemmMaps& maps, uint32_t rank) {
   using S = GemmShape;
   const int lane = threadIdx.x & 31, half = rank & 1;
-#define wr (w.n0 + half * (SWIGLU ? 64 : kGemmRows))
-#define xr (w.row0 + half * (w.N / 2))
   const uint32_t stage_bytes = S::stage(a.tokens, PER);
   const uint32_t full = cluster_map(smem_addr(sh.full), rank & ~1u);
   GemmRing ring;
@@ -416,14 +414,18 @@ __device__ __forceinline__ void gemm_copy(const GemmArgs& a, GemmShared& sh, uin
       if (half == 0 && lane == 0) mbar_arrive_expect_tx(&sh.full[ring.stage], PER * bytes);
       __syncwarp();
       // as few copies as can be: each takes the copy engine some 30 ns beside its rows
-      if (lane == 0) {
-        if (PER == 2) tma_weights2(at, &maps.w, wr, kb, w.expert, bar);
-        else if (SWIGLU) tma_gates_ups(at, &maps.w, kb * kGemmK, wr, w.expert, bar);
-        else tma_weights(at, &maps.w, kb * kGemmK, wr, w.expert, bar);
-      }
-      if (lane == 8 && !a.src) {
-        if (PER == 2) tma_tokens2(at + PER * S::ABYTES, xm, xr, kb, bar);
-        else tma_tokens(at + PER * S::ABYTES, xm, kb * kGemmK, xr, bar);
+      if constexpr (PER == 2) {
+        if (lane == 0)
+          tma_weights2(at, &maps.w, w.n0 + half * (SWIGLU ? 64 : kGemmRows), kb, w.expert, bar);
+        if (lane == 8 && !a.src)
+          tma_tokens2(at + PER * S::ABYTES, xm, w.row0 + half * (w.N / 2), kb, bar);
+      } else {
+        if (lane == 0) {
+          if (SWIGLU) tma_gates_ups(at, &maps.w, kb * kGemmK, w.n0 + half * 64, w.expert, bar);
+          else tma_weights(at, &maps.w, kb * kGemmK, w.n0 + half * kGemmRows, w.expert, bar);
+        }
+        if (!a.src && lane == 8)
+          tma_tokens(at + S::ABYTES, xm, kb * kGemmK, w.row0 + half * (w.N / 2), bar);
       }
     }
   }
