@@ -349,20 +349,23 @@ struct GemmWalk {
       expert += 32;
     }
     const int mt = sh.tiles[expert + 1] - sh.tiles[expert];
-    unsigned in = t - (unsigned)sh.tiles[expert] * nt;
-    int g = 0, gm = mt;
-    if (mt > kGemmGroup) {
-      const unsigned pass = kGemmGroup * nt;
-      g = in / pass;
-      in -= g * pass;
-      gm = min(kGemmGroup, mt - g * kGemmGroup);
-    }
-    const unsigned n = in / (unsigned)gm;
-    const int m = g * kGemmGroup + (int)(in - n * gm);
-    // an expert's tokens in equal parts, none of them empty: (mt - 1) * size <=
-    // (mt - 1) * a.tokens < rows
     const int s = sh.first[expert], rows = sh.first[expert + 1] - s;
-    const int size = (int)(((unsigned)(rows + mt - 1) / (unsigned)mt + 15) & ~15u);
+    unsigned in = t - (unsigned)sh.tiles[expert] * nt, n = in;
+    int m = 0, size = (rows + 15) & ~15;
+    if (mt > 1) {
+      int g = 0, gm = mt;
+      if (mt > kGemmGroup) {
+        const unsigned pass = kGemmGroup * nt;
+        g = in / pass;
+        in -= g * pass;
+        gm = min(kGemmGroup, mt - g * kGemmGroup);
+      }
+      n = in / (unsigned)gm;
+      m = g * kGemmGroup + (int)(in - n * gm);
+      // an expert's tokens in equal parts, none of them empty: (mt - 1) * size <=
+      // (mt - 1) * a.tokens < rows
+      size = (int)(((unsigned)(rows + mt - 1) / (unsigned)mt + 15) & ~15u);
+    }
     GemmTile r;
     r.expert = expert;
     r.row0 = s + m * size;
@@ -459,15 +462,34 @@ __device__ __forceinline__ void gemm_load_rows(const GemmArgs& a, GemmShared& sh
   // even passes' rows are 0..3 of 8, odd ones' 4..7
   const uint32_t to0 = base + PER * S::ABYTES + sub * kGemmK + ((c ^ sub) << 4);
   const uint32_t to1 = base + PER * S::ABYTES + (4 + sub) * kGemmK + ((c ^ (4 + sub)) << 4);
+  // the next tile's rows are read ahead (behind the copies under way they took 3 us a
+  // tile)
+  int ahead[4] = {};
+  auto read_rows = [&](const GemmTile& w) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (32 * i + lane < w.N / 2) ahead[i] = gemm_source(a, w, half * (w.N / 2) + 32 * i + lane);
+  };
   GemmRing ring;
   int turn = (int)(threadIdx.x >> 5) - 12;   // fills until this warp's next one
-  for (GemmWalk<SWIGLU> k(a, sh); k.t < k.tiles; k.t += k.step) {
-    const GemmTile w = k.tile(a, sh);
+  GemmWalk<SWIGLU> k(a, sh);
+  GemmTile next{};
+  if (k.t < k.tiles) {
+    next = k.tile(a, sh);
+    read_rows(next);
+  }
+  while (k.t < k.tiles) {
+    const GemmTile w = next;
     const int rows = w.N / 2;   // a multiple of 8
     unsigned src[kGemmTokens / 8];
 #pragma unroll
     for (int i = 0; i < kGemmTokens / 8; ++i)
-      if (4 * i < rows) src[i] = gemm_source(a, w, half * rows + 4 * i + sub);
+      src[i] = __shfl_sync(0xffffffffu, ahead[i / 8], i % 8 * 4 + sub);
+    k.t += k.step;
+    if (k.t < k.tiles) {
+      next = k.tile(a, sh);
+      read_rows(next);
+    }
     for (int kb = k.k0; kb < k.k1; kb += PER, ring.next(a.stages)) {
       if (turn-- > 0) continue;
       turn = kGemmLoaders - 1;
@@ -721,10 +743,18 @@ __device__ __forceinline__ void gemm_store(const GemmArgs& a, const GemmTile& w,
       if (c + i < w.rows) *reinterpret_cast<float*>(p) = v[i];
     return;
   }
+  const int f16 = a.out_dtype == MOE_DTYPE_F16;
+  if (!a.vec) {   // rows at odd places: a warp's columns of a token side by side
+    char* p = a.out + (long long)(w.row0 + c) * a.out_stride + (long long)col * 2;
+#pragma unroll
+    for (int i = 0; i < T; ++i, p += a.out_stride)
+      if (c + i < w.rows && col < a.n)
+        *reinterpret_cast<uint16_t*>(p) = (uint16_t)pack16(v[i], 0.f, f16);
+    return;
+  }
   // eight tokens of eight lanes' columns are turned among the lanes, so that each
   // stores eight columns of one token (16 bytes; by 4 bytes a lane the stores
   // took as long as a tile of K = 2,048: 692 us for 408 without them)
-  const int f16 = a.out_dtype == MOE_DTYPE_F16;
   const int b0 = lane & 1, b1 = lane >> 1 & 1, b2 = lane >> 2 & 1, col8 = col & ~7;
   char* p = a.out + (long long)(w.row0 + c + (lane & 7)) * a.out_stride + (long long)col8 * 2;
 #pragma unroll
@@ -751,7 +781,7 @@ __device__ __forceinline__ void gemm_store(const GemmArgs& a, const GemmTile& w,
     const uint32_t x1 = __shfl_xor_sync(0xffffffffu, b2 ? s[1] : s[3], 4);
     const uint4 o = b2 ? make_uint4(x0, x1, s[2], s[3]) : make_uint4(s[0], s[1], x0, x1);
     if (c + i + (lane & 7) >= w.rows) continue;
-    if (a.vec && col8 + 7 < a.n) {
+    if (col8 + 7 < a.n) {
       *reinterpret_cast<uint4*>(p) = o;
     } else {
       const uint32_t t[4] = {o.x, o.y, o.z, o.w};
@@ -822,8 +852,9 @@ __device__ __forceinline__ void gemm_results(const GemmArgs& a, GemmShared& sh, 
     if (!gemm_dead(sh)) gemm_wait(&sh.acc_full[n & 1], n >> 1 & 1, sh);   // (dead: NaN)
     tc_fence_after();
     const uint32_t acc = tm + (n & 1) * kGemmTokens;
-    // tokens go to splits and groups in turn, `unit` at a time
-    int unit = 32, c0 = 32 * (group * a.splits + split);
+    // tokens go to splits and groups in turn, `unit` at a time; the groups begin in
+    // turn too (a tile may have a unit only)
+    int unit = 32, c0 = 32 * ((group ^ (n & 1)) * a.splits + split);
     if (SWIGLU && a.out_dtype == MOE_DTYPE_E4M3) unit = 64, c0 *= 2;
     const int step = 2 * unit * a.splits;
     if (a.splits > 1) {
@@ -924,6 +955,13 @@ __device__ __forceinline__ void gemm_results(const GemmArgs& a, GemmShared& sh, 
         uint32_t u = f32x2_to_e4m3x2(h[i] * inv.x, h[i + 1] * inv.y) |
                      f32x2_to_e4m3x2(h[i + 2] * inv.z, h[i + 3] * inv.w) << 16;
         if (lost) u = 0x7F7F7F7Fu;
+        if (!a.vec) {   // rows at odd places: a warp's columns of a token side by side
+          char* p = a.out + (long long)(w.row0 + c1 + t0) * a.out_stride + col;
+#pragma unroll
+          for (int j = 0; j < 4; ++j, p += a.out_stride)
+            if (c1 + t0 + j < w.rows && col < a.n) *p = (char)(u >> (8 * j));
+          continue;
+        }
         const uint32_t x = __shfl_xor_sync(0xffffffffu, u, 1);
         u = lane & 1 ? __byte_perm(u, x, 0x3715) : __byte_perm(u, x, 0x6240);
         const uint32_t y = __shfl_xor_sync(0xffffffffu, u, 2);
@@ -931,7 +969,7 @@ __device__ __forceinline__ void gemm_results(const GemmArgs& a, GemmShared& sh, 
         const int t = c1 + t0 + (lane & 3), at = col & ~3;
         if (t >= w.rows) continue;
         char* p = a.out + (long long)(w.row0 + t) * a.out_stride + at;
-        if (a.vec && at + 3 < a.n) {
+        if (at + 3 < a.n) {
           *reinterpret_cast<uint32_t*>(p) = u;
         } else {
 #pragma unroll
