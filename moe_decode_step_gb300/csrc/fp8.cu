@@ -159,8 +159,8 @@ int launch_product(GemmArgs a, const GemmMaps& maps, int n_sm, cudaStream_t st) 
   while (a.splits < kGemmMaxSplits && 2 * a.splits * tiles <= pairs && 2 * a.splits <= groups)
     a.splits *= 2;
   const int grid = 2 * a.splits * (int)std::min<long long>(pairs / a.splits, tiles);
-  return launch(fp8_product_kernel<W4, SWIGLU, PER>, grid, 1, kGemmThreads, smem, 2 * a.splits, st, a,
-                maps);
+  return launch(fp8_product_kernel<W4, SWIGLU, PER>, grid, 1, kGemmThreads, smem, 2 * a.splits, st,
+                a, maps);
 }
 
 template <int WARPS, int ITER>
@@ -242,9 +242,10 @@ int moe_fp8_pack(void* stream, const void* w, int dtype, int64_t n_mat, int64_t 
   if (rc) return rc;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const unsigned grid = (unsigned)(blocks * n_mat);
-  if (dtype == MOE_DTYPE_F32) fp8_pack_kernel<MOE_DTYPE_F32><<<grid, 256, 0, st>>>(w, n, k, codes, scales);
-  else if (dtype == MOE_DTYPE_F16) fp8_pack_kernel<MOE_DTYPE_F16><<<grid, 256, 0, st>>>(w, n, k, codes, scales);
-  else fp8_pack_kernel<MOE_DTYPE_BF16><<<grid, 256, 0, st>>>(w, n, k, codes, scales);
+  auto kernel = dtype == MOE_DTYPE_F32   ? fp8_pack_kernel<MOE_DTYPE_F32>
+                : dtype == MOE_DTYPE_F16 ? fp8_pack_kernel<MOE_DTYPE_F16>
+                                         : fp8_pack_kernel<MOE_DTYPE_BF16>;
+  kernel<<<grid, 256, 0, st>>>(w, n, k, codes, scales);
   return end();
 }
 
@@ -260,13 +261,14 @@ int moe_fp8_product(void* stream, const moe_fp8_product_t* args) {
     return MOE_ERR_INVALID_ARG;
   if (t.n_rows == 0) return MOE_OK;
   if (!t.x || !t.x_scales || !t.w || !t.w_scales || !t.out || (codes && !t.out_scales) ||
-      t.x_rows == 0 || t.x_stride < t.k ||
-      t.w_stride < (w4 ? t.k / 2 : t.k) || overlap(t.n_rows, t.out_stride, swiglu ? t.n / 2 : t.n) ||
+      t.x_rows == 0 || t.x_stride < t.k || t.w_stride < (w4 ? t.k / 2 : t.k) ||
+      overlap(t.n_rows, t.out_stride, swiglu ? t.n / 2 : t.n) ||
       (codes && overlap(t.n_rows, t.out_scales_stride, (t.n / 2 + 127) / 128)))
     return MOE_ERR_INVALID_ARG;
   const int unit = w4 ? 32 : 16, size = codes ? 1 : t.out_dtype == MOE_DTYPE_F32 ? 4 : 2;
   if (t.k % (w4 ? 128 : 16) || t.n_experts > kGemmMaxExperts || misaligned(t.x, 16) ||
-      (t.x_stride & 15) || t.x_stride > INT32_MAX || misaligned(t.w, unit) || ((t.w_stride | t.w_expert_stride) & (unit - 1)) ||
+      (t.x_stride & 15) || t.x_stride > INT32_MAX || misaligned(t.w, unit) ||
+      ((t.w_stride | t.w_expert_stride) & (unit - 1)) ||
       t.n_rows > INT32_MAX - 256 || t.n > INT32_MAX - 256 || t.k > INT32_MAX - kGemmK ||
       misaligned(t.out, size))
     return MOE_ERR_UNSUPPORTED;
@@ -288,7 +290,7 @@ int moe_fp8_product(void* stream, const moe_fp8_product_t* args) {
   if (!t.rows) {
     // tiles of a dense call have one size, but for the last; an expert's any
     const int tiles = (t.n_rows + tokens - 1) / tokens;
-    const int size = ((t.n_rows + tiles - 1) / tiles + 15) / 16 * 16;
+    const int size = (int)(((long long)t.n_rows + tiles - 1) / tiles + 15) / 16 * 16;
     const int last = (t.n_rows - (tiles - 1) * size + 15) / 16 * 16;
     for (int n = 16; n <= tokens; n += 16)
       if ((t.offsets || n == size || n == last) &&

@@ -118,7 +118,8 @@ def rms_norm(x, gamma, residual=None, eps=1e-6, out=True, quantize=False, stream
         codes, scales = _new_codes(stream, rows, d)
     args = RMS_NORM.pack(
         x.data_ptr(), xs, residual.data_ptr() if residual is not None else 0, rs,
-        gamma.data_ptr(), out.data_ptr() if out is not None else 0, os, codes.data_ptr() if quantize else 0, d,
+        gamma.data_ptr(), out.data_ptr() if out is not None else 0, os,
+        codes.data_ptr() if quantize else 0, d,
         scales.data_ptr() if quantize else 0, _blocks(d), rows, d, _DTYPE[dtype],
         _DTYPE[gamma.dtype], eps)
     check(lib().moe_rms_norm(raw, args), "moe_rms_norm")
