@@ -930,10 +930,12 @@ __device__ __forceinline__ void gemm_results(const GemmArgs& a, GemmShared& sh, 
       const uint32_t here = cluster_map(slot, rank), there = cluster_map(slot, rank ^ 1);
       const uint32_t bar_here = cluster_map(smem_addr(bar), rank);
       const uint32_t bar_there = cluster_map(smem_addr(bar), rank ^ 1);
-      if (gt == 0) mbar_arrive_expect_tx(bar, 4 * 64 * 4);
+      const bool wide = c1 + 32 < w.N;   // more than 32 tokens left
+      if (gt == 0) mbar_arrive_expect_tx(bar, wide ? 4 * 64 * 4 : 4 * 32 * 4);
       float h[32];
 #pragma unroll
       for (int c = 0; c < 64; c += 32) {
+        if (c && !wide) continue;
         float v[32], m[16];
         gemm_sums(a, acc, part, rank, c1 + c, v);   // (past N: nobody's)
         gemm_swiglu(sh, group, q, v, h + c / 2);
@@ -958,6 +960,7 @@ __device__ __forceinline__ void gemm_results(const GemmArgs& a, GemmShared& sh, 
       asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
 #pragma unroll
       for (int i = 0; i < 32; i += 4) {
+        if (i == 16 && !wide) break;
         // four tokens' codes of this column, turned among four lanes into four
         // columns' codes of one token
         const int t0 = (i & 16) * 2 + late + (i & 15);
