@@ -105,7 +105,7 @@ struct GemmMaps {
 struct GemmShared {
   uint64_t full[kGemmMaxStages], empty[kGemmMaxStages], loaded[kGemmMaxStages];
   uint64_t sf_full[GemmShape::SFSLOTS], sf_empty[GemmShape::SFSLOTS];
-  uint64_t acc_full[2], acc_empty[2], amax_full[2], drained;
+  uint64_t acc_full[2], acc_empty[2], amax_full[2][2], drained;
   uint32_t tmem;
   int dead;                           // a wait ran out
   int first[kGemmMaxExperts + 1];     // output row of each expert
@@ -921,11 +921,14 @@ __device__ __forceinline__ void gemm_results(const GemmArgs& a, GemmShared& sh, 
     }
     // 8 bits.  A token's 128 results lie in both CTAs, in two warps each: each warp
     // sends its largest to both CTAs, 64 tokens at a time, whose results stay in
-    // registers.  A place is written again two batches later, which this CTA's warps
-    // let the other's begin only when all have read it (the barrier below).
+    // registers.  Places and barriers are taken in turn: a peer that has ended a batch
+    // may send the next one's words before all of its own of this batch have landed
+    // here, and they must not count for it; those after next it sends only when it has
+    // this CTA's of the next batch, which follow the wait for this one, and its
+    // reading (the barrier below).
 #pragma unroll 1
     for (int c1 = c0; c1 < w.N; c1 += step, ++batch) {
-      uint64_t* bar = &sh.amax_full[group];
+      uint64_t* bar = &sh.amax_full[group][batch & 1];
       const uint32_t slot = smem_addr(sh.amax[group][batch & 1][half * 2 + (q & 1)]);
       const uint32_t here = cluster_map(slot, rank), there = cluster_map(slot, rank ^ 1);
       const uint32_t bar_here = cluster_map(smem_addr(bar), rank);
@@ -947,7 +950,7 @@ __device__ __forceinline__ void gemm_results(const GemmArgs& a, GemmShared& sh, 
         st_async_f32((lane < 16 ? here : there) + t * 4, top, lane < 16 ? bar_here : bar_there);
       }
       if (c1 + step >= w.N) release();
-      const bool lost = !gemm_wait(bar, batch & 1, sh) || dead;
+      const bool lost = !gemm_wait(bar, batch >> 1 & 1, sh) || dead;
       if (gt < 64) {
         float amax = 0.f;
 #pragma unroll
@@ -1020,7 +1023,8 @@ static __global__ void __launch_bounds__(kGemmThreads, 1)
     if (s < 2) {
       mbar_init(&sh.acc_full[s], 1);
       mbar_init(&sh.acc_empty[s], 16);   // eight warps of both CTAs
-      mbar_init(&sh.amax_full[s], 1);
+      mbar_init(&sh.amax_full[s][0], 1);
+      mbar_init(&sh.amax_full[s][1], 1);
     }
     if (s == 0) {
       mbar_init(&sh.drained, 1);
