@@ -573,7 +573,9 @@ typedef enum {
  * reads, is read as within [0, x_rows).  out_dtype E4M3 (SWIGLU only) writes
  * the 8-bit form of the result: codes in out, scales in out_scales.  The
  * kernel's waits between its warps are bounded: one that runs out (none does on
- * a device that works) leaves NaN in the tile it was for. */
+ * a device that works) leaves NaN (8 bits: codes or scales of NaN) in its tile of
+ * the output, 256 columns (SWIGLU: 128) of up to 240 rows, and in what the same
+ * CTAs had still to do. */
 typedef struct {
   const uint8_t* x;         /* device [x_rows][k], 16-byte aligned */
   int64_t x_stride;         /* a multiple of 16 */
@@ -596,6 +598,14 @@ typedef struct {
 
 /* Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 int moe_fp8_product(void* stream, const moe_fp8_product_t* args);
+
+/* Failure-detection test hook of moe_fp8_product: with fault = n > 0, in this
+ * process's later calls pair n - 1 of the kernel's CTAs brings no weights (nor rows
+ * that are not by index) to its tiles, and every wait is limited to wait_ns
+ * nanoseconds (0: the default 2 s), so that the waits for them run out.  fault = 0
+ * restores normal operation.  Nothing on the GPU traps, faults or hangs.  Errors:
+ * INVALID_ARG. */
+int moe_debug_set_product_fault(int fault, unsigned long long wait_ns);
 
 /* Tokens by expert, from the choices idx device [n_tokens][top_k]: choice (t, j)
  * of an expert in [0, n_experts) is one entry; entries are ordered by expert,

@@ -110,6 +110,7 @@ _PROTOS = {
     "moe_fp8_pack": (ctypes.c_int, [_P, _P, ctypes.c_int, ctypes.c_int64, ctypes.c_int64,
                                     ctypes.c_int64, _P, _P]),
     "moe_fp8_product": (ctypes.c_int, [_P, _P]),
+    "moe_debug_set_product_fault": (ctypes.c_int, [ctypes.c_int, ctypes.c_ulonglong]),
     "moe_dispatch": (ctypes.c_int, [_P, _P, ctypes.c_int, ctypes.c_int, ctypes.c_int, _P, _P,
                                     _P]),
     "moe_combine": (ctypes.c_int, [_P, _P]),

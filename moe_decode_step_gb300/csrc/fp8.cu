@@ -143,6 +143,10 @@ long long tiles_at_most(const GemmArgs& a, bool swiglu) {
   return m * ((a.n + cols - 1) / cols);
 }
 
+// moe_debug_set_product_fault's
+std::atomic<int> product_fault{0};
+std::atomic<unsigned long long> product_wait_ns{0};
+
 template <bool W4, bool SWIGLU, int PER>
 int launch_product(GemmArgs a, const GemmMaps& maps, int n_sm, cudaStream_t st) {
   a.stages = GemmShape::stages(a.tokens, PER);
@@ -155,6 +159,9 @@ int launch_product(GemmArgs a, const GemmMaps& maps, int n_sm, cudaStream_t st) 
   const long long tiles = tiles_at_most(a, SWIGLU);
   if (tiles > INT32_MAX - 65536) return MOE_ERR_UNSUPPORTED;
   const int pairs = n_sm / 2, groups = (a.kb + 3) / 4;
+  a.fault = product_fault.load(std::memory_order_relaxed);
+  a.wait_ns = a.fault ? product_wait_ns.load(std::memory_order_relaxed) : 0;
+  if (!a.wait_ns) a.wait_ns = kWaitLimitNs;
   a.splits = 1;
   while (a.splits < kGemmMaxSplits && 2 * a.splits * tiles <= pairs && 2 * a.splits <= groups)
     a.splits *= 2;
@@ -337,6 +344,13 @@ int moe_fp8_product(void* stream, const moe_fp8_product_t* args) {
                         : launch_product<true, false, 1>(a, maps, n_sm, st);
   return swiglu ? launch_product<false, true, 1>(a, maps, n_sm, st)
                 : launch_product<false, false, 1>(a, maps, n_sm, st);
+}
+
+int moe_debug_set_product_fault(int fault, unsigned long long wait_ns) {
+  if (fault < 0) return MOE_ERR_INVALID_ARG;
+  product_wait_ns.store(wait_ns, std::memory_order_relaxed);
+  product_fault.store(fault, std::memory_order_relaxed);
+  return MOE_OK;
 }
 
 int moe_dispatch(void* stream, const int32_t* idx, int n_tokens, int top_k, int n_experts,

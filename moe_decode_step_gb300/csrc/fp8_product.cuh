@@ -95,6 +95,8 @@ struct GemmArgs {
   long long os_stride;
   int out_dtype, vec;        // vec: rows of out are aligned to 16 bytes, of codes to 4
   int xs_align, ws_align;    // of the scales' rows: 16, 8, 4 or 1
+  int fault;                 // 0, or 1 + the pair whose copies are left out (a test's)
+  unsigned long long wait_ns;   // of a wait at most
 };
 
 struct GemmMaps {
@@ -107,7 +109,8 @@ struct GemmShared {
   uint64_t sf_full[GemmShape::SFSLOTS], sf_empty[GemmShape::SFSLOTS];
   uint64_t acc_full[2], acc_empty[2], amax_full[2][2], drained;
   uint32_t tmem;
-  int dead;                           // a wait ran out
+  int dead;                           // a wait of the cluster ran out
+  unsigned long long wait_ns;
   int first[kGemmMaxExperts + 1];     // output row of each expert
   int tiles[kGemmMaxExperts + 1];     // token tiles before each expert
   int warp_scan[kGemmThreads / 32];
@@ -121,19 +124,29 @@ struct GemmShared {
 };
 
 // ---- barriers between the CTAs of a pair ----
-// Waits for a phase, two seconds at most; then the CTA is dead: its waits end
-// with false and its results become NaN.
+// Waits for a phase, two seconds at most; then the cluster is dead: the waits of its
+// CTAs end with false and their results become NaN, since a CTA's sums may be its
+// peer's products or the other pairs' parts of K.
 __device__ __forceinline__ bool gemm_dead(GemmShared& sh) { return *(volatile int*)&sh.dead != 0; }
+__device__ __forceinline__ void gemm_die(GemmShared& sh) {
+  const uint32_t ctas = cluster_size();
+  for (uint32_t c = 0; c < ctas; ++c)
+    asm volatile("st.volatile.shared::cluster.u32 [%0], 1;" ::"r"(
+                     cluster_map(smem_addr(&sh.dead), c))
+                 : "memory");
+  // (ahead of what this thread lets others begin)
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+}
 __device__ __forceinline__ bool gemm_wait(uint64_t* bar, uint32_t parity, GemmShared& sh) {
   if (mbar_try_wait_long(bar, parity)) return true;
   const unsigned long long t0 = global_ns();
-  while (!mbar_try_wait_long(bar, parity)) {
+  do {
     if (gemm_dead(sh)) return false;
-    if (global_ns() - t0 > kWaitLimitNs) {
-      *(volatile int*)&sh.dead = 1;
+    if (global_ns() - t0 > sh.wait_ns) {
+      gemm_die(sh);
       return false;
     }
-  }
+  } while (!mbar_try_wait_long(bar, parity));
   return true;
 }
 // The same for a whole warp, whose lanes go on, or give up, together.
@@ -408,6 +421,7 @@ template <bool W4, bool SWIGLU, int PER>
 __device__ __forceinline__ void gemm_copy(const GemmArgs& a, GemmShared& sh, uint32_t base,
                                           const GemmMaps& maps, uint32_t rank) {
   using S = GemmShape;
+  if (a.fault == (int)(blockIdx.x / 2) + 1) return;
   const int lane = threadIdx.x & 31, half = rank & 1;
   const uint32_t stage_bytes = S::stage(a.tokens, PER);
   const uint32_t full = cluster_map(smem_addr(sh.full), rank & ~1u);
@@ -958,7 +972,8 @@ __device__ __forceinline__ void gemm_results(const GemmArgs& a, GemmShared& sh, 
         const int e = fp8_block_exp(amax);
         sh.inv[group][gt] = pow2f(-e);
         if (half == 0 && c1 + gt < w.rows)
-          a.os[(long long)(w.row0 + c1 + gt) * a.os_stride + (w.n0 >> 7)] = (uint8_t)(e + 127);
+          a.os[(long long)(w.row0 + c1 + gt) * a.os_stride + (w.n0 >> 7)] =
+              lost ? 255 : (uint8_t)(e + 127);
       }
       asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
 #pragma unroll
@@ -1029,6 +1044,7 @@ static __global__ void __launch_bounds__(kGemmThreads, 1)
     if (s == 0) {
       mbar_init(&sh.drained, 1);
       sh.dead = 0;
+      sh.wait_ns = a.wait_ns;
       asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.w) : "memory");
     }
     fence_barrier_init();
@@ -1083,23 +1099,28 @@ static __global__ void __launch_bounds__(kGemmThreads, 1)
     const GemmWalk<SWIGLU> k(a, sh);
     if (k.t < k.tiles) cluster_sync();
   }
-  if (gemm_dead(sh) && warp == 1) {
-    // products and copies in flight, before their memory is given back: bounded too
-    if (elect_one()) {
-      if ((rank & 1) == 0) {
-        umma_commit_pair(&sh.drained, (uint16_t)(1u << rank));
-        for (int i = 0; i < 100 && !mbar_try_wait_long(&sh.drained, 0); ++i) {
-        }
-      }
-      const unsigned long long t0 = global_ns();
-      while (global_ns() - t0 < 2000000) {
-      }
-    }
-    __syncwarp();
-  }
   tc_fence_before();
   __syncthreads();
   cluster_sync();   // (nor does a CTA leave while another may read its sums)
+  if (gemm_dead(sh)) {
+    // (no wait is left to run out, so all of the cluster are here or none)  Products,
+    // copies and words in flight, before their memory is given back: bounded too
+    if (warp == 1) {
+      if (elect_one()) {
+        if ((rank & 1) == 0) {
+          umma_commit_pair(&sh.drained, (uint16_t)(1u << rank));
+          for (int i = 0; i < 100 && !mbar_try_wait_long(&sh.drained, 0); ++i) {
+          }
+        }
+        const unsigned long long t0 = global_ns();
+        while (global_ns() - t0 < 2000000) {
+        }
+      }
+      __syncwarp();
+    }
+    __syncthreads();
+    cluster_sync();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(sh.tmem);

@@ -43,3 +43,48 @@ def test_scales_of_batches_in_a_row(k, mx):
         again = M.fp8_linear(*args, activation="swiglu", quantize=True)
         assert torch.equal(_u8(again.codes), _u8(got.codes))
         assert torch.equal(_u8(again.scales), _u8(got.scales))
+
+
+def _product(mode, k, mx, rows, seed, index):
+    """A call of two tiles: what it returns, as a list of tensors of values."""
+    rng = np.random.default_rng(seed)
+    n = 512                                    # two tiles of 256, or of 128 gates and ups
+    x, xs = ref.random_x(rng, rows, k)
+    w, ws = ref.random_w(rng, n, k, mx)
+    x, xs, w, ws = _codes(x), _scales(xs), _dev(w) if mx else _codes(w), _scales(ws)
+    kw = dict(activation=None if mode == "plain" else "swiglu", quantize=mode == "quantize")
+
+    def run():
+        if index:
+            got = M.expert_linear(x, xs, w[None], ws[None],
+                                  torch.tensor([0, rows], dtype=torch.int32, device=DEV),
+                                  rows=torch.arange(rows, dtype=torch.int32, device=DEV), **kw)
+        else:
+            got = M.fp8_linear(x, xs, w, ws, **kw)
+        if mode != "quantize":
+            return got.float()
+        return got.codes.float() * got.scales.float().repeat_interleave(128, 1)
+    return run
+
+
+@pytest.mark.parametrize("mode", ["plain", "swiglu", "quantize"])
+@pytest.mark.parametrize("k,mx,index", [(256, False, False), (256, True, True),
+                                        (2048, False, True), (2048, True, False)])
+def test_a_wait_that_runs_out_leaves_nan(k, mx, index, mode):
+    """A pair of CTAs that gets no weights: its tile is NaN in both CTAs' columns, and
+    (K = 2,048 is split over four pairs) whichever pair of the cluster it is; the other
+    tile and the calls after it are right."""
+    run = _product(mode, k, mx, 16, k, index)
+    clean = run()
+    cols = 256 if mode == "plain" else 128
+    assert clean.isfinite().all()
+    for fault in (1,) if k == 256 else (1, 2, 4):
+        assert M.lib().moe_debug_set_product_fault(fault, 20_000_000) == 0
+        try:
+            got = run()
+            torch.cuda.synchronize()
+        finally:
+            assert M.lib().moe_debug_set_product_fault(0, 0) == 0
+        assert got[:, :cols].isnan().all(), fault
+        assert torch.equal(got[:, cols:], clean[:, cols:]), fault
+        assert torch.equal(run(), clean)
