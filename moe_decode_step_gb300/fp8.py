@@ -21,6 +21,9 @@ from ._binding import COMBINE, DTYPE_E4M3, FP8_PRODUCT, RMS_NORM, check, lib
 from .serving import _CODES, _DTYPE, _SCALES, _raw_stream, _vector, _want
 from .serving import _empty as _empty_on
 
+# what the ABI's 32-bit arguments hold: ctypes cuts larger ones without a word (below it
+# the library checks its limits)
+_INT_MAX = 2 ** 31 - 1
 _ACTIVATION = {None: 0, "swiglu": 1}
 
 
@@ -130,6 +133,8 @@ def fp8_quantize(x, stream=None):
     """The 8-bit form of activations x bfloat16, float16 or float32 [rows, d]
     (moe_fp8_quantize): Quantized(codes, scales)."""
     rows, d, xs = _matrix(x, "x", _DTYPE)
+    if d > _INT_MAX:
+        _want(False, "x", "rows of at most 16384 columns", x)
     raw = _stream(stream, x.device)
     codes, scales = _new_codes(stream, rows, d)
     check(lib().moe_fp8_quantize(raw, x.data_ptr(), _DTYPE[x.dtype], xs, rows, d, codes.data_ptr(),
@@ -247,7 +252,9 @@ def moe_dispatch(idx, n_experts, stream=None):
     tokens, k = idx.shape
     dev = idx.device
     n_experts = int(n_experts)
-    _want(n_experts >= 1, "n_experts", "at least 1", n_experts)
+    _want(1 <= n_experts <= _INT_MAX, "n_experts", "1 to 1024", n_experts)
+    if tokens > _INT_MAX or k > _INT_MAX:
+        _want(False, "idx", "at most 2^24 choices", idx)
     raw = _stream(stream, dev)
     offsets = _empty(stream, torch.int32, (n_experts + 1,), (1,))
     rows = _empty(stream, torch.int32, (tokens * k,), (1,))
