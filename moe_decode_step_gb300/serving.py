@@ -63,6 +63,13 @@ def _table(t, rows, device):
     return t.stride(0) if rows > 1 else t.shape[1]
 
 
+def _int32(name, *sizes):
+    """Sizes that go to the library as 32-bit integers: ctypes cuts larger ones without
+    a word (below that the library checks its limits)."""
+    if max(sizes) > 2 ** 31 - 1:
+        raise ValueError(f"{name}: want sizes below 2^31, got {sizes}")
+
+
 class KVPlan(NamedTuple):
     """What kv_plan writes (see moe_kv_plan)."""
     seq_lens: torch.Tensor     # int32 [rows]: cached tokens with this step's
@@ -90,6 +97,7 @@ def kv_plan(ctx_lens, q_lens, block_table, free_list, n_free, block_size, n_slot
     stride = _table(block_table, rows, dev)
     n_slots = int(n_slots)
     _want(n_slots >= 0, "n_slots", "a number of slots >= 0", n_slots)
+    _int32("kv_plan", n_slots, rows, *block_table.shape, free_list.shape[0], int(block_size))
     raw = _raw_stream(stream, dev)
     # one allocation, cut in one operation (no gradients: the form that keeps no record)
     buf = _empty(stream, torch.int32, dev, n_slots + 2 * rows + 3)
@@ -126,6 +134,7 @@ def kv_release(finished, seq_lens, block_table, free_list, n_free, block_size, s
     _vector(free_list, None, torch.int32, "free_list", dev)
     _vector(n_free, 1, torch.int32, "n_free", dev)
     stride = _table(block_table, rows, dev)
+    _int32("kv_release", rows, *block_table.shape, free_list.shape[0], int(block_size))
     check(lib().moe_kv_release_past(_raw_stream(stream, dev), finished.data_ptr(),
                                     None if keep_lens is None else keep_lens.data_ptr(), rows,
                                     seq_lens.data_ptr(), block_table.data_ptr(), stride,
@@ -190,6 +199,7 @@ class KVCache:
         _want(v.shape[0] == n, "v", f"{n} tokens, as k", v)
         _vector(slot_map, None, torch.int32, "slot_map", self.device)
         _want(slot_map.shape[0] >= n, "slot_map", f"at least {n} entries", slot_map)
+        _int32("append", n)
         rc = lib().moe_kv_append(_raw_stream(stream, self.device), self._struct, k.data_ptr(),
                                  v.data_ptr(), _DTYPE[k.dtype], k.stride(0), k.stride(1),
                                  v.stride(0), v.stride(1), slot_map.data_ptr(), n)
