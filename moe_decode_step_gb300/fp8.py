@@ -15,11 +15,16 @@ layout, uint8 [n, k / 2] with scales [n, k / 32].
 from typing import NamedTuple, Optional
 
 import torch
-from torch._C._dynamo.guards import _empty_strided_cuda
 
 from ._binding import COMBINE, DTYPE_E4M3, FP8_PRODUCT, RMS_NORM, check, lib
 from .serving import _CODES, _DTYPE, _SCALES, _raw_stream, _vector, _want
 from .serving import _empty as _empty_on
+
+try:   # a private entry, which a torch may lack
+    from torch._C._dynamo.guards import _empty_strided_cuda
+except ImportError:
+    def _empty_strided_cuda(shape, strides, dtype):
+        return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
 
 # what the ABI's 32-bit arguments hold: ctypes cuts larger ones without a word (below it
 # the library checks its limits)

@@ -1,11 +1,17 @@
 """Refusals of the 8-bit operators without a GPU that lie past the packed structs: the
 test hook, sizes that do not fit the ABI's integers, the package without torch's
 private allocator entry."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
 import moe_decode_step_gb300 as M
 from moe_decode_step_gb300 import fp8
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -50,3 +56,11 @@ def test_sizes_past_32_bits_are_refused(call, monkeypatch):
     monkeypatch.setattr(fp8, "_empty", lambda *a: pytest.fail("went past the checks"))
     with pytest.raises(ValueError):
         call()
+
+
+def test_import_without_torchs_private_allocator_entry():
+    """The package, MoELayer included, does not hang on it."""
+    code = ("import torch, torch._C._dynamo.guards as g; del g._empty_strided_cuda; "
+            "import moe_decode_step_gb300 as M; M.MoELayer; "
+            "assert 'moe_decode_step_gb300' in M.fp8._empty_strided_cuda.__module__")
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=ROOT)

@@ -88,3 +88,29 @@ def test_a_wait_that_runs_out_leaves_nan(k, mx, index, mode):
         assert got[:, :cols].isnan().all(), fault
         assert torch.equal(got[:, cols:], clean[:, cols:]), fault
         assert torch.equal(run(), clean)
+
+
+def test_without_torchs_private_allocator_entry(monkeypatch):
+    """What a torch without it falls back to gives the same tensors."""
+    import importlib
+    import torch._C._dynamo.guards as guards
+    from moe_decode_step_gb300 import fp8
+    x = torch.randn(5, 264, device=DEV).to(torch.bfloat16)
+    gamma = torch.ones(264, device=DEV)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    want = M.rms_norm(x, gamma, quantize=True)
+    fast = fp8._empty_strided_cuda
+    monkeypatch.delattr(guards, "_empty_strided_cuda")
+    try:
+        importlib.reload(fp8)
+        assert fp8._empty_strided_cuda is not fast
+        for stream in (None, s):
+            got = fp8.rms_norm(x, gamma, quantize=True, stream=stream)
+            torch.cuda.synchronize()
+            assert all(a.stride() == b.stride() and torch.equal(_u8(a), _u8(b))
+                       for a, b in zip(got, want))
+    finally:
+        monkeypatch.undo()
+        importlib.reload(fp8)
+    assert fp8._empty_strided_cuda is fast
