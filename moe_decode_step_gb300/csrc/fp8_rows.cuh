@@ -157,15 +157,43 @@ static __global__ void __launch_bounds__(T < 256 ? 256 : T)
     }
   }
   if (NORM) {
-    sum = warp_sum(sum);
-    if (WARPS > 1) {
-      if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = sum;
-      __syncthreads();
+    auto row_sum = [&](float s) {
+      s = warp_sum(s);
+      if (WARPS > 1) {
+        if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = s;
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + sub), "n"(T) : "memory");
+        s = 0.f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) s += s_sum[sub * WARPS + w];
+      }
+      return s;
+    };
+    sum = row_sum(sum);
+    float eps = a.eps, last = 1.f;
+    // squares past fp32's range, or (with little or no eps) so near its lower end that
+    // they lose bits: once more from values times f, a power of two.  Then values enter
+    // times f, large ones by its square root and their norm by the other one (neither
+    // leaves the range)
+    const float all = fmaf((float)a.d, eps, sum);
+    if (__builtin_expect(!(all >= 0x1p-100f && sum <= 3.4028235e38f), 0)) {
+      const bool high = !(sum <= 3.4028235e38f);
+      const float f = high ? 0x1p-80f : 0x1p100f, first = high ? 0x1p-40f : f;
       sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) sum += s_sum[sub * WARPS + w];
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float u = v[i][j] * f;
+          sum = fmaf(u, u, sum);
+          v[i][j] *= first;
+        }
+      // (s_sum has been read)
+      if (WARPS > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + sub), "n"(T) : "memory");
+      sum = row_sum(sum);
+      eps = eps * f * f;
+      if (high) last = 0x1p-40f;
     }
-    const float scale = 1.f / sqrtf(sum / (float)a.d + a.eps);
+    const float scale = last / sqrtf(sum / (float)a.d + eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = 8 * (i * T + t);

@@ -114,3 +114,49 @@ def test_without_torchs_private_allocator_entry(monkeypatch):
         monkeypatch.undo()
         importlib.reload(fp8)
     assert fp8._empty_strided_cuda is fast
+
+
+@pytest.mark.parametrize("d", [8, 264, 1032, 4104, 16384])
+@pytest.mark.parametrize("dtype,eps", [(torch.float32, 0.0), (torch.float32, 1e-6),
+                                       (torch.bfloat16, 0.0), (torch.bfloat16, 1e-36)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_norm_of_values_whose_squares_leave_fp32(d, dtype, eps, residual):
+    """Rows whose squares are infinite, zero or denormal in 32 bits, beside ordinary
+    ones; magnitudes that differ within a row.  Held to the same bounds."""
+    rng = np.random.default_rng(d)
+    size = 2.0 ** np.array([0.0, 62, 64, 66, 100, 125, -45, -52, -60, -70, -100, -120, 60, -50])
+    v = rng.standard_normal((len(size), d)) * size[:, None]
+    # (a few far smaller ones beside the large)
+    v[3, ::5] *= 2.0 ** -70
+    v[5, ::3] *= 2.0 ** -90
+    v = np.clip(v, -2.0 ** 126, 2.0 ** 126)
+    x = _dev(v, torch.float32).to(dtype)
+    r = _dev(v[:, ::-1] * 0.5, torch.float32).to(dtype) if residual else None
+    gamma = _dev(1 + 0.2 * rng.standard_normal(d), torch.float32)
+    z = x.double().cpu().numpy() + (r.double().cpu().numpy() if residual else 0.0)
+    mag = np.abs(x.double().cpu().numpy()) + (np.abs(r.double().cpu().numpy()) if residual else 0)
+    scale = 1.0 / np.sqrt((z * z).mean(axis=1, keepdims=True) + float(np.float32(eps)))
+    g = gamma.double().cpu().numpy()
+    y = z * scale * g
+    # (denormal values and sums of the inputs' type: half of fp32's smallest step)
+    tol = (64 * 2.0 ** -24 * np.abs(y) + (2.0 ** -24 * mag + 2.0 ** -150) * scale * np.abs(g)
+           + 2.0 ** -149)
+    got = M.rms_norm(x, gamma, residual=r, eps=eps, quantize=True)
+    ref.check_values(got.out, y, tol, dtype, "out")
+    ref.check_codes(got.codes, got.scales, y, tol, "codes")
+
+
+def test_norm_of_zeros_infinities_and_nan():
+    """As the formula has them: 0 / sqrt(0 + eps), 0 / 0 without eps, infinity / infinity,
+    finite values over infinity; rows beside them are as they are alone."""
+    x = torch.randn(6, 2056, device=DEV)
+    x[1] = 0
+    x[2, 7], x[3, 2000] = float("inf"), float("nan")
+    gamma = torch.ones(2056, device=DEV)
+    for eps in (0.0, 1e-6):
+        out = M.rms_norm(x, gamma, eps=eps).out
+        assert (out[1].isnan() if eps == 0 else out[1] == 0).all()
+        assert out[2, 7].isnan() and (out[2, :7] == 0).all() and (out[2, 8:] == 0).all()
+        assert out[3].isnan().all()
+        for i in (0, 4, 5):
+            assert torch.equal(out[i], M.rms_norm(x[i:i + 1], gamma, eps=eps).out[0])
