@@ -74,7 +74,7 @@ class DecoderBlock:
         lens = torch.tensor([p.shape[0] for p in prompts], dtype=torch.int32, device=x.device)
         out = self.attend(x, lens, max(p.shape[0] for p in prompts))
         y = F.linear(out.flatten(1), self.w_o)
-        logits = F.linear(x, self.weights["router_w"]).float()
+        logits = F.linear(x.float(), self.weights["router_w"].float())
         idx, _ = M.moe_route(logits, self.cfg.top_k, bias=self.weights["router_bias"],
                              routed_scale=self.cfg.routed_scale)
         load = torch.bincount(idx.flatten(), minlength=self.cfg.n_experts)
@@ -101,6 +101,7 @@ class PromptLayer:
     def __init__(self, cfg):
         self.cfg = cfg
         self.weights = synthetic.make_weights(cfg, layout=0)
+        self.router_w = self.weights["router_w"].float()
         self.shared_gu = M.fp8_pack(self.weights["shared_gu"])
         self.shared_d = M.fp8_pack(self.weights["shared_d"])
 
@@ -108,7 +109,8 @@ class PromptLayer:
         """x and residual bf16 [tokens, d], residual updated; returns the normalised
         output, as MoELayer.forward."""
         c, w = self.cfg, self.weights
-        logits = F.linear(x, w["router_w"])
+        # (in 32 bits, as MoELayer has them: rounded to 16 they choose other experts)
+        logits = F.linear(x.float(), self.router_w)
         idx, mix = M.moe_route(logits, c.top_k, bias=w["router_bias"], routed_scale=c.routed_scale)
         by = M.moe_dispatch(idx, c.n_experts)
         x8 = M.fp8_quantize(x)
