@@ -63,7 +63,8 @@ struct GemmShape {
   __host__ __device__ static constexpr int stage(int tokens, int per) {
     return per * (ABYTES + tokens / 2 * kGemmK);
   }
-  static constexpr int LIMIT = 227 * 1024 - 22 * 1024;   // beside the static part
+  static constexpr int STATIC = 22 * 1024;   // GemmShared at most
+  static constexpr int LIMIT = 227 * 1024 - STATIC;
   static constexpr int stages(int tokens, int per) {
     const int n = (LIMIT - 1024 - SFSLOTS * SFSLOT) / stage(tokens, per);
     return n < kGemmMaxStages ? n : kGemmMaxStages;
@@ -122,6 +123,8 @@ struct GemmShared {
   float amax[2][2][4][64];
   alignas(16) float inv[2][64];
 };
+static_assert(sizeof(GemmShared) <= GemmShape::STATIC, "the ring's room is the block's less this");
+static_assert(GemmShape::stages(kGemmTokens, 2) >= 3, "the rows' loaders count on three stages");
 
 // ---- barriers between the CTAs of a pair ----
 // Waits for a phase, two seconds at most; then the cluster is dead: the waits of its
