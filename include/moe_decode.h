@@ -561,7 +561,8 @@ typedef enum {
 
 typedef enum {
   MOE_ACT_NONE = 0,         /* out[., j] = p[., j] */
-  MOE_ACT_SWIGLU = 1        /* out[., j] = silu(p[., j]) * p[., n / 2 + j]: gates, then ups */
+  MOE_ACT_SWIGLU = 1        /* out[., j] = silu(p[., j]) * p[., n / 2 + j]: gates, then ups
+                             * (silu 0 below -87.3, where it is less than 1.1e-36) */
 } moe_activation;
 
 /* Products of 8-bit activations with 8-bit or MXFP4 weights: p[i, j] = sum_k

@@ -160,3 +160,91 @@ def test_norm_of_zeros_infinities_and_nan():
         assert out[3].isnan().all()
         for i in (0, 4, 5):
             assert torch.equal(out[i], M.rms_norm(x[i:i + 1], gamma, eps=eps).out[0])
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("rows,f,k", [(1, 128, 128), (33, 200, 256), (260, 129, 384),
+                                      (5, 256, 2048), (300, 144, 512)])
+def test_swiglu_in_32_bits(rows, f, k, mx):
+    rng = np.random.default_rng(rows + f + k)
+    x, xs = ref.random_x(rng, rows, k)
+    w, ws = ref.random_w(rng, 2 * f, k, mx)
+    p, tol = ref.swiglu(*ref.product(ref.row_values(x, xs), ref.weight_values(w, ws, mx)))
+    got = M.fp8_linear(_codes(x), _scales(xs), _dev(w) if mx else _codes(w), _scales(ws),
+                       activation="swiglu", out_dtype=torch.float32)
+    ref.check_values(got, p, tol, torch.float32, (rows, f, k))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_swiglu_over_the_range_of_gates(dtype):
+    """Gates of -224 to 224, each a product of one term: silu to its bound, and 0 where the
+    documentation has it 0 (below -87.3, where silu is less than 1.1e-36)."""
+    rng = np.random.default_rng(6)
+    k = f = 128
+    x = np.zeros((k, k), np.uint8)
+    np.fill_diagonal(x, 0x38)                                   # 1.0
+    w = rng.integers(0, 256, (2 * f, k), np.uint8)
+    w[(w & 127) == 127] = 0
+    xs, ws = np.full((k, 1), 127, np.uint8), np.array([[126], [110]], np.uint8)
+    p, tol = ref.product(ref.row_values(x, xs), ref.weight_values(w, ws, False))
+    low = np.where(p[:, :f] < -87.3, 1.1e-36 * np.abs(p[:, f:]), 0.0)
+    assert (p[:, :f] < -88).sum() > 500 and (p[:, :f] > 88).sum() > 500
+    want, tol = ref.swiglu(p, tol)
+    got = M.fp8_linear(_codes(x), _scales(xs), _codes(w), _scales(ws), activation="swiglu",
+                       out_dtype=dtype)
+    ref.check_values(got, want, tol + low, dtype)
+
+
+@pytest.mark.parametrize("mode", ["plain", "swiglu", "quantize"])
+def test_more_token_tiles_than_a_pass(mode):
+    """Sixteen tiles of tokens share a pass over the weights: 40 tiles of one matrix and 21,
+    1 and 17 of experts, every row compared."""
+    rng = np.random.default_rng(12)
+    kw = dict(activation=None if mode == "plain" else "swiglu", quantize=mode == "quantize")
+    k, n = 128, 300
+
+    def check(got, x, xs, w, ws, what):
+        p, tol = ref.product(ref.row_values(x, xs), ref.weight_values(w, ws, False))
+        if mode != "plain":
+            p, tol = ref.swiglu(p, tol)
+        if mode == "quantize":
+            ref.check_codes(got.codes, got.scales, p, tol, what)
+        else:
+            ref.check_values(got, p, tol, torch.bfloat16, what)
+
+    x, xs = ref.random_x(rng, 9500, k)
+    w, ws = ref.random_w(rng, n, k, False)
+    check(M.fp8_linear(_codes(x), _scales(xs), _codes(w), _scales(ws), **kw), x, xs, w, ws, "dense")
+    counts = [5000, 0, 17, 4000]
+    w, ws = (np.stack(t) for t in zip(*(ref.random_w(rng, n, k, False) for _ in counts)))
+    off = np.concatenate([[0], np.cumsum(counts)])
+    rows = rng.integers(0, 9500, off[-1])
+    for src in (None, rows):
+        got = M.expert_linear(_codes(x[:off[-1]] if src is None else x),
+                              _scales(xs[:off[-1]] if src is None else xs), _codes(w), _scales(ws),
+                              _dev(off, torch.int32),
+                              rows=None if src is None else _dev(src, torch.int32), **kw)
+        at = np.arange(off[-1]) if src is None else src
+        for e, (a, b) in enumerate(zip(off, off[1:])):
+            if a < b:
+                part = M.Quantized(*(t[a:b] for t in got)) if mode == "quantize" else got[a:b]
+                check(part, x[at[a:b]], xs[at[a:b]], w[e], ws[e], (e, src is None))
+
+
+@pytest.mark.parametrize("rows", [3, 70, 500])
+def test_rows_by_index_of_one_matrix(rows):
+    """The C call without offsets and with rows, which Python has no name for."""
+    from moe_decode_step_gb300._binding import FP8_PRODUCT
+    rng = np.random.default_rng(rows)
+    k, n = 384, 200
+    x, xs = ref.random_x(rng, 41, k)
+    w, ws = ref.random_w(rng, n, k, False)
+    src = rng.integers(0, 41, rows)
+    t = [_dev(x), _dev(xs), _dev(w), _dev(ws), _dev(src, torch.int32)]
+    out = torch.empty(rows, n, dtype=torch.float32, device=DEV)
+    args = FP8_PRODUCT.pack(t[0].data_ptr(), k, t[1].data_ptr(), 3, t[2].data_ptr(), k, 0,
+                            t[3].data_ptr(), 3, 0, 0, t[4].data_ptr(), out.data_ptr(), n, 0, 1,
+                            rows, 41, n, k, 1, 0, 0, 2)
+    assert M.lib().moe_fp8_product(torch.cuda.current_stream().cuda_stream, args) == M.MOE_OK
+    p, tol = ref.product(ref.row_values(x, xs)[src], ref.weight_values(w, ws, False))
+    ref.check_values(out, p, tol, torch.float32, rows)
