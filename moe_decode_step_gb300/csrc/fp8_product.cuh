@@ -110,8 +110,7 @@ struct GemmShared {
   uint64_t sf_full[GemmShape::SFSLOTS], sf_empty[GemmShape::SFSLOTS];
   uint64_t acc_full[2], acc_empty[2], amax_full[2][2], drained;
   uint32_t tmem;
-  int dead;                           // a wait of the cluster ran out
-  unsigned long long wait_ns;
+  int dead;                           // a wait ran out
   int first[kGemmMaxExperts + 1];     // output row of each expert
   int tiles[kGemmMaxExperts + 1];     // token tiles before each expert
   int warp_scan[kGemmThreads / 32];
@@ -127,34 +126,39 @@ static_assert(sizeof(GemmShared) <= GemmShape::STATIC, "the ring's room is the b
 static_assert(GemmShape::stages(kGemmTokens, 2) >= 3, "the rows' loaders count on three stages");
 
 // ---- barriers between the CTAs of a pair ----
-// Waits for a phase, two seconds at most; then the cluster is dead: the waits of its
-// CTAs end with false and their results become NaN, since a CTA's sums may be its
-// peer's products or the other pairs' parts of K.
+// Waits for a phase, two seconds at most; then the CTA is dead: its waits end with
+// false and its results become NaN.  So do the whole cluster's (gemm_spread), since a
+// CTA's sums are its peer's products, or the other pairs' parts of K too: every wait
+// that sums depend on ends at the issuing thread, which passes it on ahead of the
+// sums' barrier.  (Not from the waits: with that loop behind each of them a prompt's
+// gates and ups took 608 us for 485; with the limit in shared memory 500.)
 __device__ __forceinline__ bool gemm_dead(GemmShared& sh) { return *(volatile int*)&sh.dead != 0; }
-__device__ __forceinline__ void gemm_die(GemmShared& sh) {
+__device__ __forceinline__ void gemm_spread(GemmShared& sh) {
+  if (!gemm_dead(sh)) return;
   const uint32_t ctas = cluster_size();
   for (uint32_t c = 0; c < ctas; ++c)
     asm volatile("st.volatile.shared::cluster.u32 [%0], 1;" ::"r"(
                      cluster_map(smem_addr(&sh.dead), c))
                  : "memory");
-  // (ahead of what this thread lets others begin)
   asm volatile("fence.acq_rel.cluster;" ::: "memory");
 }
-__device__ __forceinline__ bool gemm_wait(uint64_t* bar, uint32_t parity, GemmShared& sh) {
+__device__ __forceinline__ bool gemm_wait(uint64_t* bar, uint32_t parity, GemmShared& sh,
+                                          const GemmArgs& a) {
   if (mbar_try_wait_long(bar, parity)) return true;
   const unsigned long long t0 = global_ns();
-  do {
+  while (!mbar_try_wait_long(bar, parity)) {
     if (gemm_dead(sh)) return false;
-    if (global_ns() - t0 > sh.wait_ns) {
-      gemm_die(sh);
+    if (global_ns() - t0 > a.wait_ns) {
+      *(volatile int*)&sh.dead = 1;
       return false;
     }
-  } while (!mbar_try_wait_long(bar, parity));
+  }
   return true;
 }
 // The same for a whole warp, whose lanes go on, or give up, together.
-__device__ __forceinline__ bool gemm_wait_warp(uint64_t* bar, uint32_t parity, GemmShared& sh) {
-  return __all_sync(0xffffffffu, gemm_wait(bar, parity, sh));
+__device__ __forceinline__ bool gemm_wait_warp(uint64_t* bar, uint32_t parity, GemmShared& sh,
+                                               const GemmArgs& a) {
+  return __all_sync(0xffffffffu, gemm_wait(bar, parity, sh, a));
 }
 __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -437,7 +441,7 @@ __device__ __forceinline__ void gemm_copy(const GemmArgs& a, GemmShared& sh, uin
         (W4 ? S::ABYTES : 2 * S::ABYTES) + (a.src ? 0u : (uint32_t)w.N * kGemmK);
     const CUtensorMap* xm = &maps.x[w.N / 16 - 1];
     for (int kb = k.k0; kb < k.k1; kb += PER, ring.next(a.stages)) {
-      if (!gemm_wait_warp(&sh.empty[ring.stage], ring.phase ^ 1, sh)) return;
+      if (!gemm_wait_warp(&sh.empty[ring.stage], ring.phase ^ 1, sh, a)) return;
       const uint32_t bar = full + ring.stage * 8, at = base + ring.stage * stage_bytes;
       if (half == 0 && lane == 0) mbar_arrive_expect_tx(&sh.full[ring.stage], PER * bytes);
       __syncwarp();
@@ -459,7 +463,7 @@ __device__ __forceinline__ void gemm_copy(const GemmArgs& a, GemmShared& sh, uin
   }
   // the last arrivals from the pair's first CTA are in before this one may leave
   for (int i = 0; i < a.stages; ++i, ring.next(a.stages))
-    if (!gemm_wait_warp(&sh.empty[ring.stage], ring.phase ^ 1, sh)) return;
+    if (!gemm_wait_warp(&sh.empty[ring.stage], ring.phase ^ 1, sh, a)) return;
 }
 
 // ---------------------------------------------------------------------------
@@ -518,7 +522,7 @@ __device__ __forceinline__ void gemm_load_rows(const GemmArgs& a, GemmShared& sh
     for (int kb = k.k0; kb < k.k1; kb += PER, ring.next(a.stages)) {
       if (turn-- > 0) continue;
       turn = kGemmLoaders - 1;
-      if (!gemm_wait_warp(&sh.empty[ring.stage], ring.phase ^ 1, sh)) {
+      if (!gemm_wait_warp(&sh.empty[ring.stage], ring.phase ^ 1, sh, a)) {
         asm volatile("cp.async.wait_all;" ::: "memory");
         return;
       }
@@ -560,7 +564,7 @@ __device__ __forceinline__ void gemm_hand_over(const GemmArgs& a, GemmShared& sh
     left = (long long)((k.tiles - 1 - k.t) / k.step + 1) * ((k.k1 - k.k0 + PER - 1) / PER);
   GemmRing ring;
   while (left > 0) {
-    if (!gemm_wait_warp(&sh.loaded[ring.stage], ring.phase, sh)) return;
+    if (!gemm_wait_warp(&sh.loaded[ring.stage], ring.phase, sh, a)) return;
     uint32_t mine = ring.stage;   // lane l's stage
     int n = 1;
     for (ring.next(a.stages); n < 4 && n < left; ++n, ring.next(a.stages)) {
@@ -647,7 +651,7 @@ __device__ __forceinline__ void gemm_scales(const GemmArgs& a, GemmShared& sh, u
 #pragma unroll
       for (int s = 0; s < BATCH / 4; ++s) {
         if (k0 + 4 * s >= k.k1) break;
-        if (!gemm_wait_warp(&sh.sf_empty[ring.stage], ring.phase ^ 1, sh)) return;
+        if (!gemm_wait_warp(&sh.sf_empty[ring.stage], ring.phase ^ 1, sh, a)) return;
         uint4* to = reinterpret_cast<uint4*>(dst + ring.stage * S::SFSLOT);
 #pragma unroll
         for (int j = 0; j < (PERK ? 4 : 1); ++j)
@@ -665,7 +669,7 @@ __device__ __forceinline__ void gemm_scales(const GemmArgs& a, GemmShared& sh, u
     }
   }
   for (int i = 0; i < S::SFSLOTS; ++i, ring.next(S::SFSLOTS))   // (as the copies' end)
-    if (!gemm_wait_warp(&sh.sf_empty[ring.stage], ring.phase ^ 1, sh)) return;
+    if (!gemm_wait_warp(&sh.sf_empty[ring.stage], ring.phase ^ 1, sh, a)) return;
 }
 
 // ---------------------------------------------------------------------------
@@ -690,12 +694,12 @@ __device__ __forceinline__ void gemm_mma(const GemmArgs& a, GemmShared& sh, uint
   for (GemmWalk<SWIGLU> k(a, sh); k.t < k.tiles; k.t += k.step, ++n) {
     const GemmTile w = k.tile(a, sh);
     const uint32_t acc = tm + (n & 1) * kGemmTokens, id = umma_idesc_mxf8(W4 ? 5 : 0, 0, 0, w.N);
-    gemm_wait(&sh.acc_empty[n & 1], (n >> 1 & 1) ^ 1, sh);
+    gemm_wait(&sh.acc_empty[n & 1], (n >> 1 & 1) ^ 1, sh, a);
     if (elect_one()) {
       for (int kb = k.k0; kb < k.k1; kb += 4) {
         const uint32_t j4 = kb >> 2 & 1, sfb = tm + S::SFCOL + 8 + 8 * j4;
         const uint64_t ds = ds0 + sr.stage * (S::SFSLOT >> 4);
-        gemm_wait(&sh.sf_full[sr.stage], sr.phase, sh);
+        gemm_wait(&sh.sf_full[sr.stage], sr.phase, sh, a);
         tc_fence_after();
         umma_sf_copy_pair(sfb, ds + (4 * S::SFA >> 4));
         if (w.N > 128) umma_sf_copy_pair(sfb + 4, ds + ((4 * S::SFA + 512) >> 4));
@@ -712,7 +716,7 @@ __device__ __forceinline__ void gemm_mma(const GemmArgs& a, GemmShared& sh, uint
             db += (b & 1) * (w.N / 2 * kGemmK >> 4);
           }
           if (PER == 1 || (b & 1) == 0) {
-            gemm_wait(&sh.full[ring.stage], ring.phase, sh);
+            gemm_wait(&sh.full[ring.stage], ring.phase, sh, a);
             tc_fence_after();
           }
           if (W4) umma_sf_copy_pair(sfa, ds + b * (S::SFA >> 4));
@@ -728,6 +732,7 @@ __device__ __forceinline__ void gemm_mma(const GemmArgs& a, GemmShared& sh, uint
         umma_commit_pair(&sh.sf_empty[sr.stage], both);
         sr.next(S::SFSLOTS);
       }
+      gemm_spread(sh);
       umma_commit_pair(&sh.acc_full[n & 1], both);
     }
     __syncwarp();
@@ -878,7 +883,7 @@ __device__ __forceinline__ void gemm_results(const GemmArgs& a, GemmShared& sh, 
   uint32_t n = 0, batch = 0;
   for (GemmWalk<SWIGLU> k(a, sh); k.t < k.tiles; k.t += k.step, ++n) {
     const GemmTile w = k.tile(a, sh);
-    if (!gemm_dead(sh)) gemm_wait(&sh.acc_full[n & 1], n >> 1 & 1, sh);   // (dead: NaN)
+    if (!gemm_dead(sh)) gemm_wait(&sh.acc_full[n & 1], n >> 1 & 1, sh, a);   // (dead: NaN)
     tc_fence_after();
     const uint32_t acc = tm + (n & 1) * kGemmTokens;
     // tokens go to splits and groups in turn, `unit` at a time; the groups begin in
@@ -969,7 +974,7 @@ __device__ __forceinline__ void gemm_results(const GemmArgs& a, GemmShared& sh, 
         st_async_f32((lane < 16 ? here : there) + t * 4, top, lane < 16 ? bar_here : bar_there);
       }
       if (c1 + step >= w.N) release();
-      const bool lost = !gemm_wait(bar, batch >> 1 & 1, sh) || dead;
+      const bool lost = !gemm_wait(bar, batch >> 1 & 1, sh, a) || dead;
       if (gt < 64) {
         float amax = 0.f;
 #pragma unroll
@@ -1049,7 +1054,6 @@ static __global__ void __launch_bounds__(kGemmThreads, 1)
     if (s == 0) {
       mbar_init(&sh.drained, 1);
       sh.dead = 0;
-      sh.wait_ns = a.wait_ns;
       asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.w) : "memory");
     }
     fence_barrier_init();
@@ -1106,6 +1110,8 @@ static __global__ void __launch_bounds__(kGemmThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0) gemm_spread(sh);
+  __syncwarp();
   cluster_sync();   // (nor does a CTA leave while another may read its sums)
   if (gemm_dead(sh)) {
     // (no wait is left to run out, so all of the cluster are here or none)  Products,
