@@ -143,6 +143,40 @@ long long tiles_at_most(const GemmArgs& a, bool swiglu) {
   return m * ((a.n + cols - 1) / cols);
 }
 
+// Clusters of `ctas` CTAs of the product kernel (each has an SM to itself) that the
+// current device holds at once: fewer than its SMs would make, where a GPC's are no
+// multiple of `ctas` (of 152, 36 of four and 15 of eight).  Asked for once per device.
+int clusters_at_once(int ctas, int* out) {
+  static std::atomic<int> known[kMaxDevices][4];   // by log2(ctas), one more than they are
+  int dev = 0, at = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  while (2 << at <= ctas) ++at;
+  int n = known[dev][at].load(std::memory_order_relaxed);
+  if (!n) {
+    void (*kernel)(GemmArgs, GemmMaps) = fp8_product_kernel<false, false, 1>;
+    cudaLaunchAttribute of{};
+    of.id = cudaLaunchAttributeClusterDimension;
+    of.val.clusterDim.x = ctas;
+    of.val.clusterDim.y = of.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kGemmThreads);
+    cfg.dynamicSmemBytes = GemmShape::LIMIT;
+    cfg.attrs = &of;
+    cfg.numAttrs = 1;
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  GemmShape::LIMIT)) ||
+        (e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg))) {
+      cudaGetLastError();
+      return cuda_fail(e);
+    }
+    known[dev][at].store(++n, std::memory_order_relaxed);   // (alike in every thread)
+  }
+  *out = n - 1;
+  return MOE_OK;
+}
+
 // moe_debug_set_product_fault's
 std::atomic<int> product_fault{0};
 std::atomic<unsigned long long> product_wait_ns{0};
@@ -163,8 +197,15 @@ int launch_product(GemmArgs a, const GemmMaps& maps, int n_sm, cudaStream_t st) 
   a.wait_ns = a.fault ? product_wait_ns.load(std::memory_order_relaxed) : 0;
   if (!a.wait_ns) a.wait_ns = kWaitLimitNs;
   a.splits = 1;
-  while (a.splits < kGemmMaxSplits && 2 * a.splits * tiles <= pairs && 2 * a.splits <= groups)
+  while (a.splits < kGemmMaxSplits && 2 * a.splits * tiles <= pairs && 2 * a.splits <= groups) {
+    // (a cluster more than fit takes the call twice as long: one row times 4,096 x
+    // 4,096, 16 tiles, by four pairs each 16.3 us, by two 9.5)
+    int fit;
+    const int rc = clusters_at_once(4 * a.splits, &fit);
+    if (rc) return rc;
+    if (tiles > fit) break;
     a.splits *= 2;
+  }
   const int grid = 2 * a.splits * (int)std::min<long long>(pairs / a.splits, tiles);
   return launch(fp8_product_kernel<W4, SWIGLU, PER>, grid, 1, kGemmThreads, smem, 2 * a.splits, st,
                 a, maps);

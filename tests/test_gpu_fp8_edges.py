@@ -248,3 +248,18 @@ def test_rows_by_index_of_one_matrix(rows):
     assert M.lib().moe_fp8_product(torch.cuda.current_stream().cuda_stream, args) == M.MOE_OK
     p, tol = ref.product(ref.row_values(x, xs)[src], ref.weight_values(w, ws, False))
     ref.check_values(out, p, tol, torch.float32, rows)
+
+
+@pytest.mark.parametrize("tiles", [9, 15, 16, 19, 20, 36, 37, 38, 39])
+@pytest.mark.parametrize("mx", [False, True])
+def test_tiles_beside_the_splits_of_k(tiles, mx):
+    """Numbers of tiles around those up to which K is split over a cluster of two and of
+    four pairs: what fits beside one another is fewer than the SMs would make."""
+    rng = np.random.default_rng(tiles)
+    rows, n, k = 5, 256 * tiles, 1024
+    x, xs = ref.random_x(rng, rows, k)
+    w, ws = ref.random_w(rng, n, k, mx)
+    p, tol = ref.product(ref.row_values(x, xs), ref.weight_values(w, ws, mx))
+    got = M.fp8_linear(_codes(x), _scales(xs), _dev(w) if mx else _codes(w), _scales(ws),
+                       out_dtype=torch.float32)
+    ref.check_values(got, p, tol, torch.float32, tiles)
