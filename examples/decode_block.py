@@ -8,7 +8,8 @@ One step is kv_plan (blocks and slots for this step's tokens), the projections
 tables and the free stack stay on the device, so the decode step is captured
 into a CUDA graph once and replayed for every token; kv_release gives a
 finished request's blocks back.  PromptLayer is the MoE layer for any number of
-rows, with 8-bit activations on the same expert weights.
+rows, with 8-bit activations.  Its products read the experts' canonical layout,
+MoELayer the tcgen05 path's, so each has the weights once.
 """
 import os
 import sys

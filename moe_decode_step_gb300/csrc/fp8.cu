@@ -331,8 +331,11 @@ int moe_fp8_product(void* stream, const moe_fp8_product_t* args) {
                                    : t.n_rows;
   const int tokens = (int)std::min<long long>(kGemmTokens, (std::max(many, 32ll) + 15) / 16 * 16);
   // Two blocks a copy where the copy engine bounds: MXFP4 weights, whose rows are
-  // half as long, with few tokens (a verify step's experts 294 us, one by one 316);
-  // elsewhere the coarser ring costs more (a prompt's gates and ups 516 us for 481).
+  // half as long, with few tokens; with more the coarser ring costs more.  Gates and
+  // ups of 64 experts, 2,048 x 7,168, by the rows of each: 10 (tiles of 32 at most) 163
+  // us, one by one 174; 42 (128) 185 and 187; 48 (144) 218 and 198; 160 (240) 303 and
+  // 277.  One matrix, 10,240 x 7,168: 32 rows 14.9 and 17.1, 128 18.9 both, 129 22.0
+  // and 20.0.  (K of 896: the same within 3% on both sides.)
   const int per = w4 && tokens <= 128 ? 2 : 1;
   GemmMaps maps;
   if (!t.rows) {

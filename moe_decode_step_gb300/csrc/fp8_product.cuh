@@ -24,13 +24,16 @@
 // tiles than pairs split K over `splits` pairs of a cluster, which add up through
 // distributed shared memory, always in the same order.
 //
-// Measured on the device: 8 tokens of 16 of 896 MXFP4 experts, gates and ups 4,096 x
-// 7,168, 286 us, 97% of a copy's rate; one row times 7,168 x 8,192 15 us, 64 rows times
-// 10,240 x 7,168 18, of which 6 to 7 are the start and the end; 8,192 rows times 7,168 x
-// 8,192 300 us, 3.2 PFLOP/s (power, and shared memory's 128 bytes a cycle); 4,096 tokens
-// of 8 of 128 experts, gates and ups 4,096 x 4,096, 490 us, and 7,168 x 2,048 in MXFP4
-// 385 us, 2.2 and 2.5 PFLOP/s (copies, shared memory and the exchange of results: the
-// tensor cores are busy half of the time).
+// Measured on the device, calls in a graph (and one by one with the caches flushed
+// between them, the host's time included): 8 tokens of 16 of 896 MXFP4 experts, gates
+// and ups 4,096 x 7,168, 288 us (286), 97% of a copy's rate; one row times 7,168 x 8,192
+// 15.6 (15.8), 28 tiles by two pairs each, of which 7 are the start, the end and the
+// join, then 7.0 TB/s; 64 rows times 10,240 x 7,168 18.6 (18.9), 40 tiles on 80 SMs, 7 and
+// 6.1 TB/s; 8,192 rows times 7,168 x 8,192 274 to 300 (320), 3.2 to 3.5 PFLOP/s (power,
+// and shared memory's 128 bytes a cycle); 4,096 tokens of 8 of 128 experts, gates and ups
+// 4,096 x 4,096, 485 to 525 (575), and 7,168 x 2,048 in MXFP4 380 to 400 (439), 2.1 to 2.3
+// and 2.4 to 2.5 PFLOP/s (copies, shared memory and the exchange of results: the tensor
+// cores are busy half of the time).
 #pragma once
 
 #include <cuda.h>

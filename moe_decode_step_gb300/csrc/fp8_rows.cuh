@@ -4,8 +4,8 @@
 // outputs, 8 elements (16 bytes of bf16) at a time, so that x and the residual
 // are read once.  HBM bounds long calls, the launch short ones.  A scale's 128
 // columns are 16 neighbouring lanes' elements: its maximum takes four shuffles.
-// Measured on the device: 8,192 rows of 7,168 with a residual and both outputs 80 us,
-// 6.6 TB/s; one row 3.4 us.
+// Measured on the device: 8,192 rows of 7,168 with a residual and both outputs 79 us,
+// 6.7 TB/s; one row 3.5 us.
 #pragma once
 
 #include <stdint.h>
@@ -223,7 +223,8 @@ static __global__ void __launch_bounds__(T < 256 ? 256 : T)
 }
 
 // Weights: a CTA of 256 threads per 128 x 128, whose elements are read singly (k
-// may be odd) and twice, the second time out of the caches.  A one-time layout.
+// may be odd) and twice, the second time out of the caches.  A one-time layout: 16
+// matrices of 4,096 x 7,168 bf16 1.74 ms, 0.81 TB/s.
 template <int DTYPE>
 __device__ __forceinline__ float pack_element(const void* w, long long at) {
   if (DTYPE == MOE_DTYPE_F32) return static_cast<const float*>(w)[at];
