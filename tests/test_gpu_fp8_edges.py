@@ -263,3 +263,26 @@ def test_tiles_beside_the_splits_of_k(tiles, mx):
     got = M.fp8_linear(_codes(x), _scales(xs), _dev(w) if mx else _codes(w), _scales(ws),
                        out_dtype=torch.float32)
     ref.check_values(got, p, tol, torch.float32, tiles)
+
+
+def test_first_call_of_a_process_is_captured():
+    """What the host asks the device once (how many clusters fit) a capture allows."""
+    code = """
+import torch, moe_decode_step_gb300 as M
+x = torch.randint(0, 120, (5, 2048), dtype=torch.uint8, device="cuda")
+w = torch.randint(0, 120, (4096, 2048), dtype=torch.uint8, device="cuda")
+xs = torch.full((5, 16), 120, dtype=torch.uint8, device="cuda")
+ws = torch.full((32, 16), 120, dtype=torch.uint8, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out = M.fp8_linear(x, xs, w, ws)
+g.replay()
+torch.cuda.synchronize()
+assert torch.equal(out, M.fp8_linear(x, xs, w, ws))
+"""
+    import os
+    import subprocess
+    import sys
+    subprocess.run([sys.executable, "-c", code], check=True,
+                   cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
